@@ -105,6 +105,19 @@ typedef enum svdq_epilogue {
     SVDQ_EPILOGUE_INT_RANGE_ = 0x7FFFFFFF    /* not an epilogue: every int is a valid value (calls reject it) */
 } svdq_epilogue;
 
+typedef enum svdq_norm {
+    SVDQ_NORM_NONE = 0,
+    SVDQ_NORM_RMS = 1,      /* v / sqrt(mean(v^2) + eps) */
+    SVDQ_NORM_LAYER = 2,    /* the same of v - mean(v) */
+    SVDQ_NORM_INT_RANGE_ = 0x7FFFFFFF        /* not a norm: every int is a valid value (calls reject it) */
+} svdq_norm;
+
+typedef enum svdq_stream_type {
+    SVDQ_STREAM_BF16 = 0,
+    SVDQ_STREAM_FP32 = 1,
+    SVDQ_STREAM_INT_RANGE_ = 0x7FFFFFFF      /* not a type: every int is a valid value (calls reject it) */
+} svdq_stream_type;
+
 #define SVDQ_RANK 32
 
 /* Every matrix a call touches (M x K, N x K, M x N) must hold fewer than
@@ -460,6 +473,46 @@ svdq_status svdq_nf4_dequantize(const uint8_t *wq, const uint8_t *qabs, const fl
 svdq_status svdq_nf4_w4a16_linear(const uint16_t *X, const uint8_t *wq, const uint8_t *qabs,
                                   const float *chunk_scale, const uint16_t *bias, int M, int N, int K, uint16_t *Y,
                                   void *stream);
+
+/*
+ * svdq_residual_norm -- the step between two linears of a transformer block:
+ * the gated residual update with the norms before and after it and the
+ * modulation of the next block's input, whose shift, scale and gate vectors a
+ * modulation layer (svdq_awq_w4a16_linear) computes.  Per row m:
+ *   t  = post(y_m) * post_w
+ *   r' = r_m + alpha * gate_b * t                            -> r_out
+ *   x  = (pre(r') * pre_w + pre_b) * (1 + scale_b) + shift_b -> x
+ * in fp32 from the loads to the stores (x is formed from the unrounded r';
+ * r_out and x are rounded once, to nearest even).  The sums of squares are
+ * fp32, so a row's values must stay below about 1e19 in magnitude.
+ *
+ *   r          [M][D], stype, device            the residual stream
+ *   stype      SVDQ_STREAM_BF16 or SVDQ_STREAM_FP32: type of r and r_out
+ *   y          [M][D] bf16 bits, device, or NULL: the block's output.  NULL:
+ *              r' = r, and r_out, post_w and gate must be NULL too and post NONE
+ *   M, D       M >= 0 (0: no-op); 8 <= D <= 16384, D % 8 == 0
+ *   post, pre  norms; pre NONE and post NONE pass the values on
+ *   post_w, pre_w, pre_b   [D] bf16 bits, device, or NULL (1, 1, 0)
+ *   gate, scale, shift     row b at b * mod_stride, [mod_rows][D] bf16 bits
+ *              (slices of one modulation output), device, or NULL (1, 0, 0)
+ *   mod_index  [M] int32, device, or NULL: b of every row; a value outside
+ *              [0, mod_rows) takes gate 1, scale 0, shift 0.  NULL: the rows
+ *              are mod_rows equal runs (SVDQ_ERR_SHAPE unless M % mod_rows == 0)
+ *   mod_rows, mod_stride   read when gate, scale or shift is given: mod_rows
+ *              >= 1; mod_stride >= D, % 8 == 0; mod_rows * mod_stride below
+ *              SVDQ_MAX_ELEMENTS
+ *   alpha      residual scale, finite;   eps  finite, >= 0 (both norms)
+ *   r_out      [M][D], stype, device (out); may be r itself
+ *   x          [M][D] bf16 bits, device (out), or NULL: only r_out; pre and
+ *              scale and shift are then not applied.  May be y itself, not r
+ * One kernel launch.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE,
+ * SVDQ_ERR_MISALIGNED, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
+ */
+svdq_status svdq_residual_norm(const void *r, svdq_stream_type stype, const uint16_t *y, int M, int D,
+                               svdq_norm post, const uint16_t *post_w, const uint16_t *gate, float alpha,
+                               svdq_norm pre, const uint16_t *pre_w, const uint16_t *pre_b, const uint16_t *scale,
+                               const uint16_t *shift, const int32_t *mod_index, int mod_rows, int mod_stride,
+                               float eps, void *r_out, uint16_t *x, void *stream);
 
 #ifdef __cplusplus
 }

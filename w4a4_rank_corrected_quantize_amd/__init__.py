@@ -15,6 +15,7 @@ Functions mirror the C ABI in include/svdq.h:
     w4a4_linear_qkv_norm_rope(...)                              device, torch tensors
     awq_pack_weights(W)                                         host, numpy in/out
     awq_w4a16_linear(X, wq, wscale, bias, ...)                  device, torch tensors
+    residual_norm(r, y, gate, ..., scale, shift, ...)           device, torch tensors
 
 Device tensors: X bf16 [M][K], smooth fp32 [K], down bf16 [32][K],
 up bf16 [N][32], bias bf16 [N] or None, xq uint8 [M][K/2],
@@ -38,6 +39,9 @@ INT4 = 0
 MXFP4 = 1
 EPI_NONE = 0
 EPI_GELU_TANH = 1
+NORM_NONE = 0
+NORM_RMS = 1
+NORM_LAYER = 2
 RANK = 32
 
 STATUS = {
@@ -50,7 +54,7 @@ EXPORTS = ("svdq_status_string", "svdq_version", "svdq_check_device", "svdq_pack
            "svdq_w4a4_linear_requant", "svdq_w4a4_linear_qkv_norm_rope", "svdq_awq_pack_weights",
            "svdq_awq_w4a16_linear", "svdq_w4a4_linear_splitk_workspace_bytes", "svdq_w4a4_linear_splitk",
            "svdq_nf4_codebook", "svdq_nf4_pack_weights", "svdq_nf4_dequantize", "svdq_nf4_w4a16_linear",
-           "svdq_w4a4_linear_splitk_noalloc")
+           "svdq_w4a4_linear_splitk_noalloc", "svdq_residual_norm")
 
 
 class SvdqError(RuntimeError):
@@ -111,6 +115,9 @@ def lib():
         L.svdq_nf4_dequantize.argtypes = [P, P, P, I, I, P, P]
         L.svdq_nf4_w4a16_linear.restype = I
         L.svdq_nf4_w4a16_linear.argtypes = [P, P, P, P, P, I, I, I, P, P]
+        F = ctypes.c_float
+        L.svdq_residual_norm.restype = I
+        L.svdq_residual_norm.argtypes = [P, I, P, I, I, I, P, P, F, I, P, P, P, P, P, I, I, F, P, P, P]
         _lib = L
     return _lib
 
@@ -494,6 +501,119 @@ def nf4_w4a16_linear(X, wq, qabs, chunk, bias=None, Y=None, stream=None):
     st = lib().svdq_nf4_w4a16_linear(pX, pq, pa, pc, pb, M, N, K, pY, _stream(stream))
     _check(st, "svdq_nf4_w4a16_linear")
     return Y
+
+
+# The calls below run between the linears, often on a few rows, so their checks
+# are kept short: one helper call per tensor, raw pointers, one device lookup.
+
+def _arg(t, dtype, name, shape=None):
+    """Pointer of a contiguous tensor of this dtype (and shape) on the current
+    device; type, dtype, shape and contiguity are checked before the device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _rows_arg(t, dtype, name, shape):
+    """A 2-D tensor whose rows are contiguous but may be a stride apart (a
+    slice of a wider tensor)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t
+
+
+def _on_device(dev, **tensors):
+    """Every tensor given lies on `dev`, and `dev` is the current device (the
+    library launches there)."""
+    torch = _torch()
+    if dev.type != "cuda":
+        raise TypeError("the tensors must be device tensors")
+    if torch.cuda.current_device() != dev.index:
+        raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NONE, post_w=None, pre: int = NORM_RMS,
+                  pre_w=None, pre_b=None, scale=None, shift=None, mod_index=None, eps: float = 1e-6, r_out=None,
+                  x=None, want_x: bool = True, stream=None):
+    """r' = r + alpha gate post(y), x = pre(r') (1 + scale) + shift (one
+    kernel).  r, y [M][D]; r bf16 or fp32, y bf16 or None (r' = r); gate,
+    scale, shift [B][D] slices of one modulation output (same row stride), row
+    of token m by mod_index [M] int32, or B equal runs of tokens.  Returns
+    (r', x): r' is `r` itself without y, x is None with want_x=False.  r_out
+    may be r (in place)."""
+    torch = _torch()
+    bf, f32 = torch.bfloat16, torch.float32
+    _ndim(r, 2, "r")
+    if r.dtype is not bf and r.dtype is not f32:
+        raise TypeError(f"r has dtype {r.dtype}, expected {(bf, f32)}")
+    shape = r.shape
+    M, D = shape
+    _arg(r, r.dtype, "r")
+    if y is not None:
+        _arg(y, bf, "y", shape)
+        r_out = torch.empty_like(r) if r_out is None else _arg(r_out, r.dtype, "r_out", shape)
+    elif r_out is not None:
+        raise ValueError("r_out without y: nothing to update")
+    if want_x:
+        x = torch.empty(shape, dtype=bf, device=r.device) if x is None else _arg(x, bf, "x", shape)
+    elif x is not None:
+        raise ValueError("x given with want_x=False")
+    vec = (D,)
+    for t, name in ((post_w, "post_w"), (pre_w, "pre_w"), (pre_b, "pre_b")):
+        if t is not None:
+            _arg(t, bf, name, vec)
+    B = ld = 0
+    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if t is None:
+            continue
+        if not B:
+            _ndim(t, 2, name)
+            B = t.shape[0]
+            if B == 0:
+                raise ValueError(f"{name} has no rows")
+        _rows_arg(t, bf, name, (B, D))
+        if B > 1:
+            if ld and t.stride(0) != ld:
+                raise ValueError("gate, scale and shift must have the same row stride")
+            ld = t.stride(0)
+    if mod_index is not None:
+        _arg(mod_index, torch.int32, "mod_index", (M,))
+    dev = r.device
+    _on_device(dev, y=y, gate=gate, scale=scale, shift=shift, mod_index=mod_index, post_w=post_w, pre_w=pre_w,
+               pre_b=pre_b, r_out=r_out, x=x)
+    st = lib().svdq_residual_norm(r.data_ptr(), 1 if r.dtype is f32 else 0, _ptr(y), M, D, post, _ptr(post_w),
+                                  _ptr(gate), alpha, pre, _ptr(pre_w), _ptr(pre_b), _ptr(scale), _ptr(shift),
+                                  _ptr(mod_index), B, ld or D, eps, _ptr(r_out), _ptr(x), _raw_stream(stream, dev))
+    if st:
+        raise SvdqError(st, "svdq_residual_norm")
+    return (r if y is None else r_out), x
 
 
 def to_device(packed: dict, device="cuda") -> dict:

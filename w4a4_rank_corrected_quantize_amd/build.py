@@ -33,6 +33,7 @@ SOURCES = {
     "w4a4_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "awq_gemv.hip": [],
     "nf4_gemm.hip": [],
+    "residual_norm.hip": [],
 }
 
 

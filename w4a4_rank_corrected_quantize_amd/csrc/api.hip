@@ -50,6 +50,8 @@ svdq_status check_common(int M, int K, int rank, svdq_precision prec)
     return SVDQ_OK;
 }
 
+bool norm_ok(svdq_norm n) { return n == SVDQ_NORM_NONE || n == SVDQ_NORM_RMS || n == SVDQ_NORM_LAYER; }
+
 // the weight and output matrices of a linear
 svdq_status check_linear_sizes(int M, int N, int K)
 {
@@ -312,6 +314,45 @@ extern "C" svdq_status svdq_nf4_w4a16_linear(const uint16_t *X, const uint8_t *w
     if (st != SVDQ_OK) return st;
     if (M == 0 || N == 0) return SVDQ_OK;
     hipError_t e = launch_nf4_linear(X, wq, qabs, chunk_scale, bias, M, N, K, nf4_levels_arg(), Y, (hipStream_t)stream);
+    return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+extern "C" svdq_status svdq_residual_norm(const void *r, svdq_stream_type stype, const uint16_t *y, int M, int D,
+                                          svdq_norm post, const uint16_t *post_w, const uint16_t *gate, float alpha,
+                                          svdq_norm pre, const uint16_t *pre_w, const uint16_t *pre_b,
+                                          const uint16_t *scale, const uint16_t *shift, const int32_t *mod_index,
+                                          int mod_rows, int mod_stride, float eps, void *r_out, uint16_t *x,
+                                          void *stream)
+{
+    if (stype != SVDQ_STREAM_BF16 && stype != SVDQ_STREAM_FP32) return SVDQ_ERR_INVALID_ARG;
+    if (!norm_ok(post) || !norm_ok(pre)) return SVDQ_ERR_INVALID_ARG;
+    if (M < 0 || D < 0) return SVDQ_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || eps > 3.0e38f || !(alpha >= -3.0e38f && alpha <= 3.0e38f)) return SVDQ_ERR_INVALID_ARG;
+    if (D < 8 || D % 8 != 0 || D > 16384 || !elems_ok(M, D)) return SVDQ_ERR_SHAPE;
+    // without a block output there is no update; without x nothing to normalize
+    if (M > 0 && y == nullptr && (post != SVDQ_NORM_NONE || post_w || gate || r_out)) return SVDQ_ERR_INVALID_ARG;
+    if (M > 0 && (!r || (y && !r_out) || (!y && !x) || (x && x == r))) return SVDQ_ERR_INVALID_ARG;
+    if (gate || scale || shift) {
+        if (mod_rows < 1) return SVDQ_ERR_INVALID_ARG;
+        if (mod_stride < D || mod_stride % 8 != 0 || !elems_ok(mod_rows, mod_stride)) return SVDQ_ERR_SHAPE;
+        if (!mod_index && M % mod_rows != 0) return SVDQ_ERR_SHAPE;
+    }
+    if (!aligned16(r) || !aligned16(y) || !aligned16(post_w) || !aligned16(gate) || !aligned16(pre_w) ||
+        !aligned16(pre_b) || !aligned16(scale) || !aligned16(shift) || !aligned16(mod_index) || !aligned16(r_out) ||
+        !aligned16(x))
+        return SVDQ_ERR_MISALIGNED;
+    svdq_status st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (M == 0) return SVDQ_OK;
+    ResidualNormArgs a{};
+    a.r = r, a.y = y, a.post_w = post_w, a.gate = gate, a.pre_w = pre_w, a.pre_b = pre_b, a.scale = scale;
+    a.shift = shift, a.r_out = r_out, a.x = x, a.M = M, a.D = D, a.post = post, a.pre = pre;
+    a.alpha = alpha, a.eps = eps, a.rows_per_mod = 1;
+    if (gate || scale || shift) {
+        a.mod_index = mod_index, a.mod_rows = mod_rows, a.mod_stride = mod_stride;
+        if (!mod_index) a.rows_per_mod = M / mod_rows;
+    }
+    hipError_t e = launch_residual_norm(a, stype == SVDQ_STREAM_FP32, (hipStream_t)stream);
     return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
 }
 

@@ -1,0 +1,226 @@
+// residual_norm.hip -- the step between two 4-bit linears of a transformer
+// block: norm of the block's output, gate and residual scale, norm of the new
+// residual stream and its modulation, in one pass over the rows.
+//
+//   t  = post(y_m) * post_w                    post: none, RMS or LayerNorm
+//   r' = r_m + (alpha gate_b) t                stored in the stream's type
+//   x  = (pre(r') * pre_w + pre_b) (1 + scale_b) + shift_b        bf16
+//   RMS(v) = v / sqrt(mean(v^2) + eps);  LayerNorm(v) = RMS(v - mean(v))
+//
+// Everything between the loads and the two stores is fp32: x is formed from
+// the unrounded r' (one rounding each for r' and x).  The variance is taken
+// of the centred values held in registers, not as a difference of moments.
+//
+// Bound by HBM: r and y are read once, r' and x written once; the modulation
+// vectors are shared by many rows and come from the L2.
+#include "svdq_internal.h"
+#include "svdq_quant.h"
+
+namespace svdq {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t rn_pack2(float lo, float hi)
+{
+    const f32x2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));   // round to nearest even
+}
+
+__device__ __forceinline__ void rn_unpack8(const uint4 &u, float (&f)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bits_f32(w[i] << 16);
+        f[2 * i + 1] = bits_f32(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 rn_pack8(const float (&f)[8])
+{
+    return make_uint4(rn_pack2(f[0], f[1]), rn_pack2(f[2], f[3]), rn_pack2(f[4], f[5]), rn_pack2(f[6], f[7]));
+}
+
+template <bool FP32>
+__device__ __forceinline__ void rn_load_stream(const void *p, size_t off, float (&f)[8])
+{
+    if constexpr (FP32) {
+        const float4 a = *reinterpret_cast<const float4 *>((const float *)p + off);
+        const float4 b = *reinterpret_cast<const float4 *>((const float *)p + off + 4);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+        rn_unpack8(*reinterpret_cast<const uint4 *>((const uint16_t *)p + off), f);
+    }
+}
+
+// Sum over the T threads of a row; every thread gets it.  The order is fixed.
+template <int T>
+__device__ __forceinline__ float rn_row_sum(float v, float *red)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    if constexpr (T > 64) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) red[wave] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < T / 64; ++w) v += red[w];
+        __syncthreads();
+    }
+    return v;
+}
+
+// v <- v / sqrt(mean(v^2) + eps), centred first for LayerNorm.  Elements past
+// D are zero on entry and stay out of the sums.
+template <int T, int C>
+__device__ __forceinline__ void rn_normalize(float (&v)[C][8], int kind, int D, float inv_d, float eps, int t,
+                                             float *red)
+{
+    if (kind == SVDQ_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[c][i];
+        const float mean = rn_row_sum<T>(s, red) * inv_d;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const bool in = 8 * (t + c * T) < D;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] = in ? v[c][i] - mean : 0.0f;
+        }
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q = __builtin_fmaf(v[c][i], v[c][i], q);
+    const float rs = 1.0f / __builtin_sqrtf(rn_row_sum<T>(q, red) * inv_d + eps);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= rs;
+}
+
+// T threads per row (64: four rows per block of 256), C chunks of 8 channels
+// per thread: chunk c of thread t is channels 8 (t + c T) .. + 7.
+template <int T, int C, bool FP32>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(ResidualNormArgs a)
+{
+    __shared__ float red[T < 256 ? 1 : T / 64];
+    constexpr int ROWS = T < 256 ? 256 / T : 1;
+    const int t = threadIdx.x % T;
+    const int m = blockIdx.x * ROWS + threadIdx.x / T;
+    if (m >= a.M) return;                           // whole waves (T = 64) or none (one row per block)
+    const int D = a.D;
+    const float inv_d = 1.0f / (float)D;
+    const size_t row = (size_t)m * D;
+    int b = a.mod_index ? a.mod_index[m] : m / a.rows_per_mod;
+    const bool mod = (uint32_t)b < (uint32_t)a.mod_rows;
+    const size_t mrow = mod ? (size_t)b * a.mod_stride : 0;
+
+    float v[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = 8 * (t + c * T);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
+        if (k < D) {
+            if (a.y) rn_unpack8(*reinterpret_cast<const uint4 *>(a.y + row + k), v[c]);
+            else rn_load_stream<FP32>(a.r, row + k, v[c]);
+        }
+    }
+    if (a.y) {
+        float r[C][8];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = 8 * (t + c * T);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[c][i] = 0.0f;
+            if (k < D) rn_load_stream<FP32>(a.r, row + k, r[c]);
+        }
+        if (a.post != SVDQ_NORM_NONE) rn_normalize<T, C>(v, a.post, D, inv_d, a.eps, t, red);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = 8 * (t + c * T);
+            if (k < D) {
+                if (a.post_w) {
+                    float w[8];
+                    rn_unpack8(*reinterpret_cast<const uint4 *>(a.post_w + k), w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
+                }
+                float g[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+                if (a.gate && mod) rn_unpack8(*reinterpret_cast<const uint4 *>(a.gate + mrow + k), g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(a.alpha * g[i], v[c][i], r[c][i]);
+                if constexpr (FP32) {
+                    float *o = (float *)a.r_out + row + k;
+                    *reinterpret_cast<float4 *>(o) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+                    *reinterpret_cast<float4 *>(o + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
+                } else {
+                    *reinterpret_cast<uint4 *>((uint16_t *)a.r_out + row + k) = rn_pack8(v[c]);
+                }
+            }
+        }
+    }
+    if (!a.x) return;
+    if (a.pre != SVDQ_NORM_NONE) rn_normalize<T, C>(v, a.pre, D, inv_d, a.eps, t, red);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = 8 * (t + c * T);
+        if (k >= D) continue;
+        float f[8];
+        if (a.pre_w) {
+            rn_unpack8(*reinterpret_cast<const uint4 *>(a.pre_w + k), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] *= f[i];
+        }
+        if (a.pre_b) {
+            rn_unpack8(*reinterpret_cast<const uint4 *>(a.pre_b + k), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] += f[i];
+        }
+        if (a.scale && mod) {
+            rn_unpack8(*reinterpret_cast<const uint4 *>(a.scale + mrow + k), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(v[c][i], f[i], v[c][i]);
+        }
+        if (a.shift && mod) {
+            rn_unpack8(*reinterpret_cast<const uint4 *>(a.shift + mrow + k), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] += f[i];
+        }
+        *reinterpret_cast<uint4 *>(a.x + row + k) = rn_pack8(v[c]);
+    }
+}
+
+template <int T, int C>
+hipError_t rn_launch(const ResidualNormArgs &a, bool fp32, hipStream_t stream)
+{
+    const int rows = T < 256 ? 256 / T : 1;
+    const dim3 grid((a.M + rows - 1) / rows), block(T < 256 ? 256 : T);
+    if (fp32) residual_norm_kernel<T, C, true><<<grid, block, 0, stream>>>(a);
+    else residual_norm_kernel<T, C, false><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_residual_norm(const ResidualNormArgs &a, bool fp32, hipStream_t stream)
+{
+    const int D = a.D;
+    if (D <= 512) return rn_launch<64, 1>(a, fp32, stream);
+    if (D <= 1024) return rn_launch<64, 2>(a, fp32, stream);
+    if (D <= 2048) return rn_launch<256, 1>(a, fp32, stream);
+    if (D <= 4096) return rn_launch<256, 2>(a, fp32, stream);
+    if (D <= 8192) return rn_launch<256, 4>(a, fp32, stream);
+    return rn_launch<256, 8>(a, fp32, stream);
+}
+
+}  // namespace svdq

@@ -79,4 +79,17 @@ hipError_t launch_nf4_linear(const uint16_t *X, const uint8_t *wq, const uint8_t
                              const uint16_t *bias, int M, int N, int K, const Nf4Levels &lv, uint16_t *Y,
                              hipStream_t stream);
 
+// Gated residual, norms and modulation between two blocks (residual_norm.hip).
+// y NULL: x from r alone; x NULL: the residual alone.
+struct ResidualNormArgs {
+    const void *r;
+    const uint16_t *y, *post_w, *gate, *pre_w, *pre_b, *scale, *shift;
+    const int32_t *mod_index;
+    void *r_out;
+    uint16_t *x;
+    int M, D, post, pre, mod_rows, mod_stride, rows_per_mod;
+    float alpha, eps;
+};
+hipError_t launch_residual_norm(const ResidualNormArgs &a, bool fp32, hipStream_t stream);
+
 }  // namespace svdq
