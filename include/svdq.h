@@ -514,6 +514,68 @@ svdq_status svdq_residual_norm(const void *r, svdq_stream_type stype, const uint
                                const uint16_t *shift, const int32_t *mod_index, int mod_rows, int mod_stride,
                                float eps, void *r_out, uint16_t *x, void *stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection: every row
+ * of a batch may carry its own adapter,
+ *   Y_m = base_m + scale_a (X_m A_a^T) B_a^T,   a = index[m]
+ * and rows without one keep base_m.  The batch's rows are grouped by adapter
+ * once per step (svdq_lora_plan); the plan then serves every projection of
+ * that step.
+ */
+#define SVDQ_LORA_MAX_RANK 128
+#define SVDQ_LORA_MAX_ADAPTERS 4096
+
+/* Device bytes of the plan of M rows and n_adapters adapters, and of the
+ * workspace of svdq_lora_linear on the current device (it holds fp32 slices
+ * of X A^T; their number depends on the device's compute units); 0 for sizes
+ * the calls do not take, and without a gfx950 device for the workspace. */
+size_t svdq_lora_plan_bytes(int M, int n_adapters);
+size_t svdq_lora_workspace_bytes(int M, int K, int rank, int n_adapters);
+
+/*
+ * svdq_lora_plan -- groups M rows by adapter.
+ *   index        [M] int32, device: adapter of every row; a value outside
+ *                [0, n_adapters) means no adapter
+ *   M            M >= 0 (0: no-op);  1 <= n_adapters <= SVDQ_LORA_MAX_ADAPTERS
+ *   plan, plan_bytes   device, at least svdq_lora_plan_bytes(M, n_adapters)
+ *                bytes, 16-byte aligned (out); valid until overwritten, read
+ *                only by the calls that use it
+ * One kernel launch (one block).  Errors: SVDQ_ERR_INVALID_ARG,
+ * SVDQ_ERR_SHAPE (M), SVDQ_ERR_UNSUPPORTED (n_adapters),
+ * SVDQ_ERR_MISALIGNED, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
+ */
+svdq_status svdq_lora_plan(const int32_t *index, int M, int n_adapters, void *plan, size_t plan_bytes,
+                           void *stream);
+
+/*
+ * svdq_lora_linear -- the adapters' part of a linear, added to `base`.
+ *   X        [M][K] bf16 bits, device: the linear's input
+ *   A        [n_adapters][rank][K] bf16 bits, device (down factors)
+ *   B        [n_adapters][N][rank] bf16 bits, device (up factors)
+ *   scale    [n_adapters] fp32, device
+ *   plan     written by svdq_lora_plan for the same M and n_adapters (a plan
+ *            of other sizes computes nothing)
+ *   base     [M][N] bf16 bits, device: the shared projection's output
+ *   M, N, K  M, N >= 0 (either 0: no-op); K >= 8; N % 8 == 0, K % 8 == 0
+ *   rank     8 .. 128, rank % 8 == 0 (SVDQ_ERR_UNSUPPORTED otherwise);
+ *            adapters of lower rank are padded with zero rows of A and zero
+ *            columns of B
+ *   Y        [M][N] bf16 bits, device (out); may be base itself (rows without
+ *            an adapter are then not touched)
+ *   work, work_bytes   device scratch of at least svdq_lora_workspace_bytes
+ *            bytes, 16-byte aligned, overwritten
+ * X A^T is summed in fp32 and enters the second product as a bf16 high and
+ * low part (16 bits of significand); that product, the scale and the sum with
+ * base are fp32, rounded once to bf16.  A row's result depends on that row
+ * and the sizes alone, so it is deterministic.  Two kernel launches.  Errors:
+ * SVDQ_ERR_INVALID_ARG (a too small workspace among them, checked after the
+ * device), SVDQ_ERR_SHAPE, SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_MISALIGNED,
+ * SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
+ */
+svdq_status svdq_lora_linear(const uint16_t *X, const uint16_t *A, const uint16_t *B, const float *scale,
+                             const void *plan, const uint16_t *base, int M, int N, int K, int rank, int n_adapters,
+                             uint16_t *Y, void *work, size_t work_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

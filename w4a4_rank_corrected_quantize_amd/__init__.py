@@ -16,6 +16,8 @@ Functions mirror the C ABI in include/svdq.h:
     awq_pack_weights(W)                                         host, numpy in/out
     awq_w4a16_linear(X, wq, wscale, bias, ...)                  device, torch tensors
     residual_norm(r, y, gate, ..., scale, shift, ...)           device, torch tensors
+    lora_plan(index, n_adapters)                                device, torch tensors
+    lora_linear(X, A, B, scale, plan, base, ...)                device, torch tensors
 
 Device tensors: X bf16 [M][K], smooth fp32 [K], down bf16 [32][K],
 up bf16 [N][32], bias bf16 [N] or None, xq uint8 [M][K/2],
@@ -54,7 +56,8 @@ EXPORTS = ("svdq_status_string", "svdq_version", "svdq_check_device", "svdq_pack
            "svdq_w4a4_linear_requant", "svdq_w4a4_linear_qkv_norm_rope", "svdq_awq_pack_weights",
            "svdq_awq_w4a16_linear", "svdq_w4a4_linear_splitk_workspace_bytes", "svdq_w4a4_linear_splitk",
            "svdq_nf4_codebook", "svdq_nf4_pack_weights", "svdq_nf4_dequantize", "svdq_nf4_w4a16_linear",
-           "svdq_w4a4_linear_splitk_noalloc", "svdq_residual_norm")
+           "svdq_w4a4_linear_splitk_noalloc", "svdq_residual_norm", "svdq_lora_plan_bytes",
+           "svdq_lora_workspace_bytes", "svdq_lora_plan", "svdq_lora_linear")
 
 
 class SvdqError(RuntimeError):
@@ -118,6 +121,15 @@ def lib():
         F = ctypes.c_float
         L.svdq_residual_norm.restype = I
         L.svdq_residual_norm.argtypes = [P, I, P, I, I, I, P, P, F, I, P, P, P, P, P, I, I, F, P, P, P]
+        Z = ctypes.c_size_t
+        L.svdq_lora_plan_bytes.restype = Z
+        L.svdq_lora_plan_bytes.argtypes = [I, I]
+        L.svdq_lora_workspace_bytes.restype = Z
+        L.svdq_lora_workspace_bytes.argtypes = [I, I, I, I]
+        L.svdq_lora_plan.restype = I
+        L.svdq_lora_plan.argtypes = [P, I, I, P, Z, P]
+        L.svdq_lora_linear.restype = I
+        L.svdq_lora_linear.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P, Z, P]
         _lib = L
     return _lib
 
@@ -614,6 +626,85 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     if st:
         raise SvdqError(st, "svdq_residual_norm")
     return (r if y is None else r_out), x
+
+
+class LoraPlan:
+    """Rows of one step grouped by adapter (`lora_plan`); `buffer` holds it on
+    the device, M and n_adapters are the sizes it was made for."""
+    __slots__ = ("buffer", "M", "n_adapters")
+
+    def __init__(self, buffer, M: int, n_adapters: int):
+        self.buffer, self.M, self.n_adapters = buffer, M, n_adapters
+
+
+def lora_plan(index, n_adapters: int, plan: Optional[LoraPlan] = None, stream=None) -> LoraPlan:
+    """Groups the rows by adapter: index [M] int32, a value outside [0,
+    n_adapters) means none (one kernel).  `plan` of the same sizes is
+    overwritten in place (as a captured graph needs)."""
+    torch = _torch()
+    _ndim(index, 1, "index")
+    _arg(index, torch.int32, "index")
+    M = index.shape[0]
+    if plan is None:
+        need = lib().svdq_lora_plan_bytes(M, n_adapters)
+        plan = LoraPlan(torch.empty(max(need, 16), dtype=torch.uint8, device=index.device), M, n_adapters)
+    elif plan.M != M or plan.n_adapters != n_adapters:
+        raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n_adapters}")
+    dev = index.device
+    _on_device(dev, plan=plan.buffer)
+    st = lib().svdq_lora_plan(index.data_ptr(), M, n_adapters, plan.buffer.data_ptr(), plan.buffer.numel(),
+                              _raw_stream(stream, dev))
+    if st:
+        raise SvdqError(st, "svdq_lora_plan")
+    return plan
+
+
+def lora_workspace_bytes(M: int, K: int, rank: int, n_adapters: int) -> int:
+    """Device scratch bytes that lora_linear needs on the current device."""
+    return int(lib().svdq_lora_workspace_bytes(M, K, rank, n_adapters))
+
+
+def lora_workspace(M: int, K: int, rank: int, n_adapters: int, device="cuda"):
+    """A workspace for lora_linear calls of these sizes (uint8 tensor)."""
+    torch = _torch()
+    return torch.empty(max(lora_workspace_bytes(M, K, rank, n_adapters), 16), dtype=torch.uint8, device=device)
+
+
+def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=None):
+    """Y = base + scale_a (X A_a^T) B_a^T for the adapter a of every row (two
+    kernels).  X [M][K], A [n][rank][K], B [n][N][rank], base [M][N] bf16,
+    scale [n] fp32; rows without an adapter keep base.  Y may be base (in
+    place).  When `work` is None it is allocated with torch."""
+    torch = _torch()
+    bf = torch.bfloat16
+    _ndim(X, 2, "X")
+    _ndim(A, 3, "A")
+    _ndim(base, 2, "base")
+    M, K = X.shape
+    n, R, _ = A.shape
+    N = base.shape[1]
+    _arg(X, bf, "X")
+    _arg(A, bf, "A", (n, R, K))
+    _arg(B, bf, "B", (n, N, R))
+    _arg(scale, torch.float32, "scale", (n,))
+    _arg(base, bf, "base", (M, N))
+    if not isinstance(plan, LoraPlan):
+        raise TypeError("plan must be a LoraPlan (lora_plan)")
+    if plan.M != M or plan.n_adapters != n:
+        raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n}")
+    dev = X.device
+    Y = torch.empty_like(base) if Y is None else _arg(Y, bf, "Y", (M, N))
+    if work is None:
+        work = torch.empty(max(lora_workspace_bytes(M, K, R, n), 16), dtype=torch.uint8, device=dev)
+    else:
+        _arg(work, torch.uint8, "work")
+    _on_device(dev, A=A, B=B, scale=scale, plan=plan.buffer, base=base, Y=Y, work=work)
+    st = lib().svdq_lora_linear(X.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), plan.buffer.data_ptr(),
+                                base.data_ptr(), M, N, K, R, n, Y.data_ptr(), work.data_ptr(), work.numel(),
+                                _raw_stream(stream, dev))
+    if st:
+        raise SvdqError(st, "svdq_lora_linear")
+    return Y
 
 
 def to_device(packed: dict, device="cuda") -> dict:

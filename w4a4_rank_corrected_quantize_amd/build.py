@@ -34,6 +34,7 @@ SOURCES = {
     "awq_gemv.hip": [],
     "nf4_gemm.hip": [],
     "residual_norm.hip": [],
+    "lora.hip": [],
 }
 
 

@@ -356,6 +356,69 @@ extern "C" svdq_status svdq_residual_norm(const void *r, svdq_stream_type stype,
     return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
 }
 
+static svdq_status check_lora(int M, int n_adapters)
+{
+    if (M < 0) return SVDQ_ERR_INVALID_ARG;
+    if (n_adapters < 1 || n_adapters > SVDQ_LORA_MAX_ADAPTERS) return SVDQ_ERR_UNSUPPORTED;
+    return elems_ok(M, 1) ? SVDQ_OK : SVDQ_ERR_SHAPE;
+}
+
+static svdq_status check_lora_down(int M, int K, int rank, int n_adapters)
+{
+    svdq_status st = check_lora(M, n_adapters);
+    if (st != SVDQ_OK) return st;
+    if (K < 0) return SVDQ_ERR_INVALID_ARG;
+    if (rank < 8 || rank > SVDQ_LORA_MAX_RANK || rank % 8 != 0) return SVDQ_ERR_UNSUPPORTED;
+    if (K < 8 || K % 8 != 0 || !elems_ok(M, K) || !elems_ok(n_adapters * rank, K)) return SVDQ_ERR_SHAPE;
+    return SVDQ_OK;
+}
+
+extern "C" size_t svdq_lora_plan_bytes(int M, int n_adapters)
+{
+    return check_lora(M, n_adapters) == SVDQ_OK && M > 0 ? lora_plan_size(M, n_adapters) : 0;
+}
+
+extern "C" size_t svdq_lora_workspace_bytes(int M, int K, int rank, int n_adapters)
+{
+    if (check_lora_down(M, K, rank, n_adapters) != SVDQ_OK || M == 0) return 0;
+    if (current_device_ok() != SVDQ_OK) return 0;       // the slices depend on the device's CU count
+    return lora_work_bytes(M, K, rank, n_adapters);
+}
+
+extern "C" svdq_status svdq_lora_plan(const int32_t *index, int M, int n_adapters, void *plan, size_t plan_bytes,
+                                      void *stream)
+{
+    svdq_status st = check_lora(M, n_adapters);
+    if (st != SVDQ_OK) return st;
+    if (M > 0 && (!index || !plan || plan_bytes < lora_plan_size(M, n_adapters))) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(index) || !aligned16(plan)) return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (M == 0) return SVDQ_OK;
+    return launch_lora_plan(index, M, n_adapters, plan, (hipStream_t)stream) == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+extern "C" svdq_status svdq_lora_linear(const uint16_t *X, const uint16_t *A, const uint16_t *B, const float *scale,
+                                        const void *plan, const uint16_t *base, int M, int N, int K, int rank,
+                                        int n_adapters, uint16_t *Y, void *work, size_t work_bytes, void *stream)
+{
+    svdq_status st = check_lora_down(M, K, rank, n_adapters);
+    if (st != SVDQ_OK) return st;
+    if (N < 0) return SVDQ_ERR_INVALID_ARG;
+    if (N % 8 != 0 || !elems_ok(M, N) || !elems_ok((int64_t)n_adapters * N, rank)) return SVDQ_ERR_SHAPE;
+    if (M > 0 && N > 0 && (!X || !A || !B || !scale || !plan || !base || !Y || !work)) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(scale) || !aligned16(plan) ||
+        !aligned16(base) || !aligned16(Y) || !aligned16(work))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (M == 0 || N == 0) return SVDQ_OK;
+    if (work_bytes < lora_work_bytes(M, K, rank, n_adapters)) return SVDQ_ERR_INVALID_ARG;
+    hipError_t e = launch_lora_linear(X, A, B, scale, plan, base, M, N, K, rank, n_adapters, Y, (float *)work,
+                                      (hipStream_t)stream);
+    return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
 // ------------------------------------------------ allocation-free split K
 //
 // svdq_w4a4_linear_splitk_noalloc keeps the split-K slice sums in this

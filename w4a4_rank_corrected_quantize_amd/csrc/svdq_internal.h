@@ -92,4 +92,14 @@ struct ResidualNormArgs {
 };
 hipError_t launch_residual_norm(const ResidualNormArgs &a, bool fp32, hipStream_t stream);
 
+// Low-rank adapters of many requests (lora.hip).  The plan groups rows by
+// adapter; `work` holds the slices of X A^T (lora_work_bytes).
+constexpr int kLoraMaxRank = 128, kLoraMaxAdapters = 4096;
+size_t lora_plan_size(int M, int n);
+size_t lora_work_bytes(int M, int K, int R, int n);
+hipError_t launch_lora_plan(const int32_t *index, int M, int n, void *plan, hipStream_t stream);
+hipError_t launch_lora_linear(const uint16_t *X, const uint16_t *A, const uint16_t *B, const float *scale,
+                              const void *plan, const uint16_t *base, int M, int N, int K, int R, int n, uint16_t *Y,
+                              float *work, hipStream_t stream);
+
 }  // namespace svdq
