@@ -52,7 +52,8 @@
  *     allocates device memory or keeps a pointer after it returns.
  *   - Device calls (svdq_quantize_act, svdq_w4a4_linear,
  *     svdq_w4a4_linear_requant, svdq_w4a4_linear_splitk,
- *     svdq_w4a4_linear_qkv_norm_rope, svdq_awq_w4a16_linear) take device
+ *     svdq_w4a4_linear_qkv_norm_rope, svdq_awq_w4a16_linear,
+ *     svdq_residual_norm, svdq_lora_*, svdq_kv4_*) take device
  *     pointers and a hipStream_t (as void*, NULL = the null stream); they
  *     validate everything first, enqueue kernels on `stream` and return
  *     without synchronizing.  On any error nothing has been enqueued or
@@ -61,8 +62,9 @@
  *   - Host calls (svdq_pack_weights, svdq_pack_residual,
  *     svdq_awq_pack_weights) take host pointers,
  *     run synchronously on the CPU and need no GPU.
- *   - Device pointers must be 16-byte aligned (SVDQ_ERR_MISALIGNED).  A
- *     buffer whose size is zero (M == 0 or N == 0) may be NULL.
+ *   - Device pointers must be 16-byte aligned, int32 index arrays 4-byte
+ *     aligned (SVDQ_ERR_MISALIGNED).  A buffer whose size is zero (M == 0 or
+ *     N == 0) may be NULL.
  *   - Inputs are expected finite; the device calls do not check the values
  *     of X (non-finite X gives unspecified codes).
  *   - Every function is thread-safe.  Calls that overlap on one stream are
@@ -575,6 +577,109 @@ svdq_status svdq_lora_plan(const int32_t *index, int M, int n_adapters, void *pl
 svdq_status svdq_lora_linear(const uint16_t *X, const uint16_t *A, const uint16_t *B, const float *scale,
                              const void *plan, const uint16_t *base, int M, int N, int K, int rank, int n_adapters,
                              uint16_t *Y, void *work, size_t work_bytes, void *stream);
+
+/*
+ * 4-bit key / value cache: keys and values in the library's two 4-bit
+ * formats, quantized along the head's channels by the same group quantizers
+ * as activations and weights (header comment; INT4 64 wide, MXFP4 32 wide),
+ * in pages that sequences share out through block tables.
+ *
+ * The caller allocates the four buffers, 16-byte aligned, of any content
+ * (D = dim, g = 64 INT4 / 32 MXFP4, P = page_size):
+ *   k_codes, v_codes     pages * heads * P * D / 2 bytes each
+ *   k_scales, v_scales   pages * heads * P * D / g elements each, fp32 (INT4)
+ *                        or uint8 E8M0 (MXFP4)
+ * Layout, per page and head, in this order of dimensions:
+ *   k_codes [P][D/2]; MXFP4: channel c in byte c / 2, nibble c % 2; INT4:
+ *           channel 64 g + 16 b + 8 s + i in byte b D/8 + 8 g + 4 s + i % 4,
+ *           nibble i / 4 (b < 4, s < 2, i < 8)
+ *   v_codes [D/2][P]; byte row 16 k + j: channel 32 k + j in the low, 32 k +
+ *           16 + j in the high nibble (j < 16)
+ *   k_scales, v_scales [D/g][P]
+ * A token's slot is page * P + place.
+ */
+typedef struct svdq_kv4_cache {
+    uint8_t *k_codes;
+    void *k_scales;
+    uint8_t *v_codes;
+    void *v_scales;
+    int pages;              /* >= 1; pages * page_size < 2^31 */
+    int page_size;          /* 16, 32, 64, 128 or 256 tokens */
+    int heads;              /* key / value heads, 1 .. 65535 */
+    int dim;                /* channels per head: 64 or 128 */
+    svdq_precision prec;
+} svdq_kv4_cache;
+
+/*
+ * svdq_kv4_append -- quantizes T tokens' keys and values into their slots.
+ *   K, V     [T][heads][dim] bf16 bits, device; row t at t * ldk, t * ldv
+ *            elements (>= heads * dim, % 8 == 0): slices of a QKV product
+ *   slots    [T] int32, device; a slot outside the cache skips that token.
+ *            The slots of one call must differ (a slot given twice holds a
+ *            mix of the two tokens afterwards)
+ * Codes and scales are bit-exact with the definition in the header comment.
+ * Other slots keep their content.  One kernel launch.  Errors:
+ * SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE (strides, cache sizes, T * heads * dim
+ * of SVDQ_MAX_ELEMENTS or more), SVDQ_ERR_UNSUPPORTED (dim, page_size),
+ * SVDQ_ERR_MISALIGNED, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
+ */
+svdq_status svdq_kv4_append(const svdq_kv4_cache *cache, const uint16_t *K, const uint16_t *V, int64_t ldk,
+                            int64_t ldv, const int32_t *slots, int T, void *stream);
+
+/*
+ * svdq_kv4_read -- the values that the cache holds for T slots:
+ *   K, V     [T][heads][dim] fp32, device (out): fl32(code * scale); zeros for
+ *            a slot outside the cache
+ * One kernel launch.  Errors as for svdq_kv4_append.
+ */
+svdq_status svdq_kv4_read(const svdq_kv4_cache *cache, const int32_t *slots, int T, float *K, float *V,
+                          void *stream);
+
+/* Device bytes that svdq_kv4_attention needs for these sizes on the current
+ * device (partial sums where the keys are split over blocks); 0 without a
+ * split, for sizes it does not take, or without a gfx950 device. */
+size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, int B, int heads_q, int max_q,
+                                          int max_kv);
+
+/*
+ * svdq_kv4_attention -- attention of the last rows of B sequences over their
+ * cached keys and values (the new tokens' own are appended first).
+ *   Q            [T][heads_q][dim] bf16 bits, device; row t at t * ldq
+ *                elements (>= heads_q * dim, % 8 == 0)
+ *   block_table  [B][table_width] int32, device: the pages of each sequence in
+ *                order.  Entries past a sequence's last page are not read; the
+ *                keys of an entry outside [0, pages) are left out
+ *   q_start      [B + 1] int32, device, not decreasing: sequence s has the
+ *                rows q_start[s] .. q_start[s + 1] - 1 (none: allowed).  Rows
+ *                of no sequence keep what O and lse hold
+ *   kv_len       [B] int32, device: keys of each sequence, the new tokens
+ *                included; read up to table_width * page_size
+ *   heads_q      a multiple of cache->heads: query head h uses key head
+ *                h / (heads_q / heads)
+ *   max_q, max_kv  >= 1, the caller's bounds on the rows and keys of a
+ *                sequence.  They choose how the work is split, results for
+ *                longer sequences are right as well
+ *   scale        finite, > 0; multiplies the scores
+ *   causal       0: a row sees all kv_len keys.  1: row i of n sees the keys
+ *                up to place kv_len - n + i, itself included
+ *   window       with causal: only the last `window` of these; 0: all
+ *   O            [T][heads_q][dim] bf16 bits, device (out)
+ *   lse          [T][heads_q] fp32, device (out), or NULL: log of the sum of
+ *                exp(score)
+ *   work, work_bytes  device scratch of at least
+ *                svdq_kv4_attention_workspace_bytes bytes, 16-byte aligned,
+ *                overwritten (NULL when that is 0)
+ * A row that sees no key gets zeros and lse -inf.  Scores, softmax and sums
+ * are fp32; the probabilities (INT4: times V's scale) enter the second
+ * product rounded to bf16.  Deterministic for given sizes and bounds.  One
+ * kernel launch, two with a split.  Errors: as for svdq_kv4_append, and
+ * SVDQ_ERR_INVALID_ARG for a too small workspace (checked after the device).
+ */
+svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
+                               const int32_t *block_table, int table_width, const int32_t *q_start,
+                               const int32_t *kv_len, int B, int T, int heads_q, int max_q, int max_kv, float scale,
+                               int causal, int window, uint16_t *O, float *lse, void *work, size_t work_bytes,
+                               void *stream);
 
 #ifdef __cplusplus
 }

@@ -4,8 +4,9 @@ Bound, u = 2^-24: h = X A^T is a sum of K products in fp32 (bf16 products are
 exact in it): the matrix instruction adds 32 at a time, so at most K / 32 + 32
 + 3 + slices additions follow one another on any path; (K / 32 + 96) u of
 sum |x a| covers them.  h enters the second product as high + low bf16 part,
-off by at most 2^-18 |h| (each part rounds by at most 2^-9, the nearest bf16
-having 8 bits of significand).  The second product has 2 R terms, then base:
+off by at most 2^-17 |h|: for |h| in [1, 2) the high part leaves at most half
+its step, 2^-8; what is left lies in a binade whose step is at most 2^-16, so
+the low part leaves at most 2^-17.  The second product has 2 R terms, then base:
 (2 R + 4) u of the magnitudes.  Storing adds half a step of bf16 (2^-8 |Y|)."""
 import sys
 
@@ -50,7 +51,7 @@ def _check(c, index, Y):
         X, A, B, s = c["X"][rows].to(F64), c["A"][a].to(F64), c["B"][a].to(F64), float(c["scale"][a])
         h, hm = X @ A.t(), X.abs() @ A.abs().t()
         want = base[rows] + s * (h @ B.t())
-        eh = (K / 32 + 96) * U * hm + 2.0 ** -18 * h.abs() + 2 * U * h.abs()
+        eh = (K / 32 + 96) * U * hm + 2.0 ** -17 * h.abs() + 2 * U * h.abs()
         bound = s * (eh @ B.abs().t()) + (2 * R + 4) * U * (s * (h.abs() @ B.abs().t()) + base[rows].abs())
         err = (Yd[rows] - want).abs()
         lim = 2.0 ** -8 * (want.abs() + bound) + bound

@@ -18,6 +18,10 @@ Functions mirror the C ABI in include/svdq.h:
     residual_norm(r, y, gate, ..., scale, shift, ...)           device, torch tensors
     lora_plan(index, n_adapters)                                device, torch tensors
     lora_linear(X, A, B, scale, plan, base, ...)                device, torch tensors
+    Kv4Cache(pages, page_size, heads, dim, prec)                device buffers of a 4-bit cache
+    kv4_append(cache, K, V, slots)                              device, torch tensors
+    kv4_read(cache, slots)                                      device, torch tensors
+    kv4_attention(Q, cache, block_table, q_start, kv_len, ...)  device, torch tensors
 
 Device tensors: X bf16 [M][K], smooth fp32 [K], down bf16 [32][K],
 up bf16 [N][32], bias bf16 [N] or None, xq uint8 [M][K/2],
@@ -57,7 +61,8 @@ EXPORTS = ("svdq_status_string", "svdq_version", "svdq_check_device", "svdq_pack
            "svdq_awq_w4a16_linear", "svdq_w4a4_linear_splitk_workspace_bytes", "svdq_w4a4_linear_splitk",
            "svdq_nf4_codebook", "svdq_nf4_pack_weights", "svdq_nf4_dequantize", "svdq_nf4_w4a16_linear",
            "svdq_w4a4_linear_splitk_noalloc", "svdq_residual_norm", "svdq_lora_plan_bytes",
-           "svdq_lora_workspace_bytes", "svdq_lora_plan", "svdq_lora_linear")
+           "svdq_lora_workspace_bytes", "svdq_lora_plan", "svdq_lora_linear", "svdq_kv4_append", "svdq_kv4_read",
+           "svdq_kv4_attention_workspace_bytes", "svdq_kv4_attention")
 
 
 class SvdqError(RuntimeError):
@@ -130,6 +135,15 @@ def lib():
         L.svdq_lora_plan.argtypes = [P, I, I, P, Z, P]
         L.svdq_lora_linear.restype = I
         L.svdq_lora_linear.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P, Z, P]
+        L64 = ctypes.c_int64
+        L.svdq_kv4_append.restype = I
+        L.svdq_kv4_append.argtypes = [P, P, P, L64, L64, P, I, P]
+        L.svdq_kv4_read.restype = I
+        L.svdq_kv4_read.argtypes = [P, P, I, P, P, P]
+        L.svdq_kv4_attention_workspace_bytes.restype = Z
+        L.svdq_kv4_attention_workspace_bytes.argtypes = [P, I, I, I, I, I]
+        L.svdq_kv4_attention.restype = I
+        L.svdq_kv4_attention.argtypes = [P, P, L64, P, I, P, P, I, I, I, I, I, F, I, I, P, P, P, Z, P]
         _lib = L
     return _lib
 
@@ -705,6 +719,156 @@ def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=
     if st:
         raise SvdqError(st, "svdq_lora_linear")
     return Y
+
+
+class _Kv4Struct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("prec", ctypes.c_int)]
+
+
+class Kv4Cache:
+    """Buffers of a paged 4-bit key / value cache (svdq_kv4_cache): `pages`
+    pages of `page_size` tokens (16, 32, 64, 128 or 256), `heads` key heads of
+    `dim` channels (64 or 128), INT4 or MXFP4.  The buffers start out
+    uninitialized; a token's slot is page * page_size + place."""
+
+    def __init__(self, pages: int, page_size: int, heads: int, dim: int, prec: int = INT4, device="cuda"):
+        torch = _torch()
+        prec = _prec(prec)
+        if page_size not in (16, 32, 64, 128, 256):
+            raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {page_size}")
+        if dim not in (64, 128):
+            raise ValueError(f"dim must be 64 or 128, got {dim}")
+        if pages < 1 or heads < 1:
+            raise ValueError("a cache has at least one page and one head")
+        self.pages, self.page_size, self.heads, self.dim, self.prec = pages, page_size, heads, dim, prec
+        g = dim // group_of(prec)
+        sdt = torch.float32 if prec == INT4 else torch.uint8
+        self._k_codes = torch.empty((pages, heads, page_size, dim // 2), dtype=torch.uint8, device=device)
+        self._v_codes = torch.empty((pages, heads, dim // 2, page_size), dtype=torch.uint8, device=device)
+        self._k_scales = torch.empty((pages, heads, g, page_size), dtype=sdt, device=device)
+        self._v_scales = torch.empty((pages, heads, g, page_size), dtype=sdt, device=device)
+        self.device = self._k_codes.device
+        self._struct = _Kv4Struct(self._k_codes.data_ptr(), self._k_scales.data_ptr(), self._v_codes.data_ptr(),
+                                  self._v_scales.data_ptr(), pages, page_size, heads, dim, prec)
+        self._ref = ctypes.addressof(self._struct)
+
+    k_codes = property(lambda self: self._k_codes)
+    v_codes = property(lambda self: self._v_codes)
+    k_scales = property(lambda self: self._k_scales)
+    v_scales = property(lambda self: self._v_scales)
+
+
+def _heads_arg(t, name, heads, dim):
+    """[T][heads][dim] bf16 with contiguous rows; returns the row stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {('T', heads, dim)}")
+    ld, sh, sd = t.stride()
+    if t.numel() and (sd != 1 or (heads > 1 and sh != dim)):
+        raise ValueError(f"{name} must have contiguous rows of heads")
+    # the stride of a single row (or of none) does not matter
+    return ld if shape[0] > 1 else heads * dim
+
+
+def _cache_arg(cache):
+    if not isinstance(cache, Kv4Cache):
+        raise TypeError("cache must be a Kv4Cache")
+    return cache.device
+
+
+def kv4_append(cache: Kv4Cache, K, V, slots, stream=None) -> None:
+    """Quantizes K, V [T][heads][dim] bf16 (rows may be a stride apart, as in a
+    QKV product) into their slots [T] int32; a slot outside the cache skips
+    its token.  The slots of one call must differ.  One kernel."""
+    torch = _torch()
+    dev = _cache_arg(cache)
+    ldk, ldv = _heads_arg(K, "K", cache.heads, cache.dim), _heads_arg(V, "V", cache.heads, cache.dim)
+    T = K.shape[0]
+    if V.shape[0] != T:
+        raise ValueError(f"V has shape {tuple(V.shape)}, expected {tuple(K.shape)}")
+    _arg(slots, torch.int32, "slots", (T,))
+    _on_device(dev, K=K, V=V, slots=slots)
+    st = lib().svdq_kv4_append(cache._ref, K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T,
+                               _raw_stream(stream, dev))
+    if st:
+        raise SvdqError(st, "svdq_kv4_append")
+
+
+def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
+    """The values the cache holds for `slots` [T] int32: (K, V) fp32
+    [T][heads][dim]; zeros for a slot outside the cache.  One kernel."""
+    torch = _torch()
+    dev = _cache_arg(cache)
+    _ndim(slots, 1, "slots")
+    _arg(slots, torch.int32, "slots")
+    T = slots.shape[0]
+    shape = (T, cache.heads, cache.dim)
+    K = torch.empty(shape, dtype=torch.float32, device=dev) if K is None else _arg(K, torch.float32, "K", shape)
+    V = torch.empty(shape, dtype=torch.float32, device=dev) if V is None else _arg(V, torch.float32, "V", shape)
+    _on_device(dev, slots=slots, K=K, V=V)
+    st = lib().svdq_kv4_read(cache._ref, slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        raise SvdqError(st, "svdq_kv4_read")
+    return K, V
+
+
+def kv4_attention_workspace_bytes(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int) -> int:
+    """Device scratch bytes that kv4_attention needs for these sizes."""
+    return int(lib().svdq_kv4_attention_workspace_bytes(cache._ref, T, B, heads_q, max_q, max_kv))
+
+
+def kv4_attention_workspace(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int):
+    """A workspace for kv4_attention calls of these sizes (uint8 tensor)."""
+    torch = _torch()
+    need = kv4_attention_workspace_bytes(cache, T, B, heads_q, max_q, max_kv)
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
+
+
+def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, max_kv: int, scale=None,
+                  causal: bool = True, window: int = 0, out=None, lse=None, work=None, stream=None):
+    """Attention of the last rows of B sequences over their cached tokens.  Q
+    [T][heads_q][dim] bf16; block_table [B][pages per sequence], q_start [B +
+    1] and kv_len [B] int32; max_q and max_kv bound the rows and keys of a
+    sequence and choose how the work is split.  scale defaults to dim^-0.5.
+    Returns out (bf16, Q's shape); lse [T][heads_q] fp32 is written when
+    given.  When `work` is None it is allocated with torch."""
+    torch = _torch()
+    i32 = torch.int32
+    dev = _cache_arg(cache)
+    _ndim(Q, 3, "Q")
+    T, H, D = Q.shape
+    if H == 0 or H % cache.heads:
+        raise ValueError(f"Q has {H} heads, the cache {cache.heads}")
+    ldq = _heads_arg(Q, "Q", H, cache.dim)
+    _ndim(block_table, 2, "block_table")
+    _arg(block_table, i32, "block_table")
+    B, width = block_table.shape
+    _arg(q_start, i32, "q_start", (B + 1,))
+    _arg(kv_len, i32, "kv_len", (B,))
+    out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev) if out is None else _arg(
+        out, torch.bfloat16, "out", (T, H, D))
+    if lse is not None:
+        _arg(lse, torch.float32, "lse", (T, H))
+    if work is None:
+        need = kv4_attention_workspace_bytes(cache, T, B, H, max_q, max_kv)
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _arg(work, torch.uint8, "work")
+    _on_device(dev, Q=Q, block_table=block_table, q_start=q_start, kv_len=kv_len, out=out, lse=lse, work=work)
+    st = lib().svdq_kv4_attention(cache._ref, Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
+                                  kv_len.data_ptr(), B, T, H, max_q, max_kv, D ** -0.5 if scale is None else scale,
+                                  1 if causal else 0, window, out.data_ptr(), _ptr(lse), _ptr(work),
+                                  0 if work is None else work.numel(), _raw_stream(stream, dev))
+    if st:
+        raise SvdqError(st, "svdq_kv4_attention")
+    return out
 
 
 def to_device(packed: dict, device="cuda") -> dict:

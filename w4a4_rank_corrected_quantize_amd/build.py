@@ -35,6 +35,8 @@ SOURCES = {
     "nf4_gemm.hip": [],
     "residual_norm.hip": [],
     "lora.hip": [],
+    "kv4_cache.hip": ["-ffp-contract=off"],
+    "kv4_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -38,6 +38,7 @@ svdq_status current_device_ok()
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }      // int32 index arrays
 
 svdq_status check_common(int M, int K, int rank, svdq_precision prec)
 {
@@ -338,7 +339,7 @@ extern "C" svdq_status svdq_residual_norm(const void *r, svdq_stream_type stype,
         if (!mod_index && M % mod_rows != 0) return SVDQ_ERR_SHAPE;
     }
     if (!aligned16(r) || !aligned16(y) || !aligned16(post_w) || !aligned16(gate) || !aligned16(pre_w) ||
-        !aligned16(pre_b) || !aligned16(scale) || !aligned16(shift) || !aligned16(mod_index) || !aligned16(r_out) ||
+        !aligned16(pre_b) || !aligned16(scale) || !aligned16(shift) || !aligned4(mod_index) || !aligned16(r_out) ||
         !aligned16(x))
         return SVDQ_ERR_MISALIGNED;
     svdq_status st = current_device_ok();
@@ -391,7 +392,7 @@ extern "C" svdq_status svdq_lora_plan(const int32_t *index, int M, int n_adapter
     svdq_status st = check_lora(M, n_adapters);
     if (st != SVDQ_OK) return st;
     if (M > 0 && (!index || !plan || plan_bytes < lora_plan_size(M, n_adapters))) return SVDQ_ERR_INVALID_ARG;
-    if (!aligned16(index) || !aligned16(plan)) return SVDQ_ERR_MISALIGNED;
+    if (!aligned4(index) || !aligned16(plan)) return SVDQ_ERR_MISALIGNED;
     st = current_device_ok();
     if (st != SVDQ_OK) return st;
     if (M == 0) return SVDQ_OK;
@@ -416,6 +417,109 @@ extern "C" svdq_status svdq_lora_linear(const uint16_t *X, const uint16_t *A, co
     if (work_bytes < lora_work_bytes(M, K, rank, n_adapters)) return SVDQ_ERR_INVALID_ARG;
     hipError_t e = launch_lora_linear(X, A, B, scale, plan, base, M, N, K, rank, n_adapters, Y, (float *)work,
                                       (hipStream_t)stream);
+    return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+// Sizes of a cache, and the view of it that the kernels take.
+static svdq_status check_kv4(const svdq_kv4_cache *c, Kv4View &v)
+{
+    if (!c || (c->prec != SVDQ_INT4 && c->prec != SVDQ_MXFP4)) return SVDQ_ERR_INVALID_ARG;
+    if (c->pages < 1 || c->heads < 1) return SVDQ_ERR_INVALID_ARG;
+    if (c->dim != 64 && c->dim != 128) return SVDQ_ERR_UNSUPPORTED;
+    int shift = 4;
+    while (shift < 8 && (1 << shift) != c->page_size) ++shift;
+    if ((1 << shift) != c->page_size) return SVDQ_ERR_UNSUPPORTED;
+    if (c->heads > 65535 || ((int64_t)c->pages << shift) > INT32_MAX) return SVDQ_ERR_SHAPE;
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+        return SVDQ_ERR_MISALIGNED;
+    v.k_codes = c->k_codes, v.v_codes = c->v_codes, v.k_scales = c->k_scales, v.v_scales = c->v_scales;
+    v.pages = c->pages, v.page_shift = shift, v.heads = c->heads, v.dim = c->dim, v.int4 = c->prec == SVDQ_INT4;
+    return SVDQ_OK;
+}
+
+static bool kv4_stride_ok(int64_t ld, int heads, int dim)
+{
+    return ld >= (int64_t)heads * dim && ld % 8 == 0 && ld < ((int64_t)1 << 40);
+}
+
+extern "C" svdq_status svdq_kv4_append(const svdq_kv4_cache *cache, const uint16_t *K, const uint16_t *V, int64_t ldk,
+                                       int64_t ldv, const int32_t *slots, int T, void *stream)
+{
+    Kv4View c;
+    svdq_status st = check_kv4(cache, c);
+    if (st != SVDQ_OK) return st;
+    if (T < 0) return SVDQ_ERR_INVALID_ARG;
+    if (!elems_ok(T, (int64_t)c.heads * c.dim)) return SVDQ_ERR_SHAPE;
+    if (!kv4_stride_ok(ldk, c.heads, c.dim) || !kv4_stride_ok(ldv, c.heads, c.dim)) return SVDQ_ERR_SHAPE;
+    if (T > 0 && (!K || !V || !slots)) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(K) || !aligned16(V) || !aligned4(slots)) return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0) return SVDQ_OK;
+    hipError_t e = launch_kv4_append(c, K, V, ldk, ldv, slots, T, (hipStream_t)stream);
+    return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+extern "C" svdq_status svdq_kv4_read(const svdq_kv4_cache *cache, const int32_t *slots, int T, float *K, float *V,
+                                     void *stream)
+{
+    Kv4View c;
+    svdq_status st = check_kv4(cache, c);
+    if (st != SVDQ_OK) return st;
+    if (T < 0) return SVDQ_ERR_INVALID_ARG;
+    if (!elems_ok(T, (int64_t)c.heads * c.dim)) return SVDQ_ERR_SHAPE;
+    if (T > 0 && (!K || !V || !slots)) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(K) || !aligned16(V) || !aligned4(slots)) return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0) return SVDQ_OK;
+    return launch_kv4_read(c, slots, T, K, V, (hipStream_t)stream) == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+static svdq_status check_kv4_attention(const Kv4View &c, int T, int B, int heads_q, int max_q, int max_kv)
+{
+    if (T < 0 || B < 0 || heads_q < 1 || max_q < 1 || max_kv < 1) return SVDQ_ERR_INVALID_ARG;
+    if (heads_q % c.heads != 0 || !elems_ok(T, (int64_t)heads_q * c.dim)) return SVDQ_ERR_SHAPE;
+    return (int64_t)B * c.heads < (1 << 24) ? SVDQ_OK : SVDQ_ERR_SHAPE;
+}
+
+extern "C" size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, int B, int heads_q, int max_q,
+                                                     int max_kv)
+{
+    Kv4View c;
+    if (check_kv4(cache, c) != SVDQ_OK || check_kv4_attention(c, T, B, heads_q, max_q, max_kv) != SVDQ_OK) return 0;
+    if (T == 0 || B == 0 || current_device_ok() != SVDQ_OK) return 0;
+    return kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv);
+}
+
+extern "C" svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
+                                          const int32_t *block_table, int table_width, const int32_t *q_start,
+                                          const int32_t *kv_len, int B, int T, int heads_q, int max_q, int max_kv,
+                                          float scale, int causal, int window, uint16_t *O, float *lse, void *work,
+                                          size_t work_bytes, void *stream)
+{
+    Kv4View c;
+    svdq_status st = check_kv4(cache, c);
+    if (st != SVDQ_OK) return st;
+    st = check_kv4_attention(c, T, B, heads_q, max_q, max_kv);
+    if (st != SVDQ_OK) return st;
+    if (!(scale > 0.0f) || scale > 3.0e38f || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
+        return SVDQ_ERR_INVALID_ARG;
+    if (!kv4_stride_ok(ldq, heads_q, c.dim)) return SVDQ_ERR_SHAPE;
+    if (table_width < 1) return SVDQ_ERR_INVALID_ARG;
+    if (((int64_t)table_width << c.page_shift) > INT32_MAX - 256) return SVDQ_ERR_SHAPE;
+    if (T > 0 && B > 0 && (!Q || !block_table || !q_start || !kv_len || !O)) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned4(block_table) || !aligned4(q_start) || !aligned4(kv_len) || !aligned16(O) ||
+        !aligned16(lse) || !aligned16(work))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0 || B == 0) return SVDQ_OK;
+    const size_t need = kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv);
+    if (need > 0 && (!work || work_bytes < need)) return SVDQ_ERR_INVALID_ARG;
+    hipError_t e = launch_kv4_attention(c, Q, ldq, block_table, table_width, q_start, kv_len, B, T, heads_q, max_q,
+                                        max_kv, scale, causal, window, O, lse, (float *)work, (hipStream_t)stream);
     return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
 }
 

@@ -102,4 +102,22 @@ hipError_t launch_lora_linear(const uint16_t *X, const uint16_t *A, const uint16
                               const void *plan, const uint16_t *base, int M, int N, int K, int R, int n, uint16_t *Y,
                               float *work, hipStream_t stream);
 
+// 4-bit key / value cache (kv4.h has the layout; kv4_cache.hip,
+// kv4_attention.hip).
+struct Kv4View {
+    uint8_t *k_codes, *v_codes;
+    void *k_scales, *v_scales;
+    int pages, page_shift, heads, dim;
+    bool int4;
+};
+hipError_t launch_kv4_append(const Kv4View &c, const uint16_t *K, const uint16_t *V, int64_t ldk, int64_t ldv,
+                             const int32_t *slots, int T, hipStream_t stream);
+hipError_t launch_kv4_read(const Kv4View &c, const int32_t *slots, int T, float *K, float *V, hipStream_t stream);
+// Splits of the keys keep their sums in `work` (0 bytes without a split).
+size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv);
+hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq, const int32_t *table, int table_width,
+                                const int32_t *q_start, const int32_t *kv_len, int B, int T, int heads_q, int max_q,
+                                int max_kv, float scale, int causal, int window, uint16_t *O, float *lse, float *work,
+                                hipStream_t stream);
+
 }  // namespace svdq
