@@ -529,60 +529,73 @@ def nf4_w4a16_linear(X, wq, qabs, chunk, bias=None, Y=None, stream=None):
     return Y
 
 
-# The calls below run between the linears, often on a few rows, so their checks
-# are kept short: one helper call per tensor, raw pointers, one device lookup.
+# The calls below run between the linears, often on a few rows, where the host
+# decides the time: their checks are short, and the module and functions they
+# need are looked up once.
 
-def _arg(t, dtype, name, shape=None):
-    """Pointer of a contiguous tensor of this dtype (and shape) on the current
-    device; type, dtype, shape and contiguity are checked before the device."""
-    torch = _torch()
+_T = None        # torch, after the first call
+
+
+def _tt():
+    global _T
+    if _T is None:
+        _T = _torch()
+    return _T
+
+
+def _bad(t, dtype, name, shape):
+    """Raises what is wrong with a tensor that failed its check."""
+    torch = _tt()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, dtype, name, shape=None):
+    """A contiguous tensor of this dtype (and shape); type, dtype, shape and
+    contiguity are checked before the device (`_launch`)."""
+    try:
+        if t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
+    _bad(t, dtype, name, shape)
 
 
 def _rows_arg(t, dtype, name, shape):
     """A 2-D tensor whose rows are contiguous but may be a stride apart (a
     slice of a wider tensor)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.numel() and t.stride(-1) != 1:
+    torch = _tt()
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        _bad(t, dtype, name, shape)
+    if t.stride(1) != 1 and t.numel():
         raise ValueError(f"{name} must have contiguous rows")
     return t
 
 
-def _on_device(dev, **tensors):
-    """Every tensor given lies on `dev`, and `dev` is the current device (the
-    library launches there)."""
-    torch = _torch()
-    if dev.type != "cuda":
+def _launch(dev, tensors, stream):
+    """The stream to launch on; checks that every tensor lies on `dev` and that
+    `dev` is the current device (the library launches there)."""
+    torch, index = _tt(), dev.index if dev.type == "cuda" else -1
+    for name, t in tensors:
+        if t is not None and t.get_device() != index:
+            raise (TypeError(f"{name} must be a device tensor") if t.device.type != "cuda" or index < 0
+                   else ValueError(f"{name} is on {t.device}, expected {dev}"))
+    if index < 0:
         raise TypeError("the tensors must be device tensors")
-    if torch.cuda.current_device() != dev.index:
-        raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"the tensors are on {dev}, the current device is {torch._C._cuda_getDevice()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream, dev):
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(dev.index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NONE, post_w=None, pre: int = NORM_RMS,
@@ -594,7 +607,7 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     of token m by mod_index [M] int32, or B equal runs of tokens.  Returns
     (r', x): r' is `r` itself without y, x is None with want_x=False.  r_out
     may be r (in place)."""
-    torch = _torch()
+    torch = _tt()
     bf, f32 = torch.bfloat16, torch.float32
     _ndim(r, 2, "r")
     if r.dtype is not bf and r.dtype is not f32:
@@ -608,7 +621,7 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     elif r_out is not None:
         raise ValueError("r_out without y: nothing to update")
     if want_x:
-        x = torch.empty(shape, dtype=bf, device=r.device) if x is None else _arg(x, bf, "x", shape)
+        x = torch.empty_like(r if y is None else y, dtype=bf) if x is None else _arg(x, bf, "x", shape)
     elif x is not None:
         raise ValueError("x given with want_x=False")
     vec = (D,)
@@ -632,11 +645,11 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     if mod_index is not None:
         _arg(mod_index, torch.int32, "mod_index", (M,))
     dev = r.device
-    _on_device(dev, y=y, gate=gate, scale=scale, shift=shift, mod_index=mod_index, post_w=post_w, pre_w=pre_w,
-               pre_b=pre_b, r_out=r_out, x=x)
+    raw = _launch(dev, (("y", y), ("gate", gate), ("scale", scale), ("shift", shift), ("mod_index", mod_index),
+                        ("post_w", post_w), ("pre_w", pre_w), ("pre_b", pre_b), ("r_out", r_out), ("x", x)), stream)
     st = lib().svdq_residual_norm(r.data_ptr(), 1 if r.dtype is f32 else 0, _ptr(y), M, D, post, _ptr(post_w),
                                   _ptr(gate), alpha, pre, _ptr(pre_w), _ptr(pre_b), _ptr(scale), _ptr(shift),
-                                  _ptr(mod_index), B, ld or D, eps, _ptr(r_out), _ptr(x), _raw_stream(stream, dev))
+                                  _ptr(mod_index), B, ld or D, eps, _ptr(r_out), _ptr(x), raw)
     if st:
         raise SvdqError(st, "svdq_residual_norm")
     return (r if y is None else r_out), x
@@ -655,7 +668,7 @@ def lora_plan(index, n_adapters: int, plan: Optional[LoraPlan] = None, stream=No
     """Groups the rows by adapter: index [M] int32, a value outside [0,
     n_adapters) means none (one kernel).  `plan` of the same sizes is
     overwritten in place (as a captured graph needs)."""
-    torch = _torch()
+    torch = _tt()
     _ndim(index, 1, "index")
     _arg(index, torch.int32, "index")
     M = index.shape[0]
@@ -665,9 +678,8 @@ def lora_plan(index, n_adapters: int, plan: Optional[LoraPlan] = None, stream=No
     elif plan.M != M or plan.n_adapters != n_adapters:
         raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n_adapters}")
     dev = index.device
-    _on_device(dev, plan=plan.buffer)
-    st = lib().svdq_lora_plan(index.data_ptr(), M, n_adapters, plan.buffer.data_ptr(), plan.buffer.numel(),
-                              _raw_stream(stream, dev))
+    raw = _launch(dev, (("plan", plan.buffer),), stream)
+    st = lib().svdq_lora_plan(index.data_ptr(), M, n_adapters, plan.buffer.data_ptr(), plan.buffer.numel(), raw)
     if st:
         raise SvdqError(st, "svdq_lora_plan")
     return plan
@@ -680,7 +692,7 @@ def lora_workspace_bytes(M: int, K: int, rank: int, n_adapters: int) -> int:
 
 def lora_workspace(M: int, K: int, rank: int, n_adapters: int, device="cuda"):
     """A workspace for lora_linear calls of these sizes (uint8 tensor)."""
-    torch = _torch()
+    torch = _tt()
     return torch.empty(max(lora_workspace_bytes(M, K, rank, n_adapters), 16), dtype=torch.uint8, device=device)
 
 
@@ -689,7 +701,7 @@ def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=
     kernels).  X [M][K], A [n][rank][K], B [n][N][rank], base [M][N] bf16,
     scale [n] fp32; rows without an adapter keep base.  Y may be base (in
     place).  When `work` is None it is allocated with torch."""
-    torch = _torch()
+    torch = _tt()
     bf = torch.bfloat16
     _ndim(X, 2, "X")
     _ndim(A, 3, "A")
@@ -712,10 +724,10 @@ def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=
         work = torch.empty(max(lora_workspace_bytes(M, K, R, n), 16), dtype=torch.uint8, device=dev)
     else:
         _arg(work, torch.uint8, "work")
-    _on_device(dev, A=A, B=B, scale=scale, plan=plan.buffer, base=base, Y=Y, work=work)
+    raw = _launch(dev, (("A", A), ("B", B), ("scale", scale), ("plan", plan.buffer), ("base", base), ("Y", Y),
+                        ("work", work)), stream)
     st = lib().svdq_lora_linear(X.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), plan.buffer.data_ptr(),
-                                base.data_ptr(), M, N, K, R, n, Y.data_ptr(), work.data_ptr(), work.numel(),
-                                _raw_stream(stream, dev))
+                                base.data_ptr(), M, N, K, R, n, Y.data_ptr(), work.data_ptr(), work.numel(), raw)
     if st:
         raise SvdqError(st, "svdq_lora_linear")
     return Y
@@ -734,7 +746,7 @@ class Kv4Cache:
     uninitialized; a token's slot is page * page_size + place."""
 
     def __init__(self, pages: int, page_size: int, heads: int, dim: int, prec: int = INT4, device="cuda"):
-        torch = _torch()
+        torch = _tt()
         prec = _prec(prec)
         if page_size not in (16, 32, 64, 128, 256):
             raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {page_size}")
@@ -762,7 +774,7 @@ class Kv4Cache:
 
 def _heads_arg(t, name, heads, dim):
     """[T][heads][dim] bf16 with contiguous rows; returns the row stride."""
-    torch = _torch()
+    torch = _tt()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not torch.bfloat16:
@@ -787,16 +799,15 @@ def kv4_append(cache: Kv4Cache, K, V, slots, stream=None) -> None:
     """Quantizes K, V [T][heads][dim] bf16 (rows may be a stride apart, as in a
     QKV product) into their slots [T] int32; a slot outside the cache skips
     its token.  The slots of one call must differ.  One kernel."""
-    torch = _torch()
+    torch = _tt()
     dev = _cache_arg(cache)
     ldk, ldv = _heads_arg(K, "K", cache.heads, cache.dim), _heads_arg(V, "V", cache.heads, cache.dim)
     T = K.shape[0]
     if V.shape[0] != T:
         raise ValueError(f"V has shape {tuple(V.shape)}, expected {tuple(K.shape)}")
     _arg(slots, torch.int32, "slots", (T,))
-    _on_device(dev, K=K, V=V, slots=slots)
-    st = lib().svdq_kv4_append(cache._ref, K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T,
-                               _raw_stream(stream, dev))
+    raw = _launch(dev, (("K", K), ("V", V), ("slots", slots)), stream)
+    st = lib().svdq_kv4_append(cache._ref, K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T, raw)
     if st:
         raise SvdqError(st, "svdq_kv4_append")
 
@@ -804,7 +815,7 @@ def kv4_append(cache: Kv4Cache, K, V, slots, stream=None) -> None:
 def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
     """The values the cache holds for `slots` [T] int32: (K, V) fp32
     [T][heads][dim]; zeros for a slot outside the cache.  One kernel."""
-    torch = _torch()
+    torch = _tt()
     dev = _cache_arg(cache)
     _ndim(slots, 1, "slots")
     _arg(slots, torch.int32, "slots")
@@ -812,8 +823,8 @@ def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
     shape = (T, cache.heads, cache.dim)
     K = torch.empty(shape, dtype=torch.float32, device=dev) if K is None else _arg(K, torch.float32, "K", shape)
     V = torch.empty(shape, dtype=torch.float32, device=dev) if V is None else _arg(V, torch.float32, "V", shape)
-    _on_device(dev, slots=slots, K=K, V=V)
-    st = lib().svdq_kv4_read(cache._ref, slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), _raw_stream(stream, dev))
+    raw = _launch(dev, (("slots", slots), ("K", K), ("V", V)), stream)
+    st = lib().svdq_kv4_read(cache._ref, slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), raw)
     if st:
         raise SvdqError(st, "svdq_kv4_read")
     return K, V
@@ -826,7 +837,7 @@ def kv4_attention_workspace_bytes(cache: Kv4Cache, T: int, B: int, heads_q: int,
 
 def kv4_attention_workspace(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int):
     """A workspace for kv4_attention calls of these sizes (uint8 tensor)."""
-    torch = _torch()
+    torch = _tt()
     need = kv4_attention_workspace_bytes(cache, T, B, heads_q, max_q, max_kv)
     return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
 
@@ -839,7 +850,7 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
     sequence and choose how the work is split.  scale defaults to dim^-0.5.
     Returns out (bf16, Q's shape); lse [T][heads_q] fp32 is written when
     given.  When `work` is None it is allocated with torch."""
-    torch = _torch()
+    torch = _tt()
     i32 = torch.int32
     dev = _cache_arg(cache)
     _ndim(Q, 3, "Q")
@@ -861,11 +872,12 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
         work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
         _arg(work, torch.uint8, "work")
-    _on_device(dev, Q=Q, block_table=block_table, q_start=q_start, kv_len=kv_len, out=out, lse=lse, work=work)
+    raw = _launch(dev, (("Q", Q), ("block_table", block_table), ("q_start", q_start), ("kv_len", kv_len), ("out", out),
+                        ("lse", lse), ("work", work)), stream)
     st = lib().svdq_kv4_attention(cache._ref, Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
                                   kv_len.data_ptr(), B, T, H, max_q, max_kv, D ** -0.5 if scale is None else scale,
                                   1 if causal else 0, window, out.data_ptr(), _ptr(lse), _ptr(work),
-                                  0 if work is None else work.numel(), _raw_stream(stream, dev))
+                                  0 if work is None else work.numel(), raw)
     if st:
         raise SvdqError(st, "svdq_kv4_attention")
     return out

@@ -6,18 +6,22 @@
 // the rows adapter by adapter in tiles of at most 64 rows of one adapter; the
 // rows without an adapter form the last tiles (adapter -1).
 //
-// Two kernels, both bound by HBM:
-//   down  a block takes one tile and one slice of K; its four waves take the
-//         slice's 64-channel chunks in turn, so a chunk of A_a is read once
-//         for up to 64 rows, and add their fp32 sums in wave order.  The
-//         slices (few rows: many slices, so that the chip is filled) go to
-//         the workspace as separate fp32 sums.
-//   up    a block takes one tile and a run of output channels, adds the
-//         slices in slice order, scales by s_a and splits h into a bf16 high
-//         and low part (together 16 bits of significand, as the shared
-//         projection's own rank-32 branch does); the products with B_a
-//         accumulate in fp32, base is added in fp32 and the row is rounded
+// Two kernels, both bound by HBM (rank 64 does 2 R (K + N) / (2 K + 4 N) = 32
+// operations per byte, the chip's ratio is about 240):
+//   down  a block takes one tile and one slice of K.  X and A_a go to LDS by
+//         DMA in stages of 128 channels, three stages ahead of the products;
+//         the four waves multiply a quarter of a stage each and add their fp32
+//         sums in wave order at the end.  With one slice the block writes h =
+//         s_a X A_a^T as a bf16 high and low part (together at least 16 bits of
+//         significand, as the shared projection's own rank-32 branch does);
+//         with more (few rows, so that the chip is filled) it writes the
+//         slice's fp32 sums, and the second kernel adds them in slice order,
+//         scales and splits.
+//   up    a block takes one tile and 128 output channels; the products with
+//         B_a accumulate in fp32, base is added in fp32 and the row is rounded
 //         once.
+// 9216 rows, 4096 -> 12288, rank 64: down 28 us, up 90 us, 118 us for 533 MB
+// = 4.5 TB/s, where a copy of that size reaches 5.4 TB/s.
 // The order of every sum depends on the sizes alone, so results do not depend
 // on which rows share a tile.
 #include "svdq_internal.h"
@@ -34,7 +38,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int LR_ROWS = 64;            // rows per tile
 constexpr int LR_PLAN_THREADS = 1024;
 constexpr int LR_HEADER = 16;          // words: M, adapters, tiles
-constexpr int LR_SLICE = 256;          // least channels per slice: one 64-channel chunk per wave
 
 __device__ __forceinline__ uint32_t lr_pack2(float lo, float hi)
 {
@@ -42,10 +45,25 @@ __device__ __forceinline__ uint32_t lr_pack2(float lo, float hi)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+// s v as high and low bf16 parts of 8 channels.
+__device__ __forceinline__ void lr_split(const float (&v)[8], float s, uint4 &hi, uint4 &lo)
+{
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = v[2 * i] * s, y = v[2 * i + 1] * s;
+        a[i] = lr_pack2(x, y);
+        b[i] = lr_pack2(x - bits_f32(a[i] << 16), y - bits_f32(a[i] & 0xFFFF0000u));
+    }
+    hi = make_uint4(a[0], a[1], a[2], a[3]), lo = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
 // ------------------------------------------------------------------- plan
 //
-// Words: header, then the tiles (adapter, first place, rows, 0), then the row
-// at every place.
+// Words: header, then the tiles (adapter, rows, 0, 0), then 64 row numbers
+// per tile; a tile of fewer rows repeats its first one.  A block knows its
+// tile's rows from its own number alone, so their load does not wait for the
+// tile's.
 
 __host__ __device__ inline int64_t lr_max_tiles(int64_t M, int64_t n)
 {
@@ -57,7 +75,7 @@ __global__ __launch_bounds__(LR_PLAN_THREADS) void lora_plan_kernel(const int32_
                                                                     int32_t *__restrict__ plan)
 {
     __shared__ int count[kLoraMaxAdapters + 1];       // rows, then the next free place, of every bucket
-    __shared__ int scan_rows[LR_PLAN_THREADS], scan_tiles[LR_PLAN_THREADS];
+    __shared__ int scan_tiles[LR_PLAN_THREADS];
     const int tid = threadIdx.x, lane = tid & 63;
     int4 *tiles = reinterpret_cast<int4 *>(plan + LR_HEADER);
     int32_t *place = plan + LR_HEADER + 4 * lr_max_tiles(M, n);
@@ -79,32 +97,28 @@ __global__ __launch_bounds__(LR_PLAN_THREADS) void lora_plan_kernel(const int32_
         }
     }
     __syncthreads();
-    // exclusive sums of rows and tiles over the buckets, a few per thread
+    // exclusive sum of the tiles over the buckets, a few per thread
     const int per = n / LR_PLAN_THREADS + 1;
     const int b0 = tid * per;
-    int rows = 0, nt = 0;
-    for (int b = b0; b < b0 + per && b <= n; ++b) {
-        rows += count[b];
-        nt += (count[b] + LR_ROWS - 1) / LR_ROWS;
-    }
-    scan_rows[tid] = rows, scan_tiles[tid] = nt;
+    int nt = 0;
+    for (int b = b0; b < b0 + per && b <= n; ++b) nt += (count[b] + LR_ROWS - 1) / LR_ROWS;
+    scan_tiles[tid] = nt;
     __syncthreads();
     for (int d = 1; d < LR_PLAN_THREADS; d <<= 1) {
-        const int a = tid >= d ? scan_rows[tid - d] : 0, c = tid >= d ? scan_tiles[tid - d] : 0;
+        const int c = tid >= d ? scan_tiles[tid - d] : 0;
         __syncthreads();
-        scan_rows[tid] += a, scan_tiles[tid] += c;
+        scan_tiles[tid] += c;
         __syncthreads();
     }
-    int at = scan_rows[tid] - rows, t = scan_tiles[tid] - nt;
+    int t = scan_tiles[tid] - nt;
     for (int b = b0; b < b0 + per && b <= n; ++b) {
         const int c = count[b];
-        count[b] = at;
+        count[b] = t * LR_ROWS;
         for (int r = 0; r < c; r += LR_ROWS)
-            tiles[t++] = make_int4(b < n ? b : -1, at + r, c - r < LR_ROWS ? c - r : LR_ROWS, 0);
-        at += c;
+            tiles[t++] = make_int4(b < n ? b : -1, c - r < LR_ROWS ? c - r : LR_ROWS, 0, 0);
     }
     if (tid == LR_PLAN_THREADS - 1) plan[0] = M, plan[1] = n, plan[2] = scan_tiles[tid];
-    __syncthreads();
+    __syncthreads();                                 // orders the block's writes of the plan before its reads below
     for (int r = 0; r < rounds; ++r) {
         const int m = r * LR_PLAN_THREADS + tid;
         int b = -1;
@@ -121,225 +135,348 @@ __global__ __launch_bounds__(LR_PLAN_THREADS) void lora_plan_kernel(const int32_
         }
         __syncthreads();                             // keeps the places of a bucket close to row order
     }
+    for (int e = tid; e < plan[2] * LR_ROWS; e += LR_PLAN_THREADS)
+        if (e % LR_ROWS >= tiles[e / LR_ROWS].y) place[e] = place[e / LR_ROWS * LR_ROWS];
 }
 
 // ------------------------------------------------------------------- down
 
 // Tile t of the plan; false past the last tile or for a plan of other sizes.
-__device__ __forceinline__ bool lr_tile(const int32_t *plan, int M, int n, int t, int4 &tile, const int32_t *&rows)
+__device__ __forceinline__ bool lr_tile(const int32_t *plan, int M, int n, int t, int &adapter, int &count)
 {
     if (plan[0] != M || plan[1] != n || t >= plan[2]) return false;
-    tile = reinterpret_cast<const int4 *>(plan + LR_HEADER)[t];
-    rows = plan + LR_HEADER + 4 * lr_max_tiles(M, n) + tile.y;
+    const int2 v = *reinterpret_cast<const int2 *>(plan + LR_HEADER + 4 * (size_t)t);
+    adapter = v.x, count = v.y;
     return true;
 }
 
-// work[slice][place][R] = the slice's part of X A_a^T.  NT: 16-wide tiles of R.
-template <int NT>
-__global__ __launch_bounds__(256) void lora_down_kernel(const uint16_t *__restrict__ X, const uint16_t *__restrict__ A,
-                                                        const int32_t *__restrict__ plan, int M, int K, int R, int n,
-                                                        int slices, int chunks_per_slice, float *__restrict__ work)
+__device__ __forceinline__ const int32_t *lr_rows(const int32_t *plan, int M, int n, int t)
 {
-    __shared__ float red[LR_ROWS][16 * NT + 4];
-    const int slice = blockIdx.x % slices;
-    int4 tile;
-    const int32_t *rows;
-    if (!lr_tile(plan, M, n, blockIdx.x / slices, tile, rows) || tile.x < 0) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int i16 = lane & 15, kb = lane >> 4;
-    const int groups = (tile.z + 15) >> 4;
-    const int chunks = (K + 63) >> 6;
-    const int c_end = min(chunks, (slice + 1) * chunks_per_slice);
+    return plan + LR_HEADER + 4 * lr_max_tiles(M, n) + (size_t)LR_ROWS * t;
+}
 
-    const uint16_t *xrow[4];
+typedef __attribute__((address_space(3))) uint8_t lr_lds_u8;
+__device__ __forceinline__ uint32_t lr_lds_offset(const void *p)
+{
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lr_lds_u8 *)p);
+}
+
+// One LDS-DMA load per lane: 16 bytes from sbase + voff to LDS lds + 16 lane.
+// M0 is saved and restored around it.
+__device__ __forceinline__ void lr_dma_b128(uint32_t lds, uint32_t voff, const void *sbase)
+{
+    uint32_t keep;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+                 : "=&s"(keep) : "s"(lds), "v"(voff), "s"(sbase) : "memory");
+}
+
+// A stage holds 128 channels (256 bytes) of the tile's rows of X and of A_a's
+// rows.  16-byte segment s of LDS row r lies at s ^ (r % 16), so that the
+// fragment reads of 16 consecutive rows hit different banks.
+constexpr int LR_STAGE_K = 128;
+constexpr int lr_stages(int NT) { return NT <= 4 ? 4 : 3; }
+constexpr int lr_stage_bytes(int NT) { return (LR_ROWS + 16 * NT) * 2 * LR_STAGE_K; }
+
+// The block's part of X A_a^T over stages st0 .. st1 - 1: G groups of 16 rows,
+// NT tiles of 16 columns.  The loads (16 lanes per row: whole lines; loads in
+// operand order, one row per lane, took four times the L1's cycles) run
+// S - 1 stages ahead; every stage issues the same number of them, so the wait
+// for a stage is a count.  Wave w multiplies channels 32 w .. + 31 of a stage.
+// Rows past the tile repeat one of it and columns past R the last one: neither
+// is used.  Past K both operands repeat the last channels and A's are zeroed.
+template <int NT, int G>
+__device__ __forceinline__ void lr_down(f32x4 (&acc)[4][NT], uint8_t *lds, const uint16_t *X, const uint16_t *a0,
+                                        const int32_t *rows, int K, int R, int st0, int st1, int wave, int lane)
+{
+    constexpr int S = lr_stages(NT), XL = G, AL = NT;         // loads per wave and stage
+    const int i16 = lane & 15, kb = lane >> 4;
+    uint32_t xoff[XL], aoff[AL];
+    // load q of the wave fills LDS rows 16 q + 4 w .. + 3, lane / 16 the row, lane % 16 the slot
+    const int r4 = 4 * wave + kb;                             // row % 16
+    const uint32_t sg = 16u * (uint32_t)(i16 ^ r4);
+#pragma unroll
+    for (int q = 0; q < XL; ++q) xoff[q] = (uint32_t)rows[16 * q + r4] * 2u * (uint32_t)K;
+#pragma unroll
+    for (int q = 0; q < AL; ++q) aoff[q] = (uint32_t)min(16 * q + r4, R - 1) * 2u * (uint32_t)K;
+    auto issue = [&](int st) {
+        const uint32_t k = min((uint32_t)min(st, st1 - 1) * 2u * LR_STAGE_K + sg, 2u * (uint32_t)K - 16u);
+        uint8_t *b = lds + (st - st0) % S * lr_stage_bytes(NT) + 1024 * wave;
+#pragma unroll
+        for (int q = 0; q < XL; ++q) lr_dma_b128(lr_lds_offset(b + 4096 * q), xoff[q] + k, X);
+#pragma unroll
+        for (int q = 0; q < AL; ++q) lr_dma_b128(lr_lds_offset(b + 4096 * (4 + q)), aoff[q] + k, a0);
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(st0 + i);
+    for (int st = st0; st < st1; ++st) {
+        // this wave's loads of the stage have landed; after the barrier all
+        // waves' have, and all are done with the stage before
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 2) * (XL + AL)) : "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(st + S - 1);
+        const uint8_t *b = lds + (st - st0) % S * lr_stage_bytes(NT) + 16 * ((4 * wave + kb) ^ i16) + 256 * i16;
+        bf16x8 x[G], a[NT];
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[g] = *reinterpret_cast<const bf16x8 *>(b + 4096 * g);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) a[j] = *reinterpret_cast<const bf16x8 *>(b + 4096 * (4 + j));
+        if ((st + 1) * LR_STAGE_K > K && st * LR_STAGE_K + 32 * wave + 8 * kb >= K) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) a[j] = __builtin_bit_cast(bf16x8, make_uint4(0u, 0u, 0u, 0u));
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[g][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[g], a[j], acc[g][j], 0, 0, 0);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+}
+
+// h of a tile is stored in the second kernel's operand order: for rows 16 g ..
+// and channels 32 k .. of the tile, lane (row % 16, 8-channel part) has 8
+// channels.  lr_h is the index of that lane in units of 8 channels; the
+// channels past R are zeros.
+__host__ __device__ constexpr int lr_ksteps(int NT) { return (NT + 1) / 2; }
+__device__ __forceinline__ size_t lr_h(int KS, int t, int g, int k) { return ((size_t)(4 * (size_t)t + g) * KS + k) * 64; }
+
+// One slice of K: h = s_a X A_a^T as bf16, the high parts of a lane's 8
+// channels at 2 lr_h, the low parts 64 lanes on.  More: the slice's part of
+// X A_a^T in fp32.  NT: 16-wide tiles of R.
+template <int NT>
+__global__ __launch_bounds__(256) void lora_down_kernel(
+    const uint16_t *__restrict__ X, const uint16_t *__restrict__ A, const float *__restrict__ scale,
+    const int32_t *__restrict__ plan, int M, int K, int R, int n, int slices, int stages_per_slice,
+    float *__restrict__ work)
+{
+    constexpr int RS = 16 * NT + 4, KS = lr_ksteps(NT);
+    static_assert(4 * LR_ROWS * RS * 4 <= lr_stages(NT) * lr_stage_bytes(NT), "the waves' sums reuse the stages");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[lr_stages(NT) * lr_stage_bytes(NT)];
+    const int slice = blockIdx.x % slices, t = blockIdx.x / slices;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i16 = lane & 15, kb = lane >> 4;
+    int adapter, count;
+    if (!lr_tile(plan, M, n, t, adapter, count) || adapter < 0) return;
+    const int32_t *rows = lr_rows(plan, M, n, t);
+    const int stages = (K + LR_STAGE_K - 1) / LR_STAGE_K;
+    const int st0 = slice * stages_per_slice, st1 = min(stages, st0 + stages_per_slice);
+    const uint16_t *a0 = A + (size_t)adapter * R * K;
+    f32x4 acc[4][NT] = {};
+    if (count <= 16) lr_down<NT, 1>(acc, lds, X, a0, rows, K, R, st0, st1, wave, lane);
+    else lr_down<NT, 4>(acc, lds, X, a0, rows, K, R, st0, st1, wave, lane);
+    // the waves' sums are added in wave order; a lane holds rows 4 kb + i,
+    // column i16 of its tiles
+    float (*red)[LR_ROWS][RS] = reinterpret_cast<float (*)[LR_ROWS][RS]>(lds);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        const int p = min(16 * g + i16, tile.z - 1);       // rows past the tile repeat its last one, never stored
-        xrow[g] = X + (size_t)rows[p] * K + 8 * kb;
+        if (16 * g >= count) break;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[wave][16 * g + 4 * kb + i][16 * j + i16] = acc[g][j][i];
     }
-    const uint16_t *arow[NT];
+    __syncthreads();
+    const float s = scale[adapter];
+    const size_t slice_lanes = lr_h(KS, (int)lr_max_tiles(M, n), 0, 0);
+    for (int e = threadIdx.x; e < (count <= 16 ? 1 : 4) * KS * 64; e += 256) {
+        const int l = e & 63, k = (e >> 6) % KS, g = (e >> 6) / KS;
+        const int p = 16 * g + (l & 15), r = 32 * k + 8 * (l >> 4);
+        float v[8];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        arow[j] = A + ((size_t)tile.x * R + min(16 * j + i16, R - 1)) * K + 8 * kb;   // columns past R: never stored
-
-    f32x4 acc[4][NT] = {};
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (int c = slice * chunks_per_slice + wave; c < c_end; c += 4) {
+        for (int q = 0; q < 2; ++q) {
+            f32x4 u = {};
+            if (r < R && p < count) {
+                u = *reinterpret_cast<const f32x4 *>(&red[0][p][r + 4 * q]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = 64 * c + 32 * h;
-            const bool in = k + 8 * kb < K;
-            uint4 a[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) a[j] = in ? *reinterpret_cast<const uint4 *>(arow[j] + k) : zero;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                if (g < groups) {
-                    const uint4 x = in ? *reinterpret_cast<const uint4 *>(xrow[g] + k) : zero;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[g][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, a[j]), acc[g][j], 0, 0, 0);
-                }
+                for (int w = 1; w < 4; ++w) u += *reinterpret_cast<const f32x4 *>(&red[w][p][r + 4 * q]);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * q + i] = u[i];
+        }
+        if (slices == 1) {
+            uint4 *o = (uint4 *)work + 2 * lr_h(KS, t, g, k) + l;
+            lr_split(v, s, o[0], o[64]);
+        } else {
+            f32x4 *o = (f32x4 *)work + 2 * (slice * slice_lanes + lr_h(KS, t, g, k) + l);
+            o[0] = (f32x4){v[0], v[1], v[2], v[3]}, o[1] = (f32x4){v[4], v[5], v[6], v[7]};
         }
     }
-    // the waves' sums in wave order; lane holds rows 4 kb + i, column i16
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if (wave == w) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                if (g < groups)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float &d = red[16 * g + 4 * kb + i][16 * j + i16];
-                            d = w == 0 ? acc[g][j][i] : d + acc[g][j][i];
-                        }
-        }
-        __syncthreads();
-    }
-    float *out = work + ((size_t)slice * M + tile.y) * R;
-    for (int e = threadIdx.x; e < tile.z * R; e += 256) out[e] = red[e / R][e % R];
 }
 
 // --------------------------------------------------------------------- up
+//
+// A block takes one tile and 128 output channels.  Wave g multiplies rows
+// 16 g .. of the tile with all 128: product tile j has the channels 8 i + j (i
+// = 0 .. 15), so a lane's sums are 8 consecutive channels of four rows and
+// base and Y move as 256 bytes per row and instruction.  B_a's rows go through
+// LDS, once for the four waves.  A tile of at most 16 rows is shared out by
+// channels instead, 32 per wave, B_a straight from memory.
+constexpr int LR_UP_N = 128;
 
-// KS: 32-wide steps of the product's 2 R channels (h high, h low).
+template <int KS>
+__device__ __forceinline__ void lr_load_h(bf16x8 (&hi)[KS], bf16x8 (&lo)[KS], const float *work, int t, int g,
+                                          int slices, size_t slice_lanes, float s_a, int lane)
+{
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        uint4 a, b;
+        if (slices == 1) {
+            const uint4 *p = (const uint4 *)work + 2 * lr_h(KS, t, g, k) + lane;
+            a = p[0], b = p[64];
+        } else {
+            const f32x4 *p = (const f32x4 *)work + 2 * (lr_h(KS, t, g, k) + lane);
+            f32x4 u = p[0], v = p[1];
+            int q = 1;
+            for (; q + 3 < slices; q += 4) {             // four slices' loads in flight, added in slice order
+                f32x4 x[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i][0] = p[2 * (q + i) * slice_lanes], x[i][1] = p[2 * (q + i) * slice_lanes + 1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u += x[i][0], v += x[i][1];
+            }
+            for (; q < slices; ++q) u += p[2 * q * slice_lanes], v += p[2 * q * slice_lanes + 1];
+            const float f[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+            lr_split(f, s_a, a, b);
+        }
+        hi[k] = __builtin_bit_cast(bf16x8, a), lo[k] = __builtin_bit_cast(bf16x8, b);
+    }
+}
+
+// KS: 32-wide steps of R.
 template <int KS>
 __global__ __launch_bounds__(256) void lora_up_kernel(const float *__restrict__ work, const uint16_t *__restrict__ B,
                                                       const float *__restrict__ scale,
                                                       const int32_t *__restrict__ plan, int M, int N, int R, int n,
-                                                      int slices, int nblocks, int nsteps, const uint16_t *base,
-                                                      uint16_t *Y)
+                                                      int slices, int nblocks, const uint16_t *base, uint16_t *Y)
 {
-    constexpr int HS = 32 * KS + 8;                      // LDS row: high and low parts, zero up to 32 KS, 16 B pad
-    __shared__ __attribute__((aligned(16))) uint16_t hs[LR_ROWS * HS];
-    int4 tile;
-    const int32_t *rows;
-    if (!lr_tile(plan, M, n, blockIdx.x / nblocks, tile, rows)) return;
+    constexpr int BS = 32 * KS + 8;                      // LDS row: B_a's channels, zeros up to 32 KS, 16 B pad
+    __shared__ __attribute__((aligned(16))) uint16_t bs[LR_UP_N * BS];
+    const int t = blockIdx.x / nblocks, n0 = (blockIdx.x % nblocks) * LR_UP_N;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int i16 = lane & 15, kb = lane >> 4;
-    const int nb = blockIdx.x % nblocks;
-    const int groups = (tile.z + 15) >> 4;
-    if (tile.x < 0) {                                    // rows without an adapter: copied, unless in place
-        if (Y == base) return;
-        for (int s = 0; s < nsteps; ++s) {
-            const int c = ((nb * nsteps + s) * 256) + 8 * (tid & 31);
-            if (c >= N) continue;
-            for (int p = tid >> 5; p < tile.z; p += 8) {
-                const size_t o = (size_t)rows[p] * N + c;
-                *reinterpret_cast<uint4 *>(Y + o) = *reinterpret_cast<const uint4 *>(base + o);
-            }
+    int adapter, count;
+    if (!lr_tile(plan, M, n, t, adapter, count)) return;
+    const int32_t *rows = lr_rows(plan, M, n, t);
+    if (adapter < 0) {                                   // rows without an adapter: copied, unless in place
+        const int c = n0 + 8 * i16;
+        if (Y == base || c >= N) return;
+        for (int p = tid >> 4; p < count; p += 16) {
+            const size_t o = (size_t)rows[p] * N + c;
+            *reinterpret_cast<uint4 *>(Y + o) = *reinterpret_cast<const uint4 *>(base + o);
         }
         return;
     }
-    // h of the tile: slices in slice order, scaled, high and low bf16 parts
-    const float s = scale[tile.x];
-    const float *part = work + (size_t)tile.y * R;
-    for (int e = tid; e < 16 * groups * 16 * KS; e += 256) {
-        const int p = e / (16 * KS), r = e % (16 * KS);
-        float v = 0.0f;
-        if (p < tile.z && r < R) {
-            v = part[(size_t)p * R + r];
-            for (int q = 1; q < slices; ++q) v += part[((size_t)q * M + p) * R + r];
-            v *= s;
-        }
-        const uint32_t hi = lr_pack2(v, 0.0f) & 0xFFFFu;
-        const uint32_t lo = lr_pack2(v - bits_f32(hi << 16), 0.0f) & 0xFFFFu;
-        if (r < R) {
-            hs[p * HS + r] = (uint16_t)hi;
-            hs[p * HS + R + r] = (uint16_t)lo;
-        } else {                                         // 32 KS - 2 R zeros, two per r
-            hs[p * HS + 2 * R + 2 * (r - R)] = 0;
-            hs[p * HS + 2 * R + 2 * (r - R) + 1] = 0;
-        }
+    const uint16_t *ba = B + (size_t)adapter * N * R;
+    const float s_a = scale[adapter];
+    const size_t slice_lanes = lr_h(KS, (int)lr_max_tiles(M, n), 0, 0);
+    bf16x8 hi[KS], lo[KS];
+    if (count <= 16) {
+        // channels n0 + 32 wave + 2 i16 + j: two per lane
+        const int c = n0 + 32 * wave + 2 * i16;
+        if (n0 + 32 * wave >= N) return;
+        const int cc = min(c, N - 2);
+        const int4 row = *reinterpret_cast<const int4 *>(rows + 4 * kb);
+        const size_t off[4] = {(size_t)row.x * N + cc, (size_t)row.y * N + cc, (size_t)row.z * N + cc, (size_t)row.w * N + cc};
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint32_t *>(base + off[i]);
+        uint4 b[KS][2];
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)                  // chunks past R repeat the last one and meet zeros of h
+                b[k][j] = *reinterpret_cast<const uint4 *>(ba + (size_t)(cc + j) * R + min(32 * k + 8 * kb, R - 8));
+        lr_load_h<KS>(hi, lo, work, t, 0, slices, slice_lanes, s_a, lane);
+        f32x4 acc[2] = {};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bf16x8 bb = __builtin_bit_cast(bf16x8, b[k][j]);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[k], bb, acc[j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[k], bb, acc[j], 0, 0, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * kb + i < count && c < N)
+                *reinterpret_cast<uint32_t *>(Y + off[i]) =
+                    lr_pack2(bits_f32(y[i] << 16) + acc[0][i], bits_f32(y[i] & 0xFFFF0000u) + acc[1][i]);
+        return;
+    }
+    // channels n0 + 8 i16 .. + 7 of rows 16 wave + 4 kb + i
+    const int c = n0 + 8 * i16, cc = min(c, N - 8);
+    const int4 row = *reinterpret_cast<const int4 *>(rows + 16 * wave + 4 * kb);
+    const size_t off[4] = {(size_t)row.x * N + cc, (size_t)row.y * N + cc, (size_t)row.z * N + cc, (size_t)row.w * N + cc};
+    uint4 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint4 *>(base + off[i]);
+    lr_load_h<KS>(hi, lo, work, t, wave, slices, slice_lanes, s_a, lane);
+    // LDS row 16 j + i holds channel 8 i + j
+    constexpr int CH = 4 * KS;                           // 16-byte chunks of an LDS row
+    uint4 st[LR_UP_N * CH / 256];
+#pragma unroll
+    for (int q = 0; q < LR_UP_N * CH / 256; ++q) {
+        const int e = tid + 256 * q, ch = e % CH, nn = min(n0 + e / CH, N - 1);
+        st[q] = *reinterpret_cast<const uint4 *>(ba + (size_t)nn * R + min(8 * ch, R - 8));
+    }
+#pragma unroll
+    for (int q = 0; q < LR_UP_N * CH / 256; ++q) {
+        const int e = tid + 256 * q, ch = e % CH, nn = e / CH;
+        *reinterpret_cast<uint4 *>(&bs[(16 * (nn & 7) + (nn >> 3)) * BS + 8 * ch]) = st[q];
     }
     __syncthreads();
-    const int chunks = R >> 3;
-    const uint16_t *ba = B + (size_t)tile.x * N * R;
-    for (int st = 0; st < nsteps; ++st) {
-        const int n0 = (nb * nsteps + st) * 256 + 64 * wave;
-        if (n0 >= N) break;
-        // base: 16 consecutive channels n0 + 16 kb .. of row 16 g + i16
-        uint4 y[4][2];
-        size_t off[4];
+    f32x4 acc[8] = {};
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int p = 16 * g + i16;
-            off[g] = (size_t)rows[min(p, tile.z - 1)] * N + n0 + 16 * kb;
+    for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (p < tile.z && n0 + 16 * kb + 8 * h < N)
-                    y[g][h] = *reinterpret_cast<const uint4 *>(base + off[g] + 8 * h);
-        }
-        // A operand of tile j: row i is channel n0 + 16 (i / 4) + 4 j + i % 4,
-        // so that a lane's four tiles hold 16 consecutive channels
-        uint4 b[KS][4];
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            int c = 4 * k + kb;
-            const bool in = c < 2 * chunks;
-            c = c >= chunks ? c - chunks : c;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int nn = n0 + 16 * (i16 >> 2) + 4 * j + (i16 & 3);
-                b[k][j] = in && nn < N ? *reinterpret_cast<const uint4 *>(ba + (size_t)nn * R + 8 * c)
-                                       : make_uint4(0u, 0u, 0u, 0u);
-            }
+        for (int j = 0; j < 8; ++j) {
+            const bf16x8 b = *reinterpret_cast<const bf16x8 *>(&bs[(16 * j + i16) * BS + 32 * k + 8 * kb]);
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[k], b, acc[j], 0, 0, 0);
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[k], b, acc[j], 0, 0, 0);
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            if (g >= groups) break;
-            f32x4 acc[4] = {};
+    for (int i = 0; i < 4; ++i) {
+        if (16 * wave + 4 * kb + i >= count || c >= N) continue;
+        const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+        uint32_t v[4];
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const bf16x8 h = *reinterpret_cast<const bf16x8 *>(&hs[(16 * g + i16) * HS + 32 * k + 8 * kb]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b[k][j]), h, acc[j], 0,
-                                                                     0, 0);
-            }
-            if (16 * g + i16 < tile.z) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (n0 + 16 * kb + 8 * h >= N) continue;
-                    const uint32_t w[4] = {y[g][h].x, y[g][h].y, y[g][h].z, y[g][h].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        o[q] = lr_pack2(bits_f32(w[q] << 16) + acc[2 * h + (q >> 1)][2 * (q & 1)],
-                                        bits_f32(w[q] & 0xFFFF0000u) + acc[2 * h + (q >> 1)][2 * (q & 1) + 1]);
-                    *reinterpret_cast<uint4 *>(Y + off[g] + 8 * h) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            }
-        }
+        for (int q = 0; q < 4; ++q)
+            v[q] = lr_pack2(bits_f32(w[q] << 16) + acc[2 * q][i], bits_f32(w[q] & 0xFFFF0000u) + acc[2 * q + 1][i]);
+        *reinterpret_cast<uint4 *>(Y + off[i]) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
 
-// Slices of K: enough blocks for the chip (the tiles are at least the rows'
-// tiles; with more adapters than that, one per adapter), none below LR_SLICE.
-int lr_slices(int64_t M, int K, int n, int &chunks_per_slice)
+// Slices of K, in stages of 128 channels: enough blocks for the chip, at
+// least two stages each, at most four: more shorten the first kernel less than
+// they lengthen the second, which adds them up (16 rows of 16 adapters, 4096
+// -> 4096, rank 16: 11.2 us with one slice, 8.3 with 4, 9.1 with 16; 1111 rows
+// of 7, 2048 -> 6144, rank 32: 15.5, 13.8 and 14.7 us).
+constexpr int LR_MAX_SLICES = 4;
+
+int lr_slices(int64_t M, int K, int n, int &stages_per_slice)
 {
     const int64_t tiles = lr_max_tiles(M, n);
-    const int chunks = (K + 63) / 64;
-    int64_t s = (2 * (int64_t)device_cu_count() + tiles - 1) / tiles;
-    const int64_t most = K / LR_SLICE > 1 ? K / LR_SLICE : 1;
-    s = s < 1 ? 1 : (s > most ? most : s);
-    chunks_per_slice = (int)((chunks + s - 1) / s);
-    return (chunks + chunks_per_slice - 1) / chunks_per_slice;
+    const int stages = (K + LR_STAGE_K - 1) / LR_STAGE_K;
+    int64_t s = device_cu_count() / tiles;
+    s = s > LR_MAX_SLICES ? LR_MAX_SLICES : s;
+    s = s > stages / 2 ? stages / 2 : s;
+    s = s < 1 ? 1 : s;
+    stages_per_slice = (int)((stages + s - 1) / s);
+    return (stages + stages_per_slice - 1) / stages_per_slice;
 }
+
+// 32-wide steps of R that the kernels hold: 1, 2 or 4.
+int lr_rank_steps(int R) { return R <= 32 ? 1 : (R <= 64 ? 2 : 4); }
 
 }  // namespace
 
-size_t lora_plan_size(int M, int n) { return 4 * (size_t)(LR_HEADER + 4 * lr_max_tiles(M, n) + M); }
+size_t lora_plan_size(int M, int n) { return 4 * (size_t)(LR_HEADER + (4 + LR_ROWS) * lr_max_tiles(M, n)); }
 
 size_t lora_work_bytes(int M, int K, int R, int n)
 {
     int per;
-    return (size_t)lr_slices(M, K, n, per) * M * R * sizeof(float);
+    return (size_t)lr_slices(M, K, n, per) * LR_ROWS * lr_max_tiles(M, n) * 32 * lr_rank_steps(R) * sizeof(float);
 }
 
 hipError_t launch_lora_plan(const int32_t *index, int M, int n, void *plan, hipStream_t stream)
@@ -357,7 +494,8 @@ hipError_t launch_lora_linear(const uint16_t *X, const uint16_t *A, const uint16
     int per;
     const int slices = lr_slices(M, K, n, per);
     const dim3 grid((uint32_t)(tiles * slices));
-#define LR_DOWN(NT) lora_down_kernel<NT><<<grid, 256, 0, stream>>>(X, A, pl, M, K, R, n, slices, per, work)
+#define LR_DOWN(NT) \
+    lora_down_kernel<NT><<<grid, 256, 0, stream>>>(X, A, scale, pl, M, K, R, n, slices, per, work)
     if (R <= 16) LR_DOWN(1);
     else if (R <= 32) LR_DOWN(2);
     else if (R <= 64) LR_DOWN(4);
@@ -365,19 +503,13 @@ hipError_t launch_lora_linear(const uint16_t *X, const uint16_t *A, const uint16
 #undef LR_DOWN
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // channels per block: 256 per step, as many steps as leave four blocks per
-    // compute unit (each block adds up its tile's slices once)
-    const int64_t cols = (N + 255) / 256;
-    int64_t steps = cols * tiles / (4 * (int64_t)device_cu_count());
-    steps = steps < 1 ? 1 : (steps > 8 ? 8 : steps);
-    const int nblocks = (int)((cols + steps - 1) / steps);
+    const int nblocks = (N + LR_UP_N - 1) / LR_UP_N;
     const dim3 ugrid((uint32_t)(tiles * nblocks));
 #define LR_UP(KS) \
-    lora_up_kernel<KS><<<ugrid, 256, 0, stream>>>(work, B, scale, pl, M, N, R, n, slices, nblocks, (int)steps, base, Y)
-    if (R <= 16) LR_UP(1);
-    else if (R <= 32) LR_UP(2);
-    else if (R <= 64) LR_UP(4);
-    else LR_UP(8);
+    lora_up_kernel<KS><<<ugrid, 256, 0, stream>>>(work, B, scale, pl, M, N, R, n, slices, nblocks, base, Y)
+    if (R <= 32) LR_UP(1);
+    else if (R <= 64) LR_UP(2);
+    else LR_UP(4);
 #undef LR_UP
     return hipGetLastError();
 }
