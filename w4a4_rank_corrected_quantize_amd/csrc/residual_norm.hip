@@ -73,10 +73,54 @@ __device__ __forceinline__ float rn_row_sum(float v, float *red)
     return v;
 }
 
+template <int C>
+__device__ __forceinline__ void rn_clear(float (&v)[C][8], const bool (&in)[C])
+{
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = in[c] ? v[c][i] : 0.0f;
+}
+
+template <int C>
+__device__ __forceinline__ void rn_raw(uint4 (&u)[C], const uint16_t *p, const int (&k)[C])
+{
+#pragma unroll
+    for (int c = 0; c < C; ++c) u[c] = *reinterpret_cast<const uint4 *>(p + k[c]);
+}
+
+template <int C>
+__device__ __forceinline__ void rn_times(float (&v)[C][8], const uint16_t *p, const int (&k)[C])
+{
+    uint4 u[C];
+    rn_raw<C>(u, p, k);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float f[8];
+        rn_unpack8(u[c], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= f[i];
+    }
+}
+
+template <int C>
+__device__ __forceinline__ void rn_plus(float (&v)[C][8], const uint16_t *p, const int (&k)[C])
+{
+    uint4 u[C];
+    rn_raw<C>(u, p, k);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float f[8];
+        rn_unpack8(u[c], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] += f[i];
+    }
+}
+
 // v <- v / sqrt(mean(v^2) + eps), centred first for LayerNorm.  Elements past
 // D are zero on entry and stay out of the sums.
 template <int T, int C>
-__device__ __forceinline__ void rn_normalize(float (&v)[C][8], int kind, int D, float inv_d, float eps, int t,
+__device__ __forceinline__ void rn_normalize(float (&v)[C][8], int kind, const bool (&in)[C], float inv_d, float eps,
                                              float *red)
 {
     if (kind == SVDQ_NORM_LAYER) {
@@ -87,11 +131,9 @@ __device__ __forceinline__ void rn_normalize(float (&v)[C][8], int kind, int D, 
             for (int i = 0; i < 8; ++i) s += v[c][i];
         const float mean = rn_row_sum<T>(s, red) * inv_d;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const bool in = 8 * (t + c * T) < D;
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] = in ? v[c][i] - mean : 0.0f;
-        }
+            for (int i = 0; i < 8; ++i) v[c][i] = in[c] ? v[c][i] - mean : 0.0f;
     }
     float q = 0.0f;
 #pragma unroll
@@ -122,82 +164,62 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(Residu
     const bool mod = (uint32_t)b < (uint32_t)a.mod_rows;
     const size_t mrow = mod ? (size_t)b * a.mod_stride : 0;
 
+    // loads carry no condition (a condition makes the compiler wait for one
+    // load before the next): chunks past D repeat the last one, count as zero
+    // and are not stored
+    int k[C];
+    bool in[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) in[c] = 8 * (t + c * T) < D, k[c] = min(8 * (t + c * T), D - 8);
     float v[C][8];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int k = 8 * (t + c * T);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
-        if (k < D) {
-            if (a.y) rn_unpack8(*reinterpret_cast<const uint4 *>(a.y + row + k), v[c]);
-            else rn_load_stream<FP32>(a.r, row + k, v[c]);
-        }
-    }
     if (a.y) {
         float r[C][8];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = 8 * (t + c * T);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[c][i] = 0.0f;
-            if (k < D) rn_load_stream<FP32>(a.r, row + k, r[c]);
+            rn_unpack8(*reinterpret_cast<const uint4 *>(a.y + row + k[c]), v[c]);
+            rn_load_stream<FP32>(a.r, row + k[c], r[c]);
         }
-        if (a.post != SVDQ_NORM_NONE) rn_normalize<T, C>(v, a.post, D, inv_d, a.eps, t, red);
+        rn_clear<C>(v, in);
+        if (a.post != SVDQ_NORM_NONE) rn_normalize<T, C>(v, a.post, in, inv_d, a.eps, red);
+        if (a.post_w) rn_times<C>(v, a.post_w, k);
+        if (a.gate && mod) rn_times<C>(v, a.gate + mrow, k);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = 8 * (t + c * T);
-            if (k < D) {
-                if (a.post_w) {
-                    float w[8];
-                    rn_unpack8(*reinterpret_cast<const uint4 *>(a.post_w + k), w);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
-                }
-                float g[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = 1.0f;
-                if (a.gate && mod) rn_unpack8(*reinterpret_cast<const uint4 *>(a.gate + mrow + k), g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(a.alpha * g[i], v[c][i], r[c][i]);
-                if constexpr (FP32) {
-                    float *o = (float *)a.r_out + row + k;
-                    *reinterpret_cast<float4 *>(o) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
-                    *reinterpret_cast<float4 *>(o + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
-                } else {
-                    *reinterpret_cast<uint4 *>((uint16_t *)a.r_out + row + k) = rn_pack8(v[c]);
-                }
+            for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(a.alpha, v[c][i], r[c][i]);
+            if (!in[c]) continue;
+            if constexpr (FP32) {
+                float *o = (float *)a.r_out + row + k[c];
+                *reinterpret_cast<float4 *>(o) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+                *reinterpret_cast<float4 *>(o + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
+            } else {
+                *reinterpret_cast<uint4 *>((uint16_t *)a.r_out + row + k[c]) = rn_pack8(v[c]);
             }
         }
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) rn_load_stream<FP32>(a.r, row + k[c], v[c]);
     }
+    rn_clear<C>(v, in);
     if (!a.x) return;
-    if (a.pre != SVDQ_NORM_NONE) rn_normalize<T, C>(v, a.pre, D, inv_d, a.eps, t, red);
+    if (a.pre != SVDQ_NORM_NONE) rn_normalize<T, C>(v, a.pre, in, inv_d, a.eps, red);
+    if (a.pre_w) rn_times<C>(v, a.pre_w, k);
+    if (a.pre_b) rn_plus<C>(v, a.pre_b, k);
+    if (a.scale && mod) {
+        uint4 u[C];
+        rn_raw<C>(u, a.scale + mrow, k);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int k = 8 * (t + c * T);
-        if (k >= D) continue;
-        float f[8];
-        if (a.pre_w) {
-            rn_unpack8(*reinterpret_cast<const uint4 *>(a.pre_w + k), f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] *= f[i];
-        }
-        if (a.pre_b) {
-            rn_unpack8(*reinterpret_cast<const uint4 *>(a.pre_b + k), f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] += f[i];
-        }
-        if (a.scale && mod) {
-            rn_unpack8(*reinterpret_cast<const uint4 *>(a.scale + mrow + k), f);
+        for (int c = 0; c < C; ++c) {
+            float f[8];
+            rn_unpack8(u[c], f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[c][i] = __builtin_fmaf(v[c][i], f[i], v[c][i]);
         }
-        if (a.shift && mod) {
-            rn_unpack8(*reinterpret_cast<const uint4 *>(a.shift + mrow + k), f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] += f[i];
-        }
-        *reinterpret_cast<uint4 *>(a.x + row + k) = rn_pack8(v[c]);
     }
+    if (a.shift && mod) rn_plus<C>(v, a.shift + mrow, k);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (in[c]) *reinterpret_cast<uint4 *>(a.x + row + k[c]) = rn_pack8(v[c]);
 }
 
 template <int T, int C>
