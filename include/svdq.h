@@ -589,13 +589,14 @@ svdq_status svdq_lora_linear(const uint16_t *X, const uint16_t *A, const uint16_
  *   k_codes, v_codes     pages * heads * P * D / 2 bytes each
  *   k_scales, v_scales   pages * heads * P * D / g elements each, fp32 (INT4)
  *                        or uint8 E8M0 (MXFP4)
- * Layout, per page and head, in this order of dimensions:
- *   k_codes [P][D/2]; MXFP4: channel c in byte c / 2, nibble c % 2; INT4:
- *           channel 64 g + 16 b + 8 s + i in byte b D/8 + 8 g + 4 s + i % 4,
- *           nibble i / 4 (b < 4, s < 2, i < 8)
- *   v_codes [D/2][P]; byte row 16 k + j: channel 32 k + j in the low, 32 k +
- *           16 + j in the high nibble (j < 16)
- *   k_scales, v_scales [D/g][P]
+ * Layout, per page and head, tokens in runs of 16:
+ *   k_codes [P/16][4][16][D/8] bytes: run, part b, token of the run, bytes.
+ *           MXFP4: channel c in part c / (D/4), byte c % (D/4) / 2, nibble c %
+ *           2; INT4: channel 64 g + 16 b + 8 s + i (b < 4, s < 2, i < 8) in
+ *           part b, byte 8 g + 4 s + i % 4, nibble i / 4
+ *   v_codes [P/16][4][16][D/32][4] bytes: run, token / 4, j, k, token % 4;
+ *           channel 32 k + j in the low, 32 k + 16 + j in the high nibble
+ *   k_scales, v_scales [P/16][D/g][16]: run, group, token
  * A token's slot is page * P + place.
  */
 typedef struct svdq_kv4_cache {
@@ -647,7 +648,7 @@ size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, in
  *   Q            [T][heads_q][dim] bf16 bits, device; row t at t * ldq
  *                elements (>= heads_q * dim, % 8 == 0)
  *   block_table  [B][table_width] int32, device: the pages of each sequence in
- *                order.  Entries past a sequence's last page are not read; the
+ *                order.  Entries past a sequence's last page are not used; the
  *                keys of an entry outside [0, pages) are left out
  *   q_start      [B + 1] int32, device, not decreasing: sequence s has the
  *                rows q_start[s] .. q_start[s + 1] - 1 (none: allowed).  Rows

@@ -114,16 +114,18 @@ def test_layout_is_the_documented_one(prec, D):
         return float(torch.tensor((-m if nib & 8 else m) * s, dtype=F64).to(F32))
     for t in (0, 11, 12, 43, 44, 49):
         page, place = divmod(int(slots[t]), P)
+        run, tok = divmod(place, 16)
         for h in range(H):
             for ch in range(0, D, 3):
                 if prec == svdq.MXFP4:
-                    byte, nib = ch // 2, ch % 2
+                    b, byte, nib = ch // (D // 4), ch % (D // 4) // 2, ch % 2
                 else:
                     gg, b, s, i = ch // 64, ch % 64 // 16, ch % 16 // 8, ch % 8
-                    byte, nib = b * (D // 8) + 8 * gg + 4 * s + i % 4, i // 4
-                assert value(int(kc[page, h, place, byte]) >> (4 * nib) & 15, ks[page, h, ch // g, place]) == k[t, h, ch]
-                row, nib = 16 * (ch // 32) + ch % 16, ch % 32 // 16
-                assert value(int(vc[page, h, row, place]) >> (4 * nib) & 15, vs[page, h, ch // g, place]) == v[t, h, ch]
+                    byte, nib = 8 * gg + 4 * s + i % 4, i // 4
+                code = int(kc[page, h, run, b, tok, byte]) >> (4 * nib) & 15
+                assert value(code, ks[page, h, run, ch // g, tok]) == k[t, h, ch]
+                code = int(vc[page, h, run, tok // 4, ch % 16, ch // 32, tok % 4]) >> (4 * (ch % 32 // 16)) & 15
+                assert value(code, vs[page, h, run, ch // g, tok]) == v[t, h, ch]
 
 
 @pytest.mark.parametrize("prec", PRECS)
@@ -143,9 +145,9 @@ def test_append_from_a_qkv_product_touches_its_slots_only(prec):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     used = torch.zeros(8 * P, dtype=torch.bool, device="cuda")
     used[slots[keep].long()] = True
-    free = ~used.view(8, P)
-    assert bool((c.k_codes.permute(0, 2, 1, 3)[free] == 255).all())
-    assert bool((c.v_codes.permute(0, 3, 1, 2)[free] == 255).all())
+    free = ~used                                       # [page][place]; place = 16 run + token
+    assert bool((c.k_codes.permute(0, 2, 4, 1, 3, 5).reshape(8 * P, -1)[free] == 255).all())
+    assert bool((c.v_codes.permute(0, 2, 3, 6, 1, 4, 5).reshape(8 * P, -1)[free] == 255).all())
     k, v = svdq.kv4_read(c, slots)
     want = _quantized(K.contiguous(), prec)
     want[~keep] = 0.0

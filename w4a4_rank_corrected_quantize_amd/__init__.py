@@ -757,10 +757,11 @@ class Kv4Cache:
         self.pages, self.page_size, self.heads, self.dim, self.prec = pages, page_size, heads, dim, prec
         g = dim // group_of(prec)
         sdt = torch.float32 if prec == INT4 else torch.uint8
-        self._k_codes = torch.empty((pages, heads, page_size, dim // 2), dtype=torch.uint8, device=device)
-        self._v_codes = torch.empty((pages, heads, dim // 2, page_size), dtype=torch.uint8, device=device)
-        self._k_scales = torch.empty((pages, heads, g, page_size), dtype=sdt, device=device)
-        self._v_scales = torch.empty((pages, heads, g, page_size), dtype=sdt, device=device)
+        runs = page_size // 16
+        self._k_codes = torch.empty((pages, heads, runs, 4, 16, dim // 8), dtype=torch.uint8, device=device)
+        self._v_codes = torch.empty((pages, heads, runs, 4, 16, dim // 32, 4), dtype=torch.uint8, device=device)
+        self._k_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
+        self._v_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
         self.device = self._k_codes.device
         self._struct = _Kv4Struct(self._k_codes.data_ptr(), self._k_scales.data_ptr(), self._v_codes.data_ptr(),
                                   self._v_scales.data_ptr(), pages, page_size, heads, dim, prec)

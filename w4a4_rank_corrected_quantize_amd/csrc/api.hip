@@ -508,7 +508,7 @@ extern "C" svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uin
         return SVDQ_ERR_INVALID_ARG;
     if (!kv4_stride_ok(ldq, heads_q, c.dim)) return SVDQ_ERR_SHAPE;
     if (table_width < 1) return SVDQ_ERR_INVALID_ARG;
-    if (((int64_t)table_width << c.page_shift) > INT32_MAX - 256) return SVDQ_ERR_SHAPE;
+    if (((int64_t)table_width << c.page_shift) > INT32_MAX - 4096) return SVDQ_ERR_SHAPE;
     if (T > 0 && B > 0 && (!Q || !block_table || !q_start || !kv_len || !O)) return SVDQ_ERR_INVALID_ARG;
     if (!aligned16(Q) || !aligned4(block_table) || !aligned4(q_start) || !aligned4(kv_len) || !aligned16(O) ||
         !aligned16(lse) || !aligned16(work))

@@ -9,15 +9,15 @@
 //
 // The products are formed transposed, S^T = K Q^T and O^T = V^T P^T, with
 // v_mfma_f32_16x16x32_bf16: a lane's column is a query row, so maximum, sum
-// and rescaling are per lane.  In a step of 64 keys, row r of K tile t is key
-// 16 (r / 4) + 4 t + r % 4: lane part b then holds the scores of its keys
-// 16 b .. 16 b + 15, which are the 16 tokens that it reads of V, so the
-// probabilities go from one product to the next in registers.  The page
-// layout (kv4.h) gives a lane its part of a K row and its V column as 16-byte
-// loads in operand order; nothing passes through LDS.
+// and rescaling are per lane.  A step is 64 keys, four runs of 16; lane part b
+// = lane / 16 gets the scores of tokens 4 b .. 4 b + 3 of every run, and these
+// are the tokens that it reads of V, so the probabilities go from one product
+// to the next in registers.  The page layout (kv4.h) has every run in operand
+// order: 16 consecutive bytes per lane, nothing passes through LDS.
 //
-// INT4 scales (fp32) belong to a key and a 64-channel group: a lane holds the
-// scale of key 16 b + lane % 16 and multiplies with a row broadcast (DPP).
+// INT4 scales (fp32) belong to a key and a 64-channel group: lane (b, j) holds
+// the scale of token 4 b + j % 4 of run j / 4 and the lanes of part b multiply
+// with a broadcast from it (DPP).
 // K's multiply the group's score sums, V's the probabilities before they are
 // rounded to bf16.  MXFP4 scales enter the fp4 -> bf16 conversion itself.
 //
@@ -46,6 +46,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLazy = 8.0f;
+constexpr int kManyTiles = 2;        // 16-row tiles per wave of a block of many rows
 
 __device__ __forceinline__ uint32_t ka_pack2(float lo, float hi)
 {
@@ -100,7 +102,7 @@ struct KvArgs {
     uint16_t *O;
     float *lse, *work;
     int64_t ldq;
-    int T, B, heads_q, group, table_width, q_tiles, splits, causal, window;
+    int T, B, heads_q, group, table_width, q_tiles, splits, split_steps, causal, window;
     float scale;
 };
 
@@ -110,63 +112,118 @@ struct KvStep {
     static constexpr int KS = D / 32;             // 32-channel product steps = dwords of a lane's K part
     static constexpr int NB = D / 32;             // 32-channel blocks of V
     static constexpr int NG = INT4 ? D / 64 : D / 32;
-    uint32_t k[4][KS];
-    u32x4 v[NB];
-    float ks[INT4 ? NG : 4];                      // INT4: of key 16 b + lane % 16; MXFP4: of the K row of tile t
-    float vs[NG];                                 // of key 16 b + lane % 16
-    bool ok;                                      // the lane part's 16 keys lie in a page of the cache
+    uint32_t k[4][KS], v[4][NB];                  // run t
+    float ks[INT4 ? NG : 4];                      // INT4: of the lane's scale key; MXFP4: of the K row of run t
+    float vs[NG];                                 // of the lane's scale key
+    int valid;                                    // bit t: run t lies in a page of the cache
 };
 
+// The block tables and lengths are read through scalar loads: their addresses
+// are uniform, and the count of vector loads in flight stays that of the codes
+// (a page number from a vector load made every step wait for the codes issued
+// before it).
+typedef const __attribute__((address_space(4))) int32_t ka_const_int;
+
+// Pages of the four runs of a step; one where a page holds a whole step.
+struct KvPages {
+    int p[4];
+};
+
+__device__ __forceinline__ KvPages ka_pages(const KvArgs &a, ka_const_int *table, int key0, int kv_end)
+{
+    KvPages g;
+    const int top = max(kv_end - 1, 0);                 // always an entry of the table
+    g.p[0] = table[min(key0, top) >> a.c.page_shift];
+    if (a.c.page_shift >= 6) {
+        g.p[1] = g.p[2] = g.p[3] = g.p[0];
+    } else {
+#pragma unroll
+        for (int t = 1; t < 4; ++t) g.p[t] = table[min(key0 + 16 * t, top) >> a.c.page_shift];
+    }
+    return g;
+}
+
+// The four runs' numbers in the cache, and which of them hold keys (bit t).
+struct KvRuns {
+    int64_t run[4];
+    int valid;
+};
+
+__device__ __forceinline__ KvRuns ka_runs(const KvArgs &a, const KvPages &pg, int head, int key0, int kv_end)
+{
+    KvRuns r;
+    const int left = kv_end - key0;
+    const int in = left > 48 ? 15 : (left > 32 ? 7 : (left > 16 ? 3 : (left > 0 ? 1 : 0)));
+    const int mask = (1 << a.c.page_shift) - 1, rs = a.c.page_shift - 4;
+    const int page = (uint32_t)pg.p[0] < (uint32_t)a.c.pages ? pg.p[0] : 0;      // not used then; page 0 exists
+    const int ok0 = (uint32_t)pg.p[0] < (uint32_t)a.c.pages ? 15 : 0;
+    r.run[0] = (((int64_t)page * a.c.heads + head) << rs) + ((key0 & mask) >> 4);
+    if (a.c.page_shift >= 6) {
+        r.run[1] = r.run[0] + 1, r.run[2] = r.run[0] + 2, r.run[3] = r.run[0] + 3;
+        r.valid = ok0 & in;
+    } else {
+        int ok = ok0 & 1;
+#pragma unroll
+        for (int t = 1; t < 4; ++t) {
+            const bool good = (uint32_t)pg.p[t] < (uint32_t)a.c.pages;
+            r.run[t] = (((int64_t)(good ? pg.p[t] : 0) * a.c.heads + head) << rs) + (((key0 + 16 * t) & mask) >> 4);
+            ok |= good ? 1 << t : 0;
+        }
+        r.valid = ok & in;
+    }
+    return r;
+}
+
+// All ones where bit 0 of `valid` is set and left > 0, else 0.  The scale of a
+// V place past the end becomes 0 with it (the place may hold anything, and 0
+// times that need not be 0); as a select, the compiler loads under a condition.
+__device__ __forceinline__ uint32_t ka_in_mask(int valid, int left)
+{
+    return (uint32_t)(-(valid & 1) & ((-left) >> 31));
+}
+
 template <int D, bool INT4>
-__device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, const int32_t *table, int head, int key0,
+__device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, const KvPages &pg, int head, int key0,
                                         int kv_end, int lane)
 {
-    constexpr int NB = D / 32, NG = KvStep<D, INT4>::NG;
-    const int P = 1 << a.c.page_shift, j = lane & 15, b = lane >> 4;
-    // page of the 16 keys that hold the lane's K rows, and of its V columns
-    const int runk = key0 + 16 * (j >> 2), runv = key0 + 16 * b;
-    int pk = runk < kv_end ? table[runk >> a.c.page_shift] : -1;
-    int pv = runv < kv_end ? table[runv >> a.c.page_shift] : -1;
-    st.ok = (uint32_t)pv < (uint32_t)a.c.pages;
-    pk = (uint32_t)pk < (uint32_t)a.c.pages ? pk : 0;       // masked below; page 0 exists
-    pv = st.ok ? pv : 0;
-    const size_t hk = (size_t)pk * a.c.heads + head, hv = (size_t)pv * a.c.heads + head;
-    const int ik = runk & (P - 1), iv = runv & (P - 1);
-    const uint8_t *kc = a.c.k_codes + (hk * P + ik + (j & 3)) * (D / 2) + b * (D / 8);
+    constexpr int NG = KvStep<D, INT4>::NG;
+    const int j = lane & 15, b = lane >> 4;
+    const KvRuns r = ka_runs(a, pg, head, key0, kv_end);
+    const int64_t *run = r.run;
+    st.valid = r.valid;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
+        const uint8_t *kp = a.c.k_codes + run[t] * (8 * D) + (D / 8) * lane;
+        const uint8_t *vp = a.c.v_codes + run[t] * (8 * D) + (D / 8) * lane;
         if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(kc + 4 * t * (D / 2));
+            const uint4 u = *reinterpret_cast<const uint4 *>(kp), w = *reinterpret_cast<const uint4 *>(vp);
             st.k[t][0] = u.x, st.k[t][1] = u.y, st.k[t][2] = u.z, st.k[t][3] = u.w;
+            st.v[t][0] = w.x, st.v[t][1] = w.y, st.v[t][2] = w.z, st.v[t][3] = w.w;
         } else {
-            const uint2 u = *reinterpret_cast<const uint2 *>(kc + 4 * t * (D / 2));
+            const uint2 u = *reinterpret_cast<const uint2 *>(kp), w = *reinterpret_cast<const uint2 *>(vp);
             st.k[t][0] = u.x, st.k[t][1] = u.y;
+            st.v[t][0] = w.x, st.v[t][1] = w.y;
         }
     }
-    const uint8_t *vc = a.c.v_codes + (hv * (D / 2) + j) * P + iv;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) st.v[n] = *reinterpret_cast<const u32x4 *>(vc + (size_t)16 * n * P);
-    const bool in = st.ok && runv + j < kv_end;
+    // the lane's scale key: token 4 b + j % 4 of run j / 4
+    const int sr = j >> 2, tok = 4 * b + (j & 3);
+    const int64_t mine = sr & 2 ? (sr & 1 ? run[3] : run[2]) : (sr & 1 ? run[1] : run[0]);
+    const uint32_t in = ka_in_mask(st.valid >> sr, kv_end - key0 - 16 * sr - tok);
+    const int64_t so = mine * (16 * NG) + tok;
     if constexpr (INT4) {
-        const float *ks = (const float *)a.c.k_scales + hv * NG * P + iv + j;
-        const float *vs = (const float *)a.c.v_scales + hv * NG * P + iv + j;
+        const float *ks = (const float *)a.c.k_scales + so, *vs = (const float *)a.c.v_scales + so;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            st.ks[g] = ks[g * P];
-            const float s = vs[g * P];
-            st.vs[g] = in ? s : 0.0f;             // a place past the end may hold anything: 0, not 0 times that
-        }
+        for (int g = 0; g < NG; ++g) st.ks[g] = ks[16 * g];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) st.vs[g] = bits_f32(f32_bits(vs[16 * g]) & in);
     } else {
         const int blk = D == 128 ? b : b >> 1;    // the 32-channel block of the lane's K part
-        const uint8_t *ks = (const uint8_t *)a.c.k_scales + (hk * NG + blk) * P + ik + (j & 3);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) st.ks[t] = bits_f32((uint32_t)ks[4 * t] << 23);
-        const uint8_t *vs = (const uint8_t *)a.c.v_scales + hv * NG * P + iv + j;
+        for (int t = 0; t < 4; ++t)
+            st.ks[t] = bits_f32((uint32_t)((const uint8_t *)a.c.k_scales)[run[t] * (16 * NG) + 16 * blk + j] << 23);
+        const uint8_t *vs = (const uint8_t *)a.c.v_scales + so;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const uint32_t e = vs[g * P];
-            st.vs[g] = in ? bits_f32(e << 23) : 0.0f;
-        }
+        for (int g = 0; g < NG; ++g) st.vs[g] = bits_f32(((uint32_t)vs[16 * g] << 23) & in);
     }
 }
 
@@ -184,8 +241,8 @@ __device__ __forceinline__ bf16x8 ka_k_operand(uint32_t w, float scale)
     return __builtin_bit_cast(bf16x8, o);
 }
 
-// Operands of 8 keys (two dwords of V codes) for the low- and the high-nibble
-// channel.  S: the 8-key half of the lane's 16 keys (for the scales).
+// Operands of 8 keys (the dwords of two runs) for the low- and the high-nibble
+// channel.  S: runs 0 and 1 or 2 and 3 (for the scales).
 template <bool INT4, int S>
 __device__ __forceinline__ void ka_v_operands(uint32_t w0, uint32_t w1, float vs, bf16x8 &lo, bf16x8 &hi)
 {
@@ -215,7 +272,7 @@ __device__ __forceinline__ void ka_v_operands(uint32_t w0, uint32_t w1, float vs
     }
 }
 
-// x[4 t + i] *= / += with the scale of key 4 t + i of the lane's part.
+// o[4 t + i] = / += x[4 t + i] times the scale of token i of the lane's part of run t.
 template <int J = 0>
 __device__ __forceinline__ void ka_scale_keys(float (&o)[16], const float (&x)[16], float s)
 {
@@ -234,325 +291,549 @@ __device__ __forceinline__ void ka_fma_keys(float (&o)[16], const float (&x)[16]
     }
 }
 
+// A wave's rows: 16 CT query rows of one key head, column 16 ct + j each.
+template <int D, int CT>
+struct KvRows {
+    bf16x8 q[CT][D / 32];
+    f32x4 acc[CT][D / 16];                        // O^T, tile (block n, half h) at 2 n + h
+    float m[CT], l[CT];                           // running maximum; the lane part's share of the sum
+    int hi_key[CT], lo_key[CT];                   // the columns' keys: lo <= key < hi
+    int all_hi, all_lo;                           // over the columns: the least hi, the greatest lo
+};
+
 template <int D, bool INT4, int CT>
-__global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
+__device__ __forceinline__ void ka_rows(KvRows<D, CT> &w, const KvArgs &a, int head, int qs, int qn, int kv, int64_t r0,
+                                        int64_t rows, int lane)
 {
-    constexpr int KS = D / 32, NB = D / 32, NG = KvStep<D, INT4>::NG;
-    constexpr int R = 16 * CT;                        // rows of a wave
-    __shared__ float om[R][D + 4];                    // the waves' sums, where they share rows
-    __shared__ float mm[4][R], ll[4][R];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int j = lane & 15, b = lane >> 4;
-    // blocks of one head are consecutive multiples of heads * B apart, so they
-    // meet in one XCD's L2 where that is a multiple of 8
-    int idx = blockIdx.x;
-    const int head = idx % a.c.heads;
-    idx /= a.c.heads;
-    const int seq = idx % a.B;
-    idx /= a.B;
-    const int split = idx % a.splits;
-    const int qt0 = idx / a.splits;
-    const int qs = min(max(a.q_start[seq], 0), a.T);
-    const int qn = min(max(a.q_start[seq + 1], qs), a.T) - qs;
-    const int kv = min(max(a.kv_len[seq], 0), a.table_width << a.c.page_shift);
-    const int32_t *table = a.table + (size_t)seq * a.table_width;
-    const int G = a.group;
-    const int64_t rows = (int64_t)qn * G;
-    const bool shared = rows <= R;                    // one list of rows for the four waves
-    const int block_rows = shared ? R : 4 * R;
-    const int steps = (kv + 63) >> 6;
-    const int per = (steps + a.splits - 1) / a.splits;
-    const float c2 = a.scale * kLog2e;
+    const int j = lane & 15, b = lane >> 4, G = a.group;
+    w.all_hi = kv, w.all_lo = 0;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const int64_t r = min(r0 + 16 * ct + j, rows - 1);      // rows past the last repeat it, never stored
+        const int tok = (int)(r / G), hd = head * G + (int)(r % G);
+        const uint16_t *qp = a.Q + (qs + tok) * a.ldq + (int64_t)hd * D;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            const int ch = INT4 ? 64 * (k >> 1) + 16 * b + 8 * (k & 1) : (D / 4) * b + 8 * k;
+            w.q[ct][k] = *reinterpret_cast<const bf16x8 *>(qp + ch);
+        }
+        const int place = kv - qn + tok;
+        w.hi_key[ct] = a.causal ? min(place + 1, kv) : kv;
+        w.lo_key[ct] = a.causal && a.window > 0 ? place - a.window + 1 : 0;
+        w.all_hi = min(w.all_hi, w.hi_key[ct]), w.all_lo = max(w.all_lo, w.lo_key[ct]);
+        w.m[ct] = -INFINITY, w.l[ct] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) w.acc[ct][n] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1)
+        w.all_hi = min(w.all_hi, __shfl_xor(w.all_hi, d)), w.all_lo = max(w.all_lo, __shfl_xor(w.all_lo, d));
+    w.all_hi = __builtin_amdgcn_readfirstlane(w.all_hi), w.all_lo = __builtin_amdgcn_readfirstlane(w.all_lo);
+}
 
-    // the last tiles first: under a causal mask they are the longest
-    const int64_t tiles = (rows + block_rows - 1) / block_rows;
-    for (int64_t qt = tiles - 1 - qt0; qt >= 0; qt -= a.q_tiles) {
-        const int64_t r0 = qt * block_rows + (shared ? 0 : wave * R);
-        // Q, limits of every column
-        bf16x8 q[CT][KS];
-        int hi_key[CT], lo_key[CT];
-        int all_hi = kv, any_hi = 0, any_lo = kv, all_lo = 0;
+// One step's scores (run t, token 4 b + i at 4 t + i) to probabilities: masks,
+// the running maximum, the sum.
+template <int D, int CT>
+__device__ __forceinline__ void ka_softmax(KvRows<D, CT> &w, float (&p)[CT][16], int key0, int valid, float c2, int b)
+{
+    if (key0 + 64 > w.all_hi || key0 < w.all_lo || valid != 15) {
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            const int64_t r = min(r0 + 16 * ct + j, rows - 1);
-            const int tok = (int)(r / G), hd = head * G + (int)(r % G);
-            const uint16_t *qp = a.Q + (qs + tok) * a.ldq + (int64_t)hd * D;
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const int ch = INT4 ? 64 * (k >> 1) + 16 * b + 8 * (k & 1) : (D / 4) * b + 8 * k;
-                q[ct][k] = *reinterpret_cast<const bf16x8 *>(qp + ch);
+            for (int i = 0; i < 16; ++i) {
+                const int key = key0 + 16 * (i >> 2) + 4 * b + (i & 3);
+                const bool see = ((valid >> (i >> 2)) & 1) && key < w.hi_key[ct] && key >= w.lo_key[ct];
+                p[ct][i] = see ? p[ct][i] : -INFINITY;
             }
-            const int place = kv - qn + tok;
-            hi_key[ct] = a.causal ? min(place + 1, kv) : kv;
-            lo_key[ct] = a.causal && a.window > 0 ? place - a.window + 1 : 0;
-            all_hi = min(all_hi, hi_key[ct]), any_hi = max(any_hi, hi_key[ct]);
-            any_lo = min(any_lo, lo_key[ct]), all_lo = max(all_lo, lo_key[ct]);
+    }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        // the reference m stays until a score exceeds it by kLazy (seen in any
+        // lane): p is at most 2^kLazy then, and its relative rounding the same
+        float mx = p[ct][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[ct][i]);
+        if (__any((mx - w.m[ct]) * c2 > kLazy)) {
+            mx = fmaxf(ka_max_parts(mx), w.m[ct]);
+            const float f = w.m[ct] == mx ? 1.0f : __builtin_amdgcn_exp2f((w.m[ct] - mx) * c2);
+            w.l[ct] *= f;
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) w.acc[ct][n] *= f;
+            w.m[ct] = mx;
         }
+        const float base = w.m[ct] == -INFINITY ? 0.0f : -w.m[ct] * c2;
+        float sum = 0.0f;
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) {
-            all_hi = min(all_hi, __shfl_xor(all_hi, d)), any_hi = max(any_hi, __shfl_xor(any_hi, d));
-            any_lo = min(any_lo, __shfl_xor(any_lo, d)), all_lo = max(all_lo, __shfl_xor(all_lo, d));
+        for (int i = 0; i < 16; ++i) {
+            p[ct][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[ct][i], c2, base));
+            sum += p[ct][i];
         }
-        all_hi = __builtin_amdgcn_readfirstlane(all_hi), any_hi = __builtin_amdgcn_readfirstlane(any_hi);
-        any_lo = __builtin_amdgcn_readfirstlane(any_lo), all_lo = __builtin_amdgcn_readfirstlane(all_lo);
-        // the split's steps, cut to the keys that some column sees
-        int s0 = max(split * per, max(any_lo, 0) >> 6);
-        int s1 = min(min((split + 1) * per, steps), (max(any_hi, 0) + 63) >> 6);
-        if (r0 >= rows) s1 = s0;
-        const int stride = shared ? 4 : 1;
-        if (shared) s0 += wave;
-
-        f32x4 acc[CT][2 * NB] = {};
-        float m[CT], l[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) m[ct] = -INFINITY, l[ct] = 0.0f;
-        KvStep<D, INT4> cur, nxt;
-        if (s0 < s1) ka_load<D, INT4>(cur, a, table, head, 64 * s0, kv, lane);
-        for (int s = s0; s < s1; s += stride) {
-            if (s + stride < s1) ka_load<D, INT4>(nxt, a, table, head, 64 * (s + stride), kv, lane);
-            const int key0 = 64 * s;
-            // scores of keys 16 b + 4 t + i
-            float p[CT][16];
-#pragma unroll
-            for (int g = 0; g < (INT4 ? NG : 1); ++g) {
-                f32x4 sc[CT][4] = {};
-#pragma unroll
-                for (int k = (INT4 ? 2 * g : 0); k < (INT4 ? 2 * g + 2 : KS); ++k) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const bf16x8 kk = ka_k_operand<INT4>(cur.k[t][k], INT4 ? 0.0f : cur.ks[t]);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-                            sc[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[ct][k], sc[ct][t], 0, 0, 0);
-                    }
-                }
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    float x[16];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[4 * t + i] = sc[ct][t][i];
-                    if constexpr (!INT4) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) p[ct][i] = x[i];
-                    } else if (g == 0) {
-                        ka_scale_keys(p[ct], x, cur.ks[0]);
-                    } else {
-                        ka_fma_keys(p[ct], x, cur.ks[g]);
-                    }
-                }
-            }
-            const bool mask = key0 + 64 > all_hi || key0 < all_lo || __any(!cur.ok);
-            if (mask) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int key = key0 + 16 * b + i;
-                        const bool see = cur.ok && key < hi_key[ct] && key >= lo_key[ct];
-                        p[ct][i] = see ? p[ct][i] : -INFINITY;
-                    }
-            }
-            // running maximum; probabilities
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                float mx = p[ct][0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[ct][i]);
-                mx = fmaxf(ka_max_parts(mx), m[ct]);
-                if (__any(mx > m[ct])) {
-                    const float f = m[ct] == mx ? 1.0f : __builtin_amdgcn_exp2f((m[ct] - mx) * c2);
-                    l[ct] *= f;
-#pragma unroll
-                    for (int n = 0; n < 2 * NB; ++n) acc[ct][n] *= f;
-                    m[ct] = mx;
-                }
-                const float base = mx == -INFINITY ? 0.0f : -mx * c2;
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    p[ct][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[ct][i], c2, base));
-                    sum += p[ct][i];
-                }
-                l[ct] += sum;
-            }
-            // O^T += V^T P^T
-            constexpr int PG = INT4 ? NG : 1;
-#pragma unroll
-            for (int g = 0; g < PG; ++g) {
-                bf16x8 pb[CT][2];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    float x[16];
-                    if constexpr (INT4) {
-                        ka_scale_keys(x, p[ct], cur.vs[g]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = p[ct][i];
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        pb[ct][h] = __builtin_bit_cast(bf16x8, (u32x4){ka_pack2(x[8 * h], x[8 * h + 1]), ka_pack2(x[8 * h + 2], x[8 * h + 3]),
-                                                                       ka_pack2(x[8 * h + 4], x[8 * h + 5]), ka_pack2(x[8 * h + 6], x[8 * h + 7])});
-                }
-#pragma unroll
-                for (int n = g * (NB / PG); n < (g + 1) * (NB / PG); ++n) {
-                    bf16x8 lo, hi;
-                    ka_v_operands<INT4, 0>(cur.v[n][0], cur.v[n][1], INT4 ? 0.0f : cur.vs[n % NG], lo, hi);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        acc[ct][2 * n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, pb[ct][0], acc[ct][2 * n], 0, 0, 0);
-                        acc[ct][2 * n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, pb[ct][0], acc[ct][2 * n + 1], 0, 0, 0);
-                    }
-                    ka_v_operands<INT4, 1>(cur.v[n][2], cur.v[n][3], INT4 ? 0.0f : cur.vs[n % NG], lo, hi);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        acc[ct][2 * n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, pb[ct][1], acc[ct][2 * n], 0, 0, 0);
-                        acc[ct][2 * n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, pb[ct][1], acc[ct][2 * n + 1], 0, 0, 0);
-                    }
-                }
-            }
-            cur = nxt;
-        }
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) l[ct] = ka_sum_parts(l[ct]);
-
-        if (shared) {
-            // the waves' parts, in wave order, into om
-            if (b == 0) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) mm[wave][16 * ct + j] = m[ct], ll[wave][16 * ct + j] = l[ct];
-            }
-            __syncthreads();
-            float f[CT];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const int r = 16 * ct + j;
-                const float mx = fmaxf(fmaxf(mm[0][r], mm[1][r]), fmaxf(mm[2][r], mm[3][r]));
-                f[ct] = m[ct] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m[ct] - mx) * c2);
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if (wave == w) {
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                        for (int n = 0; n < 2 * NB; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float &o = om[16 * ct + j][16 * n + 4 * b + i];
-                                o = (w == 0 ? 0.0f : o) + acc[ct][n][i] * f[ct];
-                            }
-                }
-                __syncthreads();
-            }
-            const int nr = (int)rows;
-            for (int e = tid; e < nr * (D / 4); e += 256) {
-                const int r = e / (D / 4), c = 4 * (e % (D / 4));
-                const float mx = fmaxf(fmaxf(mm[0][r], mm[1][r]), fmaxf(mm[2][r], mm[3][r]));
-                float sum = 0.0f;
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    sum += mm[w][r] == -INFINITY ? 0.0f : ll[w][r] * __builtin_amdgcn_exp2f((mm[w][r] - mx) * c2);
-                const size_t row = (size_t)(qs + r / G) * a.heads_q + head * G + r % G;
-                const float4 o = *reinterpret_cast<const float4 *>(&om[r][c]);
-                if (a.splits > 1) {
-                    const size_t part = (size_t)split * a.T * a.heads_q + row;
-                    *reinterpret_cast<float4 *>(a.work + part * D + c) = o;
-                    if (c == 0) {
-                        float *ml = a.work + (size_t)a.splits * a.T * a.heads_q * D + 2 * part;
-                        ml[0] = mx * a.scale, ml[1] = sum;
-                    }
-                } else {
-                    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-                    *reinterpret_cast<uint2 *>(a.O + row * D + c) =
-                        make_uint2(ka_pack2(o.x * inv, o.y * inv), ka_pack2(o.z * inv, o.w * inv));
-                    if (c == 0 && a.lse)
-                        a.lse[row] = sum == 0.0f ? -INFINITY : mx * a.scale + kLn2 * __builtin_amdgcn_logf(sum);
-                }
-            }
-            __syncthreads();
-        } else {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const int64_t r = r0 + 16 * ct + j;
-                if (r >= rows) continue;
-                const size_t row = (size_t)(qs + (int)(r / G)) * a.heads_q + head * G + (int)(r % G);
-                if (a.splits > 1) {
-                    const size_t part = (size_t)split * a.T * a.heads_q + row;
-#pragma unroll
-                    for (int n = 0; n < 2 * NB; ++n)
-                        *reinterpret_cast<float4 *>(a.work + part * D + 16 * n + 4 * b) =
-                            make_float4(acc[ct][n][0], acc[ct][n][1], acc[ct][n][2], acc[ct][n][3]);
-                    if (b == 0) {
-                        float *ml = a.work + (size_t)a.splits * a.T * a.heads_q * D + 2 * part;
-                        ml[0] = m[ct] * a.scale, ml[1] = l[ct];
-                    }
-                } else {
-                    const float inv = l[ct] > 0.0f ? 1.0f / l[ct] : (l[ct] == 0.0f ? 0.0f : l[ct]);
-#pragma unroll
-                    for (int n = 0; n < 2 * NB; ++n)
-                        *reinterpret_cast<uint2 *>(a.O + row * D + 16 * n + 4 * b) =
-                            make_uint2(ka_pack2(acc[ct][n][0] * inv, acc[ct][n][1] * inv),
-                                       ka_pack2(acc[ct][n][2] * inv, acc[ct][n][3] * inv));
-                    if (b == 0 && a.lse)
-                        a.lse[row] = l[ct] == 0.0f ? -INFINITY : m[ct] * a.scale + kLn2 * __builtin_amdgcn_logf(l[ct]);
-                }
-            }
-        }
+        w.l[ct] += sum;
     }
 }
 
-// O = sum over the splits, in split order; one wave per row.
+// Operands of the second product: keys of runs 2 h and 2 h + 1.
+__device__ __forceinline__ void ka_p_operands(const float (&x)[16], bf16x8 (&pb)[2])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        pb[h] = __builtin_bit_cast(bf16x8, (u32x4){ka_pack2(x[8 * h], x[8 * h + 1]), ka_pack2(x[8 * h + 2], x[8 * h + 3]),
+                                                   ka_pack2(x[8 * h + 4], x[8 * h + 5]), ka_pack2(x[8 * h + 6], x[8 * h + 7])});
+}
+
+// Order of a product whose operands come from LDS: `first` reads ahead, then
+// one read per CT products.  Left to itself the compiler reads each operand
+// right before its product and waits for it.
+template <int FIRST, int READS, int CT>
+__device__ __forceinline__ void ka_interleave()
+{
+    __builtin_amdgcn_sched_group_barrier(0x100, FIRST, 0);
+#pragma unroll
+    for (int i = FIRST; i < READS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, CT * FIRST, 0);
+}
+
+// One step of 64 keys for the wave's rows.  k_op(t, k) gives K's operand of
+// run t and product step k, v_op(n, h, lo, hi) V's of block n and runs 2 h, 2 h
+// + 1; ks and vs are the lane's INT4 scales.  LDS: the operands are read from
+// LDS.
+template <int D, bool INT4, int CT, bool LDS, class KOp, class VOp, class During>
+__device__ __forceinline__ void ka_step(KvRows<D, CT> &w, int key0, int valid, const float *ks, const float *vs, float c2,
+                                        int b, KOp k_op, VOp v_op, During during)
+{
+    constexpr int KS = D / 32, NB = D / 32, NG = INT4 ? D / 64 : 1;
+    float p[CT][16];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        f32x4 sc[CT][4] = {};
+#pragma unroll
+        for (int k = g * (KS / NG); k < (g + 1) * (KS / NG); ++k)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const bf16x8 kk = k_op(t, k);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    sc[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, w.q[ct][k], sc[ct][t], 0, 0, 0);
+            }
+        if constexpr (LDS) ka_interleave<4, 4 * KS / NG, CT>();
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = sc[ct][i >> 2][i & 3];
+            if constexpr (!INT4) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[ct][i] = x[i];
+            } else if (g == 0) {
+                ka_scale_keys(p[ct], x, ks[0]);
+            } else {
+                ka_fma_keys(p[ct], x, ks[g]);
+            }
+        }
+    }
+    // V's first operands are on their way during the softmax
+    bf16x8 lo[NB][2], hi[NB][2];
+    if constexpr (LDS) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v_op(0, h, lo[0][h], hi[0][h]);
+    }
+    ka_softmax<D, CT>(w, p, key0, valid, c2, b);
+    bf16x8 pb[NG][CT][2];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            if constexpr (INT4) {
+                float x[16];
+                ka_scale_keys(x, p[ct], vs[g]);
+                ka_p_operands(x, pb[g][ct]);
+            } else {
+                ka_p_operands(p[ct], pb[g][ct]);
+            }
+        }
+    if constexpr (LDS) __builtin_amdgcn_sched_barrier(0);
+    during();
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int n = g * (NB / NG); n < (g + 1) * (NB / NG); ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!LDS || n > 0) v_op(n, h, lo[n][h], hi[n][h]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    w.acc[ct][2 * n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[n][h], pb[g][ct][h], w.acc[ct][2 * n], 0, 0, 0);
+                    w.acc[ct][2 * n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[n][h], pb[g][ct][h], w.acc[ct][2 * n + 1], 0, 0, 0);
+                }
+            }
+    }
+    if constexpr (LDS) {
+        // CT products, then a share of the conversions, the next read of V, and
+        // towards the end the writes
+#pragma unroll
+        for (int i = 0; i < 4 * NB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, INT4 ? 6 : 5, 0);
+            if (i < 4 * NB - 4) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (i >= 2 * NB) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Few rows: the wave converts its own codes, steps s0, s0 + stride, .. < s1.
+// Codes are one step ahead, their pages two; past the end the last run's page
+// is looked up and nothing of it is used.
+template <int D, bool INT4, int CT>
+__device__ __forceinline__ void ka_walk(KvRows<D, CT> &w, const KvArgs &a, ka_const_int *table, int head, int kv, int s0,
+                                        int s1, int stride, float c2, int lane)
+{
+    constexpr int NG = KvStep<D, INT4>::NG;
+    KvStep<D, INT4> x, y;
+    if (s0 >= s1) return;
+    auto compute = [&](const KvStep<D, INT4> &c, int s) {
+        ka_step<D, INT4, CT, false>(
+            w, 64 * s, c.valid, c.ks, c.vs, c2, lane >> 4,
+            [&](int t, int k) { return ka_k_operand<INT4>(c.k[t][k], INT4 ? 0.0f : c.ks[t]); },
+            [&](int n, int h, bf16x8 &lo, bf16x8 &hi) {
+                const float vs = INT4 ? 0.0f : c.vs[n % NG];
+                if (h == 0) ka_v_operands<INT4, 0>(c.v[0][n], c.v[1][n], vs, lo, hi);
+                else ka_v_operands<INT4, 1>(c.v[2][n], c.v[3][n], vs, lo, hi);
+            },
+            [] {});
+    };
+    ka_load<D, INT4>(x, a, ka_pages(a, table, 64 * s0, kv), head, 64 * s0, kv, lane);
+    KvPages pages = ka_pages(a, table, 64 * (s0 + stride), kv);
+    for (int s = s0;; s += 2 * stride) {
+        ka_load<D, INT4>(y, a, pages, head, 64 * (s + stride), kv, lane);
+        pages = ka_pages(a, table, 64 * (s + 2 * stride), kv);
+        compute(x, s);
+        if (s + stride >= s1) break;
+        ka_load<D, INT4>(x, a, pages, head, 64 * (s + 2 * stride), kv, lane);
+        pages = ka_pages(a, table, 64 * (s + 3 * stride), kv);
+        compute(y, s + stride);
+        if (s + 2 * stride >= s1) break;
+    }
+}
+
+// Many rows: the block's four waves convert a step's codes together, a quarter
+// each, into LDS (operand order, 16 bytes per lane: no bank conflicts), and
+// every wave multiplies the whole step.  Two stages: the next step is written
+// while the current one is read; its codes were loaded a step before that.
+template <int D, bool INT4>
+struct KvShare {
+    static constexpr int KS = D / 32, NB = D / 32;
+    static constexpr int K_BYTES = 4 * KS * 1024, V_BYTES = 4 * NB * 1024, STAGE = K_BYTES + V_BYTES;
+    // K of run `wave`; V of runs 2 (wave / 2) and + 1, blocks NB / 2 (wave % 2) ..
+    uint32_t k[KS], v[2][NB / 2];
+    float ks;                                     // MXFP4: of the K row
+    float vq[NB / 2];                             // MXFP4: of token 4 b + j % 4 of run 2 (wave / 2) + (j / 4) % 2
+    float iks[2], ivs[2];                         // INT4: the lane's scales, as in KvStep
+    int valid;
+};
+
+template <int D, bool INT4>
+__device__ __forceinline__ void ka_share_load(KvShare<D, INT4> &st, const KvArgs &a, const KvPages &pg, int head, int key0,
+                                              int kv_end, int wave, int lane)
+{
+    constexpr int KS = D / 32, NB = D / 32, NG = INT4 ? D / 64 : D / 32;
+    const int j = lane & 15, b = lane >> 4;
+    const KvRuns r = ka_runs(a, pg, head, key0, kv_end);
+    const int64_t *run = r.run;
+    st.valid = r.valid;
+    const int s2 = wave >> 1;
+    const int64_t rv[2] = {s2 ? run[2] : run[0], s2 ? run[3] : run[1]};
+    const int64_t rk = wave & 1 ? rv[1] : rv[0];
+    const uint8_t *kp = a.c.k_codes + rk * (8 * D) + (D / 8) * lane;
+    if constexpr (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(kp);
+        st.k[0] = u.x, st.k[1] = u.y, st.k[2] = u.z, st.k[3] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(kp);
+        st.k[0] = u.x, st.k[1] = u.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint8_t *vp = a.c.v_codes + rv[i] * (8 * D) + (D / 8) * lane + 2 * NB * (wave & 1);
+        if constexpr (D == 128) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(vp);
+            st.v[i][0] = u.x, st.v[i][1] = u.y;
+        } else {
+            st.v[i][0] = *reinterpret_cast<const uint32_t *>(vp);
+        }
+    }
+    if constexpr (INT4) {
+        const int sr = j >> 2, tok = 4 * b + (j & 3);
+        const int64_t mine = sr & 2 ? (sr & 1 ? run[3] : run[2]) : (sr & 1 ? run[1] : run[0]);
+        const uint32_t in = ka_in_mask(st.valid >> sr, kv_end - key0 - 16 * sr - tok);
+        const float *ks = (const float *)a.c.k_scales + mine * (16 * NG) + tok;
+        const float *vs = (const float *)a.c.v_scales + mine * (16 * NG) + tok;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) st.iks[g] = ks[16 * g];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) st.ivs[g] = bits_f32(f32_bits(vs[16 * g]) & in);
+    } else {
+        const int blk = D == 128 ? b : b >> 1;
+        st.ks = bits_f32((uint32_t)((const uint8_t *)a.c.k_scales)[rk * (16 * NG) + 16 * blk + j] << 23);
+        const int sr = (j >> 2) & 1, tok = 4 * b + (j & 3);
+        const uint32_t in = ka_in_mask(st.valid >> (2 * s2 + sr), kv_end - key0 - 16 * (2 * s2 + sr) - tok);
+        const uint8_t *vs = (const uint8_t *)a.c.v_scales + (sr ? rv[1] : rv[0]) * (16 * NG) + tok;
+#pragma unroll
+        for (int n = 0; n < NB / 2; ++n)
+            st.vq[n] = bits_f32(((uint32_t)vs[16 * (n + NB / 2 * (wave & 1))] << 23) & in);
+    }
+}
+
+template <int D, bool INT4>
+__device__ __forceinline__ void ka_share_write(const KvShare<D, INT4> &st, uint8_t *stage, int wave, int lane)
+{
+    constexpr int KS = D / 32, NB = D / 32;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+        *reinterpret_cast<bf16x8 *>(stage + 1024 * (KS * wave + k) + 16 * lane) = ka_k_operand<INT4>(st.k[k], INT4 ? 0.0f : st.ks);
+    uint8_t *vb = stage + KvShare<D, INT4>::K_BYTES + 2048 * (NB * (wave >> 1) + NB / 2 * (wave & 1)) + 16 * lane;
+#pragma unroll
+    for (int n = 0; n < NB / 2; ++n) {
+        bf16x8 lo, hi;
+        ka_v_operands<INT4, 0>(st.v[0][n], st.v[1][n], INT4 ? 0.0f : st.vq[n], lo, hi);
+        *reinterpret_cast<bf16x8 *>(vb + 2048 * n) = lo;
+        *reinterpret_cast<bf16x8 *>(vb + 2048 * n + 1024) = hi;
+    }
+}
+
+template <int D, bool INT4, int CT>
+__device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, const KvArgs &a, ka_const_int *table,
+                                               int head, int kv, int s0, int s1, float c2, int wave, int lane)
+{
+    constexpr int KS = D / 32, NB = D / 32, STAGE = KvShare<D, INT4>::STAGE, NG = INT4 ? D / 64 : 1;
+    if (s0 >= s1) return;                             // the same for the whole block
+    KvShare<D, INT4> st, st2;
+    ka_share_load<D, INT4>(st, a, ka_pages(a, table, 64 * s0, kv), head, 64 * s0, kv, wave, lane);
+    ka_share_write<D, INT4>(st, lds, wave, lane);
+    int valid = st.valid;
+    float ks[2] = {}, vs[2] = {};
+#pragma unroll
+    for (int g = 0; g < (INT4 ? NG : 0); ++g) ks[g] = st.iks[g], vs[g] = st.ivs[g];
+    ka_share_load<D, INT4>(st, a, ka_pages(a, table, 64 * (s0 + 1), kv), head, 64 * (s0 + 1), kv, wave, lane);
+    KvPages pages = ka_pages(a, table, 64 * (s0 + 2), kv);
+    for (int s = s0; s < s1; ++s) {
+        __syncthreads();                              // step s is written, the other stage free
+        uint8_t *cur = lds + ((s - s0) & 1) * STAGE, *nxt = lds + ((s - s0 + 1) & 1) * STAGE;
+        ka_share_load<D, INT4>(st2, a, pages, head, 64 * (s + 2), kv, wave, lane);
+        pages = ka_pages(a, table, 64 * (s + 3), kv);
+        // no skipping of steps that none of this wave's rows sees: the branch
+        // costs every step a copy of the accumulators
+        ka_step<D, INT4, CT, true>(
+            w, 64 * s, valid, ks, vs, c2, lane >> 4,
+            [&](int t, int k) { return *reinterpret_cast<const bf16x8 *>(cur + 1024 * (KS * t + k) + 16 * lane); },
+            [&](int n, int h, bf16x8 &lo, bf16x8 &hi) {
+                const uint8_t *v = cur + KvShare<D, INT4>::K_BYTES + 2048 * (NB * h + n) + 16 * lane;
+                lo = *reinterpret_cast<const bf16x8 *>(v), hi = *reinterpret_cast<const bf16x8 *>(v + 1024);
+            },
+            [&] { ka_share_write<D, INT4>(st, nxt, wave, lane); });
+        valid = st.valid;
+#pragma unroll
+        for (int g = 0; g < (INT4 ? NG : 0); ++g) ks[g] = st.iks[g], vs[g] = st.ivs[g];
+        st = st2;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float ka_inverse(float sum) { return sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum); }
+
+__device__ __forceinline__ float ka_lse(float mx, float sum, float scale)
+{
+    return sum == 0.0f ? -INFINITY : mx * scale + kLn2 * __builtin_amdgcn_logf(sum);
+}
+
+// Keys, in steps, of a tile of rows and a split.
+struct KvRange {
+    int s0, s1;
+};
+
+__device__ __forceinline__ KvRange ka_range(const KvArgs &a, int split, int qn, int kv, int64_t r0, int64_t r1)
+{
+    const int steps = (kv + 63) >> 6;
+    // every split the same number of steps, so that long and short sequences
+    // give blocks of equal length; more only past the caller's bound
+    const int per = max(a.split_steps, (steps + a.splits - 1) / a.splits);
+    const int first = kv - qn + (int)(r0 / a.group), last = kv - qn + (int)((r1 - 1) / a.group);
+    const int lo = a.causal && a.window > 0 ? max(first - a.window + 1, 0) : 0;
+    const int hi = a.causal ? max(min(last + 1, kv), 0) : kv;
+    return {max(split * per, lo >> 6), min(min((split + 1) * per, steps), (hi + 63) >> 6)};
+}
+
+// One row's four channels c .. of a block's or a wave's sums.
+template <int D>
+__device__ __forceinline__ void ka_store(const KvArgs &a, int split, size_t row, int c, f32x4 o, float mx, float sum)
+{
+    if (a.splits > 1) {
+        const size_t part = (size_t)split * a.T * a.heads_q + row;
+        *reinterpret_cast<f32x4 *>(a.work + part * D + c) = o;
+        if (c == 0) {
+            float *ml = a.work + (size_t)a.splits * a.T * a.heads_q * D + 2 * part;
+            ml[0] = mx * a.scale, ml[1] = sum;
+        }
+    } else {
+        o *= ka_inverse(sum);
+        *reinterpret_cast<uint2 *>(a.O + row * D + c) = make_uint2(ka_pack2(o[0], o[1]), ka_pack2(o[2], o[3]));
+        if (c == 0 && a.lse) a.lse[row] = ka_lse(mx, sum, a.scale);
+    }
+}
+
+// 16 rows, shared by the block's waves, which take the steps in turn.
+template <int D, bool INT4>
+__device__ __forceinline__ void ka_few_rows(float *om, const KvArgs &a, ka_const_int *table, int split, int head, int qs,
+                                            int qn, int kv, int64_t r0, int64_t rows, int wave, int lane)
+{
+    const int j = lane & 15, b = lane >> 4, G = a.group;
+    float (*mm)[16] = reinterpret_cast<float (*)[16]>(om + 16 * (D + 4)), (*ll)[16] = mm + 4;
+    const float c2 = a.scale * kLog2e;
+    KvRows<D, 1> w;
+    ka_rows<D, INT4, 1>(w, a, head, qs, qn, kv, r0, rows, lane);
+    const KvRange g = ka_range(a, split, qn, kv, r0, min(r0 + 16, rows));
+    ka_walk<D, INT4, 1>(w, a, table, head, kv, g.s0 + wave, g.s1, 4, c2, lane);
+    // the waves' parts, in wave order, into om
+    const float l = ka_sum_parts(w.l[0]);
+    if (b == 0) mm[wave][j] = w.m[0], ll[wave][j] = l;
+    __syncthreads();
+    const float mw = fmaxf(fmaxf(mm[0][j], mm[1][j]), fmaxf(mm[2][j], mm[3][j]));
+    const float f = w.m[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((w.m[0] - mw) * c2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (wave == q) {
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                f32x4 *o = reinterpret_cast<f32x4 *>(om + j * (D + 4) + 16 * n + 4 * b);
+                const f32x4 v = w.acc[0][n] * f;
+                *o = q == 0 ? v : *o + v;
+            }
+        }
+        __syncthreads();
+    }
+    const int nr = (int)min((int64_t)16, rows - r0);
+    for (int e = 64 * wave + lane; e < nr * (D / 4); e += 256) {
+        const int r = e / (D / 4), c = 4 * (e % (D / 4));
+        const float mx = fmaxf(fmaxf(mm[0][r], mm[1][r]), fmaxf(mm[2][r], mm[3][r]));
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            sum += mm[q][r] == -INFINITY ? 0.0f : ll[q][r] * __builtin_amdgcn_exp2f((mm[q][r] - mx) * c2);
+        const int64_t rr = r0 + r;
+        const size_t row = (size_t)(qs + (int)(rr / G)) * a.heads_q + head * G + (int)(rr % G);
+        ka_store<D>(a, split, row, c, *reinterpret_cast<const f32x4 *>(om + r * (D + 4) + c), mx, sum);
+    }
+    __syncthreads();
+}
+
+// 64 CT rows, 16 CT per wave.
+template <int D, bool INT4, int CT>
+__device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_const_int *table, int split, int head,
+                                             int qs, int qn, int kv, int64_t r0, int64_t rows, int wave, int lane)
+{
+    const int j = lane & 15, b = lane >> 4, G = a.group;
+    KvRows<D, CT> w;
+    ka_rows<D, INT4, CT>(w, a, head, qs, qn, kv, r0 + 16 * CT * wave, rows, lane);
+    const KvRange g = ka_range(a, split, qn, kv, r0, min(r0 + 64 * CT, rows));
+    ka_walk_shared<D, INT4, CT>(w, lds, a, table, head, kv, g.s0, g.s1, a.scale * kLog2e, wave, lane);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const float l = ka_sum_parts(w.l[ct]);
+        const int64_t r = r0 + 16 * CT * wave + 16 * ct + j;
+        if (r >= rows) continue;
+        const size_t row = (size_t)(qs + (int)(r / G)) * a.heads_q + head * G + (int)(r % G);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) ka_store<D>(a, split, row, 16 * n + 4 * b, w.acc[ct][n], w.m[ct], l);
+    }
+}
+
+// CT > 0: blocks of 64 CT rows for the sequences of more than 16.  0: every list
+// of rows is taken 16 at a time.
+template <int D, bool INT4, int CT>
+__global__ __launch_bounds__(256, CT == 4 && D == 128 ? 1 : 2) void kv4_attention_kernel(KvArgs a)
+{
+    constexpr int SUMS = 4 * (16 * (D + 4) + 8 * 16), STAGES = 2 * KvShare<D, INT4>::STAGE;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[CT > 0 && STAGES > SUMS ? STAGES : SUMS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // workgroups go to the XCDs in turn: rotating each round of heads and
+    // sequences by one spreads a long sequence's tiles and splits over all
+    const int n = a.c.heads * a.B, round = blockIdx.x / n;
+    const int item = (int)((blockIdx.x % n + (uint32_t)round) % n);
+    const int head = item % a.c.heads, seq = item / a.c.heads;
+    const int split = round % a.splits, qt0 = round / a.splits;
+    const int qs = min(max(((ka_const_int *)a.q_start)[seq], 0), a.T);
+    const int qn = min(max(((ka_const_int *)a.q_start)[seq + 1], qs), a.T) - qs;
+    const int kv = min(max(((ka_const_int *)a.kv_len)[seq], 0), a.table_width << a.c.page_shift);
+    ka_const_int *table = (ka_const_int *)a.table + (size_t)seq * a.table_width;
+    const int64_t rows = (int64_t)qn * a.group;
+    const int block_rows = CT == 0 || rows <= 16 ? 16 : 64 * CT;
+    // the last tiles first: under a causal mask they are the longest
+    for (int64_t qt = (rows + block_rows - 1) / block_rows - 1 - qt0; qt >= 0; qt -= a.q_tiles) {
+        if (block_rows == 16) ka_few_rows<D, INT4>(reinterpret_cast<float *>(lds), a, table, split, head, qs, qn, kv, 16 * qt, rows, wave, lane);
+        else if constexpr (CT > 0) ka_many_rows<D, INT4, CT>(lds, a, table, split, head, qs, qn, kv, 64 * CT * qt, rows, wave, lane);
+    }
+}
+
+// O = sum over the splits, in split order; D / 4 lanes per row.  Every split of
+// every row of a sequence has been written, the ones without keys as zeros with
+// a maximum of -infinity.
 template <int D>
 __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    constexpr int L = D / 4;
+    const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int c = 4 * (threadIdx.x % L);
     const int64_t n = (int64_t)a.T * a.heads_q;
     // rows outside the sequences keep what they hold
     if (row >= n || row < (int64_t)a.q_start[0] * a.heads_q || row >= (int64_t)a.q_start[a.B] * a.heads_q) return;
-    const float *ml = a.work + (size_t)a.splits * n * D;
-    float mx = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, ml[2 * (s * n + row)]);
-    float sum = 0.0f;
-    constexpr int C = D / 64;
-    float o[C] = {};
+    const float2 *ml = reinterpret_cast<const float2 *>(a.work + (size_t)a.splits * n * D) + row;
+    const float *part = a.work + row * D + c;
+    float mx = -INFINITY, sum = 0.0f;
+    f32x4 o = {};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, ml[s * n].x);
+#pragma unroll 4
     for (int s = 0; s < a.splits; ++s) {
-        const float ms = ml[2 * (s * n + row)];
-        if (ms == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f((ms - mx) * kLog2e);
-        sum = __builtin_fmaf(ml[2 * (s * n + row) + 1], f, sum);
-#pragma unroll
-        for (int c = 0; c < C; ++c) o[c] = __builtin_fmaf(a.work[(s * n + row) * D + C * lane + c], f, o[c]);
+        const float2 v = ml[s * n];
+        const float f = v.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((v.x - mx) * kLog2e);
+        sum = __builtin_fmaf(v.y, f, sum);
+        o += *reinterpret_cast<const f32x4 *>(part + s * n * D) * f;
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-    if constexpr (C == 2) *reinterpret_cast<uint32_t *>(a.O + row * D + 2 * lane) = ka_pack2(o[0] * inv, o[1] * inv);
-    else a.O[row * D + lane] = (uint16_t)ka_pack2(o[0] * inv, 0.0f);
-    if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : mx + kLn2 * __builtin_amdgcn_logf(sum);
+    o *= ka_inverse(sum);
+    *reinterpret_cast<uint2 *>(a.O + row * D + c) = make_uint2(ka_pack2(o[0], o[1]), ka_pack2(o[2], o[3]));
+    if (c == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : mx + kLn2 * __builtin_amdgcn_logf(sum);
 }
 
-// Tiles of rows, rows per wave and splits of the keys, from the sizes and the
-// caller's bounds.  Few rows: 16 per wave, shared by the block's waves.
+// Form, tiles of rows and splits of the keys, from the sizes and the caller's
+// bounds.  Up to 16 packed rows: 16 per block; more: 32 per wave, 128 per block.
 struct KvPlan {
-    int ct, q_tiles, splits;
+    bool many;
+    int q_tiles, splits, split_steps;
 };
 
-KvPlan ka_plan(int B, int heads, int group, int max_q, int max_kv)
+KvPlan ka_plan(int T, int B, int heads, int group, int max_q, int max_kv)
 {
     KvPlan p;
     const int64_t rows = (int64_t)max_q * group;
     const int cus = device_cu_count();
-    p.ct = rows <= 16 ? 1 : 2;
-    const int block_rows = rows <= 16 * p.ct ? 16 * p.ct : 64 * p.ct;
+    p.many = rows > 16;
+    const int block_rows = p.many ? 64 * kManyTiles : 16;
     const int64_t tiles = (rows + block_rows - 1) / block_rows;
-    const int64_t blocks = tiles * B * heads;
-    // a split keeps at least eight steps of 64 keys (two per wave)
-    const int64_t most = max_kv / 512;
-    int64_t s = (2 * (int64_t)cus + blocks - 1) / blocks;
-    s = s > most ? most : s;
-    p.splits = (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+    // blocks of rows: at most every sequence's, and the rows' own number and one more per sequence
+    int64_t blocks = (int64_t)T * group / block_rows + B;
+    blocks = (blocks < tiles * B ? blocks : tiles * B) * heads;
+    // splits of equal length, at least one step per wave.  Many rows: none where
+    // the rows alone give two blocks per compute unit (a split writes and reads
+    // their fp32 sums), else about four.  Few rows: about six.
+    const int64_t steps = ((int64_t)max_kv + 63) / 64;
+    int64_t s = p.many && blocks >= 2 * (int64_t)cus ? 1 : ((p.many ? 4 : 6) * (int64_t)cus + blocks - 1) / blocks;
+    s = s > (steps + 3) / 4 ? (steps + 3) / 4 : s;
+    s = s > 64 ? 64 : s;
+    p.split_steps = (int)((steps + s - 1) / s + 3) & ~3;
+    p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
     const int64_t cap = (int64_t)(1 << 24) / ((int64_t)B * heads * p.splits) + 1;    // grid; further tiles in a loop
     p.q_tiles = (int)(tiles > cap ? cap : tiles);
     return p;
@@ -562,7 +843,7 @@ KvPlan ka_plan(int B, int heads, int group, int max_q, int max_kv)
 
 size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv)
 {
-    const KvPlan p = ka_plan(B, heads, heads_q / heads, max_q, max_kv);
+    const KvPlan p = ka_plan(T, B, heads, heads_q / heads, max_q, max_kv);
     return p.splits > 1 ? (size_t)p.splits * T * heads_q * (dim + 2) * sizeof(float) : 0;
 }
 
@@ -571,14 +852,15 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
                                 int max_kv, float scale, int causal, int window, uint16_t *O, float *lse, float *work,
                                 hipStream_t stream)
 {
-    const KvPlan p = ka_plan(B, c.heads, heads_q / c.heads, max_q, max_kv);
+    const KvPlan p = ka_plan(T, B, c.heads, heads_q / c.heads, max_q, max_kv);
     KvArgs a{};
     a.c = c, a.Q = Q, a.ldq = ldq, a.table = table, a.q_start = q_start, a.kv_len = kv_len, a.O = O, a.lse = lse;
     a.work = work, a.T = T, a.B = B, a.heads_q = heads_q, a.group = heads_q / c.heads, a.table_width = table_width;
-    a.q_tiles = p.q_tiles, a.splits = p.splits, a.causal = causal, a.window = window, a.scale = scale;
+    a.q_tiles = p.q_tiles, a.splits = p.splits, a.split_steps = p.split_steps, a.causal = causal, a.window = window, a.scale = scale;
     const dim3 grid((uint32_t)((int64_t)p.q_tiles * p.splits * B * c.heads));
 #define KA_LAUNCH(D, I) \
-    (p.ct == 1 ? kv4_attention_kernel<D, I, 1><<<grid, 256, 0, stream>>>(a) : kv4_attention_kernel<D, I, 2><<<grid, 256, 0, stream>>>(a))
+    (p.many ? kv4_attention_kernel<D, I, kManyTiles><<<grid, 256, 0, stream>>>(a) \
+            : kv4_attention_kernel<D, I, 0><<<grid, 256, 0, stream>>>(a))
     if (c.int4 && c.dim == 64) KA_LAUNCH(64, true);
     else if (c.int4) KA_LAUNCH(128, true);
     else if (c.dim == 64) KA_LAUNCH(64, false);
@@ -586,7 +868,8 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
 #undef KA_LAUNCH
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const dim3 cgrid((uint32_t)(((int64_t)T * heads_q + 3) / 4));
+    const int per = 256 / (c.dim / 4);
+    const dim3 cgrid((uint32_t)(((int64_t)T * heads_q + per - 1) / per));
     if (c.dim == 64) kv4_combine_kernel<64><<<cgrid, 256, 0, stream>>>(a);
     else kv4_combine_kernel<128><<<cgrid, 256, 0, stream>>>(a);
     return hipGetLastError();

@@ -6,9 +6,9 @@
 // (K and V in bf16) and writes about 1.1 bytes per channel.
 //
 // A block takes one head of 2048 / D consecutive tokens, 8 channels per
-// thread.  K rows are written as they come out, one dword per thread; V
-// columns are turned in LDS so that neighbouring lanes write neighbouring
-// tokens (bytes of one line where the slots are consecutive).
+// thread.  K codes are written as they come out, one dword per thread; V codes
+// are turned in LDS so that four lanes write the bytes of four tokens, which
+// form a dword where the slots are consecutive.
 #include "kv4.h"
 
 namespace svdq {
@@ -109,12 +109,12 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_append_kernel(Kv4View c, const
     size_t page;
     int place;
     if (kc_slot(c, sl[tk], page, place)) {
-        const size_t ph = page * c.heads + head;
+        const size_t run = ((page * c.heads + head) * P + place) >> 4;
         const uint32_t w = INT4 ? kc_interleave(kw) : kw;
-        reinterpret_cast<uint32_t *>(c.k_codes + (ph * P + place) * (D / 2))[kv4_k_dword<INT4>(8 * q, D)] = w;
+        *reinterpret_cast<uint32_t *>(c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(place & 15, 8 * q, D)) = w;
         constexpr int G = INT4 ? 64 : 32;
         if ((8 * q) % G == 0) {
-            const size_t o = (ph * (D / G) + 8 * q / G) * P + place;
+            const size_t o = run * (16 * D / G) + 16 * (8 * q / G) + (place & 15);
             if constexpr (INT4) ((float *)c.k_scales)[o] = ks, ((float *)c.v_scales)[o] = vs;
             else ((uint8_t *)c.k_scales)[o] = (uint8_t)ke, ((uint8_t *)c.v_scales)[o] = (uint8_t)ve;
         }
@@ -122,8 +122,8 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_append_kernel(Kv4View c, const
     __syncthreads();
     const int vtk = tid % TB;
     if (kc_slot(c, sl[vtk], page, place)) {
-        uint8_t *col = c.v_codes + (page * c.heads + head) * (D / 2) * P + place;
-        for (int r = tid / TB; r < D / 2; r += TPT) col[(size_t)r * P] = vt[r][vtk];
+        uint8_t *run = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
+        for (int r = tid / TB; r < D / 2; r += TPT) run[kv4_v_offset(place & 15, r >> 4, r & 15, D)] = vt[r][vtk];
     }
 }
 
@@ -160,17 +160,17 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_read_kernel(Kv4View c, const i
     int place;
     const int vtk = tid % TB;
     if (kc_slot(c, sl[vtk], page, place)) {
-        const uint8_t *col = c.v_codes + (page * c.heads + head) * (D / 2) * P + place;
-        for (int r = tid / TB; r < D / 2; r += TPT) vt[r][vtk] = col[(size_t)r * P];
+        const uint8_t *run = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
+        for (int r = tid / TB; r < D / 2; r += TPT) vt[r][vtk] = run[kv4_v_offset(place & 15, r >> 4, r & 15, D)];
     }
     __syncthreads();
     if (t0 + tk >= T) return;
     float fk[8] = {}, fv[8] = {};
     if (kc_slot(c, sl[tk], page, place)) {
-        const size_t ph = page * c.heads + head;
-        uint32_t w = reinterpret_cast<const uint32_t *>(c.k_codes + (ph * P + place) * (D / 2))[kv4_k_dword<INT4>(8 * q, D)];
+        const size_t run = ((page * c.heads + head) * P + place) >> 4;
+        uint32_t w = *reinterpret_cast<const uint32_t *>(c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(place & 15, 8 * q, D));
         if (INT4) w = kc_deinterleave(w);
-        const size_t o = (ph * (D / G) + 8 * q / G) * P + place;
+        const size_t o = run * (16 * D / G) + 16 * (8 * q / G) + (place & 15);
         float ks, vs;
         if constexpr (INT4) ks = ((const float *)c.k_scales)[o], vs = ((const float *)c.v_scales)[o];
         else ks = kv4_e8m0(((const uint8_t *)c.k_scales)[o]), vs = kv4_e8m0(((const uint8_t *)c.v_scales)[o]);
