@@ -26,46 +26,84 @@ __device__ __forceinline__ void kc_unpack8(const uint4 &u, float (&f)[8])
     }
 }
 
-// Codes of 8 channels (element i in nibble i of `natural`) and the group's
-// scale; the group is 8 (INT4) or 4 (MXFP4) neighbouring lanes.
+// The top bytes of four floats.
+__device__ __forceinline__ uint32_t kc_top_bytes(const float *f)
+{
+    return __builtin_amdgcn_perm(f32_bits(f[1]), f32_bits(f[0]), 0x0c0c0703u) |
+           __builtin_amdgcn_perm(f32_bits(f[3]), f32_bits(f[2]), 0x07030c0cu);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float kc_dpp(float x)
+{
+    return bits_f32(__builtin_amdgcn_update_dpp(0, f32_bits(x), CTRL, 0xF, 0xF, true));
+}
+
+// The group's largest magnitude; the group is 8 (INT4) or 4 (MXFP4) neighbouring lanes of 8
+// channels each.
 template <bool INT4>
-__device__ __forceinline__ uint32_t kc_quantize8(const float (&f)[8], float &scale, uint32_t &e8m0)
+__device__ __forceinline__ float kc_absmax(const float (&f)[8])
 {
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = fmaxf(a, __builtin_fabsf(f[i]));
+    a = fmaxf(a, kc_dpp<0xB1>(a));                      // lane ^ 1
+    a = fmaxf(a, kc_dpp<0x4E>(a));                      // lane ^ 2
+    if (INT4) a = fmaxf(a, kc_dpp<0x141>(a));           // the other four of eight (mirrored)
+    return a;
+}
+
+// Codes of 8 channels, byte i channel i (low nibble) and i + 4 (high).  |q| =
+// rint(|v| / scale) by the reciprocal, exact unless the quotient is within
+// 2^-19 of a half-integer (settled by the exact remainder) or the group needs
+// the exact path's lift.
+__device__ __forceinline__ uint32_t kc_int4_codes(const float (&f)[8], float scale)
+{
+    const bool lifted = scale < 7.88860905e-31f;        // 2^-100: exact path only
+    const float inv = scale == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(scale);
+    float q[8], far = 0.0f;
 #pragma unroll
-    for (int d = 1; d < (INT4 ? 8 : 4); d <<= 1) a = fmaxf(a, __shfl_xor(a, d));
-    uint32_t w = 0;
-    if constexpr (INT4) {
-        scale = int4_group_scale(a);
+    for (int i = 0; i < 8; ++i) {
+        const float t = __builtin_fabsf(f[i]) * inv;    // off by less than 7.5 (2^-23 + 2^-24) < 2^-19
+        q[i] = __builtin_rintf(t);
+        far = fmaxf(far, __builtin_fabsf(t - q[i]));
+    }
+    if (lifted) {
         const Int4Group g = int4_group_prepare(scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w |= int4_nibble(f[i], g) << (4 * i);
-    } else {
-        e8m0 = mx_block_e8m0(a);
-        const float inv = mx_inv_scale(e8m0);
+        for (int i = 0; i < 8; ++i) q[i] = (float)int4_mag(__builtin_fabsf(f[i]), g);
+    } else if (far >= kNearTie) {
+        // the remainder is exact, so its size against half the scale decides
+        // (bf16 values meet ties often: one group in seven has a scale that is
+        // exact in few bits)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w |= e2m1_code(f[i], inv) << (4 * i);
+        for (int i = 0; i < 8; ++i) {
+            const float e = __builtin_fmaf(-q[i], scale, __builtin_fabsf(f[i]));
+            const float d = __builtin_fabsf(e) - 0.5f * scale;
+            const bool odd = __builtin_rintf(0.5f * q[i]) * 2.0f != q[i];
+            if (d > 0.0f || (d == 0.0f && odd)) q[i] += e < 0.0f ? -1.0f : 1.0f;
+        }
     }
-    return w;
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo = __builtin_amdgcn_cvt_pk_u8_f32(q[i], i, lo);
+        hi = __builtin_amdgcn_cvt_pk_u8_f32(q[i + 4], i, hi);
+    }
+    return lo | (hi << 4) | ((kc_top_bytes(f) >> 4) & 0x08080808u) | (kc_top_bytes(f + 4) & 0x80808080u);
 }
 
-// nibbles 0 .. 7 -> byte i holds element i (low) and i + 4 (high)
-__device__ __forceinline__ uint32_t kc_interleave(uint32_t w)
+// The conversion instruction rounds v / 2^X (exact) to the E2M1 grid, ties to
+// the even index, saturates at 6 and keeps the sign of zero.  SPLIT: byte i
+// holds channels i and i + 4, else 2 i and 2 i + 1.
+template <bool SPLIT>
+__device__ __forceinline__ uint32_t kc_e2m1_codes(const float (&f)[8], float inv)
 {
-    uint32_t lo = w & 0xFFFFu, hi = w >> 16;
-    lo = (lo | (lo << 8)) & 0x00FF00FFu, lo = (lo | (lo << 4)) & 0x0F0F0F0Fu;
-    hi = (hi | (hi << 8)) & 0x00FF00FFu, hi = (hi | (hi << 4)) & 0x0F0F0F0Fu;
-    return lo | (hi << 4);
-}
-
-__device__ __forceinline__ uint32_t kc_deinterleave(uint32_t w)
-{
-    uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-    lo = (lo | (lo >> 4)) & 0x00FF00FFu, lo = (lo | (lo >> 8)) & 0xFFFFu;
-    hi = (hi | (hi >> 4)) & 0x00FF00FFu, hi = (hi | (hi >> 8)) & 0xFFFFu;
-    return lo | (hi << 16);
+    constexpr int A = SPLIT ? 1 : 2, B = SPLIT ? 4 : 1;
+    uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, f[0] * inv, f[B] * inv, 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[A] * inv, f[A + B] * inv, 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2 * A] * inv, f[2 * A + B] * inv, 1.0f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[3 * A] * inv, f[3 * A + B] * inv, 1.0f, 3);
 }
 
 // A slot's page and place, false outside the cache.
@@ -84,7 +122,7 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_append_kernel(Kv4View c, const
 {
     constexpr int TPT = D / 8;                  // threads per token
     constexpr int TB = KC_THREADS / TPT;        // tokens per block
-    __shared__ uint8_t vt[D / 2][TB + 4];
+    __shared__ __attribute__((aligned(16))) uint8_t vt[D / 2][TB + 4];
     __shared__ int sl[TB];
     const int tid = threadIdx.x, tk = tid / TPT, q = tid % TPT;
     const int head = blockIdx.x % c.heads, t0 = (int)(blockIdx.x / c.heads) * TB;
@@ -95,23 +133,30 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_append_kernel(Kv4View c, const
     kc_unpack8(*reinterpret_cast<const uint4 *>(K + t * ldk + head * D + 8 * q), fk);
     kc_unpack8(*reinterpret_cast<const uint4 *>(V + t * ldv + head * D + 8 * q), fv);
     __syncthreads();
+    const float ka = kc_absmax<INT4>(fk), va = kc_absmax<INT4>(fv);
     float ks = 0.0f, vs = 0.0f;
-    uint32_t ke = 0, ve = 0;
-    const uint32_t kw = kc_quantize8<INT4>(fk, ks, ke), vw = kc_quantize8<INT4>(fv, vs, ve);
+    uint32_t ke = 0, ve = 0, kw, vw;
+    if constexpr (INT4) {
+        ks = int4_group_scale(ka), vs = int4_group_scale(va);
+        kw = kc_int4_codes(fk, ks), vw = kc_int4_codes(fv, vs);
+    } else {
+        ke = mx_block_e8m0(ka), ve = mx_block_e8m0(va);
+        kw = kc_e2m1_codes<false>(fk, mx_inv_scale(ke)), vw = kc_e2m1_codes<true>(fv, mx_inv_scale(ve));
+    }
     // channels 8 q .. of a 32-block: parts 0, 1 are low nibbles, 2, 3 high
     const uint32_t other = __shfl_xor(vw, 2);
     if ((q & 2) == 0) {
+        const uint32_t lo = (vw & 0x0F0F0F0Fu) | ((other << 4) & 0xF0F0F0F0u);
+        const uint32_t hi = ((vw >> 4) & 0x0F0F0F0Fu) | (other & 0xF0F0F0F0u);
+        uint8_t (*r)[TB + 4] = vt + 16 * (q >> 2) + 8 * (q & 1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            vt[16 * (q >> 2) + 8 * (q & 1) + i][tk] =
-                (uint8_t)(((vw >> (4 * i)) & 15u) | (((other >> (4 * i)) & 15u) << 4));
+        for (int i = 0; i < 4; ++i) r[i][tk] = (uint8_t)(lo >> (8 * i)), r[i + 4][tk] = (uint8_t)(hi >> (8 * i));
     }
     size_t page;
     int place;
     if (kc_slot(c, sl[tk], page, place)) {
         const size_t run = ((page * c.heads + head) * P + place) >> 4;
-        const uint32_t w = INT4 ? kc_interleave(kw) : kw;
-        *reinterpret_cast<uint32_t *>(c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(place & 15, 8 * q, D)) = w;
+        *reinterpret_cast<uint32_t *>(c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(place & 15, 8 * q, D)) = kw;
         constexpr int G = INT4 ? 64 : 32;
         if ((8 * q) % G == 0) {
             const size_t o = run * (16 * D / G) + 16 * (8 * q / G) + (place & 15);
@@ -120,10 +165,25 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_append_kernel(Kv4View c, const
         }
     }
     __syncthreads();
-    const int vtk = tid % TB;
-    if (kc_slot(c, sl[vtk], page, place)) {
-        uint8_t *run = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
-        for (int r = tid / TB; r < D / 2; r += TPT) run[kv4_v_offset(place & 15, r >> 4, r & 15, D)] = vt[r][vtk];
+    // four tokens at a time: a dword where their slots are consecutive and
+    // aligned, else bytes
+    const int g4 = 4 * (tid % (TB / 4));
+    const int s0 = sl[g4];
+    const bool quad = (s0 & 3) == 0 && sl[g4 + 1] == s0 + 1 && sl[g4 + 2] == s0 + 2 && sl[g4 + 3] == s0 + 3;
+    if (quad) {
+        if (kc_slot(c, s0, page, place)) {
+            uint8_t *run = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
+            for (int r = tid / (TB / 4); r < D / 2; r += 4 * TPT)
+                *reinterpret_cast<uint32_t *>(run + kv4_v_offset(place & 15, r >> 4, r & 15, D)) =
+                    *reinterpret_cast<const uint32_t *>(&vt[r][g4]);
+        }
+    } else {
+        for (int i = 0; i < 4; ++i) {
+            if (!kc_slot(c, sl[g4 + i], page, place)) continue;
+            uint8_t *run = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
+            for (int r = tid / (TB / 4); r < D / 2; r += 4 * TPT)
+                run[kv4_v_offset(place & 15, r >> 4, r & 15, D)] = vt[r][g4 + i];
+        }
     }
 }
 
@@ -141,7 +201,8 @@ __device__ __forceinline__ float kc_value(uint32_t code, float scale, bool int4)
     return code & 8u ? -v : v;
 }
 
-// A slot outside the cache reads as zeros.
+// A slot outside the cache reads as zeros.  A thread has four channels of two
+// tokens, so that a wave's stores are whole lines.
 template <bool INT4, int D>
 __global__ __launch_bounds__(KC_THREADS) void kv4_read_kernel(Kv4View c, const int32_t *__restrict__ slots, int T,
                                                               float *__restrict__ K, float *__restrict__ V)
@@ -149,43 +210,70 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_read_kernel(Kv4View c, const i
     constexpr int TPT = D / 8;
     constexpr int TB = KC_THREADS / TPT;
     constexpr int G = INT4 ? 64 : 32;
-    __shared__ uint8_t vt[D / 2][TB + 4];
+    __shared__ __attribute__((aligned(16))) uint8_t vt[D / 2][TB + 4];
     __shared__ int sl[TB];
-    const int tid = threadIdx.x, tk = tid / TPT, q = tid % TPT;
+    const int tid = threadIdx.x;
     const int head = blockIdx.x % c.heads, t0 = (int)(blockIdx.x / c.heads) * TB;
     const int P = 1 << c.page_shift;
     if (tid < TB) sl[tid] = t0 + tid < T ? slots[t0 + tid] : -1;
-    __syncthreads();
+    // K's codes and the scales, on their way while V's codes go through LDS
+    const int ch = 4 * (tid % (D / 4));
     size_t page;
     int place;
-    const int vtk = tid % TB;
-    if (kc_slot(c, sl[vtk], page, place)) {
-        const uint8_t *run = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
-        for (int r = tid / TB; r < D / 2; r += TPT) vt[r][vtk] = run[kv4_v_offset(place & 15, r >> 4, r & 15, D)];
-    }
-    __syncthreads();
-    if (t0 + tk >= T) return;
-    float fk[8] = {}, fv[8] = {};
-    if (kc_slot(c, sl[tk], page, place)) {
-        const size_t run = ((page * c.heads + head) * P + place) >> 4;
-        uint32_t w = *reinterpret_cast<const uint32_t *>(c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(place & 15, 8 * q, D));
-        if (INT4) w = kc_deinterleave(w);
-        const size_t o = run * (16 * D / G) + 16 * (8 * q / G) + (place & 15);
-        float ks, vs;
-        if constexpr (INT4) ks = ((const float *)c.k_scales)[o], vs = ((const float *)c.v_scales)[o];
-        else ks = kv4_e8m0(((const uint8_t *)c.k_scales)[o]), vs = kv4_e8m0(((const uint8_t *)c.v_scales)[o]);
-        const int sh = q & 2 ? 4 : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            fk[i] = kc_value((w >> (4 * i)) & 15u, ks, INT4);
-            fv[i] = kc_value((uint32_t)(vt[16 * (q >> 2) + 8 * (q & 1) + i][tk] >> sh) & 15u, vs, INT4);
-        }
-    }
-    const size_t o = ((size_t)(t0 + tk) * c.heads + head) * D + 8 * q;
+    bool mine[2];
+    uint32_t w[2];
+    float ks[2], vs[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<float4 *>(K + o + 4 * h) = make_float4(fk[4 * h], fk[4 * h + 1], fk[4 * h + 2], fk[4 * h + 3]);
-        *reinterpret_cast<float4 *>(V + o + 4 * h) = make_float4(fv[4 * h], fv[4 * h + 1], fv[4 * h + 2], fv[4 * h + 3]);
+        const int t = t0 + tid / (D / 4) + h * (TB / 2);
+        mine[h] = kc_slot(c, t < T ? slots[t] : -1, page, place);
+        const size_t run = mine[h] ? ((page * c.heads + head) * P + place) >> 4 : 0;        // run 0 exists
+        const int tok = mine[h] ? place & 15 : 0;
+        w[h] = *reinterpret_cast<const uint32_t *>(c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(tok, ch & ~7, D));
+        const size_t so = run * (16 * D / G) + 16 * (ch / G) + tok;
+        if constexpr (INT4) ks[h] = ((const float *)c.k_scales)[so], vs[h] = ((const float *)c.v_scales)[so];
+        else ks[h] = kv4_e8m0(((const uint8_t *)c.k_scales)[so]), vs[h] = kv4_e8m0(((const uint8_t *)c.v_scales)[so]);
+    }
+    __syncthreads();
+    const int g4 = 4 * (tid % (TB / 4));
+    const int s0 = sl[g4];
+    const bool quad = (s0 & 3) == 0 && sl[g4 + 1] == s0 + 1 && sl[g4 + 2] == s0 + 2 && sl[g4 + 3] == s0 + 3;
+    if (quad) {
+        if (kc_slot(c, s0, page, place)) {
+            const uint8_t *vr = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
+#pragma unroll
+            for (int i = 0; i < D / 2 / (4 * TPT); ++i) {
+                const int r = tid / (TB / 4) + 4 * TPT * i;
+                *reinterpret_cast<uint32_t *>(&vt[r][g4]) =
+                    *reinterpret_cast<const uint32_t *>(vr + kv4_v_offset(place & 15, r >> 4, r & 15, D));
+            }
+        }
+    } else {
+        for (int i = 0; i < 4; ++i) {
+            if (!kc_slot(c, sl[g4 + i], page, place)) continue;
+            const uint8_t *vr = c.v_codes + (((page * c.heads + head) * P + place) >> 4) * (8 * D);
+            for (int r = tid / (TB / 4); r < D / 2; r += 4 * TPT)
+                vt[r][g4 + i] = vr[kv4_v_offset(place & 15, r >> 4, r & 15, D)];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int tk = tid / (D / 4) + h * (TB / 2);
+        if (t0 + tk >= T) continue;
+        float fk[4] = {}, fv[4] = {};
+        if (mine[h]) {
+            const int row = 16 * (ch >> 5) + (ch & 15), vsh = (ch >> 4) & 1 ? 4 : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ksh = INT4 ? 8 * i + (ch & 4) : 4 * (i + (ch & 4));
+                fk[i] = kc_value((w[h] >> ksh) & 15u, ks[h], INT4);
+                fv[i] = kc_value((uint32_t)(vt[row + i][tk] >> vsh) & 15u, vs[h], INT4);
+            }
+        }
+        const size_t o = ((size_t)(t0 + tk) * c.heads + head) * D + ch;
+        *reinterpret_cast<float4 *>(K + o) = make_float4(fk[0], fk[1], fk[2], fk[3]);
+        *reinterpret_cast<float4 *>(V + o) = make_float4(fv[0], fv[1], fv[2], fv[3]);
     }
 }
 
