@@ -81,7 +81,8 @@ __device__ __forceinline__ uint32_t kc_int4_codes(const float (&f)[8], float sca
             const float e = __builtin_fmaf(-q[i], scale, __builtin_fabsf(f[i]));
             const float d = __builtin_fabsf(e) - 0.5f * scale;
             const bool odd = __builtin_rintf(0.5f * q[i]) * 2.0f != q[i];
-            if (d > 0.0f || (d == 0.0f && odd)) q[i] += e < 0.0f ? -1.0f : 1.0f;
+            const bool move = (d > 0.0f) | ((d == 0.0f) & odd);
+            q[i] += move ? __builtin_copysignf(1.0f, e) : 0.0f;
         }
     }
     uint32_t lo = 0, hi = 0;
