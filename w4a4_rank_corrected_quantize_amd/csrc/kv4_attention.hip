@@ -62,6 +62,29 @@ __device__ __forceinline__ float ka_row_bcast(float x)
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x150 + J, 0xF, 0xF, true));
 }
 
+// The same for a J known after unrolling.
+__device__ __forceinline__ float ka_bcast(float x, int j)
+{
+    switch (j) {
+    case 0: return ka_row_bcast<0>(x);
+    case 1: return ka_row_bcast<1>(x);
+    case 2: return ka_row_bcast<2>(x);
+    case 3: return ka_row_bcast<3>(x);
+    case 4: return ka_row_bcast<4>(x);
+    case 5: return ka_row_bcast<5>(x);
+    case 6: return ka_row_bcast<6>(x);
+    case 7: return ka_row_bcast<7>(x);
+    case 8: return ka_row_bcast<8>(x);
+    case 9: return ka_row_bcast<9>(x);
+    case 10: return ka_row_bcast<10>(x);
+    case 11: return ka_row_bcast<11>(x);
+    case 12: return ka_row_bcast<12>(x);
+    case 13: return ka_row_bcast<13>(x);
+    case 14: return ka_row_bcast<14>(x);
+    default: return ka_row_bcast<15>(x);
+    }
+}
+
 __device__ __forceinline__ float ka_max_parts(float x)     // over the four lane parts
 {
     auto a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
@@ -174,6 +197,15 @@ __device__ __forceinline__ KvRuns ka_runs(const KvArgs &a, const KvPages &pg, in
     return r;
 }
 
+// Run t (values, not a choice between addresses, which would put the runs in
+// memory).
+__device__ __forceinline__ int64_t ka_pick(const KvRuns &r, int t)
+{
+    const int64_t a = r.run[0], b = r.run[1], c = r.run[2], d = r.run[3];
+    const int64_t lo = t & 1 ? b : a, hi = t & 1 ? d : c;
+    return t & 2 ? hi : lo;
+}
+
 // All ones where bit 0 of `valid` is set and left > 0, else 0.  The scale of a
 // V place past the end becomes 0 with it (the place may hold anything, and 0
 // times that need not be 0); as a select, the compiler loads under a condition.
@@ -189,12 +221,11 @@ __device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, co
     constexpr int NG = KvStep<D, INT4>::NG;
     const int j = lane & 15, b = lane >> 4;
     const KvRuns r = ka_runs(a, pg, head, key0, kv_end);
-    const int64_t *run = r.run;
     st.valid = r.valid;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const uint8_t *kp = a.c.k_codes + run[t] * (8 * D) + (D / 8) * lane;
-        const uint8_t *vp = a.c.v_codes + run[t] * (8 * D) + (D / 8) * lane;
+        const uint8_t *kp = a.c.k_codes + r.run[t] * (8 * D) + (D / 8) * lane;
+        const uint8_t *vp = a.c.v_codes + r.run[t] * (8 * D) + (D / 8) * lane;
         if constexpr (D == 128) {
             const uint4 u = *reinterpret_cast<const uint4 *>(kp), w = *reinterpret_cast<const uint4 *>(vp);
             st.k[t][0] = u.x, st.k[t][1] = u.y, st.k[t][2] = u.z, st.k[t][3] = u.w;
@@ -207,7 +238,7 @@ __device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, co
     }
     // the lane's scale key: token 4 b + j % 4 of run j / 4
     const int sr = j >> 2, tok = 4 * b + (j & 3);
-    const int64_t mine = sr & 2 ? (sr & 1 ? run[3] : run[2]) : (sr & 1 ? run[1] : run[0]);
+    const int64_t mine = ka_pick(r, sr);
     const uint32_t in = ka_in_mask(st.valid >> sr, kv_end - key0 - 16 * sr - tok);
     const int64_t so = mine * (16 * NG) + tok;
     if constexpr (INT4) {
@@ -220,7 +251,7 @@ __device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, co
         const int blk = D == 128 ? b : b >> 1;    // the 32-channel block of the lane's K part
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            st.ks[t] = bits_f32((uint32_t)((const uint8_t *)a.c.k_scales)[run[t] * (16 * NG) + 16 * blk + j] << 23);
+            st.ks[t] = bits_f32((uint32_t)((const uint8_t *)a.c.k_scales)[r.run[t] * (16 * NG) + 16 * blk + j] << 23);
         const uint8_t *vs = (const uint8_t *)a.c.v_scales + so;
 #pragma unroll
         for (int g = 0; g < NG; ++g) st.vs[g] = bits_f32(((uint32_t)vs[16 * g] << 23) & in);
@@ -331,10 +362,12 @@ __device__ __forceinline__ void ka_rows(KvRows<D, CT> &w, const KvArgs &a, int h
     w.all_hi = __builtin_amdgcn_readfirstlane(w.all_hi), w.all_lo = __builtin_amdgcn_readfirstlane(w.all_lo);
 }
 
-// One step's scores (run t, token 4 b + i at 4 t + i) to probabilities: masks,
-// the running maximum, the sum.
+// Before a step's exponentials: scores (run t, token 4 b + i at 4 t + i) that a
+// row does not see become -infinity, and the reference m moves where a score
+// exceeds it by more than kLazy (seen in any lane): p is at most 2^kLazy then,
+// and its relative rounding the same.
 template <int D, int CT>
-__device__ __forceinline__ void ka_softmax(KvRows<D, CT> &w, float (&p)[CT][16], int key0, int valid, float c2, int b)
+__device__ __forceinline__ void ka_reference(KvRows<D, CT> &w, float (&p)[CT][16], int key0, int valid, float c2, int b)
 {
     if (key0 + 64 > w.all_hi || key0 < w.all_lo || valid != 15) {
 #pragma unroll
@@ -346,21 +379,34 @@ __device__ __forceinline__ void ka_softmax(KvRows<D, CT> &w, float (&p)[CT][16],
                 p[ct][i] = see ? p[ct][i] : -INFINITY;
             }
     }
+    float mx[CT];
+    bool up = false;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-        // the reference m stays until a score exceeds it by kLazy (seen in any
-        // lane): p is at most 2^kLazy then, and its relative rounding the same
-        float mx = p[ct][0];
+        mx[ct] = p[ct][0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[ct][i]);
-        if (__any((mx - w.m[ct]) * c2 > kLazy)) {
-            mx = fmaxf(ka_max_parts(mx), w.m[ct]);
-            const float f = w.m[ct] == mx ? 1.0f : __builtin_amdgcn_exp2f((w.m[ct] - mx) * c2);
+        for (int i = 1; i < 16; ++i) mx[ct] = fmaxf(mx[ct], p[ct][i]);
+        up |= (mx[ct] - w.m[ct]) * c2 > kLazy;
+    }
+    if (__any(up)) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const float top = fmaxf(ka_max_parts(mx[ct]), w.m[ct]);
+            const float f = w.m[ct] == top ? 1.0f : __builtin_amdgcn_exp2f((w.m[ct] - top) * c2);
             w.l[ct] *= f;
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) w.acc[ct][n] *= f;
-            w.m[ct] = mx;
+            w.m[ct] = top;
         }
+    }
+}
+
+// Probabilities, and their sum.
+template <int D, int CT>
+__device__ __forceinline__ void ka_exponentials(KvRows<D, CT> &w, float (&p)[CT][16], float c2)
+{
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
         const float base = w.m[ct] == -INFINITY ? 0.0f : -w.m[ct] * c2;
         float sum = 0.0f;
 #pragma unroll
@@ -381,31 +427,12 @@ __device__ __forceinline__ void ka_p_operands(const float (&x)[16], bf16x8 (&pb)
                                                    ka_pack2(x[8 * h + 4], x[8 * h + 5]), ka_pack2(x[8 * h + 6], x[8 * h + 7])});
 }
 
-// Order of a product whose operands come from LDS: `first` reads ahead, then
-// one read per CT products.  Left to itself the compiler reads each operand
-// right before its product and waits for it.
-template <int FIRST, int READS, int CT>
-__device__ __forceinline__ void ka_interleave()
+// Scores of a step: k_op(t, k) gives K's operand of run t and product step k, ks
+// the lane's INT4 scales.
+template <int D, bool INT4, int CT, class KOp>
+__device__ __forceinline__ void ka_scores(const KvRows<D, CT> &w, float (&p)[CT][16], const float *ks, KOp k_op)
 {
-    __builtin_amdgcn_sched_group_barrier(0x100, FIRST, 0);
-#pragma unroll
-    for (int i = FIRST; i < READS; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, CT * FIRST, 0);
-}
-
-// One step of 64 keys for the wave's rows.  k_op(t, k) gives K's operand of
-// run t and product step k, v_op(n, h, lo, hi) V's of block n and runs 2 h, 2 h
-// + 1; ks and vs are the lane's INT4 scales.  LDS: the operands are read from
-// LDS.
-template <int D, bool INT4, int CT, bool LDS, class KOp, class VOp, class During>
-__device__ __forceinline__ void ka_step(KvRows<D, CT> &w, int key0, int valid, const float *ks, const float *vs, float c2,
-                                        int b, KOp k_op, VOp v_op, During during)
-{
-    constexpr int KS = D / 32, NB = D / 32, NG = INT4 ? D / 64 : 1;
-    float p[CT][16];
+    constexpr int KS = D / 32, NG = INT4 ? D / 64 : 1;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         f32x4 sc[CT][4] = {};
@@ -418,7 +445,6 @@ __device__ __forceinline__ void ka_step(KvRows<D, CT> &w, int key0, int valid, c
                 for (int ct = 0; ct < CT; ++ct)
                     sc[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, w.q[ct][k], sc[ct][t], 0, 0, 0);
             }
-        if constexpr (LDS) ka_interleave<4, 4 * KS / NG, CT>();
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             float x[16];
@@ -434,54 +460,52 @@ __device__ __forceinline__ void ka_step(KvRows<D, CT> &w, int key0, int valid, c
             }
         }
     }
-    // V's first operands are on their way during the softmax
-    bf16x8 lo[NB][2], hi[NB][2];
-    if constexpr (LDS) {
+}
+
+// Operands of the second product from the probabilities; vs: the lane's INT4
+// scales, one set of operands per 64-channel group.
+template <int D, bool INT4, int CT>
+struct KvP {
+    static constexpr int NG = INT4 ? D / 64 : 1;
+    bf16x8 b[NG][CT][2];
+};
+
+template <int D, bool INT4, int CT>
+__device__ __forceinline__ void ka_p(KvP<D, INT4, CT> &o, const float (&p)[CT][16], const float *vs)
+{
 #pragma unroll
-        for (int h = 0; h < 2; ++h) v_op(0, h, lo[0][h], hi[0][h]);
-    }
-    ka_softmax<D, CT>(w, p, key0, valid, c2, b);
-    bf16x8 pb[NG][CT][2];
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < KvP<D, INT4, CT>::NG; ++g)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             if constexpr (INT4) {
                 float x[16];
                 ka_scale_keys(x, p[ct], vs[g]);
-                ka_p_operands(x, pb[g][ct]);
+                ka_p_operands(x, o.b[g][ct]);
             } else {
-                ka_p_operands(p[ct], pb[g][ct]);
+                ka_p_operands(p[ct], o.b[g][ct]);
             }
         }
-    if constexpr (LDS) __builtin_amdgcn_sched_barrier(0);
-    during();
+}
+
+// O^T += V^T P^T: v_op(n, h, lo, hi) gives V's operands of block n and runs 2 h,
+// 2 h + 1.
+template <int D, bool INT4, int CT, class VOp>
+__device__ __forceinline__ void ka_values(KvRows<D, CT> &w, const KvP<D, INT4, CT> &pb, VOp v_op)
+{
+    constexpr int NB = D / 32, NG = KvP<D, INT4, CT>::NG;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int n = g * (NB / NG); n < (g + 1) * (NB / NG); ++n)
+        for (int h = 0; h < 2; ++h) {
+            bf16x8 lo, hi;
+            v_op(n, h, lo, hi);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!LDS || n > 0) v_op(n, h, lo[n][h], hi[n][h]);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    w.acc[ct][2 * n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[n][h], pb[g][ct][h], w.acc[ct][2 * n], 0, 0, 0);
-                    w.acc[ct][2 * n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[n][h], pb[g][ct][h], w.acc[ct][2 * n + 1], 0, 0, 0);
-                }
+            for (int ct = 0; ct < CT; ++ct) {
+                const bf16x8 b = pb.b[n / (NB / NG)][ct][h];
+                w.acc[ct][2 * n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, b, w.acc[ct][2 * n], 0, 0, 0);
+                w.acc[ct][2 * n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, b, w.acc[ct][2 * n + 1], 0, 0, 0);
             }
-    }
-    if constexpr (LDS) {
-        // CT products, then a share of the conversions, the next read of V, and
-        // towards the end the writes
-#pragma unroll
-        for (int i = 0; i < 4 * NB; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, INT4 ? 6 : 5, 0);
-            if (i < 4 * NB - 4) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if (i >= 2 * NB) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-    }
 }
 
 // Few rows: the wave converts its own codes, steps s0, s0 + stride, .. < s1.
@@ -495,15 +519,17 @@ __device__ __forceinline__ void ka_walk(KvRows<D, CT> &w, const KvArgs &a, ka_co
     KvStep<D, INT4> x, y;
     if (s0 >= s1) return;
     auto compute = [&](const KvStep<D, INT4> &c, int s) {
-        ka_step<D, INT4, CT, false>(
-            w, 64 * s, c.valid, c.ks, c.vs, c2, lane >> 4,
-            [&](int t, int k) { return ka_k_operand<INT4>(c.k[t][k], INT4 ? 0.0f : c.ks[t]); },
-            [&](int n, int h, bf16x8 &lo, bf16x8 &hi) {
-                const float vs = INT4 ? 0.0f : c.vs[n % NG];
-                if (h == 0) ka_v_operands<INT4, 0>(c.v[0][n], c.v[1][n], vs, lo, hi);
-                else ka_v_operands<INT4, 1>(c.v[2][n], c.v[3][n], vs, lo, hi);
-            },
-            [] {});
+        float p[CT][16];
+        KvP<D, INT4, CT> pb;
+        ka_scores<D, INT4, CT>(w, p, c.ks, [&](int t, int k) { return ka_k_operand<INT4>(c.k[t][k], INT4 ? 0.0f : c.ks[t]); });
+        ka_reference<D, CT>(w, p, 64 * s, c.valid, c2, lane >> 4);
+        ka_exponentials<D, CT>(w, p, c2);
+        ka_p<D, INT4, CT>(pb, p, c.vs);
+        ka_values<D, INT4, CT>(w, pb, [&](int n, int h, bf16x8 &lo, bf16x8 &hi) {
+            const float vs = INT4 ? 0.0f : c.vs[n % NG];
+            if (h == 0) ka_v_operands<INT4, 0>(c.v[0][n], c.v[1][n], vs, lo, hi);
+            else ka_v_operands<INT4, 1>(c.v[2][n], c.v[3][n], vs, lo, hi);
+        });
     };
     ka_load<D, INT4>(x, a, ka_pages(a, table, 64 * s0, kv), head, 64 * s0, kv, lane);
     KvPages pages = ka_pages(a, table, 64 * (s0 + stride), kv);
@@ -521,32 +547,35 @@ __device__ __forceinline__ void ka_walk(KvRows<D, CT> &w, const KvArgs &a, ka_co
 
 // Many rows: the block's four waves convert a step's codes together, a quarter
 // each, into LDS (operand order, 16 bytes per lane: no bank conflicts), and
-// every wave multiplies the whole step.  Two stages: the next step is written
-// while the current one is read; its codes were loaded a step before that.
+// every wave multiplies the whole step.
+//
+// The loop is skewed so that the matrix cores have work during the softmax: an
+// iteration computes the scores of step s + 1 between the exponentials of step
+// s, then the second product of step s between the conversions of K of step s
+// + 2 and V of step s + 1.  K and V have two stages each; what an iteration
+// writes was last read in the iteration before.
 template <int D, bool INT4>
-struct KvShare {
-    static constexpr int KS = D / 32, NB = D / 32;
-    static constexpr int K_BYTES = 4 * KS * 1024, V_BYTES = 4 * NB * 1024, STAGE = K_BYTES + V_BYTES;
-    // K of run `wave`; V of runs 2 (wave / 2) and + 1, blocks NB / 2 (wave % 2) ..
-    uint32_t k[KS], v[2][NB / 2];
+struct KvShareK {
+    uint32_t k[D / 32];                           // run `wave`
     float ks;                                     // MXFP4: of the K row
-    float vq[NB / 2];                             // MXFP4: of token 4 b + j % 4 of run 2 (wave / 2) + (j / 4) % 2
-    float iks[2], ivs[2];                         // INT4: the lane's scales, as in KvStep
+    float iks[2];                                 // INT4: the lane's scales, as in KvStep
     int valid;
 };
 
 template <int D, bool INT4>
-__device__ __forceinline__ void ka_share_load(KvShare<D, INT4> &st, const KvArgs &a, const KvPages &pg, int head, int key0,
-                                              int kv_end, int wave, int lane)
+struct KvShareV {
+    uint32_t v[2][D / 64];                        // runs 2 (wave / 2) and + 1, blocks D / 64 (wave % 2) ..
+    float vq[D / 64];                             // MXFP4: of token 4 b + j % 4 of run 2 (wave / 2) + (j / 4) % 2
+    float ivs[2];                                 // INT4: the lane's scales
+};
+
+template <int D, bool INT4>
+__device__ __forceinline__ void ka_share_load_k(KvShareK<D, INT4> &st, const KvArgs &a, const KvRuns &r, int wave, int lane)
 {
-    constexpr int KS = D / 32, NB = D / 32, NG = INT4 ? D / 64 : D / 32;
+    constexpr int NG = INT4 ? D / 64 : D / 32;
     const int j = lane & 15, b = lane >> 4;
-    const KvRuns r = ka_runs(a, pg, head, key0, kv_end);
-    const int64_t *run = r.run;
     st.valid = r.valid;
-    const int s2 = wave >> 1;
-    const int64_t rv[2] = {s2 ? run[2] : run[0], s2 ? run[3] : run[1]};
-    const int64_t rk = wave & 1 ? rv[1] : rv[0];
+    const int64_t rk = ka_pick(r, wave);
     const uint8_t *kp = a.c.k_codes + rk * (8 * D) + (D / 8) * lane;
     if constexpr (D == 128) {
         const uint4 u = *reinterpret_cast<const uint4 *>(kp);
@@ -555,9 +584,28 @@ __device__ __forceinline__ void ka_share_load(KvShare<D, INT4> &st, const KvArgs
         const uint2 u = *reinterpret_cast<const uint2 *>(kp);
         st.k[0] = u.x, st.k[1] = u.y;
     }
+    if constexpr (INT4) {
+        const int sr = j >> 2, tok = 4 * b + (j & 3);
+        const int64_t mine = ka_pick(r, sr);
+        const float *ks = (const float *)a.c.k_scales + mine * (16 * NG) + tok;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) st.iks[g] = ks[16 * g];
+    } else {
+        const int blk = D == 128 ? b : b >> 1;
+        st.ks = bits_f32((uint32_t)((const uint8_t *)a.c.k_scales)[rk * (16 * NG) + 16 * blk + j] << 23);
+    }
+}
+
+template <int D, bool INT4>
+__device__ __forceinline__ void ka_share_load_v(KvShareV<D, INT4> &st, const KvArgs &a, const KvRuns &r, int left, int wave,
+                                                int lane)
+{
+    constexpr int NB = D / 32, NG = INT4 ? D / 64 : D / 32;
+    const int j = lane & 15, b = lane >> 4, s2 = wave >> 1;
+    const int64_t rv0 = ka_pick(r, 2 * s2), rv1 = ka_pick(r, 2 * s2 + 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint8_t *vp = a.c.v_codes + rv[i] * (8 * D) + (D / 8) * lane + 2 * NB * (wave & 1);
+        const uint8_t *vp = a.c.v_codes + (i ? rv1 : rv0) * (8 * D) + (D / 8) * lane + 2 * NB * (wave & 1);
         if constexpr (D == 128) {
             const uint2 u = *reinterpret_cast<const uint2 *>(vp);
             st.v[i][0] = u.x, st.v[i][1] = u.y;
@@ -567,77 +615,232 @@ __device__ __forceinline__ void ka_share_load(KvShare<D, INT4> &st, const KvArgs
     }
     if constexpr (INT4) {
         const int sr = j >> 2, tok = 4 * b + (j & 3);
-        const int64_t mine = sr & 2 ? (sr & 1 ? run[3] : run[2]) : (sr & 1 ? run[1] : run[0]);
-        const uint32_t in = ka_in_mask(st.valid >> sr, kv_end - key0 - 16 * sr - tok);
-        const float *ks = (const float *)a.c.k_scales + mine * (16 * NG) + tok;
+        const int64_t mine = ka_pick(r, sr);
+        const uint32_t in = ka_in_mask(r.valid >> sr, left - 16 * sr - tok);
         const float *vs = (const float *)a.c.v_scales + mine * (16 * NG) + tok;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) st.iks[g] = ks[16 * g];
 #pragma unroll
         for (int g = 0; g < NG; ++g) st.ivs[g] = bits_f32(f32_bits(vs[16 * g]) & in);
     } else {
-        const int blk = D == 128 ? b : b >> 1;
-        st.ks = bits_f32((uint32_t)((const uint8_t *)a.c.k_scales)[rk * (16 * NG) + 16 * blk + j] << 23);
         const int sr = (j >> 2) & 1, tok = 4 * b + (j & 3);
-        const uint32_t in = ka_in_mask(st.valid >> (2 * s2 + sr), kv_end - key0 - 16 * (2 * s2 + sr) - tok);
-        const uint8_t *vs = (const uint8_t *)a.c.v_scales + (sr ? rv[1] : rv[0]) * (16 * NG) + tok;
+        const uint32_t in = ka_in_mask(r.valid >> (2 * s2 + sr), left - 16 * (2 * s2 + sr) - tok);
+        const uint8_t *vs = (const uint8_t *)a.c.v_scales + (sr ? rv1 : rv0) * (16 * NG) + tok;
 #pragma unroll
         for (int n = 0; n < NB / 2; ++n)
             st.vq[n] = bits_f32(((uint32_t)vs[16 * (n + NB / 2 * (wave & 1))] << 23) & in);
     }
 }
 
+// Product step k of the wave's run.
 template <int D, bool INT4>
-__device__ __forceinline__ void ka_share_write(const KvShare<D, INT4> &st, uint8_t *stage, int wave, int lane)
+__device__ __forceinline__ void ka_share_write_k(const KvShareK<D, INT4> &st, uint8_t *stage, int k, int wave, int lane)
 {
-    constexpr int KS = D / 32, NB = D / 32;
+    *reinterpret_cast<bf16x8 *>(stage + 1024 * (D / 32 * wave + k) + 16 * lane) = ka_k_operand<INT4>(st.k[k], INT4 ? 0.0f : st.ks);
+}
+
+// The wave's n-th block.
+template <int D, bool INT4>
+__device__ __forceinline__ void ka_share_write_v(const KvShareV<D, INT4> &st, uint8_t *stage, int n, int wave, int lane)
+{
+    constexpr int NB = D / 32;
+    uint8_t *vb = stage + 2048 * (NB * (wave >> 1) + NB / 2 * (wave & 1) + n) + 16 * lane;
+    bf16x8 lo, hi;
+    ka_v_operands<INT4, 0>(st.v[0][n], st.v[1][n], INT4 ? 0.0f : st.vq[n], lo, hi);
+    *reinterpret_cast<bf16x8 *>(vb) = lo;
+    *reinterpret_cast<bf16x8 *>(vb + 1024) = hi;
+}
+
+typedef __attribute__((address_space(3))) uint8_t ka_lds_u8;
+typedef const __attribute__((address_space(3))) bf16x8 ka_lds_bf16x8;
+
+__device__ __forceinline__ bf16x8 ka_lds_read(uint32_t base, int off) { return *(ka_lds_bf16x8 *)(uintptr_t)(base + off); }
+
+// Half e % 2 (low, high channel) of operand pair e / 2 of the second product.
+template <int NB, int N>
+__device__ __forceinline__ void ka_v_read(bf16x8 (&vf)[N][2], uint32_t base, int e)
+{
+    const int i = e >> 1;
+    vf[i][e & 1] = ka_lds_read(base, 2048 * (NB * (i & 1) + (i >> 1)) + 1024 * (e & 1));
+}
+
+// Scores e, e + 1 (of column tile e / 16) to probabilities, their sum, and
+// their place in the second product's operands.
+template <int D, bool INT4, int CT>
+__device__ __forceinline__ void ka_exp_pair(KvP<D, INT4, CT> &pb, const float (&p)[CT][16], float (&sum)[CT],
+                                            const float (&base)[CT], float c2, const float *vs, int e)
+{
+    const int ct = e >> 4, i = e & 15;
+    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[ct][i], c2, base[ct]));
+    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(p[ct][i + 1], c2, base[ct]));
+    sum[ct] += x;
+    sum[ct] += y;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-        *reinterpret_cast<bf16x8 *>(stage + 1024 * (KS * wave + k) + 16 * lane) = ka_k_operand<INT4>(st.k[k], INT4 ? 0.0f : st.ks);
-    uint8_t *vb = stage + KvShare<D, INT4>::K_BYTES + 2048 * (NB * (wave >> 1) + NB / 2 * (wave & 1)) + 16 * lane;
-#pragma unroll
-    for (int n = 0; n < NB / 2; ++n) {
-        bf16x8 lo, hi;
-        ka_v_operands<INT4, 0>(st.v[0][n], st.v[1][n], INT4 ? 0.0f : st.vq[n], lo, hi);
-        *reinterpret_cast<bf16x8 *>(vb + 2048 * n) = lo;
-        *reinterpret_cast<bf16x8 *>(vb + 2048 * n + 1024) = hi;
+    for (int g = 0; g < KvP<D, INT4, CT>::NG; ++g) {
+        uint32_t u;
+        if constexpr (INT4) u = ka_pack2(x * ka_bcast(vs[g], i), y * ka_bcast(vs[g], i + 1));
+        else u = ka_pack2(x, y);
+        u32x4 q = __builtin_bit_cast(u32x4, pb.b[g][ct][i >> 3]);
+        q[(i & 7) >> 1] = u;
+        pb.b[g][ct][i >> 3] = __builtin_bit_cast(bf16x8, q);
     }
 }
+
+// A group's sums into the scores.
+template <bool INT4, int CT>
+__device__ __forceinline__ void ka_take_scores(float (&p)[CT][16], const f32x4 (&sc)[CT][4], const float *ks, int g)
+{
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = sc[ct][i >> 2][i & 3];
+        if constexpr (!INT4) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[ct][i] = x[i];
+        } else if (g == 0) {
+            ka_scale_keys(p[ct], x, ks[0]);
+        } else {
+            ka_fma_keys(p[ct], x, ks[g]);
+        }
+    }
+}
+
+// Bytes of one stage of K or of V.
+constexpr int ka_stage(int D) { return 128 * D; }
 
 template <int D, bool INT4, int CT>
 __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, const KvArgs &a, ka_const_int *table,
                                                int head, int kv, int s0, int s1, float c2, int wave, int lane)
 {
-    constexpr int KS = D / 32, NB = D / 32, STAGE = KvShare<D, INT4>::STAGE, NG = INT4 ? D / 64 : 1;
+    constexpr int KS = D / 32, NB = D / 32, STAGE = ka_stage(D), NG = INT4 ? D / 64 : 0, NS = INT4 ? NG : 1;
+    constexpr int KO = 4 * KS, VO = 2 * NB;           // operands of the scores, operand pairs of the second product
+    // INT4 heads of 128 need two sets of second operands and of sums: with the
+    // scores next to the exponentials they spill (995 us against 476 at 4608 x
+    // 4608, 24 heads), so the scores come after the second product there
+    constexpr bool MIX = !(INT4 && D == 128);
     if (s0 >= s1) return;                             // the same for the whole block
-    KvShare<D, INT4> st, st2;
-    ka_share_load<D, INT4>(st, a, ka_pages(a, table, 64 * s0, kv), head, 64 * s0, kv, wave, lane);
-    ka_share_write<D, INT4>(st, lds, wave, lane);
-    int valid = st.valid;
-    float ks[2] = {}, vs[2] = {};
+    uint8_t *kb = lds, *vb = lds + 2 * STAGE;
+    const uint32_t lb = (uint32_t)(uintptr_t)(const ka_lds_u8 *)lds + 16 * lane;
+    auto runs = [&](int s, const KvPages &pg) { return ka_runs(a, pg, head, 64 * s, kv); };
+    auto left = [&](int s) { return kv - 64 * s; };
+
+    KvShareK<D, INT4> k2, k3;                         // K of step s + 2 (and s + 3, on its way)
+    KvShareV<D, INT4> v1, v2;                         // V of step s + 1 (and s + 2)
+    float ks1[2] = {}, vs0[2] = {};                   // INT4 scales: K of step s + 1, V of step s
+    int valid1;                                       // of step s + 1
+    float pa[CT][16], pc[CT][16];
+    KvRuns r = runs(s0, ka_pages(a, table, 64 * s0, kv));
+    ka_share_load_k<D, INT4>(k2, a, r, wave, lane);
+    ka_share_load_v<D, INT4>(v1, a, r, left(s0), wave, lane);
+    r = runs(s0 + 1, ka_pages(a, table, 64 * (s0 + 1), kv));
+    ka_share_load_k<D, INT4>(k3, a, r, wave, lane);
+    ka_share_load_v<D, INT4>(v2, a, r, left(s0 + 1), wave, lane);
 #pragma unroll
-    for (int g = 0; g < (INT4 ? NG : 0); ++g) ks[g] = st.iks[g], vs[g] = st.ivs[g];
-    ka_share_load<D, INT4>(st, a, ka_pages(a, table, 64 * (s0 + 1), kv), head, 64 * (s0 + 1), kv, wave, lane);
-    KvPages pages = ka_pages(a, table, 64 * (s0 + 2), kv);
-    for (int s = s0; s < s1; ++s) {
-        __syncthreads();                              // step s is written, the other stage free
-        uint8_t *cur = lds + ((s - s0) & 1) * STAGE, *nxt = lds + ((s - s0 + 1) & 1) * STAGE;
-        ka_share_load<D, INT4>(st2, a, pages, head, 64 * (s + 2), kv, wave, lane);
-        pages = ka_pages(a, table, 64 * (s + 3), kv);
-        // no skipping of steps that none of this wave's rows sees: the branch
-        // costs every step a copy of the accumulators
-        ka_step<D, INT4, CT, true>(
-            w, 64 * s, valid, ks, vs, c2, lane >> 4,
-            [&](int t, int k) { return *reinterpret_cast<const bf16x8 *>(cur + 1024 * (KS * t + k) + 16 * lane); },
-            [&](int n, int h, bf16x8 &lo, bf16x8 &hi) {
-                const uint8_t *v = cur + KvShare<D, INT4>::K_BYTES + 2048 * (NB * h + n) + 16 * lane;
-                lo = *reinterpret_cast<const bf16x8 *>(v), hi = *reinterpret_cast<const bf16x8 *>(v + 1024);
-            },
-            [&] { ka_share_write<D, INT4>(st, nxt, wave, lane); });
-        valid = st.valid;
+    for (int k = 0; k < KS; ++k) ka_share_write_k<D, INT4>(k2, kb, k, wave, lane), ka_share_write_k<D, INT4>(k3, kb + STAGE, k, wave, lane);
 #pragma unroll
-        for (int g = 0; g < (INT4 ? NG : 0); ++g) ks[g] = st.iks[g], vs[g] = st.ivs[g];
-        st = st2;
+    for (int n = 0; n < NB / 2; ++n) ka_share_write_v<D, INT4>(v1, vb, n, wave, lane);
+    valid1 = k3.valid;
+    float ks0[2] = {};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) ks0[g] = k2.iks[g], ks1[g] = k3.iks[g], vs0[g] = v1.ivs[g];
+    const int valid0 = k2.valid;
+    v1 = v2;
+    r = runs(s0 + 2, ka_pages(a, table, 64 * (s0 + 2), kv));
+    ka_share_load_k<D, INT4>(k2, a, r, wave, lane);
+    KvPages pages = ka_pages(a, table, 64 * (s0 + 3), kv);
+    __syncthreads();
+    ka_scores<D, INT4, CT>(w, pa, ks0, [&](int t, int k) { return ka_lds_read(lb, 1024 * (KS * t + k)); });
+    ka_reference<D, CT>(w, pa, 64 * s0, valid0, c2, lane >> 4);
+
+    auto iteration = [&](int s, float (&cur)[CT][16], float (&nxt)[CT][16]) {
+        const int x = (s - s0) & 1;
+        uint8_t *k_now = kb + x * STAGE, *v_next = vb + (x ^ 1) * STAGE;
+        const uint32_t lk = lb + (x ^ 1) * STAGE, lv = lb + (2 + x) * STAGE;
+        __syncthreads();                              // K of step s + 1 and V of step s are written; the other stages free
+        bf16x8 kf[KO], vf[VO][2];
+        if (MIX) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kf[i] = ka_lds_read(lk, 1024 * (KS * (i & 3) + (i >> 2)));
+        }
+        // codes of the steps after
+        ka_share_load_v<D, INT4>(v2, a, r, left(s + 2), wave, lane);
+        r = runs(s + 3, pages);
+        ka_share_load_k<D, INT4>(k3, a, r, wave, lane);
+        pages = ka_pages(a, table, 64 * (s + 4), kv);
+        float base[CT], sum[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) base[ct] = w.m[ct] == -INFINITY ? 0.0f : -w.m[ct] * c2, sum[ct] = 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
+        KvP<D, INT4, CT> pb;
+        // scores of step s + 1 (operand i: run i % 4, product step i / 4) and, in
+        // between, the exponentials of step s: fenced pieces of CT products, an
+        // operand read ahead, E exponentials and their bf16 pairs
+        auto scores = [&] {
+            constexpr int E = CT * 16 / KO;
+            f32x4 sc[CT][4];
+#pragma unroll
+            for (int i = 0; i < KO; ++i) {
+                if (i % (KO / NS) == 0) {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) sc[ct][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+                }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    sc[ct][i & 3] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], w.q[ct][i >> 2], sc[ct][i & 3], 0, 0, 0);
+                if (i + 4 < KO) kf[i + 4] = ka_lds_read(lk, 1024 * (KS * (i & 3) + ((i + 4) >> 2)));
+                else if (MIX) ka_v_read<NB>(vf, lv, i + 4 - KO);
+                if (MIX) {
+#pragma unroll
+                    for (int e = E * i; e < E * (i + 1); e += 2) ka_exp_pair<D, INT4, CT>(pb, cur, sum, base, c2, vs0, e);
+                }
+                if ((i + 1) % (KO / NS) == 0) ka_take_scores<INT4, CT>(nxt, sc, ks1, (i + 1) / (KO / NS) - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (MIX) {
+            scores();
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ka_v_read<NB>(vf, lv, e);
+#pragma unroll
+            for (int e = 0; e < 16 * CT; e += 2) ka_exp_pair<D, INT4, CT>(pb, cur, sum, base, c2, vs0, e);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) w.l[ct] += sum[ct];
+        // second product of step s (operand pair i: block i / 2, runs 2 (i % 2)
+        // and + 1) and the conversions
+#pragma unroll
+        for (int i = 0; i < VO; ++i) {
+            const int n = i >> 1, h = i & 1;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const bf16x8 p = pb.b[n / (NB / NS)][ct][h];
+                w.acc[ct][2 * n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[i][0], p, w.acc[ct][2 * n], 0, 0, 0);
+                w.acc[ct][2 * n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[i][1], p, w.acc[ct][2 * n + 1], 0, 0, 0);
+            }
+            if (i + 2 < VO) ka_v_read<NB>(vf, lv, 2 * i + 4), ka_v_read<NB>(vf, lv, 2 * i + 5);
+            if (i < KS) ka_share_write_k<D, INT4>(k2, k_now, i, wave, lane);
+            else if (i < KS + NB / 2) ka_share_write_v<D, INT4>(v1, v_next, i - KS, wave, lane);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!MIX) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kf[i] = ka_lds_read(lk, 1024 * (KS * (i & 3) + (i >> 2)));
+            scores();
+        }
+        if (s + 1 < s1) ka_reference<D, CT>(w, nxt, 64 * (s + 1), valid1, c2, lane >> 4);
+        valid1 = k2.valid;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) ks1[g] = k2.iks[g], vs0[g] = v1.ivs[g];
+        k2 = k3, v1 = v2;
+    };
+    for (int s = s0;; s += 2) {
+        iteration(s, pa, pc);
+        if (s + 1 >= s1) break;
+        iteration(s + 1, pc, pa);
+        if (s + 2 >= s1) break;
     }
     __syncthreads();
 }
@@ -755,7 +958,7 @@ __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_c
 template <int D, bool INT4, int CT>
 __global__ __launch_bounds__(256, CT == 4 && D == 128 ? 1 : 2) void kv4_attention_kernel(KvArgs a)
 {
-    constexpr int SUMS = 4 * (16 * (D + 4) + 8 * 16), STAGES = 2 * KvShare<D, INT4>::STAGE;
+    constexpr int SUMS = 4 * (16 * (D + 4) + 8 * 16), STAGES = 4 * ka_stage(D);
     __shared__ __attribute__((aligned(16))) uint8_t lds[CT > 0 && STAGES > SUMS ? STAGES : SUMS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // workgroups go to the XCDs in turn: rotating each round of heads and
