@@ -507,6 +507,7 @@ svdq_status svdq_nf4_w4a16_linear(const uint16_t *X, const uint8_t *wq, const ui
  *   r_out      [M][D], stype, device (out); may be r itself
  *   x          [M][D] bf16 bits, device (out), or NULL: only r_out; pre and
  *              scale and shift are then not applied.  May be y itself, not r
+ *              or r_out
  * One kernel launch.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE,
  * SVDQ_ERR_MISALIGNED, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
  */

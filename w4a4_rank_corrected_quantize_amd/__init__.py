@@ -598,6 +598,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(shape, dtype, dev, stream):
+    """A new tensor; with `stream` given it belongs to that stream, on which the
+    kernel runs (an int is a raw stream of this device)."""
+    torch = _tt()
+    if stream is None or dev.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NONE, post_w=None, pre: int = NORM_RMS,
                   pre_w=None, pre_b=None, scale=None, shift=None, mod_index=None, eps: float = 1e-6, r_out=None,
                   x=None, want_x: bool = True, stream=None):
@@ -617,18 +629,18 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     _arg(r, r.dtype, "r")
     if y is not None:
         _arg(y, bf, "y", shape)
-        r_out = torch.empty_like(r) if r_out is None else _arg(r_out, r.dtype, "r_out", shape)
+        r_out = _empty(shape, r.dtype, r.device, stream) if r_out is None else _arg(r_out, r.dtype, "r_out", shape)
     elif r_out is not None:
         raise ValueError("r_out without y: nothing to update")
     if want_x:
-        x = torch.empty_like(r if y is None else y, dtype=bf) if x is None else _arg(x, bf, "x", shape)
+        x = _empty(shape, bf, r.device, stream) if x is None else _arg(x, bf, "x", shape)
     elif x is not None:
         raise ValueError("x given with want_x=False")
     vec = (D,)
     for t, name in ((post_w, "post_w"), (pre_w, "pre_w"), (pre_b, "pre_b")):
         if t is not None:
             _arg(t, bf, name, vec)
-    B = ld = 0
+    B, ld, sets = 0, D, 0
     for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
         if t is None:
             continue
@@ -639,9 +651,10 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
                 raise ValueError(f"{name} has no rows")
         _rows_arg(t, bf, name, (B, D))
         if B > 1:
-            if ld and t.stride(0) != ld:
+            if sets and t.stride(0) != ld:
                 raise ValueError("gate, scale and shift must have the same row stride")
             ld = t.stride(0)
+        sets += 1
     if mod_index is not None:
         _arg(mod_index, torch.int32, "mod_index", (M,))
     dev = r.device
@@ -649,7 +662,7 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
                         ("post_w", post_w), ("pre_w", pre_w), ("pre_b", pre_b), ("r_out", r_out), ("x", x)), stream)
     st = lib().svdq_residual_norm(r.data_ptr(), 1 if r.dtype is f32 else 0, _ptr(y), M, D, post, _ptr(post_w),
                                   _ptr(gate), alpha, pre, _ptr(pre_w), _ptr(pre_b), _ptr(scale), _ptr(shift),
-                                  _ptr(mod_index), B, ld or D, eps, _ptr(r_out), _ptr(x), raw)
+                                  _ptr(mod_index), B, ld, eps, _ptr(r_out), _ptr(x), raw)
     if st:
         raise SvdqError(st, "svdq_residual_norm")
     return (r if y is None else r_out), x
@@ -674,7 +687,7 @@ def lora_plan(index, n_adapters: int, plan: Optional[LoraPlan] = None, stream=No
     M = index.shape[0]
     if plan is None:
         need = lib().svdq_lora_plan_bytes(M, n_adapters)
-        plan = LoraPlan(torch.empty(max(need, 16), dtype=torch.uint8, device=index.device), M, n_adapters)
+        plan = LoraPlan(_empty(max(need, 16), torch.uint8, index.device, stream), M, n_adapters)
     elif plan.M != M or plan.n_adapters != n_adapters:
         raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n_adapters}")
     dev = index.device
@@ -719,9 +732,9 @@ def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=
     if plan.M != M or plan.n_adapters != n:
         raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n}")
     dev = X.device
-    Y = torch.empty_like(base) if Y is None else _arg(Y, bf, "Y", (M, N))
+    Y = _empty((M, N), bf, dev, stream) if Y is None else _arg(Y, bf, "Y", (M, N))
     if work is None:
-        work = torch.empty(max(lora_workspace_bytes(M, K, R, n), 16), dtype=torch.uint8, device=dev)
+        work = _empty(max(lora_workspace_bytes(M, K, R, n), 16), torch.uint8, dev, stream)
     else:
         _arg(work, torch.uint8, "work")
     raw = _launch(dev, (("A", A), ("B", B), ("scale", scale), ("plan", plan.buffer), ("base", base), ("Y", Y),
@@ -763,9 +776,17 @@ class Kv4Cache:
         self._k_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
         self._v_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
         self.device = self._k_codes.device
-        self._struct = _Kv4Struct(self._k_codes.data_ptr(), self._k_scales.data_ptr(), self._v_codes.data_ptr(),
-                                  self._v_scales.data_ptr(), pages, page_size, heads, dim, prec)
-        self._ref = ctypes.addressof(self._struct)
+        self._struct = _Kv4Struct(None, None, None, None, pages, page_size, heads, dim, prec)
+
+    def _ref(self):
+        """Address of the C structure, its pointers those of the buffers now."""
+        s = self._struct
+        s.k_codes, s.k_scales = self._k_codes.data_ptr(), self._k_scales.data_ptr()
+        s.v_codes, s.v_scales = self._v_codes.data_ptr(), self._v_scales.data_ptr()
+        return ctypes.addressof(s)
+
+    def __reduce__(self):
+        raise TypeError("a Kv4Cache cannot be copied or pickled; copy its buffers")
 
     k_codes = property(lambda self: self._k_codes)
     v_codes = property(lambda self: self._v_codes)
@@ -808,7 +829,7 @@ def kv4_append(cache: Kv4Cache, K, V, slots, stream=None) -> None:
         raise ValueError(f"V has shape {tuple(V.shape)}, expected {tuple(K.shape)}")
     _arg(slots, torch.int32, "slots", (T,))
     raw = _launch(dev, (("K", K), ("V", V), ("slots", slots)), stream)
-    st = lib().svdq_kv4_append(cache._ref, K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T, raw)
+    st = lib().svdq_kv4_append(cache._ref(), K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T, raw)
     if st:
         raise SvdqError(st, "svdq_kv4_append")
 
@@ -822,10 +843,10 @@ def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
     _arg(slots, torch.int32, "slots")
     T = slots.shape[0]
     shape = (T, cache.heads, cache.dim)
-    K = torch.empty(shape, dtype=torch.float32, device=dev) if K is None else _arg(K, torch.float32, "K", shape)
-    V = torch.empty(shape, dtype=torch.float32, device=dev) if V is None else _arg(V, torch.float32, "V", shape)
+    K = _empty(shape, torch.float32, dev, stream) if K is None else _arg(K, torch.float32, "K", shape)
+    V = _empty(shape, torch.float32, dev, stream) if V is None else _arg(V, torch.float32, "V", shape)
     raw = _launch(dev, (("slots", slots), ("K", K), ("V", V)), stream)
-    st = lib().svdq_kv4_read(cache._ref, slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), raw)
+    st = lib().svdq_kv4_read(cache._ref(), slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), raw)
     if st:
         raise SvdqError(st, "svdq_kv4_read")
     return K, V
@@ -833,7 +854,7 @@ def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
 
 def kv4_attention_workspace_bytes(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int) -> int:
     """Device scratch bytes that kv4_attention needs for these sizes."""
-    return int(lib().svdq_kv4_attention_workspace_bytes(cache._ref, T, B, heads_q, max_q, max_kv))
+    return int(lib().svdq_kv4_attention_workspace_bytes(cache._ref(), T, B, heads_q, max_q, max_kv))
 
 
 def kv4_attention_workspace(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int):
@@ -864,18 +885,17 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
     B, width = block_table.shape
     _arg(q_start, i32, "q_start", (B + 1,))
     _arg(kv_len, i32, "kv_len", (B,))
-    out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev) if out is None else _arg(
-        out, torch.bfloat16, "out", (T, H, D))
+    out = _empty((T, H, D), torch.bfloat16, dev, stream) if out is None else _arg(out, torch.bfloat16, "out", (T, H, D))
     if lse is not None:
         _arg(lse, torch.float32, "lse", (T, H))
     if work is None:
         need = kv4_attention_workspace_bytes(cache, T, B, H, max_q, max_kv)
-        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        work = _empty(need, torch.uint8, dev, stream) if need else None
     else:
         _arg(work, torch.uint8, "work")
     raw = _launch(dev, (("Q", Q), ("block_table", block_table), ("q_start", q_start), ("kv_len", kv_len), ("out", out),
                         ("lse", lse), ("work", work)), stream)
-    st = lib().svdq_kv4_attention(cache._ref, Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
+    st = lib().svdq_kv4_attention(cache._ref(), Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
                                   kv_len.data_ptr(), B, T, H, max_q, max_kv, D ** -0.5 if scale is None else scale,
                                   1 if causal else 0, window, out.data_ptr(), _ptr(lse), _ptr(work),
                                   0 if work is None else work.numel(), raw)

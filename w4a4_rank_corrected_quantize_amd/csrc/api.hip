@@ -104,7 +104,7 @@ extern "C" const char *svdq_status_string(svdq_status status)
     return "unknown status";
 }
 
-extern "C" int svdq_version(void) { return 100; }
+extern "C" int svdq_version(void) { return 200; }
 
 extern "C" svdq_status svdq_check_device(void) { return current_device_ok(); }
 
@@ -332,7 +332,7 @@ extern "C" svdq_status svdq_residual_norm(const void *r, svdq_stream_type stype,
     if (D < 8 || D % 8 != 0 || D > 16384 || !elems_ok(M, D)) return SVDQ_ERR_SHAPE;
     // without a block output there is no update; without x nothing to normalize
     if (M > 0 && y == nullptr && (post != SVDQ_NORM_NONE || post_w || gate || r_out)) return SVDQ_ERR_INVALID_ARG;
-    if (M > 0 && (!r || (y && !r_out) || (!y && !x) || (x && x == r))) return SVDQ_ERR_INVALID_ARG;
+    if (M > 0 && (!r || (y && !r_out) || (!y && !x) || (x && (x == r || x == r_out)))) return SVDQ_ERR_INVALID_ARG;
     if (gate || scale || shift) {
         if (mod_rows < 1) return SVDQ_ERR_INVALID_ARG;
         if (mod_stride < D || mod_stride % 8 != 0 || !elems_ok(mod_rows, mod_stride)) return SVDQ_ERR_SHAPE;

@@ -322,6 +322,12 @@ __device__ __forceinline__ void ka_fma_keys(float (&o)[16], const float (&x)[16]
     }
 }
 
+// First key that a row at this place sees.
+__device__ __forceinline__ int ka_window(const KvArgs &a, int place)
+{
+    return a.causal && a.window > 0 ? (int)max((int64_t)place - a.window + 1, (int64_t)0) : 0;
+}
+
 // A wave's rows: 16 CT query rows of one key head, column 16 ct + j each.
 template <int D, int CT>
 struct KvRows {
@@ -350,7 +356,7 @@ __device__ __forceinline__ void ka_rows(KvRows<D, CT> &w, const KvArgs &a, int h
         }
         const int place = kv - qn + tok;
         w.hi_key[ct] = a.causal ? min(place + 1, kv) : kv;
-        w.lo_key[ct] = a.causal && a.window > 0 ? place - a.window + 1 : 0;
+        w.lo_key[ct] = ka_window(a, place);
         w.all_hi = min(w.all_hi, w.hi_key[ct]), w.all_lo = max(w.all_lo, w.lo_key[ct]);
         w.m[ct] = -INFINITY, w.l[ct] = 0.0f;
 #pragma unroll
@@ -864,7 +870,7 @@ __device__ __forceinline__ KvRange ka_range(const KvArgs &a, int split, int qn, 
     // give blocks of equal length; more only past the caller's bound
     const int per = max(a.split_steps, (steps + a.splits - 1) / a.splits);
     const int first = kv - qn + (int)(r0 / a.group), last = kv - qn + (int)((r1 - 1) / a.group);
-    const int lo = a.causal && a.window > 0 ? max(first - a.window + 1, 0) : 0;
+    const int lo = ka_window(a, first);
     const int hi = a.causal ? max(min(last + 1, kv), 0) : kv;
     return {max(split * per, lo >> 6), min(min((split + 1) * per, steps), (hi + 63) >> 6)};
 }
