@@ -620,7 +620,9 @@ typedef struct svdq_kv4_cache {
  *            The slots of one call must differ (a slot given twice holds a
  *            mix of the two tokens afterwards)
  * Codes and scales are bit-exact with the definition in the header comment.
- * Other slots keep their content.  One kernel launch.  Errors:
+ * Values should be finite: a NaN is stored as some value of its group, an
+ * infinity makes its group zeros (INT4) or is cut (MXFP4), so what a row does
+ * not see cannot reach it.  Other slots keep their content.  One kernel launch.  Errors:
  * SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE (strides, cache sizes, T * heads * dim
  * of SVDQ_MAX_ELEMENTS or more), SVDQ_ERR_UNSUPPORTED (dim, page_size),
  * SVDQ_ERR_MISALIGNED, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.

@@ -598,11 +598,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _empty(shape, dtype, dev, stream):
+def _empty(shape, dtype, dev, stream, like=None):
     """A new tensor; with `stream` given it belongs to that stream, on which the
-    kernel runs (an int is a raw stream of this device)."""
+    kernel runs (an int is a raw stream of this device).  `like`: a tensor
+    of this shape; if its type fits too, 1 us less than from the shape."""
     torch = _tt()
     if stream is None or dev.type != "cuda":
+        if like is not None and like.dtype is dtype and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), dev)
@@ -629,11 +632,11 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     _arg(r, r.dtype, "r")
     if y is not None:
         _arg(y, bf, "y", shape)
-        r_out = _empty(shape, r.dtype, r.device, stream) if r_out is None else _arg(r_out, r.dtype, "r_out", shape)
+        r_out = _empty(shape, r.dtype, r.device, stream, r) if r_out is None else _arg(r_out, r.dtype, "r_out", shape)
     elif r_out is not None:
         raise ValueError("r_out without y: nothing to update")
     if want_x:
-        x = _empty(shape, bf, r.device, stream) if x is None else _arg(x, bf, "x", shape)
+        x = _empty(shape, bf, r.device, stream, r if y is None else y) if x is None else _arg(x, bf, "x", shape)
     elif x is not None:
         raise ValueError("x given with want_x=False")
     vec = (D,)
@@ -732,7 +735,7 @@ def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=
     if plan.M != M or plan.n_adapters != n:
         raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n}")
     dev = X.device
-    Y = _empty((M, N), bf, dev, stream) if Y is None else _arg(Y, bf, "Y", (M, N))
+    Y = _empty((M, N), bf, dev, stream, base) if Y is None else _arg(Y, bf, "Y", (M, N))
     if work is None:
         work = _empty(max(lora_workspace_bytes(M, K, R, n), 16), torch.uint8, dev, stream)
     else:
@@ -885,7 +888,8 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
     B, width = block_table.shape
     _arg(q_start, i32, "q_start", (B + 1,))
     _arg(kv_len, i32, "kv_len", (B,))
-    out = _empty((T, H, D), torch.bfloat16, dev, stream) if out is None else _arg(out, torch.bfloat16, "out", (T, H, D))
+    out = _empty((T, H, D), torch.bfloat16, dev, stream, Q) if out is None else _arg(
+        out, torch.bfloat16, "out", (T, H, D))
     if lse is not None:
         _arg(lse, torch.float32, "lse", (T, H))
     if work is None:
@@ -897,7 +901,7 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
                         ("lse", lse), ("work", work)), stream)
     st = lib().svdq_kv4_attention(cache._ref(), Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
                                   kv_len.data_ptr(), B, T, H, max_q, max_kv, D ** -0.5 if scale is None else scale,
-                                  1 if causal else 0, window, out.data_ptr(), _ptr(lse), _ptr(work),
+                                  1 if causal else 0, min(window, 0x7FFFFFFF), out.data_ptr(), _ptr(lse), _ptr(work),
                                   0 if work is None else work.numel(), raw)
     if st:
         raise SvdqError(st, "svdq_kv4_attention")

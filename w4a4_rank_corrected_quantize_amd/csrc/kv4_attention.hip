@@ -206,21 +206,27 @@ __device__ __forceinline__ int64_t ka_pick(const KvRuns &r, int t)
     return t & 2 ? hi : lo;
 }
 
-// All ones where bit 0 of `valid` is set and left > 0, else 0.  The scale of a
-// V place past the end becomes 0 with it (the place may hold anything, and 0
-// times that need not be 0); as a select, the compiler loads under a condition.
-__device__ __forceinline__ uint32_t ka_in_mask(int valid, int left)
+// The keys that a block's rows see: steps s0 .. s1 - 1, keys lo .. hi - 1.
+struct KvRange {
+    int s0, s1, lo, hi;
+};
+
+// All ones where bit 0 of `valid` is set and the key lies in the range, else 0.
+// The scale of a V place that no row sees becomes 0 with it (the place may hold
+// anything, and 0 times that need not be 0; what append wrote is finite); as a
+// select, the compiler loads under a condition.
+__device__ __forceinline__ uint32_t ka_in_mask(int valid, int key, const KvRange &g)
 {
-    return (uint32_t)(-(valid & 1) & ((-left) >> 31));
+    return (uint32_t)(-(valid & 1) & ((key - g.hi) >> 31) & ((g.lo - 1 - key) >> 31));
 }
 
 template <int D, bool INT4>
 __device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, const KvPages &pg, int head, int key0,
-                                        int kv_end, int lane)
+                                        const KvRange &g, int lane)
 {
     constexpr int NG = KvStep<D, INT4>::NG;
     const int j = lane & 15, b = lane >> 4;
-    const KvRuns r = ka_runs(a, pg, head, key0, kv_end);
+    const KvRuns r = ka_runs(a, pg, head, key0, g.hi);
     st.valid = r.valid;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -239,14 +245,14 @@ __device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, co
     // the lane's scale key: token 4 b + j % 4 of run j / 4
     const int sr = j >> 2, tok = 4 * b + (j & 3);
     const int64_t mine = ka_pick(r, sr);
-    const uint32_t in = ka_in_mask(st.valid >> sr, kv_end - key0 - 16 * sr - tok);
+    const uint32_t in = ka_in_mask(st.valid >> sr, key0 + 16 * sr + tok, g);
     const int64_t so = mine * (16 * NG) + tok;
     if constexpr (INT4) {
         const float *ks = (const float *)a.c.k_scales + so, *vs = (const float *)a.c.v_scales + so;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) st.ks[g] = ks[16 * g];
+        for (int i = 0; i < NG; ++i) st.ks[i] = ks[16 * i];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) st.vs[g] = bits_f32(f32_bits(vs[16 * g]) & in);
+        for (int i = 0; i < NG; ++i) st.vs[i] = bits_f32(f32_bits(vs[16 * i]) & in);
     } else {
         const int blk = D == 128 ? b : b >> 1;    // the 32-channel block of the lane's K part
 #pragma unroll
@@ -254,7 +260,7 @@ __device__ __forceinline__ void ka_load(KvStep<D, INT4> &st, const KvArgs &a, co
             st.ks[t] = bits_f32((uint32_t)((const uint8_t *)a.c.k_scales)[r.run[t] * (16 * NG) + 16 * blk + j] << 23);
         const uint8_t *vs = (const uint8_t *)a.c.v_scales + so;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) st.vs[g] = bits_f32(((uint32_t)vs[16 * g] << 23) & in);
+        for (int i = 0; i < NG; ++i) st.vs[i] = bits_f32(((uint32_t)vs[16 * i] << 23) & in);
     }
 }
 
@@ -518,10 +524,11 @@ __device__ __forceinline__ void ka_values(KvRows<D, CT> &w, const KvP<D, INT4, C
 // Codes are one step ahead, their pages two; past the end the last run's page
 // is looked up and nothing of it is used.
 template <int D, bool INT4, int CT>
-__device__ __forceinline__ void ka_walk(KvRows<D, CT> &w, const KvArgs &a, ka_const_int *table, int head, int kv, int s0,
-                                        int s1, int stride, float c2, int lane)
+__device__ __forceinline__ void ka_walk(KvRows<D, CT> &w, const KvArgs &a, ka_const_int *table, int head, const KvRange &g,
+                                        int s0, int stride, float c2, int lane)
 {
     constexpr int NG = KvStep<D, INT4>::NG;
+    const int s1 = g.s1;
     KvStep<D, INT4> x, y;
     if (s0 >= s1) return;
     auto compute = [&](const KvStep<D, INT4> &c, int s) {
@@ -537,15 +544,15 @@ __device__ __forceinline__ void ka_walk(KvRows<D, CT> &w, const KvArgs &a, ka_co
             else ka_v_operands<INT4, 1>(c.v[2][n], c.v[3][n], vs, lo, hi);
         });
     };
-    ka_load<D, INT4>(x, a, ka_pages(a, table, 64 * s0, kv), head, 64 * s0, kv, lane);
-    KvPages pages = ka_pages(a, table, 64 * (s0 + stride), kv);
+    ka_load<D, INT4>(x, a, ka_pages(a, table, 64 * s0, g.hi), head, 64 * s0, g, lane);
+    KvPages pages = ka_pages(a, table, 64 * (s0 + stride), g.hi);
     for (int s = s0;; s += 2 * stride) {
-        ka_load<D, INT4>(y, a, pages, head, 64 * (s + stride), kv, lane);
-        pages = ka_pages(a, table, 64 * (s + 2 * stride), kv);
+        ka_load<D, INT4>(y, a, pages, head, 64 * (s + stride), g, lane);
+        pages = ka_pages(a, table, 64 * (s + 2 * stride), g.hi);
         compute(x, s);
         if (s + stride >= s1) break;
-        ka_load<D, INT4>(x, a, pages, head, 64 * (s + 2 * stride), kv, lane);
-        pages = ka_pages(a, table, 64 * (s + 3 * stride), kv);
+        ka_load<D, INT4>(x, a, pages, head, 64 * (s + 2 * stride), g, lane);
+        pages = ka_pages(a, table, 64 * (s + 3 * stride), g.hi);
         compute(y, s + stride);
         if (s + 2 * stride >= s1) break;
     }
@@ -603,8 +610,8 @@ __device__ __forceinline__ void ka_share_load_k(KvShareK<D, INT4> &st, const KvA
 }
 
 template <int D, bool INT4>
-__device__ __forceinline__ void ka_share_load_v(KvShareV<D, INT4> &st, const KvArgs &a, const KvRuns &r, int left, int wave,
-                                                int lane)
+__device__ __forceinline__ void ka_share_load_v(KvShareV<D, INT4> &st, const KvArgs &a, const KvRuns &r, int key0,
+                                                const KvRange &g, int wave, int lane)
 {
     constexpr int NB = D / 32, NG = INT4 ? D / 64 : D / 32;
     const int j = lane & 15, b = lane >> 4, s2 = wave >> 1;
@@ -622,13 +629,13 @@ __device__ __forceinline__ void ka_share_load_v(KvShareV<D, INT4> &st, const KvA
     if constexpr (INT4) {
         const int sr = j >> 2, tok = 4 * b + (j & 3);
         const int64_t mine = ka_pick(r, sr);
-        const uint32_t in = ka_in_mask(r.valid >> sr, left - 16 * sr - tok);
+        const uint32_t in = ka_in_mask(r.valid >> sr, key0 + 16 * sr + tok, g);
         const float *vs = (const float *)a.c.v_scales + mine * (16 * NG) + tok;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) st.ivs[g] = bits_f32(f32_bits(vs[16 * g]) & in);
+        for (int i = 0; i < NG; ++i) st.ivs[i] = bits_f32(f32_bits(vs[16 * i]) & in);
     } else {
         const int sr = (j >> 2) & 1, tok = 4 * b + (j & 3);
-        const uint32_t in = ka_in_mask(r.valid >> (2 * s2 + sr), left - 16 * (2 * s2 + sr) - tok);
+        const uint32_t in = ka_in_mask(r.valid >> (2 * s2 + sr), key0 + 16 * (2 * s2 + sr) + tok, g);
         const uint8_t *vs = (const uint8_t *)a.c.v_scales + (sr ? rv1 : rv0) * (16 * NG) + tok;
 #pragma unroll
         for (int n = 0; n < NB / 2; ++n)
@@ -715,7 +722,7 @@ constexpr int ka_stage(int D) { return 128 * D; }
 
 template <int D, bool INT4, int CT>
 __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, const KvArgs &a, ka_const_int *table,
-                                               int head, int kv, int s0, int s1, float c2, int wave, int lane)
+                                               int head, const KvRange &g, float c2, int wave, int lane)
 {
     constexpr int KS = D / 32, NB = D / 32, STAGE = ka_stage(D), NG = INT4 ? D / 64 : 0, NS = INT4 ? NG : 1;
     constexpr int KO = 4 * KS, VO = 2 * NB;           // operands of the scores, operand pairs of the second product
@@ -723,23 +730,23 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, c
     // scores next to the exponentials they spill (995 us against 476 at 4608 x
     // 4608, 24 heads), so the scores come after the second product there
     constexpr bool MIX = !(INT4 && D == 128);
+    const int s0 = g.s0, s1 = g.s1;
     if (s0 >= s1) return;                             // the same for the whole block
     uint8_t *kb = lds, *vb = lds + 2 * STAGE;
     const uint32_t lb = (uint32_t)(uintptr_t)(const ka_lds_u8 *)lds + 16 * lane;
-    auto runs = [&](int s, const KvPages &pg) { return ka_runs(a, pg, head, 64 * s, kv); };
-    auto left = [&](int s) { return kv - 64 * s; };
+    auto runs = [&](int s, const KvPages &pg) { return ka_runs(a, pg, head, 64 * s, g.hi); };
 
     KvShareK<D, INT4> k2, k3;                         // K of step s + 2 (and s + 3, on its way)
     KvShareV<D, INT4> v1, v2;                         // V of step s + 1 (and s + 2)
     float ks1[2] = {}, vs0[2] = {};                   // INT4 scales: K of step s + 1, V of step s
     int valid1;                                       // of step s + 1
     float pa[CT][16], pc[CT][16];
-    KvRuns r = runs(s0, ka_pages(a, table, 64 * s0, kv));
+    KvRuns r = runs(s0, ka_pages(a, table, 64 * s0, g.hi));
     ka_share_load_k<D, INT4>(k2, a, r, wave, lane);
-    ka_share_load_v<D, INT4>(v1, a, r, left(s0), wave, lane);
-    r = runs(s0 + 1, ka_pages(a, table, 64 * (s0 + 1), kv));
+    ka_share_load_v<D, INT4>(v1, a, r, 64 * s0, g, wave, lane);
+    r = runs(s0 + 1, ka_pages(a, table, 64 * (s0 + 1), g.hi));
     ka_share_load_k<D, INT4>(k3, a, r, wave, lane);
-    ka_share_load_v<D, INT4>(v2, a, r, left(s0 + 1), wave, lane);
+    ka_share_load_v<D, INT4>(v2, a, r, 64 * (s0 + 1), g, wave, lane);
 #pragma unroll
     for (int k = 0; k < KS; ++k) ka_share_write_k<D, INT4>(k2, kb, k, wave, lane), ka_share_write_k<D, INT4>(k3, kb + STAGE, k, wave, lane);
 #pragma unroll
@@ -747,12 +754,12 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, c
     valid1 = k3.valid;
     float ks0[2] = {};
 #pragma unroll
-    for (int g = 0; g < NG; ++g) ks0[g] = k2.iks[g], ks1[g] = k3.iks[g], vs0[g] = v1.ivs[g];
+    for (int i = 0; i < NG; ++i) ks0[i] = k2.iks[i], ks1[i] = k3.iks[i], vs0[i] = v1.ivs[i];
     const int valid0 = k2.valid;
     v1 = v2;
-    r = runs(s0 + 2, ka_pages(a, table, 64 * (s0 + 2), kv));
+    r = runs(s0 + 2, ka_pages(a, table, 64 * (s0 + 2), g.hi));
     ka_share_load_k<D, INT4>(k2, a, r, wave, lane);
-    KvPages pages = ka_pages(a, table, 64 * (s0 + 3), kv);
+    KvPages pages = ka_pages(a, table, 64 * (s0 + 3), g.hi);
     __syncthreads();
     ka_scores<D, INT4, CT>(w, pa, ks0, [&](int t, int k) { return ka_lds_read(lb, 1024 * (KS * t + k)); });
     ka_reference<D, CT>(w, pa, 64 * s0, valid0, c2, lane >> 4);
@@ -768,10 +775,10 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, c
             for (int i = 0; i < 4; ++i) kf[i] = ka_lds_read(lk, 1024 * (KS * (i & 3) + (i >> 2)));
         }
         // codes of the steps after
-        ka_share_load_v<D, INT4>(v2, a, r, left(s + 2), wave, lane);
+        ka_share_load_v<D, INT4>(v2, a, r, 64 * (s + 2), g, wave, lane);
         r = runs(s + 3, pages);
         ka_share_load_k<D, INT4>(k3, a, r, wave, lane);
-        pages = ka_pages(a, table, 64 * (s + 4), kv);
+        pages = ka_pages(a, table, 64 * (s + 4), g.hi);
         float base[CT], sum[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) base[ct] = w.m[ct] == -INFINITY ? 0.0f : -w.m[ct] * c2, sum[ct] = 0.0f;
@@ -839,7 +846,7 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, c
         if (s + 1 < s1) ka_reference<D, CT>(w, nxt, 64 * (s + 1), valid1, c2, lane >> 4);
         valid1 = k2.valid;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) ks1[g] = k2.iks[g], vs0[g] = v1.ivs[g];
+        for (int i = 0; i < NG; ++i) ks1[i] = k2.iks[i], vs0[i] = v1.ivs[i];
         k2 = k3, v1 = v2;
     };
     for (int s = s0;; s += 2) {
@@ -858,11 +865,7 @@ __device__ __forceinline__ float ka_lse(float mx, float sum, float scale)
     return sum == 0.0f ? -INFINITY : mx * scale + kLn2 * __builtin_amdgcn_logf(sum);
 }
 
-// Keys, in steps, of a tile of rows and a split.
-struct KvRange {
-    int s0, s1;
-};
-
+// The keys of a tile of rows and a split.
 __device__ __forceinline__ KvRange ka_range(const KvArgs &a, int split, int qn, int kv, int64_t r0, int64_t r1)
 {
     const int steps = (kv + 63) >> 6;
@@ -872,7 +875,7 @@ __device__ __forceinline__ KvRange ka_range(const KvArgs &a, int split, int qn, 
     const int first = kv - qn + (int)(r0 / a.group), last = kv - qn + (int)((r1 - 1) / a.group);
     const int lo = ka_window(a, first);
     const int hi = a.causal ? max(min(last + 1, kv), 0) : kv;
-    return {max(split * per, lo >> 6), min(min((split + 1) * per, steps), (hi + 63) >> 6)};
+    return {max(split * per, lo >> 6), min(min((split + 1) * per, steps), (hi + 63) >> 6), lo, hi};
 }
 
 // One row's four channels c .. of a block's or a wave's sums.
@@ -904,7 +907,7 @@ __device__ __forceinline__ void ka_few_rows(float *om, const KvArgs &a, ka_const
     KvRows<D, 1> w;
     ka_rows<D, INT4, 1>(w, a, head, qs, qn, kv, r0, rows, lane);
     const KvRange g = ka_range(a, split, qn, kv, r0, min(r0 + 16, rows));
-    ka_walk<D, INT4, 1>(w, a, table, head, kv, g.s0 + wave, g.s1, 4, c2, lane);
+    ka_walk<D, INT4, 1>(w, a, table, head, g, g.s0 + wave, 4, c2, lane);
     // the waves' parts, in wave order, into om
     const float l = ka_sum_parts(w.l[0]);
     if (b == 0) mm[wave][j] = w.m[0], ll[wave][j] = l;
@@ -947,7 +950,7 @@ __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_c
     KvRows<D, CT> w;
     ka_rows<D, INT4, CT>(w, a, head, qs, qn, kv, r0 + 16 * CT * wave, rows, lane);
     const KvRange g = ka_range(a, split, qn, kv, r0, min(r0 + 64 * CT, rows));
-    ka_walk_shared<D, INT4, CT>(w, lds, a, table, head, kv, g.s0, g.s1, a.scale * kLog2e, wave, lane);
+    ka_walk_shared<D, INT4, CT>(w, lds, a, table, head, g, a.scale * kLog2e, wave, lane);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const float l = ka_sum_parts(w.l[ct]);
@@ -962,7 +965,7 @@ __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_c
 // CT > 0: blocks of 64 CT rows for the sequences of more than 16.  0: every list
 // of rows is taken 16 at a time.
 template <int D, bool INT4, int CT>
-__global__ __launch_bounds__(256, CT == 4 && D == 128 ? 1 : 2) void kv4_attention_kernel(KvArgs a)
+__global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
 {
     constexpr int SUMS = 4 * (16 * (D + 4) + 8 * 16), STAGES = 4 * ka_stage(D);
     __shared__ __attribute__((aligned(16))) uint8_t lds[CT > 0 && STAGES > SUMS ? STAGES : SUMS];
@@ -1026,7 +1029,7 @@ struct KvPlan {
 KvPlan ka_plan(int T, int B, int heads, int group, int max_q, int max_kv)
 {
     KvPlan p;
-    const int64_t rows = (int64_t)max_q * group;
+    const int64_t rows = (int64_t)(max_q < T ? max_q : T) * group;
     const int cus = device_cu_count();
     p.many = rows > 16;
     const int block_rows = p.many ? 64 * kManyTiles : 16;

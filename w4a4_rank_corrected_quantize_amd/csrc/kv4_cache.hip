@@ -53,6 +53,13 @@ __device__ __forceinline__ float kc_absmax(const float (&f)[8])
     return a;
 }
 
+// Stored scales are finite, so that a place that a row does not see (weight 0)
+// cannot reach it: a group that holds an infinity is stored as zeros (INT4) or
+// with 6 * 2^125 for it (MXFP4; 2^125 is the largest scale that finite bf16
+// values give).
+__device__ __forceinline__ float kc_finite(float scale) { return scale < INFINITY ? scale : 0.0f; }
+__device__ __forceinline__ uint32_t kc_finite(uint32_t e8m0) { return min(e8m0, 252u); }
+
 // Codes of 8 channels, byte i channel i (low nibble) and i + 4 (high).  |q| =
 // rint(|v| / scale) by the reciprocal, exact unless the quotient is within
 // 2^-19 of a half-integer (settled by the exact remainder) or the group needs
@@ -138,10 +145,10 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_append_kernel(Kv4View c, const
     float ks = 0.0f, vs = 0.0f;
     uint32_t ke = 0, ve = 0, kw, vw;
     if constexpr (INT4) {
-        ks = int4_group_scale(ka), vs = int4_group_scale(va);
+        ks = kc_finite(int4_group_scale(ka)), vs = kc_finite(int4_group_scale(va));
         kw = kc_int4_codes(fk, ks), vw = kc_int4_codes(fv, vs);
     } else {
-        ke = mx_block_e8m0(ka), ve = mx_block_e8m0(va);
+        ke = kc_finite(mx_block_e8m0(ka)), ve = kc_finite(mx_block_e8m0(va));
         kw = kc_e2m1_codes<false>(fk, mx_inv_scale(ke)), vw = kc_e2m1_codes<true>(fv, mx_inv_scale(ve));
     }
     // channels 8 q .. of a 32-block: parts 0, 1 are low nibbles, 2, 3 high
