@@ -13,26 +13,49 @@
 // = lane / 16 gets the scores of tokens 4 b .. 4 b + 3 of every run, and these
 // are the tokens that it reads of V, so the probabilities go from one product
 // to the next in registers.  The page layout (kv4.h) has every run in operand
-// order: 16 consecutive bytes per lane, nothing passes through LDS.
+// order: a lane's part is 16 (D = 64: 8) consecutive bytes, a wave's one run
+// (in plain token order, a lane per token, the loads took four times the L1's
+// cycles).
 //
 // INT4 scales (fp32) belong to a key and a 64-channel group: lane (b, j) holds
 // the scale of token 4 b + j % 4 of run j / 4 and the lanes of part b multiply
-// with a broadcast from it (DPP).
-// K's multiply the group's score sums, V's the probabilities before they are
-// rounded to bf16.  MXFP4 scales enter the fp4 -> bf16 conversion itself.
+// with a broadcast from it (DPP).  K's multiply the group's score sums, V's the
+// probabilities before they are rounded to bf16.  MXFP4 scales enter the fp4 ->
+// bf16 conversion itself.
 //
 // Rounding choices: p (INT4: p times V's scale) is rounded to bf16 for the
 // second product (at most 2^-8 relative, as the output's own type rounds);
 // the sum of p is taken of the unrounded values.
 //
 // Rows are packed: the G = heads_q / heads query heads that share a key head
-// and the sequence's new tokens form one list, row = token G + head, so
-// single tokens of grouped heads fill the 16 columns of a product.  A block
-// of four waves takes 16 CT rows per wave; if the sequence has no more than
-// 16 CT rows its waves share them and take every fourth step of keys instead,
-// and add up at the end.  Sequences are further split over blocks where the
-// grid would not fill the chip; the splits' sums then go to the workspace and
-// a second kernel adds them in split order.
+// and the sequence's new tokens form one list, row = token G + head, so single
+// tokens of grouped heads fill the 16 columns of a product.
+//   Up to 16 rows (decoding): a block takes 16 rows, its four waves every
+//   fourth step each, codes straight from memory to registers one step ahead;
+//   the waves' sums are added in LDS in wave order.
+//   More: a block takes 128 rows, 32 per wave.  The conversion of a step's codes
+//   is shared: each wave converts a quarter into LDS and all read the whole.
+// The keys are split over blocks where rows alone do not fill the chip; the
+// splits' sums then go to the workspace and a second kernel adds them in split
+// order.
+//
+// What bounds it, and what it measured (both kernels):
+//   32 x 4097 .. 16384 keys, 32 heads over 8 of 128, MXFP4, one token each:
+//   76 us for 335 MB = 4.4 TB/s (a large copy: 5.4 TB/s).  Bound by HBM; the
+//   first form, with codes in token order and block tables in vector loads,
+//   took 109 us.
+//   4608 rows over 4608 keys, 24 heads: D = 128 MXFP4 292 us = 893 TFLOP/s,
+//   INT4 404 us; D = 64 213 and 277 us.  Bound by instruction issue: a step of a
+//   wave issues 64 (32) matrix instructions, 32 exponentials and about 210
+//   other vector instructions, which the products do not hide (a matrix
+//   instruction holds the port for half of its time), and by the 864 tiles over
+//   512 places.  Before scores, exponentials and conversions were interleaved:
+//   340 us; before the shared conversion: 445 us.
+//   One token over 700 keys: 7.5 + 2.6 us, latencies of four dependent loads
+//   (lengths, table, codes) and of the second launch.
+// Not kept: 48 and 64 rows per wave and three waves per SIMD (spills), a branch
+// around the rescaling per column (copies of the sums), ordering hints instead
+// of fences (the compiler regrouped the pieces), several heads per block.
 #include "kv4.h"
 
 namespace svdq {
@@ -307,6 +330,14 @@ __device__ __forceinline__ void ka_v_operands(uint32_t w0, uint32_t w1, float vs
         lo = __builtin_bit_cast(bf16x8, l);
         hi = __builtin_bit_cast(bf16x8, h);
     }
+}
+
+// A second register with the same value: the compiler shares a lane's
+// broadcast among its uses and folds it (DPP) only into a single one.
+__device__ __forceinline__ float ka_copy(float x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 // o[4 t + i] = / += x[4 t + i] times the scale of token i of the lane's part of run t.
@@ -679,7 +710,7 @@ __device__ __forceinline__ void ka_v_read(bf16x8 (&vf)[N][2], uint32_t base, int
 // their place in the second product's operands.
 template <int D, bool INT4, int CT>
 __device__ __forceinline__ void ka_exp_pair(KvP<D, INT4, CT> &pb, const float (&p)[CT][16], float (&sum)[CT],
-                                            const float (&base)[CT], float c2, const float *vs, int e)
+                                            const float (&base)[CT], float c2, const float (&vs)[CT][2], int e)
 {
     const int ct = e >> 4, i = e & 15;
     const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[ct][i], c2, base[ct]));
@@ -689,7 +720,7 @@ __device__ __forceinline__ void ka_exp_pair(KvP<D, INT4, CT> &pb, const float (&
 #pragma unroll
     for (int g = 0; g < KvP<D, INT4, CT>::NG; ++g) {
         uint32_t u;
-        if constexpr (INT4) u = ka_pack2(x * ka_bcast(vs[g], i), y * ka_bcast(vs[g], i + 1));
+        if constexpr (INT4) u = ka_pack2(x * ka_bcast(vs[ct][g], i), y * ka_bcast(vs[ct][g], i + 1));
         else u = ka_pack2(x, y);
         u32x4 q = __builtin_bit_cast(u32x4, pb.b[g][ct][i >> 3]);
         q[(i & 7) >> 1] = u;
@@ -710,9 +741,13 @@ __device__ __forceinline__ void ka_take_scores(float (&p)[CT][16], const f32x4 (
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[ct][i] = x[i];
         } else if (g == 0) {
-            ka_scale_keys(p[ct], x, ks[0]);
+            ka_scale_keys(p[ct], x, ka_copy(ks[0]));
         } else {
             ka_fma_keys(p[ct], x, ks[g]);
+        }
+        if constexpr (INT4) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+v"(p[ct][i]));
         }
     }
 }
@@ -782,6 +817,11 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, c
         float base[CT], sum[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) base[ct] = w.m[ct] == -INFINITY ? 0.0f : -w.m[ct] * c2, sum[ct] = 0.0f;
+        float vsc[CT][2] = {};
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int i = 0; i < NG; ++i) vsc[ct][i] = ka_copy(vs0[i]);
         __builtin_amdgcn_sched_barrier(0);
         KvP<D, INT4, CT> pb;
         // scores of step s + 1 (operand i: run i % 4, product step i / 4) and, in
@@ -805,7 +845,7 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, c
                 else if (MIX) ka_v_read<NB>(vf, lv, i + 4 - KO);
                 if (MIX) {
 #pragma unroll
-                    for (int e = E * i; e < E * (i + 1); e += 2) ka_exp_pair<D, INT4, CT>(pb, cur, sum, base, c2, vs0, e);
+                    for (int e = E * i; e < E * (i + 1); e += 2) ka_exp_pair<D, INT4, CT>(pb, cur, sum, base, c2, vsc, e);
                 }
                 if ((i + 1) % (KO / NS) == 0) ka_take_scores<INT4, CT>(nxt, sc, ks1, (i + 1) / (KO / NS) - 1);
                 __builtin_amdgcn_sched_barrier(0);
@@ -817,7 +857,7 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, c
 #pragma unroll
             for (int e = 0; e < 4; ++e) ka_v_read<NB>(vf, lv, e);
 #pragma unroll
-            for (int e = 0; e < 16 * CT; e += 2) ka_exp_pair<D, INT4, CT>(pb, cur, sum, base, c2, vs0, e);
+            for (int e = 0; e < 16 * CT; e += 2) ka_exp_pair<D, INT4, CT>(pb, cur, sum, base, c2, vsc, e);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -868,14 +908,15 @@ __device__ __forceinline__ float ka_lse(float mx, float sum, float scale)
 // The keys of a tile of rows and a split.
 __device__ __forceinline__ KvRange ka_range(const KvArgs &a, int split, int qn, int kv, int64_t r0, int64_t r1)
 {
-    const int steps = (kv + 63) >> 6;
-    // every split the same number of steps, so that long and short sequences
-    // give blocks of equal length; more only past the caller's bound
-    const int per = max(a.split_steps, (steps + a.splits - 1) / a.splits);
     const int first = kv - qn + (int)(r0 / a.group), last = kv - qn + (int)((r1 - 1) / a.group);
     const int lo = ka_window(a, first);
     const int hi = a.causal ? max(min(last + 1, kv), 0) : kv;
-    return {max(split * per, lo >> 6), min(min((split + 1) * per, steps), (hi + 63) >> 6), lo, hi};
+    // the tile's steps in as many equal parts as it takes for none to be longer
+    // than split_steps (past the caller's bound: longer ones)
+    const int s0 = lo >> 6, s1 = (hi + 63) >> 6, steps = max(s1 - s0, 0);
+    const int parts = min(a.splits, (steps + a.split_steps - 1) / a.split_steps);
+    const int per = parts > 1 ? ((steps + parts - 1) / parts + 3) & ~3 : steps;        // a step per wave
+    return {min(s0 + split * per, s1), split < parts ? min(s0 + (split + 1) * per, s1) : s0, lo, hi};
 }
 
 // One row's four channels c .. of a block's or a wave's sums.
@@ -884,7 +925,7 @@ __device__ __forceinline__ void ka_store(const KvArgs &a, int split, size_t row,
 {
     if (a.splits > 1) {
         const size_t part = (size_t)split * a.T * a.heads_q + row;
-        *reinterpret_cast<f32x4 *>(a.work + part * D + c) = o;
+        if (mx != -INFINITY) *reinterpret_cast<f32x4 *>(a.work + part * D + c) = o;      // else not read
         if (c == 0) {
             float *ml = a.work + (size_t)a.splits * a.T * a.heads_q * D + 2 * part;
             ml[0] = mx * a.scale, ml[1] = sum;
@@ -990,8 +1031,8 @@ __global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
 }
 
 // O = sum over the splits, in split order; D / 4 lanes per row.  Every split of
-// every row of a sequence has been written, the ones without keys as zeros with
-// a maximum of -infinity.
+// every row of a sequence has been written, the ones without keys as a
+// maximum of -infinity alone.
 template <int D>
 __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 {
@@ -1010,9 +1051,12 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 #pragma unroll 4
     for (int s = 0; s < a.splits; ++s) {
         const float2 v = ml[s * n];
-        const float f = v.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((v.x - mx) * kLog2e);
+        const bool none = v.x == -INFINITY;              // its sums are not written: any valid address, and 0
+        const float f = none ? 0.0f : __builtin_amdgcn_exp2f((v.x - mx) * kLog2e);
         sum = __builtin_fmaf(v.y, f, sum);
-        o += *reinterpret_cast<const f32x4 *>(part + s * n * D) * f;
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(part + (none ? 0 : s) * n * D);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = none ? o[i] : __builtin_fmaf(x[i], f, o[i]);
     }
     o *= ka_inverse(sum);
     *reinterpret_cast<uint2 *>(a.O + row * D + c) = make_uint2(ka_pack2(o[0], o[1]), ka_pack2(o[2], o[3]));
@@ -1020,7 +1064,7 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 }
 
 // Form, tiles of rows and splits of the keys, from the sizes and the caller's
-// bounds.  Up to 16 packed rows: 16 per block; more: 32 per wave, 128 per block.
+// bounds.
 struct KvPlan {
     bool many;
     int q_tiles, splits, split_steps;
@@ -1037,9 +1081,11 @@ KvPlan ka_plan(int T, int B, int heads, int group, int max_q, int max_kv)
     // blocks of rows: at most every sequence's, and the rows' own number and one more per sequence
     int64_t blocks = (int64_t)T * group / block_rows + B;
     blocks = (blocks < tiles * B ? blocks : tiles * B) * heads;
-    // splits of equal length, at least one step per wave.  Many rows: none where
-    // the rows alone give two blocks per compute unit (a split writes and reads
-    // their fp32 sums), else about four.  Few rows: about six.
+    // at least one step per wave and split.  Many rows: no split where the rows
+    // alone give two blocks per compute unit (a split writes and reads their
+    // fp32 sums), else about four (8 sequences of 1 .. 700 rows over up to 6000
+    // keys, 16 heads over 4: 2 blocks 129 us, 3 124, 4 107, 6 107, 8 115).  Few
+    // rows: about six (4 or 8: the same to 1 us)
     const int64_t steps = ((int64_t)max_kv + 63) / 64;
     int64_t s = p.many && blocks >= 2 * (int64_t)cus ? 1 : ((p.many ? 4 : 6) * (int64_t)cus + blocks - 1) / blocks;
     s = s > (steps + 3) / 4 ? (steps + 3) / 4 : s;
