@@ -17,11 +17,13 @@
 //         with more (few rows, so that the chip is filled) it writes the
 //         slice's fp32 sums, and the second kernel adds them in slice order,
 //         scales and splits.
-//   up    a block takes one tile and 128 output channels; the products with
-//         B_a accumulate in fp32, base is added in fp32 and the row is rounded
-//         once.
-// 9216 rows, 4096 -> 12288, rank 64: down 28 us, up 90 us, 118 us for 533 MB
-// = 4.5 TB/s, where a copy of that size reaches 5.4 TB/s.
+//   up    a block takes one tile and 128 output channels, or up to eight times
+//         128 in turn; the products with B_a accumulate in fp32, base is added
+//         in fp32 and the row is rounded once.
+// 9216 rows, 4096 -> 12288, rank 64: 118 us for 533 MB = 4.5 TB/s, where a copy
+// of that size reaches 5.4 TB/s (128 channels per block: 139 us).  16 rows of
+// 16 adapters, 4096 -> 4096, rank 16: 4.4 + 4.0 us, latencies of the dependent
+// loads (plan, rows, operands) and of two launches.
 // The order of every sum depends on the sizes alone, so results do not depend
 // on which rows share a tile.
 #include "svdq_internal.h"
@@ -34,6 +36,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int LR_ROWS = 64;            // rows per tile
 constexpr int LR_PLAN_THREADS = 1024;
@@ -306,12 +309,13 @@ __global__ __launch_bounds__(256) void lora_down_kernel(
 
 // --------------------------------------------------------------------- up
 //
-// A block takes one tile and 128 output channels.  Wave g multiplies rows
-// 16 g .. of the tile with all 128: product tile j has the channels 8 i + j (i
-// = 0 .. 15), so a lane's sums are 8 consecutive channels of four rows and
-// base and Y move as 256 bytes per row and instruction.  B_a's rows go through
-// LDS, once for the four waves.  A tile of at most 16 rows is shared out by
-// channels instead, 32 per wave, B_a straight from memory.
+// A block takes one tile and `width` output channels, 128 at a time, base's and
+// B_a's next 128 on their way during the products.  Wave g multiplies rows 16 g
+// .. of the tile with all 128: product tile j has the channels 8 i + j (i = 0 ..
+// 15), so a lane's sums are 8 consecutive channels of four rows and base and Y
+// move as 256 bytes per row and instruction.  B_a's rows go through LDS, once
+// for the four waves.  A tile of at most 16 rows is shared out by channels
+// instead, 32 per wave, B_a straight from memory.
 constexpr int LR_UP_N = 128;
 
 template <int KS>
@@ -348,23 +352,23 @@ template <int KS>
 __global__ __launch_bounds__(256) void lora_up_kernel(const float *__restrict__ work, const uint16_t *__restrict__ B,
                                                       const float *__restrict__ scale,
                                                       const int32_t *__restrict__ plan, int M, int N, int R, int n,
-                                                      int slices, int nblocks, const uint16_t *base, uint16_t *Y)
+                                                      int slices, int nblocks, int width, const uint16_t *base, uint16_t *Y)
 {
     constexpr int BS = 32 * KS + 8;                      // LDS row: B_a's channels, zeros up to 32 KS, 16 B pad
     __shared__ __attribute__((aligned(16))) uint16_t bs[LR_UP_N * BS];
-    const int t = blockIdx.x / nblocks, n0 = (blockIdx.x % nblocks) * LR_UP_N;
+    const int t = blockIdx.x / nblocks, n_first = (blockIdx.x % nblocks) * width, n_end = min(N, n_first + width);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int i16 = lane & 15, kb = lane >> 4;
     int adapter, count;
     if (!lr_tile(plan, M, n, t, adapter, count)) return;
     const int32_t *rows = lr_rows(plan, M, n, t);
     if (adapter < 0) {                                   // rows without an adapter: copied, unless in place
-        const int c = n0 + 8 * i16;
-        if (Y == base || c >= N) return;
-        for (int p = tid >> 4; p < count; p += 16) {
-            const size_t o = (size_t)rows[p] * N + c;
-            *reinterpret_cast<uint4 *>(Y + o) = *reinterpret_cast<const uint4 *>(base + o);
-        }
+        if (Y == base) return;
+        for (int c = n_first + 8 * i16; c < n_end; c += LR_UP_N)
+            for (int p = tid >> 4; p < count; p += 16) {
+                const size_t o = (size_t)rows[p] * N + c;
+                *reinterpret_cast<uint4 *>(Y + o) = *reinterpret_cast<const uint4 *>(base + o);
+            }
         return;
     }
     const uint16_t *ba = B + (size_t)adapter * N * R;
@@ -372,78 +376,92 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const float *__restrict__ 
     const size_t slice_lanes = lr_h(KS, (int)lr_max_tiles(M, n), 0, 0);
     bf16x8 hi[KS], lo[KS];
     if (count <= 16) {
-        // channels n0 + 32 wave + 2 i16 + j: two per lane
-        const int c = n0 + 32 * wave + 2 * i16;
-        if (n0 + 32 * wave >= N) return;
-        const int cc = min(c, N - 2);
-        const int4 row = *reinterpret_cast<const int4 *>(rows + 4 * kb);
-        const size_t off[4] = {(size_t)row.x * N + cc, (size_t)row.y * N + cc, (size_t)row.z * N + cc, (size_t)row.w * N + cc};
-        uint32_t y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint32_t *>(base + off[i]);
-        uint4 b[KS][2];
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)                  // chunks past R repeat the last one and meet zeros of h
-                b[k][j] = *reinterpret_cast<const uint4 *>(ba + (size_t)(cc + j) * R + min(32 * k + 8 * kb, R - 8));
         lr_load_h<KS>(hi, lo, work, t, 0, slices, slice_lanes, s_a, lane);
-        f32x4 acc[2] = {};
+        const int4 row = *reinterpret_cast<const int4 *>(rows + 4 * kb);
+        for (int n0 = n_first + 32 * wave; n0 < n_end; n0 += LR_UP_N) {
+            // channels n0 + 2 i16 + j: two per lane
+            const int c = n0 + 2 * i16, cc = min(c, N - 2);
+            const size_t off[4] = {(size_t)row.x * N + cc, (size_t)row.y * N + cc, (size_t)row.z * N + cc, (size_t)row.w * N + cc};
+            uint32_t y[4];
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+            for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint32_t *>(base + off[i]);
+            uint4 b[KS][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const bf16x8 bb = __builtin_bit_cast(bf16x8, b[k][j]);
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[k], bb, acc[j], 0, 0, 0);
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[k], bb, acc[j], 0, 0, 0);
-            }
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (4 * kb + i < count && c < N)
-                *reinterpret_cast<uint32_t *>(Y + off[i]) =
-                    lr_pack2(bits_f32(y[i] << 16) + acc[0][i], bits_f32(y[i] & 0xFFFF0000u) + acc[1][i]);
+                for (int j = 0; j < 2; ++j)              // chunks past R repeat the last one and meet zeros of h
+                    b[k][j] = *reinterpret_cast<const uint4 *>(ba + (size_t)(cc + j) * R + min(32 * k + 8 * kb, R - 8));
+            f32x4 acc[2] = {};
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const bf16x8 bb = __builtin_bit_cast(bf16x8, b[k][j]);
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[k], bb, acc[j], 0, 0, 0);
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[k], bb, acc[j], 0, 0, 0);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * kb + i < count && c < N)
+                    *reinterpret_cast<uint32_t *>(Y + off[i]) =
+                        lr_pack2(bits_f32(y[i] << 16) + acc[0][i], bits_f32(y[i] & 0xFFFF0000u) + acc[1][i]);
+        }
         return;
     }
     // channels n0 + 8 i16 .. + 7 of rows 16 wave + 4 kb + i
-    const int c = n0 + 8 * i16, cc = min(c, N - 8);
     const int4 row = *reinterpret_cast<const int4 *>(rows + 16 * wave + 4 * kb);
-    const size_t off[4] = {(size_t)row.x * N + cc, (size_t)row.y * N + cc, (size_t)row.z * N + cc, (size_t)row.w * N + cc};
-    uint4 y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const uint4 *>(base + off[i]);
-    lr_load_h<KS>(hi, lo, work, t, wave, slices, slice_lanes, s_a, lane);
+    const size_t off[4] = {(size_t)row.x * N, (size_t)row.y * N, (size_t)row.z * N, (size_t)row.w * N};
     // LDS row 16 j + i holds channel 8 i + j
-    constexpr int CH = 4 * KS;                           // 16-byte chunks of an LDS row
-    uint4 st[LR_UP_N * CH / 256];
+    constexpr int CH = 4 * KS, ST = LR_UP_N * CH / 256;  // 16-byte chunks of an LDS row, of a thread
+    u32x4 y[4], st[ST];
+    auto load = [&](u32x4 (&y)[4], u32x4 (&st)[ST], int n0) {
+        const int cc = min(n0 + 8 * i16, N - 8);
 #pragma unroll
-    for (int q = 0; q < LR_UP_N * CH / 256; ++q) {
-        const int e = tid + 256 * q, ch = e % CH, nn = min(n0 + e / CH, N - 1);
-        st[q] = *reinterpret_cast<const uint4 *>(ba + (size_t)nn * R + min(8 * ch, R - 8));
-    }
+        for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const u32x4 *>(base + off[i] + cc);
 #pragma unroll
-    for (int q = 0; q < LR_UP_N * CH / 256; ++q) {
-        const int e = tid + 256 * q, ch = e % CH, nn = e / CH;
-        *reinterpret_cast<uint4 *>(&bs[(16 * (nn & 7) + (nn >> 3)) * BS + 8 * ch]) = st[q];
-    }
-    __syncthreads();
-    f32x4 acc[8] = {};
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bf16x8 b = *reinterpret_cast<const bf16x8 *>(&bs[(16 * j + i16) * BS + 32 * k + 8 * kb]);
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[k], b, acc[j], 0, 0, 0);
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[k], b, acc[j], 0, 0, 0);
+        for (int q = 0; q < ST; ++q) {
+            const int e = tid + 256 * q, ch = e % CH, nn = min(n0 + e / CH, N - 1);
+            st[q] = *reinterpret_cast<const u32x4 *>(ba + (size_t)nn * R + min(8 * ch, R - 8));
         }
+    };
+    load(y, st, n_first);
+    lr_load_h<KS>(hi, lo, work, t, wave, slices, slice_lanes, s_a, lane);
+    for (int n0 = n_first;; n0 += LR_UP_N) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (16 * wave + 4 * kb + i >= count || c >= N) continue;
-        const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
-        uint32_t v[4];
+        for (int q = 0; q < ST; ++q) {
+            const int e = tid + 256 * q, ch = e % CH, nn = e / CH;
+            *reinterpret_cast<u32x4 *>(&bs[(16 * (nn & 7) + (nn >> 3)) * BS + 8 * ch]) = st[q];
+        }
+        const bool more = n0 + LR_UP_N < n_end;
+        u32x4 y2[4], st2[ST];
+        load(y2, st2, more ? n0 + LR_UP_N : n0);         // on their way during the products
+        __syncthreads();
+        f32x4 acc[8] = {};
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            v[q] = lr_pack2(bits_f32(w[q] << 16) + acc[2 * q][i], bits_f32(w[q] & 0xFFFF0000u) + acc[2 * q + 1][i]);
-        *reinterpret_cast<uint4 *>(Y + off[i]) = make_uint4(v[0], v[1], v[2], v[3]);
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bf16x8 b = *reinterpret_cast<const bf16x8 *>(&bs[(16 * j + i16) * BS + 32 * k + 8 * kb]);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[k], b, acc[j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[k], b, acc[j], 0, 0, 0);
+            }
+        const int c = n0 + 8 * i16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (16 * wave + 4 * kb + i >= count || c >= N) continue;
+            const uint32_t w[4] = {y[i][0], y[i][1], y[i][2], y[i][3]};
+            uint32_t v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = lr_pack2(bits_f32(w[q] << 16) + acc[2 * q][i], bits_f32(w[q] & 0xFFFF0000u) + acc[2 * q + 1][i]);
+            *reinterpret_cast<uint4 *>(Y + off[i] + c) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        if (!more) break;
+        __syncthreads();                                 // all have read B_a's channels
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = y2[i];
+#pragma unroll
+        for (int q = 0; q < ST; ++q) st[q] = st2[q];
     }
 }
 
@@ -503,10 +521,17 @@ hipError_t launch_lora_linear(const uint16_t *X, const uint16_t *A, const uint16
 #undef LR_DOWN
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int nblocks = (N + LR_UP_N - 1) / LR_UP_N;
+    // several times 128 channels per block, so that h is loaded once for them,
+    // where at least four blocks per compute unit are left.  9216 rows, 4096 ->
+    // 12288, rank 64: 1 x 139 us, 2 x 126, 4 x 118, 8 x 116 to 119; 13 of 96
+    // parts, which leave uneven blocks, 128.
+    const int64_t each = (N + LR_UP_N - 1) / LR_UP_N;
+    const int64_t many = tiles * each / (4 * (int64_t)device_cu_count());      // blocks of 128 over the least number
+    const int width = LR_UP_N * (int)(many < 1 ? 1 : (many > 8 ? 8 : many));
+    const int nblocks = (N + width - 1) / width;
     const dim3 ugrid((uint32_t)(tiles * nblocks));
 #define LR_UP(KS) \
-    lora_up_kernel<KS><<<ugrid, 256, 0, stream>>>(work, B, scale, pl, M, N, R, n, slices, nblocks, base, Y)
+    lora_up_kernel<KS><<<ugrid, 256, 0, stream>>>(work, B, scale, pl, M, N, R, n, slices, nblocks, width, base, Y)
     if (R <= 32) LR_UP(1);
     else if (R <= 64) LR_UP(2);
     else LR_UP(4);
