@@ -1030,26 +1030,32 @@ __global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
     }
 }
 
-// O = sum over the splits, in split order; D / 4 lanes per row.  Every split of
-// every row of a sequence has been written, the ones without keys as a
-// maximum of -infinity alone.
-template <int D>
+// O = sum over the splits; D / 4 lanes per row and P parts of a block, part p
+// with the splits p, p + P, .., the parts added in order.  Every split of every
+// row of a sequence has been written, the ones without keys as a maximum of
+// -infinity alone.
+template <int D, int P>
 __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 {
-    constexpr int L = D / 4;
-    const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-    const int c = 4 * (threadIdx.x % L);
+    constexpr int L = D / 4, R = 256 / (L * P);
+    __shared__ f32x4 os[P > 1 ? P : 1][P > 1 ? R * L : 1];
+    __shared__ float2 mls[P > 1 ? P : 1][P > 1 ? R : 1];
+    const int lane = threadIdx.x % L, r = threadIdx.x / L % R, p = threadIdx.x / (L * R);
+    const int64_t row = (int64_t)blockIdx.x * R + r;
+    const int c = 4 * lane;
     const int64_t n = (int64_t)a.T * a.heads_q;
     // rows outside the sequences keep what they hold
-    if (row >= n || row < (int64_t)a.q_start[0] * a.heads_q || row >= (int64_t)a.q_start[a.B] * a.heads_q) return;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.work + (size_t)a.splits * n * D) + row;
-    const float *part = a.work + row * D + c;
+    const bool in = row < n && row >= (int64_t)a.q_start[0] * a.heads_q && row < (int64_t)a.q_start[a.B] * a.heads_q;
+    if (P == 1 && !in) return;
+    const int64_t at = in ? row : 0;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.work + (size_t)a.splits * n * D) + at;
+    const float *part = a.work + at * D + c;
     float mx = -INFINITY, sum = 0.0f;
     f32x4 o = {};
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, ml[s * n].x);
+    for (int s = p; s < a.splits; s += P) mx = fmaxf(mx, ml[s * n].x);
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
+    for (int s = p; s < a.splits; s += P) {
         const float2 v = ml[s * n];
         const bool none = v.x == -INFINITY;              // its sums are not written: any valid address, and 0
         const float f = none ? 0.0f : __builtin_amdgcn_exp2f((v.x - mx) * kLog2e);
@@ -1057,6 +1063,22 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
         const f32x4 x = *reinterpret_cast<const f32x4 *>(part + (none ? 0 : s) * n * D);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = none ? o[i] : __builtin_fmaf(x[i], f, o[i]);
+    }
+    if constexpr (P > 1) {
+        os[p][r * L + lane] = o;
+        if (lane == 0) mls[p][r] = make_float2(mx, sum);
+        __syncthreads();
+        if (p > 0 || !in) return;
+#pragma unroll
+        for (int q = 1; q < P; ++q) mx = fmaxf(mx, mls[q][r].x);
+        o = (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const float2 v = mls[q][r];
+            const float f = v.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((v.x - mx) * kLog2e);
+            sum = __builtin_fmaf(v.y, f, sum);
+            o += os[q][r * L + lane] * f;
+        }
     }
     o *= ka_inverse(sum);
     *reinterpret_cast<uint2 *>(a.O + row * D + c) = make_uint2(ka_pack2(o[0], o[1]), ka_pack2(o[2], o[3]));
@@ -1081,14 +1103,24 @@ KvPlan ka_plan(int T, int B, int heads, int group, int max_q, int max_kv)
     // blocks of rows: at most every sequence's, and the rows' own number and one more per sequence
     int64_t blocks = (int64_t)T * group / block_rows + B;
     blocks = (blocks < tiles * B ? blocks : tiles * B) * heads;
-    // at least one step per wave and split.  Many rows: no split where the rows
-    // alone give two blocks per compute unit (a split writes and reads their
-    // fp32 sums), else about four (8 sequences of 1 .. 700 rows over up to 6000
-    // keys, 16 heads over 4: 2 blocks 129 us, 3 124, 4 107, 6 107, 8 115).  Few
-    // rows: about six (4 or 8: the same to 1 us)
+    // Splits.  Many rows: none where the rows alone give two blocks per compute
+    // unit (a split writes and reads their fp32 sums), else about four blocks (8
+    // sequences of 1 .. 700 rows over up to 6000 keys, 16 heads over 4: 2 blocks
+    // 129 us, 3 124, 4 107, 6 107, 8 115), of at least four steps.
+    // Few rows: none up to 12 steps (700 keys: 10.1 us, split 10.6); up to a block
+    // per compute unit of at least four steps, one per wave (8000 keys, 8 heads:
+    // 9.3 us, of eight 10.9); beyond that up to six of at least 16 (2 x 16000
+    // keys: 17 us, of four steps 25).
     const int64_t steps = ((int64_t)max_kv + 63) / 64;
-    int64_t s = p.many && blocks >= 2 * (int64_t)cus ? 1 : ((p.many ? 4 : 6) * (int64_t)cus + blocks - 1) / blocks;
-    s = s > (steps + 3) / 4 ? (steps + 3) / 4 : s;
+    auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+    auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+    int64_t s;
+    if (p.many) {
+        s = blocks >= 2 * (int64_t)cus ? 1 : least(up(steps, 4), up(4 * (int64_t)cus, blocks));
+    } else {
+        const int64_t a = least(up(steps, 4), up(cus, blocks)), b = least(up(steps, 16), up(6 * (int64_t)cus, blocks));
+        s = steps <= 12 ? 1 : (a > b ? a : b);
+    }
     s = s > 64 ? 64 : s;
     p.split_steps = (int)((steps + s - 1) / s + 3) & ~3;
     p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
@@ -1126,10 +1158,12 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
 #undef KA_LAUNCH
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int per = 256 / (c.dim / 4);
-    const dim3 cgrid((uint32_t)(((int64_t)T * heads_q + per - 1) / per));
-    if (c.dim == 64) kv4_combine_kernel<64><<<cgrid, 256, 0, stream>>>(a);
-    else kv4_combine_kernel<128><<<cgrid, 256, 0, stream>>>(a);
+    const int64_t n = (int64_t)T * heads_q;
+#define KA_COMBINE(D, P) \
+    kv4_combine_kernel<D, P><<<(uint32_t)((n * (D / 4 * P) + 255) / 256), 256, 0, stream>>>(a)
+    if (p.splits <= 4) c.dim == 64 ? KA_COMBINE(64, 1) : KA_COMBINE(128, 1);
+    else c.dim == 64 ? KA_COMBINE(64, 8) : KA_COMBINE(128, 8);
+#undef KA_COMBINE
     return hipGetLastError();
 }
 
