@@ -912,7 +912,7 @@ __device__ __forceinline__ KvRange ka_range(const KvArgs &a, int split, int qn, 
     const int lo = ka_window(a, first);
     const int hi = a.causal ? max(min(last + 1, kv), 0) : kv;
     // the tile's steps in as many equal parts as it takes for none to be longer
-    // than split_steps (past the caller's bound: longer ones)
+    // than split_steps (at most `splits` parts: longer ones then)
     const int s0 = lo >> 6, s1 = (hi + 63) >> 6, steps = max(s1 - s0, 0);
     const int parts = min(a.splits, (steps + a.split_steps - 1) / a.split_steps);
     const int per = parts > 1 ? ((steps + parts - 1) / parts + 3) & ~3 : steps;        // a step per wave
@@ -1089,7 +1089,7 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 // bounds.
 struct KvPlan {
     bool many;
-    int q_tiles, splits, split_steps;
+    int q_tiles, splits, split_steps;             // a split's least length (many rows: its length within the bound)
 };
 
 KvPlan ka_plan(int T, int B, int heads, int group, int max_q, int max_kv)
@@ -1110,20 +1110,23 @@ KvPlan ka_plan(int T, int B, int heads, int group, int max_q, int max_kv)
     // Few rows: none up to 12 steps (700 keys: 10.1 us, split 10.6); up to a block
     // per compute unit of at least four steps, one per wave (8000 keys, 8 heads:
     // 9.3 us, of eight 10.9); beyond that up to six of at least 16 (2 x 16000
-    // keys: 17 us, of four steps 25).
+    // keys: 17 us, of four steps 25).  Sequences shorter than the bound take as
+    // many parts of that least length (one of 1500 keys under a bound of 32768:
+    // 10.3 us, in parts of the bound's length 13.0).
     const int64_t steps = ((int64_t)max_kv + 63) / 64;
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
-    int64_t s;
+    int64_t s, least_steps = 0;
     if (p.many) {
         s = blocks >= 2 * (int64_t)cus ? 1 : least(up(steps, 4), up(4 * (int64_t)cus, blocks));
     } else {
         const int64_t a = least(up(steps, 4), up(cus, blocks)), b = least(up(steps, 16), up(6 * (int64_t)cus, blocks));
-        s = steps <= 12 ? 1 : (a > b ? a : b);
+        s = steps <= 12 ? 1 : (a > b ? a : b), least_steps = a >= b ? 4 : 16;
     }
     s = s > 64 ? 64 : s;
     p.split_steps = (int)((steps + s - 1) / s + 3) & ~3;
     p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
+    if (!p.many) p.split_steps = (int)least_steps;
     const int64_t cap = (int64_t)(1 << 24) / ((int64_t)B * heads * p.splits) + 1;    // grid; further tiles in a loop
     p.q_tiles = (int)(tiles > cap ? cap : tiles);
     return p;
