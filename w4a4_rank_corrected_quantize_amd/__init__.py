@@ -568,29 +568,42 @@ def _arg(t, dtype, name, shape=None):
 
 def _rows_arg(t, dtype, name, shape):
     """A 2-D tensor whose rows are contiguous but may be a stride apart (a
-    slice of a wider tensor)."""
+    slice of a wider tensor); returns the stride."""
+    try:
+        if t.dtype is dtype and t.shape == shape:
+            ld, one = t.stride()
+            if one == 1 or not t.numel():
+                return ld
+            raise ValueError(f"{name} must have contiguous rows")
+    except AttributeError:
+        pass
+    _bad(t, dtype, name, shape)
+
+
+def _bad_device(dev, names, tensors):
+    """Raises what is wrong with the tensors' devices."""
     torch = _tt()
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
-        _bad(t, dtype, name, shape)
-    if t.stride(1) != 1 and t.numel():
-        raise ValueError(f"{name} must have contiguous rows")
-    return t
+    for name, t in zip(names, tensors):
+        if t is not None and t.device != dev:
+            raise (TypeError(f"{name} must be a device tensor") if t.device.type != "cuda" or dev.type != "cuda"
+                   else ValueError(f"{name} is on {t.device}, expected {dev}"))
+    if dev.type != "cuda":
+        raise TypeError("the tensors must be device tensors")
+    raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
 
 
-def _launch(dev, tensors, stream):
+def _launch(dev, names, tensors, stream):
     """The stream to launch on; checks that every tensor lies on `dev` and that
     `dev` is the current device (the library launches there)."""
-    torch, index = _tt(), dev.index if dev.type == "cuda" else -1
-    for name, t in tensors:
+    index = dev.index                                   # None on the CPU
+    for t in tensors:
         if t is not None and t.get_device() != index:
-            raise (TypeError(f"{name} must be a device tensor") if t.device.type != "cuda" or index < 0
-                   else ValueError(f"{name} is on {t.device}, expected {dev}"))
-    if index < 0:
-        raise TypeError("the tensors must be device tensors")
-    if torch._C._cuda_getDevice() != index:
-        raise ValueError(f"the tensors are on {dev}, the current device is {torch._C._cuda_getDevice()}")
+            _bad_device(dev, names, tensors)
+    C = _T._C
+    if index is None or C._cuda_getDevice() != index:
+        _bad_device(dev, names, tensors)
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        return C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -652,17 +665,17 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
             B = t.shape[0]
             if B == 0:
                 raise ValueError(f"{name} has no rows")
-        _rows_arg(t, bf, name, (B, D))
+        stride = _rows_arg(t, bf, name, (B, D))
         if B > 1:
-            if sets and t.stride(0) != ld:
+            if sets and stride != ld:
                 raise ValueError("gate, scale and shift must have the same row stride")
-            ld = t.stride(0)
+            ld = stride
         sets += 1
     if mod_index is not None:
         _arg(mod_index, torch.int32, "mod_index", (M,))
     dev = r.device
-    raw = _launch(dev, (("y", y), ("gate", gate), ("scale", scale), ("shift", shift), ("mod_index", mod_index),
-                        ("post_w", post_w), ("pre_w", pre_w), ("pre_b", pre_b), ("r_out", r_out), ("x", x)), stream)
+    raw = _launch(dev, ("y", "gate", "scale", "shift", "mod_index", "post_w", "pre_w", "pre_b", "r_out", "x"),
+                  (y, gate, scale, shift, mod_index, post_w, pre_w, pre_b, r_out, x), stream)
     st = lib().svdq_residual_norm(r.data_ptr(), 1 if r.dtype is f32 else 0, _ptr(y), M, D, post, _ptr(post_w),
                                   _ptr(gate), alpha, pre, _ptr(pre_w), _ptr(pre_b), _ptr(scale), _ptr(shift),
                                   _ptr(mod_index), B, ld, eps, _ptr(r_out), _ptr(x), raw)
@@ -694,7 +707,8 @@ def lora_plan(index, n_adapters: int, plan: Optional[LoraPlan] = None, stream=No
     elif plan.M != M or plan.n_adapters != n_adapters:
         raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n_adapters}")
     dev = index.device
-    raw = _launch(dev, (("plan", plan.buffer),), stream)
+    raw = _launch(dev, ("plan",),
+                  (plan.buffer,), stream)
     st = lib().svdq_lora_plan(index.data_ptr(), M, n_adapters, plan.buffer.data_ptr(), plan.buffer.numel(), raw)
     if st:
         raise SvdqError(st, "svdq_lora_plan")
@@ -740,8 +754,8 @@ def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=
         work = _empty(max(lora_workspace_bytes(M, K, R, n), 16), torch.uint8, dev, stream)
     else:
         _arg(work, torch.uint8, "work")
-    raw = _launch(dev, (("A", A), ("B", B), ("scale", scale), ("plan", plan.buffer), ("base", base), ("Y", Y),
-                        ("work", work)), stream)
+    raw = _launch(dev, ("A", "B", "scale", "plan", "base", "Y", "work"),
+                  (A, B, scale, plan.buffer, base, Y, work), stream)
     st = lib().svdq_lora_linear(X.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), plan.buffer.data_ptr(),
                                 base.data_ptr(), M, N, K, R, n, Y.data_ptr(), work.data_ptr(), work.numel(), raw)
     if st:
@@ -831,7 +845,8 @@ def kv4_append(cache: Kv4Cache, K, V, slots, stream=None) -> None:
     if V.shape[0] != T:
         raise ValueError(f"V has shape {tuple(V.shape)}, expected {tuple(K.shape)}")
     _arg(slots, torch.int32, "slots", (T,))
-    raw = _launch(dev, (("K", K), ("V", V), ("slots", slots)), stream)
+    raw = _launch(dev, ("K", "V", "slots"),
+                  (K, V, slots), stream)
     st = lib().svdq_kv4_append(cache._ref(), K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T, raw)
     if st:
         raise SvdqError(st, "svdq_kv4_append")
@@ -847,8 +862,9 @@ def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
     T = slots.shape[0]
     shape = (T, cache.heads, cache.dim)
     K = _empty(shape, torch.float32, dev, stream) if K is None else _arg(K, torch.float32, "K", shape)
-    V = _empty(shape, torch.float32, dev, stream) if V is None else _arg(V, torch.float32, "V", shape)
-    raw = _launch(dev, (("slots", slots), ("K", K), ("V", V)), stream)
+    V = _empty(shape, torch.float32, dev, stream, K) if V is None else _arg(V, torch.float32, "V", shape)
+    raw = _launch(dev, ("slots", "K", "V"),
+                  (slots, K, V), stream)
     st = lib().svdq_kv4_read(cache._ref(), slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), raw)
     if st:
         raise SvdqError(st, "svdq_kv4_read")
@@ -897,8 +913,8 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
         work = _empty(need, torch.uint8, dev, stream) if need else None
     else:
         _arg(work, torch.uint8, "work")
-    raw = _launch(dev, (("Q", Q), ("block_table", block_table), ("q_start", q_start), ("kv_len", kv_len), ("out", out),
-                        ("lse", lse), ("work", work)), stream)
+    raw = _launch(dev, ("Q", "block_table", "q_start", "kv_len", "out", "lse", "work"),
+                  (Q, block_table, q_start, kv_len, out, lse, work), stream)
     st = lib().svdq_kv4_attention(cache._ref(), Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
                                   kv_len.data_ptr(), B, T, H, max_q, max_kv, D ** -0.5 if scale is None else scale,
                                   1 if causal else 0, min(window, 0x7FFFFFFF), out.data_ptr(), _ptr(lse), _ptr(work),
