@@ -41,7 +41,7 @@
 //
 // What bounds it, and what it measured (both kernels):
 //   32 x 4097 .. 16384 keys, 32 heads over 8 of 128, MXFP4, one token each:
-//   76 us for 335 MB = 4.4 TB/s (a large copy: 5.4 TB/s).  Bound by HBM; the
+//   75 us for 335 MB = 4.5 TB/s (a large copy: 5.4 TB/s).  Bound by HBM; the
 //   first form, with codes in token order and block tables in vector loads,
 //   took 109 us.
 //   4608 rows over 4608 keys, 24 heads: D = 128 MXFP4 292 us = 893 TFLOP/s,
@@ -51,8 +51,11 @@
 //   instruction holds the port for half of its time), and by the 864 tiles over
 //   512 places.  Before scores, exponentials and conversions were interleaved:
 //   340 us; before the shared conversion: 445 us.
-//   One token over 700 keys: 7.5 + 2.6 us, latencies of four dependent loads
-//   (lengths, table, codes) and of the second launch.
+//   One token over 1000 keys, 32 heads over 8: 7.6 + 2.6 us, latencies of the
+//   dependent loads (lengths, table, codes) and of the second launch.
+//   8 sequences of 1 .. 700 rows over up to 6000 keys, 16 heads over 4 of 64,
+//   INT4, causal: 106 us = 281 TFLOP/s; tiles and splits of unequal length leave
+//   a third of the places idle at the end.
 // Not kept: 48 and 64 rows per wave and three waves per SIMD (spills), a branch
 // around the rescaling per column (copies of the sums), ordering hints instead
 // of fences (the compiler regrouped the pieces), several heads per block.
