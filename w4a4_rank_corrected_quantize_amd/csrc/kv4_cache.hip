@@ -7,7 +7,7 @@
 // with fp32 values.  4608 tokens, 32 heads of 64, INT4: 15 us for 46 MB and 16
 // us for 88 MB (3.1 and 5.6 TB/s); 1024 tokens, 24 heads of 128, MXFP4: 5.5 and
 // 8.5 us.  Append is held by the quantizer's arithmetic next to the loads
-// (about 150 instructions per 8 channels of K and V).
+// (about 300 vector instructions per 8 channels of K and of V, ties included).
 //
 // A block takes one head of 2048 / D consecutive tokens, 8 channels per
 // thread.  K codes are written as they come out, one dword per thread; V codes
