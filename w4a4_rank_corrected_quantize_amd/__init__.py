@@ -635,27 +635,56 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     of token m by mod_index [M] int32, or B equal runs of tokens.  Returns
     (r', x): r' is `r` itself without y, x is None with want_x=False.  r_out
     may be r (in place)."""
-    torch = _tt()
+    torch = _T or _tt()
     bf, f32 = torch.bfloat16, torch.float32
     _ndim(r, 2, "r")
-    if r.dtype is not bf and r.dtype is not f32:
-        raise TypeError(f"r has dtype {r.dtype}, expected {(bf, f32)}")
-    shape = r.shape
+    stype = r.dtype
+    if stype is not bf and stype is not f32:
+        raise TypeError(f"r has dtype {stype}, expected {(bf, f32)}")
+    shape, dev = r.shape, r.device
     M, D = shape
-    _arg(r, r.dtype, "r")
+    _arg(r, stype, "r")
+    pY = pO = pX = pG = pS = pH = pPost = pPre = pBias = pI = None
     if y is not None:
-        _arg(y, bf, "y", shape)
-        r_out = _empty(shape, r.dtype, r.device, stream, r) if r_out is None else _arg(r_out, r.dtype, "r_out", shape)
+        pY = _arg(y, bf, "y", shape).data_ptr()
+        if r_out is not None:
+            _arg(r_out, stype, "r_out", shape)
+        else:
+            r_out = torch.empty_like(r) if stream is None else _empty(shape, stype, dev, stream)
+        pO = r_out.data_ptr()
     elif r_out is not None:
         raise ValueError("r_out without y: nothing to update")
     if want_x:
-        x = _empty(shape, bf, r.device, stream, r if y is None else y) if x is None else _arg(x, bf, "x", shape)
+        if x is not None:
+            _arg(x, bf, "x", shape)
+        else:
+            x = _empty(shape, bf, dev, stream, r if y is None else y)
+        pX = x.data_ptr()
     elif x is not None:
         raise ValueError("x given with want_x=False")
-    vec = (D,)
-    for t, name in ((post_w, "post_w"), (pre_w, "pre_w"), (pre_b, "pre_b")):
-        if t is not None:
-            _arg(t, bf, name, vec)
+    if post_w is not None:
+        pPost = _arg(post_w, bf, "post_w", (D,)).data_ptr()
+    if pre_w is not None:
+        pPre = _arg(pre_w, bf, "pre_w", (D,)).data_ptr()
+    if pre_b is not None:
+        pBias = _arg(pre_b, bf, "pre_b", (D,)).data_ptr()
+    B, ld = 0, D
+    if gate is not None or scale is not None or shift is not None:
+        B, ld = _mod_rows(D, gate, scale, shift)
+        pG, pS, pH = _ptr(gate), _ptr(scale), _ptr(shift)
+    if mod_index is not None:
+        pI = _arg(mod_index, torch.int32, "mod_index", (M,)).data_ptr()
+    raw = _launch(dev, ("y", "gate", "scale", "shift", "mod_index", "post_w", "pre_w", "pre_b", "r_out", "x"),
+                  (y, gate, scale, shift, mod_index, post_w, pre_w, pre_b, r_out, x), stream)
+    st = lib().svdq_residual_norm(r.data_ptr(), 1 if stype is f32 else 0, pY, M, D, post, pPost, pG, alpha, pre, pPre,
+                                  pBias, pS, pH, pI, B, ld, eps, pO, pX, raw)
+    if st:
+        raise SvdqError(st, "svdq_residual_norm")
+    return (r if y is None else r_out), x
+
+
+def _mod_rows(D, gate, scale, shift):
+    """Rows and row stride of the modulation vectors given."""
     B, ld, sets = 0, D, 0
     for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
         if t is None:
@@ -665,23 +694,13 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
             B = t.shape[0]
             if B == 0:
                 raise ValueError(f"{name} has no rows")
-        stride = _rows_arg(t, bf, name, (B, D))
+        stride = _rows_arg(t, _T.bfloat16, name, (B, D))
         if B > 1:
             if sets and stride != ld:
                 raise ValueError("gate, scale and shift must have the same row stride")
             ld = stride
         sets += 1
-    if mod_index is not None:
-        _arg(mod_index, torch.int32, "mod_index", (M,))
-    dev = r.device
-    raw = _launch(dev, ("y", "gate", "scale", "shift", "mod_index", "post_w", "pre_w", "pre_b", "r_out", "x"),
-                  (y, gate, scale, shift, mod_index, post_w, pre_w, pre_b, r_out, x), stream)
-    st = lib().svdq_residual_norm(r.data_ptr(), 1 if r.dtype is f32 else 0, _ptr(y), M, D, post, _ptr(post_w),
-                                  _ptr(gate), alpha, pre, _ptr(pre_w), _ptr(pre_b), _ptr(scale), _ptr(shift),
-                                  _ptr(mod_index), B, ld, eps, _ptr(r_out), _ptr(x), raw)
-    if st:
-        raise SvdqError(st, "svdq_residual_norm")
-    return (r if y is None else r_out), x
+    return B, ld
 
 
 class LoraPlan:
