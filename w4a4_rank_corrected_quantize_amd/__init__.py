@@ -812,14 +812,9 @@ class Kv4Cache:
         self._k_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
         self._v_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
         self.device = self._k_codes.device
-        self._struct = _Kv4Struct(None, None, None, None, pages, page_size, heads, dim, prec)
-
-    def _ref(self):
-        """Address of the C structure, its pointers those of the buffers now."""
-        s = self._struct
-        s.k_codes, s.k_scales = self._k_codes.data_ptr(), self._k_scales.data_ptr()
-        s.v_codes, s.v_scales = self._v_codes.data_ptr(), self._v_scales.data_ptr()
-        return ctypes.addressof(s)
+        self._struct = _Kv4Struct(self._k_codes.data_ptr(), self._k_scales.data_ptr(), self._v_codes.data_ptr(),
+                                  self._v_scales.data_ptr(), pages, page_size, heads, dim, prec)
+        self._ref = ctypes.addressof(self._struct)
 
     def __reduce__(self):
         raise TypeError("a Kv4Cache cannot be copied or pickled; copy its buffers")
@@ -831,8 +826,8 @@ class Kv4Cache:
 
 
 def _heads_arg(t, name, heads, dim):
-    """[T][heads][dim] bf16 with contiguous rows; returns the row stride."""
-    torch = _tt()
+    """[T][heads][dim] bf16 with contiguous rows; returns T and the row stride."""
+    torch = _T or _tt()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not torch.bfloat16:
@@ -841,10 +836,11 @@ def _heads_arg(t, name, heads, dim):
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected {('T', heads, dim)}")
     ld, sh, sd = t.stride()
-    if t.numel() and (sd != 1 or (heads > 1 and sh != dim)):
+    if (sd != 1 or (heads > 1 and sh != dim)) and t.numel():
         raise ValueError(f"{name} must have contiguous rows of heads")
     # the stride of a single row (or of none) does not matter
-    return ld if shape[0] > 1 else heads * dim
+    T = shape[0]
+    return T, ld if T > 1 else heads * dim
 
 
 def _cache_arg(cache):
@@ -857,16 +853,15 @@ def kv4_append(cache: Kv4Cache, K, V, slots, stream=None) -> None:
     """Quantizes K, V [T][heads][dim] bf16 (rows may be a stride apart, as in a
     QKV product) into their slots [T] int32; a slot outside the cache skips
     its token.  The slots of one call must differ.  One kernel."""
-    torch = _tt()
     dev = _cache_arg(cache)
-    ldk, ldv = _heads_arg(K, "K", cache.heads, cache.dim), _heads_arg(V, "V", cache.heads, cache.dim)
-    T = K.shape[0]
-    if V.shape[0] != T:
+    T, ldk = _heads_arg(K, "K", cache.heads, cache.dim)
+    TV, ldv = _heads_arg(V, "V", cache.heads, cache.dim)
+    if TV != T:
         raise ValueError(f"V has shape {tuple(V.shape)}, expected {tuple(K.shape)}")
-    _arg(slots, torch.int32, "slots", (T,))
+    _arg(slots, _T.int32, "slots", (T,))
     raw = _launch(dev, ("K", "V", "slots"),
                   (K, V, slots), stream)
-    st = lib().svdq_kv4_append(cache._ref(), K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T, raw)
+    st = lib().svdq_kv4_append(cache._ref, K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), T, raw)
     if st:
         raise SvdqError(st, "svdq_kv4_append")
 
@@ -884,7 +879,7 @@ def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
     V = _empty(shape, torch.float32, dev, stream, K) if V is None else _arg(V, torch.float32, "V", shape)
     raw = _launch(dev, ("slots", "K", "V"),
                   (slots, K, V), stream)
-    st = lib().svdq_kv4_read(cache._ref(), slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), raw)
+    st = lib().svdq_kv4_read(cache._ref, slots.data_ptr(), T, K.data_ptr(), V.data_ptr(), raw)
     if st:
         raise SvdqError(st, "svdq_kv4_read")
     return K, V
@@ -892,7 +887,7 @@ def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
 
 def kv4_attention_workspace_bytes(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int) -> int:
     """Device scratch bytes that kv4_attention needs for these sizes."""
-    return int(lib().svdq_kv4_attention_workspace_bytes(cache._ref(), T, B, heads_q, max_q, max_kv))
+    return int(lib().svdq_kv4_attention_workspace_bytes(cache._ref, T, B, heads_q, max_q, max_kv))
 
 
 def kv4_attention_workspace(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int):
@@ -914,10 +909,10 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
     i32 = torch.int32
     dev = _cache_arg(cache)
     _ndim(Q, 3, "Q")
-    T, H, D = Q.shape
+    H, D = Q.shape[1], cache.dim
     if H == 0 or H % cache.heads:
         raise ValueError(f"Q has {H} heads, the cache {cache.heads}")
-    ldq = _heads_arg(Q, "Q", H, cache.dim)
+    T, ldq = _heads_arg(Q, "Q", H, D)
     _ndim(block_table, 2, "block_table")
     _arg(block_table, i32, "block_table")
     B, width = block_table.shape
@@ -934,7 +929,7 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
         _arg(work, torch.uint8, "work")
     raw = _launch(dev, ("Q", "block_table", "q_start", "kv_len", "out", "lse", "work"),
                   (Q, block_table, q_start, kv_len, out, lse, work), stream)
-    st = lib().svdq_kv4_attention(cache._ref(), Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
+    st = lib().svdq_kv4_attention(cache._ref, Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
                                   kv_len.data_ptr(), B, T, H, max_q, max_kv, D ** -0.5 if scale is None else scale,
                                   1 if causal else 0, min(window, 0x7FFFFFFF), out.data_ptr(), _ptr(lse), _ptr(work),
                                   0 if work is None else work.numel(), raw)
