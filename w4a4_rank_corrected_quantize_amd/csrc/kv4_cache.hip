@@ -4,10 +4,10 @@
 // Codes and scales are those of the library's group quantizers (svdq_quant.h)
 // along the head's channels, bit for bit.  Bound by HBM: append reads 4 bytes
 // (K and V in bf16) and writes about 1.1 bytes per channel, read the reverse
-// with fp32 values.  4608 tokens, 32 heads of 64, INT4: 15 us for 46 MB and 16
-// us for 88 MB (3.1 and 5.6 TB/s); 1024 tokens, 24 heads of 128, MXFP4: 5.5 and
+// with fp32 values.  4608 tokens, 32 heads of 64, INT4: 14 us for 48 MB and 16
+// us for 86 MB (3.5 and 5.4 TB/s); 1024 tokens, 24 heads of 128, MXFP4: 5.5 and
 // 8.5 us.  Append is held by the quantizer's arithmetic next to the loads
-// (about 300 vector instructions per 8 channels of K and of V, ties included).
+// (about 120 vector instructions per 8 channels of K and as many of V).
 //
 // A block takes one head of 2048 / D consecutive tokens, 8 channels per
 // thread.  K codes are written as they come out, one dword per thread; V codes
@@ -64,45 +64,46 @@ __device__ __forceinline__ float kc_absmax(const float (&f)[8])
 __device__ __forceinline__ float kc_finite(float scale) { return scale < INFINITY ? scale : 0.0f; }
 __device__ __forceinline__ uint32_t kc_finite(uint32_t e8m0) { return min(e8m0, 252u); }
 
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t kc_low_bytes(const uint32_t *w)
+{
+    return __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u) | __builtin_amdgcn_perm(w[3], w[2], 0x04000c0cu);
+}
+
 // Codes of 8 channels, byte i channel i (low nibble) and i + 4 (high).  |q| =
-// rint(|v| / scale) by the reciprocal, exact unless the quotient is within
-// 2^-19 of a half-integer (settled by the exact remainder) or the group needs
-// the exact path's lift.
+// rint(|v| / scale): added to 1.5 2^23 the product with the reciprocal leaves
+// q in the sum's low bits.  The remainder |v| - q scale is exact in one fma, and
+// q is right wherever it lies strictly within half the scale; a group with one
+// that does not (the reciprocal's error, and ties: bf16 values meet these often,
+// one group in seven has a scale that is exact in few bits) moves it by one.
 __device__ __forceinline__ uint32_t kc_int4_codes(const float (&f)[8], float scale)
 {
-    const bool lifted = scale < 7.88860905e-31f;        // 2^-100: exact path only
-    const float inv = scale == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(scale);
-    float q[8], far = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = __builtin_fabsf(f[i]) * inv;    // off by less than 7.5 (2^-23 + 2^-24) < 2^-19
-        q[i] = __builtin_rintf(t);
-        far = fmaxf(far, __builtin_fabsf(t - q[i]));
-    }
-    if (lifted) {
+    constexpr float kMagic = 12582912.0f;
+    uint32_t q[8];
+    if (scale < 7.88860905e-31f) {                      // 2^-100: the exact path's lift
         const Int4Group g = int4_group_prepare(scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = (float)int4_mag(__builtin_fabsf(f[i]), g);
-    } else if (far >= kNearTie) {
-        // the remainder is exact, so its size against half the scale decides
-        // (bf16 values meet ties often: one group in seven has a scale that is
-        // exact in few bits)
+        for (int i = 0; i < 8; ++i) q[i] = int4_mag(__builtin_fabsf(f[i]), g);
+    } else {
+        const float inv = __builtin_amdgcn_rcpf(scale), half = 0.5f * scale;
+        float e[8], far = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float e = __builtin_fmaf(-q[i], scale, __builtin_fabsf(f[i]));
-            const float d = __builtin_fabsf(e) - 0.5f * scale;
-            const bool odd = __builtin_rintf(0.5f * q[i]) * 2.0f != q[i];
-            const bool move = (d > 0.0f) | ((d == 0.0f) & odd);
-            q[i] += move ? __builtin_copysignf(1.0f, e) : 0.0f;
+            const float m = __builtin_fmaf(__builtin_fabsf(f[i]), inv, kMagic);
+            e[i] = __builtin_fmaf(kMagic - m, scale, __builtin_fabsf(f[i]));
+            q[i] = f32_bits(m);
+            far = fmaxf(far, __builtin_fabsf(e[i]));
+        }
+        if (far >= half) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float h = bits_f32(f32_bits(half) - (q[i] & 1u));     // an odd q loses a tie
+                q[i] += (uint32_t)(e[i] > h) - (uint32_t)(e[i] < -h);
+            }
         }
     }
-    uint32_t lo = 0, hi = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo = __builtin_amdgcn_cvt_pk_u8_f32(q[i], i, lo);
-        hi = __builtin_amdgcn_cvt_pk_u8_f32(q[i + 4], i, hi);
-    }
-    return lo | (hi << 4) | ((kc_top_bytes(f) >> 4) & 0x08080808u) | (kc_top_bytes(f + 4) & 0x80808080u);
+    return kc_low_bytes(q) | (kc_low_bytes(q + 4) << 4) | ((kc_top_bytes(f) >> 4) & 0x08080808u) |
+           (kc_top_bytes(f + 4) & 0x80808080u);
 }
 
 // The conversion instruction rounds v / 2^X (exact) to the E2M1 grid, ties to
