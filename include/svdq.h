@@ -566,7 +566,8 @@ svdq_status svdq_lora_plan(const int32_t *index, int M, int n_adapters, void *pl
  *   Y        [M][N] bf16 bits, device (out); may be base itself (rows without
  *            an adapter are then not touched)
  *   work, work_bytes   device scratch of at least svdq_lora_workspace_bytes
- *            bytes, 16-byte aligned, overwritten
+ *            bytes, 16-byte aligned, overwritten (calls, or replays of captured
+ *            ones, that may run at the same time need one each)
  * X A^T is summed in fp32 and enters the second product as a bf16 high and
  * low part (16 bits of significand); that product, the scale and the sum with
  * base are fp32, rounded once to bf16.  A row's result depends on that row
@@ -652,7 +653,9 @@ size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, in
  *                elements (>= heads_q * dim, % 8 == 0)
  *   block_table  [B][table_width] int32, device: the pages of each sequence in
  *                order.  Entries past a sequence's last page are not used; the
- *                keys of an entry outside [0, pages) are left out
+ *                keys of an entry outside [0, pages) are left out.  Pages that
+ *                only hold keys that no row sees (behind a window) may be any,
+ *                of any content
  *   q_start      [B + 1] int32, device, not decreasing: sequence s has the
  *                rows q_start[s] .. q_start[s + 1] - 1 (none: allowed).  Rows
  *                of no sequence keep what O and lse hold
@@ -663,7 +666,7 @@ size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, in
  *   max_q, max_kv  >= 1, the caller's bounds on the rows and keys of a
  *                sequence.  They choose how the work is split, results for
  *                longer sequences are right as well
- *   scale        finite, > 0; multiplies the scores
+ *   scale        > 0, at most 2e38; multiplies the scores
  *   causal       0: a row sees all kv_len keys.  1: row i of n sees the keys
  *                up to place kv_len - n + i, itself included
  *   window       with causal: only the last `window` of these; 0: all
@@ -672,9 +675,11 @@ size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, in
  *                exp(score)
  *   work, work_bytes  device scratch of at least
  *                svdq_kv4_attention_workspace_bytes bytes, 16-byte aligned,
- *                overwritten (NULL when that is 0)
+ *                overwritten (NULL when that is 0; calls, or replays of
+ *                captured ones, that may run at the same time need one each)
  * A row that sees no key gets zeros and lse -inf.  Scores, softmax and sums
- * are fp32; the probabilities (INT4: times V's scale) enter the second
+ * are fp32 (a score, and 256 times the sum of a row's values of V, must stay
+ * within its range); the probabilities (INT4: times V's scale) enter the second
  * product rounded to bf16.  Deterministic for given sizes and bounds.  One
  * kernel launch, two with a split.  Errors: as for svdq_kv4_append, and
  * SVDQ_ERR_INVALID_ARG for a too small workspace (checked after the device).

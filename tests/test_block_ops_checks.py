@@ -215,7 +215,7 @@ def test_kv4_refusals():
     for want, kw in ((INVALID, dict(T=-1)), (INVALID, dict(B=-1)), (INVALID, dict(H=0)), (SHAPE, dict(H=3)),
                      (INVALID, dict(mq=0)), (INVALID, dict(mk=0)), (SHAPE, dict(T=1 << 23)), (SHAPE, dict(B=1 << 24)),
                      (INVALID, dict(scale=0.0)), (INVALID, dict(scale=-1.0)), (INVALID, dict(scale=float("nan"))),
-                     (INVALID, dict(scale=float("inf"))), (INVALID, dict(causal=2)), (INVALID, dict(window=-1)),
+                     (INVALID, dict(scale=float("inf"))), (INVALID, dict(scale=2.1e38)), (INVALID, dict(causal=2)), (INVALID, dict(window=-1)),
                      (INVALID, dict(causal=0, window=3)), (SHAPE, dict(ldq=248)), (SHAPE, dict(ldq=260)),
                      (INVALID, dict(width=0)), (SHAPE, dict(width=1 << 27)), (INVALID, dict(Q=None)),
                      (INVALID, dict(table=None)), (INVALID, dict(start=None)), (INVALID, dict(kv=None)),
@@ -228,7 +228,8 @@ def test_kv4_binding_checks():
     c = svdq.Kv4Cache(4, 16, 2, 64, svdq.INT4, device="cpu")
     assert c.k_codes.numel() == c.v_codes.numel() == 4 * 2 * 16 * 32 and c.k_scales.dtype is F32
     assert svdq.Kv4Cache(4, 16, 2, 64, svdq.MXFP4, device="cpu").v_scales.numel() == 4 * 2 * 16 * 2
-    for kw in (dict(pages=0), dict(page_size=24), dict(heads=0), dict(dim=32), dict(prec=5)):
+    for kw in (dict(pages=0), dict(page_size=24), dict(heads=0), dict(dim=32), dict(prec=5),
+               dict(pages=1 << 27), dict(heads=65536)):
         with pytest.raises(ValueError):
             svdq.Kv4Cache(**dict(dict(pages=4, page_size=16, heads=2, dim=64, prec=0, device="cpu"), **kw))
     K, s = z(5, 2, 64), z(5, dtype=I32)

@@ -803,6 +803,8 @@ class Kv4Cache:
             raise ValueError(f"dim must be 64 or 128, got {dim}")
         if pages < 1 or heads < 1:
             raise ValueError("a cache has at least one page and one head")
+        if pages * page_size > 0x7FFFFFFF or heads > 65535:
+            raise ValueError(f"{pages} pages of {page_size} tokens and {heads} heads are more than a cache takes")
         self.pages, self.page_size, self.heads, self.dim, self.prec = pages, page_size, heads, dim, prec
         g = dim // group_of(prec)
         sdt = torch.float32 if prec == INT4 else torch.uint8

@@ -504,7 +504,7 @@ extern "C" svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uin
     if (st != SVDQ_OK) return st;
     st = check_kv4_attention(c, T, B, heads_q, max_q, max_kv);
     if (st != SVDQ_OK) return st;
-    if (!(scale > 0.0f) || scale > 3.0e38f || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
+    if (!(scale > 0.0f) || scale > 2.0e38f || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
         return SVDQ_ERR_INVALID_ARG;
     if (!kv4_stride_ok(ldq, heads_q, c.dim)) return SVDQ_ERR_SHAPE;
     if (table_width < 1) return SVDQ_ERR_INVALID_ARG;
