@@ -44,8 +44,8 @@
 //   75 us for 335 MB = 4.5 TB/s (a large copy: 5.4 TB/s).  Bound by HBM; the
 //   first form, with codes in token order and block tables in vector loads,
 //   took 109 us.
-//   4608 rows over 4608 keys, 24 heads: D = 128 MXFP4 292 us = 893 TFLOP/s,
-//   INT4 404 us; D = 64 213 and 277 us.  Bound by instruction issue: a step of a
+//   4608 rows over 4608 keys, 24 heads: D = 128 MXFP4 288 us = 906 TFLOP/s,
+//   INT4 399 us; D = 64 208 and 265 us.  Bound by instruction issue: a step of a
 //   wave issues 64 (32) matrix instructions, 32 exponentials and about 210
 //   other vector instructions, which the products do not hide (a matrix
 //   instruction holds the port for half of its time), and by the 864 tiles over
@@ -151,7 +151,7 @@ struct KvArgs {
     uint16_t *O;
     float *lse, *work;
     int64_t ldq;
-    int T, B, heads_q, group, table_width, q_tiles, splits, split_steps, causal, window;
+    int T, B, heads_q, group, table_width, q_tiles, splits, split_steps, causal, window, cus;
     float scale;
 };
 
@@ -994,6 +994,13 @@ __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_c
     KvRows<D, CT> w;
     ka_rows<D, INT4, CT>(w, a, head, qs, qn, kv, r0 + 16 * CT * wave, rows, lane);
     const KvRange g = ka_range(a, split, qn, kv, r0, min(r0 + 64 * CT, rows));
+    // Two blocks share a compute unit, so two waves a SIMD.  Blocks go out one per
+    // compute unit at first: every other round of them gets precedence, and its
+    // waves' waits are filled by the other's instead of both waiting in step
+    // (4608 x 4608, 24 heads: MXFP4 300 -> 288 us, D = 64 218 -> 208; INT4 414
+    // -> 399, 277 -> 265; by wave slots, which mixes a block's waves, slower than
+    // without).
+    if ((blockIdx.x / (uint32_t)a.cus) & 1) __builtin_amdgcn_s_setprio(2);
     ka_walk_shared<D, INT4, CT>(w, lds, a, table, head, g, a.scale * kLog2e, wave, lane);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
@@ -1153,6 +1160,7 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
     a.c = c, a.Q = Q, a.ldq = ldq, a.table = table, a.q_start = q_start, a.kv_len = kv_len, a.O = O, a.lse = lse;
     a.work = work, a.T = T, a.B = B, a.heads_q = heads_q, a.group = heads_q / c.heads, a.table_width = table_width;
     a.q_tiles = p.q_tiles, a.splits = p.splits, a.split_steps = p.split_steps, a.causal = causal, a.window = window, a.scale = scale;
+    a.cus = device_cu_count();
     const dim3 grid((uint32_t)((int64_t)p.q_tiles * p.splits * B * c.heads));
 #define KA_LAUNCH(D, I) \
     (p.many ? kv4_attention_kernel<D, I, kManyTiles><<<grid, 256, 0, stream>>>(a) \
