@@ -48,16 +48,16 @@
 //   INT4 399 us; D = 64 208 and 265 us.  Bound by instruction issue: a step of a
 //   wave issues 64 (32) matrix instructions, 32 exponentials and about 210
 //   other vector instructions, which the products do not hide (a matrix
-//   instruction holds the port for half of its time; one block fills a compute
-//   unit's port: INT4, D = 64, 512 blocks of 30 steps take 72 us, 256 of 60
-//   steps 77), and by the 864 tiles over 256 units.  Before scores, exponentials and conversions were interleaved:
+//   instruction holds the port for half of its time), and by the 864 tiles over
+//   512 places.  Before scores, exponentials and conversions were interleaved:
 //   340 us; before the shared conversion: 445 us.
 //   One token over 1000 keys, 32 heads over 8: 7.6 + 2.6 us, latencies of the
 //   dependent loads (lengths, table, codes) and of the second launch.
 //   8 sequences of 1 .. 700 rows over up to 6000 keys, 16 heads over 4 of 64,
-//   INT4, causal: 106 us = 281 TFLOP/s; three pieces of about 20 steps per unit,
-//   four on the busiest.
-// Not kept: 48 and 64 rows per wave and three waves per SIMD (spills), a branch
+//   INT4, causal: 106 us = 281 TFLOP/s; some 780 pieces of about 20 steps over
+//   512 places, two rounds.
+// Not kept: 48 rows per wave and three waves per SIMD (spills), 64 rows and one
+// wave per SIMD (443 us: nothing beside a wave's waits), a branch
 // around the rescaling per column (copies of the sums), ordering hints instead
 // of fences (the compiler regrouped the pieces), several heads per block.
 #include "kv4.h"
