@@ -187,3 +187,41 @@ def test_decoding_step_in_a_graph(prec):
         full = [p for i, h in enumerate(have) for p in table[i, :(h + n) // P].tolist()]
         for x, y in ((b.cache.k_codes, e.cache.k_codes), (b.cache.v_codes, e.cache.v_codes)):
             assert torch.equal(x[full], y[full])
+
+
+@pytest.mark.parametrize("prec", PRECS)
+def test_two_batches_on_two_streams(prec):
+    """Two batches through blocks of their own at once, one per stream, a long
+    prompt beside single tokens: each as alone."""
+    H, D, P = 4, 64, 32
+    jobs = []
+    for n, (new, have) in enumerate([([300, 40], [300, 40]), ([1, 1, 1], [900, 33, 1])]):
+        B = len(new)
+        table = torch.arange(B * 32, dtype=I32, device="cuda").view(B, 32)
+        blocks = [Block(prec, H, D, 3, B * 32, P, seed=n) for _ in range(2)]
+        for b in blocks:
+            for i, (k, h) in enumerate(zip(new, have)):
+                p = torch.arange(h - k, device="cuda")
+                svdq.kv4_append(b.cache, kv4._rand(i, h - k, H, D), kv4._rand(i + 9, h - k, H, D),
+                                (table[i][p // P] * P + p % P).to(I32))
+        request = torch.cat([torch.full((k,), i, dtype=I32) for i, k in enumerate(new)]).cuda()
+        place = torch.cat([torch.arange(h - k, h) for k, h in zip(new, have)]).cuda()
+        slots = (table[request.long(), place // P] * P + place % P).to(I32)
+        r, mods = _inputs(n, len(request), H * D, B)
+        args = (r, mods, request, (request % 4 - 1).to(I32), slots, table, _ints(*np.cumsum([0] + new).tolist()),
+                _ints(*have), max(new), max(have))
+        jobs.append((blocks, args))
+    want = [blocks[0].step(*args) for blocks, args in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[n].append(jobs[n][0][1].step(*jobs[n][1]))
+    for s in streams:
+        s.synchronize()
+    for n in range(2):
+        for v in got[n]:
+            for k in want[n]:
+                assert torch.equal(v[k], want[n][k]), (n, k)
