@@ -61,6 +61,7 @@
 // around the rescaling per column (copies of the sums), ordering hints instead
 // of fences (the compiler regrouped the pieces), several heads per block.
 #include "kv4.h"
+#include "kv4_plan.h"
 
 namespace svdq {
 namespace {
@@ -74,7 +75,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLazy = 8.0f;
-constexpr int kManyTiles = 2;        // 16-row tiles per wave of a block of many rows
 
 __device__ __forceinline__ uint32_t ka_pack2(float lo, float hi)
 {
@@ -1096,58 +1096,11 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
     if (c == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : mx + kLn2 * __builtin_amdgcn_logf(sum);
 }
 
-// Form, tiles of rows and splits of the keys, from the sizes and the caller's
-// bounds.
-struct KvPlan {
-    bool many;
-    int q_tiles, splits, split_steps;             // a split's least length (many rows: its length within the bound)
-};
-
-KvPlan ka_plan(int T, int B, int heads, int group, int max_q, int max_kv)
-{
-    KvPlan p;
-    const int64_t rows = (int64_t)(max_q < T ? max_q : T) * group;
-    const int cus = device_cu_count();
-    p.many = rows > 16;
-    const int block_rows = p.many ? 64 * kManyTiles : 16;
-    const int64_t tiles = (rows + block_rows - 1) / block_rows;
-    // blocks of rows: at most every sequence's, and the rows' own number and one more per sequence
-    int64_t blocks = (int64_t)T * group / block_rows + B;
-    blocks = (blocks < tiles * B ? blocks : tiles * B) * heads;
-    // Splits.  Many rows: none where the rows alone give two blocks per compute
-    // unit (a split writes and reads their fp32 sums), else about four blocks (8
-    // sequences of 1 .. 700 rows over up to 6000 keys, 16 heads over 4: 2 blocks
-    // 129 us, 3 124, 4 107, 6 107, 8 115), of at least four steps.
-    // Few rows: none up to 12 steps (700 keys: 10.1 us, split 10.6); up to a block
-    // per compute unit of at least four steps, one per wave (8000 keys, 8 heads:
-    // 9.3 us, of eight 10.9); beyond that up to six of at least 16 (2 x 16000
-    // keys: 17 us, of four steps 25).  Sequences shorter than the bound take as
-    // many parts of that least length (one of 1500 keys under a bound of 32768:
-    // 10.3 us, in parts of the bound's length 13.0).
-    const int64_t steps = ((int64_t)max_kv + 63) / 64;
-    auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-    auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
-    int64_t s, least_steps = 0;
-    if (p.many) {
-        s = blocks >= 2 * (int64_t)cus ? 1 : least(up(steps, 4), up(4 * (int64_t)cus, blocks));
-    } else {
-        const int64_t a = least(up(steps, 4), up(cus, blocks)), b = least(up(steps, 16), up(6 * (int64_t)cus, blocks));
-        s = steps <= 12 ? 1 : (a > b ? a : b), least_steps = a >= b ? 4 : 16;
-    }
-    s = s > 64 ? 64 : s;
-    p.split_steps = (int)((steps + s - 1) / s + 3) & ~3;
-    p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
-    if (!p.many) p.split_steps = (int)least_steps;
-    const int64_t cap = (int64_t)(1 << 24) / ((int64_t)B * heads * p.splits) + 1;    // grid; further tiles in a loop
-    p.q_tiles = (int)(tiles > cap ? cap : tiles);
-    return p;
-}
-
 }  // namespace
 
 size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv)
 {
-    const KvPlan p = ka_plan(T, B, heads, heads_q / heads, max_q, max_kv);
+    const KvPlan p = kv4_plan(T, B, heads, heads_q / heads, max_q, max_kv, device_cu_count());
     return p.splits > 1 ? (size_t)p.splits * T * heads_q * (dim + 2) * sizeof(float) : 0;
 }
 
@@ -1156,15 +1109,16 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
                                 int max_kv, float scale, int causal, int window, uint16_t *O, float *lse, float *work,
                                 hipStream_t stream)
 {
-    const KvPlan p = ka_plan(T, B, c.heads, heads_q / c.heads, max_q, max_kv);
+    const int cus = device_cu_count();
+    const KvPlan p = kv4_plan(T, B, c.heads, heads_q / c.heads, max_q, max_kv, cus);
     KvArgs a{};
     a.c = c, a.Q = Q, a.ldq = ldq, a.table = table, a.q_start = q_start, a.kv_len = kv_len, a.O = O, a.lse = lse;
     a.work = work, a.T = T, a.B = B, a.heads_q = heads_q, a.group = heads_q / c.heads, a.table_width = table_width;
     a.q_tiles = p.q_tiles, a.splits = p.splits, a.split_steps = p.split_steps, a.causal = causal, a.window = window, a.scale = scale;
-    a.cus = device_cu_count();
-    const dim3 grid((uint32_t)((int64_t)p.q_tiles * p.splits * B * c.heads));
+    a.cus = cus;
+    const dim3 grid((uint32_t)kv4_blocks(p, B, c.heads));
 #define KA_LAUNCH(D, I) \
-    (p.many ? kv4_attention_kernel<D, I, kManyTiles><<<grid, 256, 0, stream>>>(a) \
+    (p.many ? kv4_attention_kernel<D, I, kKv4ManyTiles><<<grid, 256, 0, stream>>>(a) \
             : kv4_attention_kernel<D, I, 0><<<grid, 256, 0, stream>>>(a))
     if (c.int4 && c.dim == 64) KA_LAUNCH(64, true);
     else if (c.int4) KA_LAUNCH(128, true);
