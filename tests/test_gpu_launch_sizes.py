@@ -33,3 +33,17 @@ def test_attention_of_many_sequences_under_a_loose_bound(prec):
     x.update(table=table, q_start=q_start, kv_len=kv_len)
     out, lse = _call(x, max_q=2 ** 31 - 1)
     _verify(x, out, lse, True, 0, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("M", [2 ** 26 + 5, 2 ** 27 - 1])
+def test_residual_norm_of_many_short_rows(M):
+    """8 channels, four rows per block: 2^24 blocks and more.  Rows do not
+    depend on each other, so two calls of half the rows give the same bits."""
+    _say(f"residual_norm of {M} rows")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    r, y = (torch.randn(M, 8, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    got = svdq.residual_norm(r, y, post=svdq.NORM_RMS, pre=svdq.NORM_LAYER)
+    half = M // 2
+    for rows in (slice(0, half), slice(half, M)):
+        want = svdq.residual_norm(r[rows], y[rows], post=svdq.NORM_RMS, pre=svdq.NORM_LAYER)
+        assert torch.equal(got[0][rows], want[0]) and torch.equal(got[1][rows], want[1])

@@ -24,3 +24,7 @@ def _run(source, tmp_path):
 
 def test_attention_launches(tmp_path):
     _run("kv4_plan_check.cpp", tmp_path)
+
+
+def test_residual_norm_launches(tmp_path):
+    _run("launch_grid_check.cpp", tmp_path)

@@ -2,12 +2,11 @@
 // arithmetic alone: it needs no HIP header.
 #pragma once
 
-#include <stdint.h>
+#include "launch_grid.h"
 
 namespace svdq {
 
 constexpr int kKv4ManyTiles = 2;                  // 16-row tiles per wave of a block of many rows
-constexpr int64_t kKv4MaxBlocks = (1 << 24) - 1;  // of 256 threads, in one launch
 
 // Form, tiles of rows and splits of the keys, from the sizes and the caller's
 // bounds.
@@ -51,7 +50,7 @@ inline KvPlan kv4_plan(int T, int B, int heads, int group, int max_q, int max_kv
     p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
     if (!p.many) p.split_steps = (int)least_steps;
     // the runtime takes fewer than 2^32 threads along x; a block takes further tiles in a loop
-    const int64_t cap = kKv4MaxBlocks / ((int64_t)B * heads * p.splits);
+    const int64_t cap = kMaxBlocks / ((int64_t)B * heads * p.splits);
     p.q_tiles = (int)(tiles > cap ? cap : tiles);
     return p;
 }

@@ -19,6 +19,7 @@
 // (with conditions on the loads: 61 us).  1337 x 2560, fp32 stream, a norm on
 // both sides: 11 us = 3.7 TB/s, five rows per compute unit and two sums in turn.
 // One row of 4096: 3 us, the launch and three dependent passes of sums.
+#include "launch_grid.h"
 #include "svdq_internal.h"
 #include "svdq_quant.h"
 
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(Residu
     __shared__ float red[T < 256 ? 1 : T / 64];
     constexpr int ROWS = T < 256 ? 256 / T : 1;
     const int t = threadIdx.x % T;
-    const int m = blockIdx.x * ROWS + threadIdx.x / T;
+    const int m = (int)(blockIdx.y * a.grid_x + blockIdx.x) * ROWS + threadIdx.x / T;
     if (m >= a.M) return;                           // whole waves (T = 64) or none (one row per block)
     const int D = a.D;
     const float inv_d = 1.0f / (float)D;
@@ -229,10 +230,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(Residu
 }
 
 template <int T, int C>
-hipError_t rn_launch(const ResidualNormArgs &a, bool fp32, hipStream_t stream)
+hipError_t rn_launch(ResidualNormArgs a, bool fp32, hipStream_t stream)
 {
     const int rows = T < 256 ? 256 / T : 1;
-    const dim3 grid((a.M + rows - 1) / rows), block(T < 256 ? 256 : T);
+    const LaunchGrid g = launch_grid(((int64_t)a.M + rows - 1) / rows);
+    const dim3 grid(g.x, g.y), block(T < 256 ? 256 : T);
+    a.grid_x = (int)g.x;
     if (fp32) residual_norm_kernel<T, C, true><<<grid, block, 0, stream>>>(a);
     else residual_norm_kernel<T, C, false><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();

@@ -88,6 +88,7 @@ struct ResidualNormArgs {
     void *r_out;
     uint16_t *x;
     int M, D, post, pre, mod_rows, mod_stride, rows_per_mod;
+    int grid_x;                     // blocks along x, set by the launch
     float alpha, eps;
 };
 hipError_t launch_residual_norm(const ResidualNormArgs &a, bool fp32, hipStream_t stream);
