@@ -212,9 +212,10 @@ __device__ __forceinline__ void lr_down(f32x4 (&acc)[4][NT], uint8_t *lds, const
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue(st0 + i);
     for (int st = st0; st < st1; ++st) {
-        // this wave's loads of the stage have landed; after the barrier all
-        // waves' have, and all are done with the stage before
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 2) * (XL + AL)) : "memory");
+        // this wave's loads of the stage have landed and its reads of the stage
+        // before, which the next loads overwrite, are complete; after the
+        // barrier all waves' are
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * (XL + AL)) : "memory");
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         issue(st + S - 1);
