@@ -723,6 +723,8 @@ def lora_plan(index, n_adapters: int, plan: Optional[LoraPlan] = None, stream=No
     if plan is None:
         need = lib().svdq_lora_plan_bytes(M, n_adapters)
         plan = LoraPlan(_empty(max(need, 16), torch.uint8, index.device, stream), M, n_adapters)
+    elif not isinstance(plan, LoraPlan):
+        raise TypeError("plan must be a LoraPlan (lora_plan)")
     elif plan.M != M or plan.n_adapters != n_adapters:
         raise ValueError(f"plan is for {plan.M} rows and {plan.n_adapters} adapters, not {M} and {n_adapters}")
     dev = index.device
