@@ -534,6 +534,8 @@ def nf4_w4a16_linear(X, wq, qabs, chunk, bias=None, Y=None, stream=None):
 # need are looked up once.
 
 _T = None        # torch, after the first call
+_I32 = 0x7FFFFFFF          # the largest size the C interface takes (ctypes passes the low 32 bits of a larger one on)
+_ELEMENTS = 1 << 30        # SVDQ_MAX_ELEMENTS
 
 
 def _tt():
@@ -644,6 +646,8 @@ def residual_norm(r, y=None, gate=None, alpha: float = 1.0, post: int = NORM_NON
     shape, dev = r.shape, r.device
     M, D = shape
     _arg(r, stype, "r")
+    if r.numel() >= _ELEMENTS:
+        raise SvdqError(-2, "svdq_residual_norm")
     pY = pO = pX = pG = pS = pH = pPost = pPre = pBias = pI = None
     if y is not None:
         pY = _arg(y, bf, "y", shape).data_ptr()
@@ -700,6 +704,8 @@ def _mod_rows(D, gate, scale, shift):
                 raise ValueError("gate, scale and shift must have the same row stride")
             ld = stride
         sets += 1
+    if B > _I32 or ld > _I32:
+        raise SvdqError(-2, "svdq_residual_norm")
     return B, ld
 
 
@@ -720,6 +726,8 @@ def lora_plan(index, n_adapters: int, plan: Optional[LoraPlan] = None, stream=No
     _ndim(index, 1, "index")
     _arg(index, torch.int32, "index")
     M = index.shape[0]
+    if M > _I32 or not 0 < n_adapters <= _I32:
+        raise SvdqError(-2 if M > _I32 else -4, "svdq_lora_plan")
     if plan is None:
         need = lib().svdq_lora_plan_bytes(M, n_adapters)
         plan = LoraPlan(_empty(max(need, 16), torch.uint8, index.device, stream), M, n_adapters)
@@ -765,6 +773,8 @@ def lora_linear(X, A, B, scale, plan: LoraPlan, base, Y=None, work=None, stream=
     _arg(B, bf, "B", (n, N, R))
     _arg(scale, torch.float32, "scale", (n,))
     _arg(base, bf, "base", (M, N))
+    if X.numel() >= _ELEMENTS or A.numel() >= _ELEMENTS or B.numel() >= _ELEMENTS or base.numel() >= _ELEMENTS:
+        raise SvdqError(-2, "svdq_lora_linear")
     if not isinstance(plan, LoraPlan):
         raise TypeError("plan must be a LoraPlan (lora_plan)")
     if plan.M != M or plan.n_adapters != n:
@@ -889,8 +899,15 @@ def kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
     return K, V
 
 
+def _bound(v):
+    """A bound on lengths (int32 on the device): a larger one is as loose as
+    the largest; 0, which the library refuses, for a negative one."""
+    return v if 0 <= v <= _I32 else (_I32 if v > 0 else 0)
+
+
 def kv4_attention_workspace_bytes(cache: Kv4Cache, T: int, B: int, heads_q: int, max_q: int, max_kv: int) -> int:
     """Device scratch bytes that kv4_attention needs for these sizes."""
+    max_q, max_kv = _bound(max_q), _bound(max_kv)
     return int(lib().svdq_kv4_attention_workspace_bytes(cache._ref, T, B, heads_q, max_q, max_kv))
 
 
@@ -922,6 +939,11 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
     B, width = block_table.shape
     _arg(q_start, i32, "q_start", (B + 1,))
     _arg(kv_len, i32, "kv_len", (B,))
+    if B > _I32 or width > _I32:
+        raise SvdqError(-2, "svdq_kv4_attention")
+    if window < 0:
+        raise SvdqError(-1, "svdq_kv4_attention")
+    max_q, max_kv = _bound(max_q), _bound(max_kv)
     out = _empty((T, H, D), torch.bfloat16, dev, stream, Q) if out is None else _arg(
         out, torch.bfloat16, "out", (T, H, D))
     if lse is not None:
@@ -935,7 +957,7 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
                   (Q, block_table, q_start, kv_len, out, lse, work), stream)
     st = lib().svdq_kv4_attention(cache._ref, Q.data_ptr(), ldq, block_table.data_ptr(), width, q_start.data_ptr(),
                                   kv_len.data_ptr(), B, T, H, max_q, max_kv, D ** -0.5 if scale is None else scale,
-                                  1 if causal else 0, min(window, 0x7FFFFFFF), out.data_ptr(), _ptr(lse), _ptr(work),
+                                  1 if causal else 0, min(window, _I32), out.data_ptr(), _ptr(lse), _ptr(work),
                                   0 if work is None else work.numel(), raw)
     if st:
         raise SvdqError(st, "svdq_kv4_attention")
