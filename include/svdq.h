@@ -571,7 +571,9 @@ svdq_status svdq_lora_plan(const int32_t *index, int M, int n_adapters, void *pl
  * X A^T is summed in fp32 and enters the second product as a bf16 high and
  * low part (16 bits of significand); that product, the scale and the sum with
  * base are fp32, rounded once to bf16.  A row's result depends on that row
- * and the sizes alone, so it is deterministic.  Two kernel launches.  Errors:
+ * and the sizes alone, so it is deterministic.  The work is divided for the
+ * most tiles that M and n_adapters allow, so A and B of the adapters in use
+ * alone take less time than a large pool's.  Two kernel launches.  Errors:
  * SVDQ_ERR_INVALID_ARG (a too small workspace among them, checked after the
  * device), SVDQ_ERR_SHAPE, SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_MISALIGNED,
  * SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
@@ -678,8 +680,8 @@ size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, in
  *                overwritten (NULL when that is 0; calls, or replays of
  *                captured ones, that may run at the same time need one each)
  * A row that sees no key gets zeros and lse -inf.  Scores, softmax and sums
- * are fp32 (a score, and 256 times the sum of a row's values of V, must stay
- * within its range); the probabilities (INT4: times V's scale) enter the second
+ * are fp32 (a score must stay below 2e38 in magnitude, 256 times the sum of a
+ * row's values of V within the range of fp32); the probabilities (INT4: times V's scale) enter the second
  * product rounded to bf16.  Deterministic for given sizes and bounds.  One
  * kernel launch, two with a split.  Errors: as for svdq_kv4_append, and
  * SVDQ_ERR_INVALID_ARG for a too small workspace (checked after the device).

@@ -924,8 +924,8 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
     [T][heads_q][dim] bf16; block_table [B][pages per sequence], q_start [B +
     1] and kv_len [B] int32; max_q and max_kv bound the rows and keys of a
     sequence and choose how the work is split.  scale defaults to dim^-0.5.
-    Returns out (bf16, Q's shape); lse [T][heads_q] fp32 is written when
-    given.  When `work` is None it is allocated with torch."""
+    Returns out (bf16, Q's shape; rows of no sequence keep what it holds,
+    anything in a new one); lse [T][heads_q] fp32 is written when given.  When `work` is None it is allocated with torch."""
     torch = _tt()
     i32 = torch.int32
     dev = _cache_arg(cache)

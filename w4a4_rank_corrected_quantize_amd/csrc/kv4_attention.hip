@@ -39,22 +39,23 @@
 // splits' sums then go to the workspace and a second kernel adds them in split
 // order.
 //
-// What bounds it, and what it measured (both kernels):
-//   32 x 4097 .. 16384 keys, 32 heads over 8 of 128, MXFP4, one token each:
-//   75 us for 335 MB = 4.5 TB/s (a large copy: 5.4 TB/s).  Bound by HBM; the
-//   first form, with codes in token order and block tables in vector loads,
-//   took 109 us.
-//   4608 rows over 4608 keys, 24 heads: D = 128 MXFP4 288 us = 906 TFLOP/s,
-//   INT4 399 us; D = 64 208 and 265 us.  Bound by instruction issue: a step of a
+// What bounds it, and what it measured (both kernels, in a captured graph):
+//   32 x 4097 .. 16384 keys, 32 heads over 8 of 128, one token each: MXFP4 76 us
+//   for 335 MB = 4.4 TB/s (a large copy: 5.4 TB/s), INT4 81 us for 355 MB.  Bound
+//   by HBM; the first form, with codes in token order and block tables in vector
+//   loads, took 109 us (MXFP4).
+//   4608 rows over 4608 keys, 24 heads: D = 128 MXFP4 290 us = 900 TFLOP/s,
+//   INT4 375 us; D = 64 203 and 238 us; causal, 32 heads over 8 of 128: 190 and
+//   237 us.  Bound by instruction issue: a step of a
 //   wave issues 64 (32) matrix instructions, 32 exponentials and about 210
 //   other vector instructions, which the products do not hide (a matrix
 //   instruction holds the port for half of its time), and by the 864 tiles over
 //   512 places.  Before scores, exponentials and conversions were interleaved:
 //   340 us; before the shared conversion: 445 us.
-//   One token over 1000 keys, 32 heads over 8: 7.6 + 2.6 us, latencies of the
+//   One token over 1000 keys, 32 heads over 8: 7.7 + 2.6 us, latencies of the
 //   dependent loads (lengths, table, codes) and of the second launch.
 //   8 sequences of 1 .. 700 rows over up to 6000 keys, 16 heads over 4 of 64,
-//   INT4, causal: 106 us = 281 TFLOP/s; some 780 pieces of about 20 steps over
+//   INT4, causal: 103 us = 288 TFLOP/s; some 780 pieces of about 20 steps over
 //   512 places, two rounds.
 // Not kept: 48 rows per wave and three waves per SIMD (spills), 64 rows and one
 // wave per SIMD (443 us: nothing beside a wave's waits), a branch

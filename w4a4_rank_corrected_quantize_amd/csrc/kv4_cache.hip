@@ -4,9 +4,9 @@
 // Codes and scales are those of the library's group quantizers (svdq_quant.h)
 // along the head's channels, bit for bit.  Bound by HBM: append reads 4 bytes
 // (K and V in bf16) and writes about 1.1 bytes per channel, read the reverse
-// with fp32 values.  4608 tokens, 32 heads of 64, INT4: 14 us for 48 MB and 16
-// us for 86 MB (3.5 and 5.4 TB/s); 1024 tokens, 24 heads of 128, MXFP4: 5.5 and
-// 8.5 us.  Append is held by the quantizer's arithmetic next to the loads
+// with fp32 values.  4608 tokens, 32 heads of 64, INT4: 13 us for 48 MB and 16
+// us for 86 MB (3.7 and 5.4 TB/s), MXFP4 11 and 17 us; 1024 tokens, 24 heads of
+// 128, MXFP4: 4.5 and 8.6 us.  Append is held by the quantizer's arithmetic next to the loads
 // (about 120 vector instructions per 8 channels of K and as many of V).
 //
 // A block takes one head of 2048 / D consecutive tokens, 8 channels per

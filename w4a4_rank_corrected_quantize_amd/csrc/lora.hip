@@ -6,8 +6,10 @@
 // the rows adapter by adapter in tiles of at most 64 rows of one adapter; the
 // rows without an adapter form the last tiles (adapter -1).
 //
-// Two kernels, both bound by HBM (rank 64 does 2 R (K + N) / (2 K + 4 N) = 32
-// operations per byte, the chip's ratio is about 240):
+// Two kernels, both bound by HBM (rank 64 does 2 R (K + N) / (2 K + 4 N)
+// operations per byte: 32 for N >> K, 37 at 4096 -> 12288, 43 at N = K; the
+// second product runs twice, with the high and the low part of h; the chip's
+// ratio is about 240):
 //   down  a block takes one tile and one slice of K.  X and A_a go to LDS by
 //         DMA in stages of 128 channels, three stages ahead of the products;
 //         the four waves multiply a quarter of a stage each and add their fp32
@@ -21,9 +23,12 @@
 //         128 in turn; the products with B_a accumulate in fp32, base is added
 //         in fp32 and the row is rounded once.
 // 9216 rows, 4096 -> 12288, rank 64: 118 us for 533 MB = 4.5 TB/s, where a copy
-// of that size reaches 5.4 TB/s (128 channels per block: 139 us).  16 rows of
-// 16 adapters, 4096 -> 4096, rank 16: 4.4 + 4.0 us, latencies of the dependent
-// loads (plan, rows, operands) and of two launches.
+// of that size reaches 5.4 TB/s (128 channels per block: 139 us); rank 128: 140
+// us.  16 rows of 16 adapters, 4096 -> 4096, rank 16: 4.3 + 4.2 us, latencies of
+// the dependent loads (plan, rows, operands) and of two launches.  K and the
+// widths are divided for the most tiles that rows and pool allow (the tiles in
+// use are known on the device alone): 256 rows of one adapter take 9.5 us with a
+// pool of 1 and 19.8 with one of 256.
 // The order of every sum depends on the sizes alone, so results do not depend
 // on which rows share a tile.
 #include "svdq_internal.h"

@@ -15,8 +15,9 @@
 // vectors are shared by many rows and come from the L2.  Rows of up to 1024
 // channels take a wave each (no barrier), longer ones a block of four; a row
 // stays in registers between its sums.  9216 x 4096 bf16, LayerNorm and
-// modulation: 52 us in the kernel for 302 MB = 5.8 TB/s, a large copy's rate
-// (with conditions on the loads: 61 us).  1337 x 2560, fp32 stream, a norm on
+// modulation: 53 us in the kernel for 302 MB = 5.7 TB/s (a large copy: 5.4; the
+// last-level cache keeps part of the buffers from pass to pass; with conditions
+// on the loads: 61 us); fp32 stream, a norm on both sides: 88 us for 453 MB.  1337 x 2560, fp32 stream, a norm on
 // both sides: 11 us = 3.7 TB/s, five rows per compute unit and two sums in turn.
 // One row of 4096: 3 us, the launch and three dependent passes of sums.
 #include "launch_grid.h"
