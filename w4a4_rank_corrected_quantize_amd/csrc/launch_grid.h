@@ -8,7 +8,7 @@ namespace svdq {
 
 constexpr int64_t kMaxBlocks = (1 << 24) - 1;     // of 256 threads along x: fewer than 2^32 threads
 
-// At least `blocks` blocks of 256 threads as y rows of x; one row where that does.
+// At least `blocks` blocks of 256 threads, as y rows of x; y is 1 up to kMaxBlocks.
 struct LaunchGrid {
     uint32_t x, y;
 };
