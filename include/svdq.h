@@ -53,14 +53,15 @@
  *   - Device calls (svdq_quantize_act, svdq_w4a4_linear,
  *     svdq_w4a4_linear_requant, svdq_w4a4_linear_splitk,
  *     svdq_w4a4_linear_qkv_norm_rope, svdq_awq_w4a16_linear,
- *     svdq_residual_norm, svdq_lora_*, svdq_kv4_*) take device
+ *     svdq_residual_norm, svdq_lora_*, svdq_rope_table, svdq_qk_norm_rope,
+ *     svdq_kv4_*) take device
  *     pointers and a hipStream_t (as void*, NULL = the null stream); they
  *     validate everything first, enqueue kernels on `stream` and return
  *     without synchronizing.  On any error nothing has been enqueued or
  *     written.  The current HIP device must be a gfx950; otherwise
  *     SVDQ_ERR_UNSUPPORTED_DEVICE is returned and nothing runs.
  *   - Host calls (svdq_pack_weights, svdq_pack_residual,
- *     svdq_awq_pack_weights) take host pointers,
+ *     svdq_awq_pack_weights, svdq_rope_frequencies) take host pointers,
  *     run synchronously on the CPU and need no GPU.
  *   - Device pointers must be 16-byte aligned, int32 index arrays 4-byte
  *     aligned (SVDQ_ERR_MISALIGNED).  A buffer whose size is zero (M == 0 or
@@ -119,6 +120,22 @@ typedef enum svdq_stream_type {
     SVDQ_STREAM_FP32 = 1,
     SVDQ_STREAM_INT_RANGE_ = 0x7FFFFFFF      /* not a type: every int is a valid value (calls reject it) */
 } svdq_stream_type;
+
+/* Which channels of a head form the pairs that a rotation turns. */
+typedef enum svdq_rope_pairs {
+    SVDQ_ROPE_ADJACENT = 0,   /* pair p: channels 2 p and 2 p + 1 */
+    SVDQ_ROPE_HALVES = 1,     /* pair p: channels p and pairs + p */
+    SVDQ_ROPE_PAIRS_INT_RANGE_ = 0x7FFFFFFF  /* not a form: every int is a valid value (calls reject it) */
+} svdq_rope_pairs;
+
+/* How several axes share a head's pairs (sections[a] pairs of axis a, n in all). */
+typedef enum svdq_rope_axes {
+    SVDQ_ROPE_AXES_BLOCKS = 0,      /* runs of pairs, each with frequencies of its own: theta^(-j / sections[a]) */
+    SVDQ_ROPE_AXES_SECTIONS = 1,    /* runs of pairs, the frequencies falling over all: theta^(-p / n) */
+    SVDQ_ROPE_AXES_INTERLEAVED = 2, /* pair p: axis p % axes while p / axes is below that axis' number of pairs,
+                                       else axis 0; theta^(-p / n) */
+    SVDQ_ROPE_AXES_INT_RANGE_ = 0x7FFFFFFF   /* not a layout: every int is a valid value (calls reject it) */
+} svdq_rope_axes;
 
 #define SVDQ_RANK 32
 
@@ -583,6 +600,74 @@ svdq_status svdq_lora_linear(const uint16_t *X, const uint16_t *A, const uint16_
                              uint16_t *Y, void *work, size_t work_bytes, void *stream);
 
 /*
+ * Rotary positions with several axes (time, height and width of images and
+ * video, or a single one).  Pair p of a head's channels turns by the angle
+ *   angle_tp = pos[t][axis[p]] * freq[p]
+ * whose cosine and sine a table holds, [T][pairs] fp32 each: the tables that
+ * svdq_w4a4_linear_qkv_norm_rope takes (pairs = 64 there), made once per step
+ * for all layers, or once for all positions with rows by position.
+ */
+#define SVDQ_ROPE_MAX_AXES 8
+
+/*
+ * svdq_rope_frequencies -- axis and frequency of every pair, on the host.
+ *   sections   [axes] pairs of each axis, >= 0, their sum n <= 128, n % 8 == 0
+ *   axes       1 .. SVDQ_ROPE_MAX_AXES;  theta  finite, > 0
+ *   freq       [n] fp64 (out);  axis  [n] int32 (out)
+ * Frequencies of another scheme (scaled for longer contexts, positions with a
+ * unit of their own) are the caller's to write: the device calls take any.
+ * Host, synchronous.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE (n).
+ */
+svdq_status svdq_rope_frequencies(const int *sections, int axes, double theta, svdq_rope_axes layout, double *freq,
+                                  int32_t *axis);
+
+/*
+ * svdq_rope_table -- cosines and sines of T tokens' angles.
+ *   pos        [T][axes] int32, device;  axes  1 .. SVDQ_ROPE_MAX_AXES
+ *   freq       [pairs] fp64, device (radians per unit);  axis  [pairs] int32,
+ *              device: a value outside [0, axes) does not turn (cos 1, sin 0)
+ *   pairs      8 .. 128, pairs % 8 == 0
+ *   cos, sin   [T][pairs] fp32, device (out)
+ * The angle is the product rounded once to 64 bits; for angles below 2^30 the
+ * results are within 2^-23 of its cosine and sine.  One kernel launch.  Errors:
+ * SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE (pairs; T * pairs or T * axes of
+ * SVDQ_MAX_ELEMENTS or more), SVDQ_ERR_MISALIGNED (pos and axis 4 bytes, freq 8,
+ * cos and sin 16), SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
+ */
+svdq_status svdq_rope_table(const int32_t *pos, int T, int axes, const double *freq, const int32_t *axis, int pairs,
+                            float *cos, float *sin, void *stream);
+
+/*
+ * svdq_qk_norm_rope -- RMS-norm and rotation of query and key heads:
+ *   u = x / sqrt(mean_d(x_d^2) + eps) w (or x, without a weight);
+ *   pair (a, b) of u -> (a cos - b sin, b cos + a sin); channels behind 2 pairs
+ *   are u
+ * in 64 bits from the loads to one rounding (to fp32 and from there to bf16,
+ * each to nearest even).
+ *   Q, K       [T][heads_q][dim], [T][heads_k][dim] bf16 bits, device; row t
+ *              at t * ldq, t * ldk elements (>= heads * dim, % 8 == 0): slices of
+ *              a QKV product.  heads_q >= 1, heads_k >= 0 (0: K, K_out, norm_k are
+ *              not read)
+ *   dim        64, 128 or 256
+ *   norm_q, norm_k   [dim] bf16 bits, device, or NULL: no norm on that side
+ *   eps        finite, >= 0
+ *   cos, sin   [table_rows][pairs] fp32, device;  pairs  8 .. dim / 2, % 8 == 0
+ *   index      [T] int32, device: row of the tables for every token; a value
+ *              outside [0, table_rows) does not turn (norm only).  NULL: row t of
+ *              token t (tokens past table_rows do not turn)
+ *   Q_out, K_out  as Q and K, rows at ldqo, ldko; may be Q and K themselves
+ *              (with the same strides), not overlap them otherwise
+ * One kernel launch.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE (strides,
+ * pairs, T * heads * dim of SVDQ_MAX_ELEMENTS or more), SVDQ_ERR_UNSUPPORTED
+ * (dim), SVDQ_ERR_MISALIGNED, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
+ */
+svdq_status svdq_qk_norm_rope(const uint16_t *Q, int64_t ldq, int heads_q, const uint16_t *K, int64_t ldk,
+                              int heads_k, int T, int dim, const uint16_t *norm_q, const uint16_t *norm_k, double eps,
+                              const float *cos, const float *sin, const int32_t *index, int table_rows, int pairs,
+                              svdq_rope_pairs style, uint16_t *Q_out, int64_t ldqo, uint16_t *K_out, int64_t ldko,
+                              void *stream);
+
+/*
  * 4-bit key / value cache: keys and values in the library's two 4-bit
  * formats, quantized along the head's channels by the same group quantizers
  * as activations and weights (header comment; INT4 64 wide, MXFP4 32 wide),
@@ -632,6 +717,20 @@ typedef struct svdq_kv4_cache {
  */
 svdq_status svdq_kv4_append(const svdq_kv4_cache *cache, const uint16_t *K, const uint16_t *V, int64_t ldk,
                             int64_t ldv, const int32_t *slots, int T, void *stream);
+
+/*
+ * svdq_kv4_rope_append -- svdq_qk_norm_rope on the way into the cache: Q is
+ * normed and rotated to Q_out, K is normed, rotated, rounded to bf16 and
+ * appended with V as svdq_kv4_append does it (the codes are those of the two
+ * calls).  Arguments as for these; heads and dim of K and V are the cache's.
+ * One kernel launch.  Errors as for svdq_qk_norm_rope and svdq_kv4_append.
+ */
+svdq_status svdq_kv4_rope_append(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq, int heads_q,
+                                 const uint16_t *K, const uint16_t *V, int64_t ldk, int64_t ldv,
+                                 const uint16_t *norm_q, const uint16_t *norm_k, double eps, const float *cos,
+                                 const float *sin, const int32_t *index, int table_rows, int pairs,
+                                 svdq_rope_pairs style, const int32_t *slots, int T, uint16_t *Q_out, int64_t ldqo,
+                                 void *stream);
 
 /*
  * svdq_kv4_read -- the values that the cache holds for T slots:
@@ -691,6 +790,72 @@ svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q, i
                                const int32_t *kv_len, int B, int T, int heads_q, int max_q, int max_kv, float scale,
                                int causal, int window, uint16_t *O, float *lse, void *work, size_t work_bytes,
                                void *stream);
+
+/*
+ * Drafted tokens as a tree.  The last rows of a sequence are tokens that a
+ * draft proposes, each the child of another or of the sequence's last known
+ * token: a step checks them all at once, a row seeing the known tokens, its
+ * ancestors and itself.  kv_len counts the drafted tokens; they are appended at
+ * their places in order (place kv_len - n + i of row i of n), however deep they
+ * lie.
+ */
+#define SVDQ_TREE_MAX_WORDS 32      /* 1024 drafted tokens per sequence */
+
+/*
+ * svdq_kv4_tree_plan -- what the step needs of the tree, on the device.
+ *   parent       [T] int32, device: the parent's number among its sequence's
+ *                rows, smaller than the row's own; any other value: a child of
+ *                the last known token
+ *   q_start, kv_len, block_table, table_width, B, T   as for svdq_kv4_attention
+ *   pages, page_size   of the cache
+ *   mask         [T][mask_words] uint32, device (out): bit j % 32 of word j / 32
+ *                is set where row j is the row itself or an ancestor; rows past
+ *                32 mask_words are in no mask
+ *   mask_words   1 .. SVDQ_TREE_MAX_WORDS
+ *   position     [T] int32, device (out), or NULL: kv_len - n + the number of
+ *                ancestors, the token's position in its text
+ *   slots        [T] int32, device (out), or NULL: the slot of the row's place,
+ *                -1 where the table has none
+ * Rows of no sequence keep what the outputs hold.  One kernel launch.  Errors:
+ * SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE, SVDQ_ERR_UNSUPPORTED (page_size),
+ * SVDQ_ERR_MISALIGNED (4 bytes), SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
+ */
+svdq_status svdq_kv4_tree_plan(const int32_t *parent, const int32_t *q_start, const int32_t *kv_len,
+                               const int32_t *block_table, int table_width, int pages, int page_size, int B, int T,
+                               uint32_t *mask, int mask_words, int32_t *position, int32_t *slots, void *stream);
+
+/*
+ * svdq_kv4_tree_attention -- svdq_kv4_attention of drafted tokens: row i of n
+ * sees the keys before place kv_len - n, and the key at place kv_len - n + j
+ * where bit j of its mask is set.
+ *   mask, mask_words   as written by svdq_kv4_tree_plan, or any other: rows that
+ *                see each other, or nothing (device, 4-byte aligned).  Bits past a
+ *                sequence's rows are not used
+ * Other arguments, workspace, arithmetic and errors as for svdq_kv4_attention.
+ */
+svdq_status svdq_kv4_tree_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
+                                    const int32_t *block_table, int table_width, const int32_t *q_start,
+                                    const int32_t *kv_len, const uint32_t *mask, int mask_words, int B, int T,
+                                    int heads_q, int max_q, int max_kv, float scale, uint16_t *O, float *lse,
+                                    void *work, size_t work_bytes, void *stream);
+
+/*
+ * svdq_kv4_keep_path -- after the check: the accepted tokens' keys and values
+ * close up behind the known ones, node path[i] to place kv_len - n + i.
+ *   path         [B][max_path] int32, device: the accepted rows of every
+ *                sequence, ascending from the first; it ends at the first that is
+ *                negative, not above the one before it, or not below n
+ *   max_path     >= 1
+ *   new_len      [B] int32, device (out): kv_len - n + the path's length; not
+ *                kv_len itself
+ *   others       as for svdq_kv4_tree_plan
+ * The bytes move as they are.  A place whose page is outside the cache is left
+ * out of the move.  Places behind the path keep some of the drafted tokens.  One
+ * kernel launch per layer's cache.  Errors: as for svdq_kv4_append.
+ */
+svdq_status svdq_kv4_keep_path(const svdq_kv4_cache *cache, const int32_t *path, int max_path,
+                               const int32_t *q_start, const int32_t *kv_len, const int32_t *block_table,
+                               int table_width, int B, int T, int32_t *new_len, void *stream);
 
 #ifdef __cplusplus
 }

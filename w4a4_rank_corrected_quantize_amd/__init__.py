@@ -22,6 +22,13 @@ Functions mirror the C ABI in include/svdq.h:
     kv4_append(cache, K, V, slots)                              device, torch tensors
     kv4_read(cache, slots)                                      device, torch tensors
     kv4_attention(Q, cache, block_table, q_start, kv_len, ...)  device, torch tensors
+    rope_frequencies(sections, theta, layout)                   host, numpy out
+    rope_table(pos, freq, axis)                                 device, torch tensors
+    qk_norm_rope(Q, K, cos, sin, ...)                           device, torch tensors
+    kv4_rope_append(cache, Q, K, V, cos, sin, slots, ...)       device, torch tensors
+    kv4_tree_plan(cache, parent, q_start, kv_len, ...)          device, torch tensors
+    kv4_tree_attention(Q, cache, block_table, ..., mask, ...)   device, torch tensors
+    kv4_keep_path(cache, path, q_start, kv_len, ...)            device, torch tensors
 
 Device tensors: X bf16 [M][K], smooth fp32 [K], down bf16 [32][K],
 up bf16 [N][32], bias bf16 [N] or None, xq uint8 [M][K/2],
@@ -48,6 +55,11 @@ EPI_GELU_TANH = 1
 NORM_NONE = 0
 NORM_RMS = 1
 NORM_LAYER = 2
+ROPE_ADJACENT = 0
+ROPE_HALVES = 1
+ROPE_AXES_BLOCKS = 0
+ROPE_AXES_SECTIONS = 1
+ROPE_AXES_INTERLEAVED = 2
 RANK = 32
 
 STATUS = {
@@ -62,7 +74,9 @@ EXPORTS = ("svdq_status_string", "svdq_version", "svdq_check_device", "svdq_pack
            "svdq_nf4_codebook", "svdq_nf4_pack_weights", "svdq_nf4_dequantize", "svdq_nf4_w4a16_linear",
            "svdq_w4a4_linear_splitk_noalloc", "svdq_residual_norm", "svdq_lora_plan_bytes",
            "svdq_lora_workspace_bytes", "svdq_lora_plan", "svdq_lora_linear", "svdq_kv4_append", "svdq_kv4_read",
-           "svdq_kv4_attention_workspace_bytes", "svdq_kv4_attention")
+           "svdq_kv4_attention_workspace_bytes", "svdq_kv4_attention", "svdq_rope_frequencies", "svdq_rope_table",
+           "svdq_qk_norm_rope", "svdq_kv4_rope_append", "svdq_kv4_tree_plan", "svdq_kv4_tree_attention",
+           "svdq_kv4_keep_path")
 
 
 class SvdqError(RuntimeError):
@@ -144,6 +158,21 @@ def lib():
         L.svdq_kv4_attention_workspace_bytes.argtypes = [P, I, I, I, I, I]
         L.svdq_kv4_attention.restype = I
         L.svdq_kv4_attention.argtypes = [P, P, L64, P, I, P, P, I, I, I, I, I, F, I, I, P, P, P, Z, P]
+        D64 = ctypes.c_double
+        L.svdq_rope_frequencies.restype = I
+        L.svdq_rope_frequencies.argtypes = [P, I, D64, I, P, P]
+        L.svdq_rope_table.restype = I
+        L.svdq_rope_table.argtypes = [P, I, I, P, P, I, P, P, P]
+        L.svdq_qk_norm_rope.restype = I
+        L.svdq_qk_norm_rope.argtypes = [P, L64, I, P, L64, I, I, I, P, P, D64, P, P, P, I, I, I, P, L64, P, L64, P]
+        L.svdq_kv4_rope_append.restype = I
+        L.svdq_kv4_rope_append.argtypes = [P, P, L64, I, P, P, L64, L64, P, P, D64, P, P, P, I, I, I, P, I, P, L64, P]
+        L.svdq_kv4_tree_plan.restype = I
+        L.svdq_kv4_tree_plan.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, P, P]
+        L.svdq_kv4_tree_attention.restype = I
+        L.svdq_kv4_tree_attention.argtypes = [P, P, L64, P, I, P, P, P, I, I, I, I, I, I, F, P, P, P, Z, P]
+        L.svdq_kv4_keep_path.restype = I
+        L.svdq_kv4_keep_path.argtypes = [P, P, I, P, P, P, I, I, I, P, P]
         _lib = L
     return _lib
 
@@ -962,6 +991,258 @@ def kv4_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, max_q: int, 
     if st:
         raise SvdqError(st, "svdq_kv4_attention")
     return out
+
+
+def kv4_tree_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, mask, max_q: int, max_kv: int, scale=None,
+                       out=None, lse=None, work=None, stream=None):
+    """kv4_attention of drafted tokens: row i of a sequence's n sees the keys
+    before place kv_len - n, and of the drafted ones those in its mask [T][words]
+    int32 (kv4_tree_plan).  Workspace as for kv4_attention."""
+    torch = _tt()
+    i32 = torch.int32
+    dev = _cache_arg(cache)
+    _ndim(Q, 3, "Q")
+    H, D = Q.shape[1], cache.dim
+    if H == 0 or H % cache.heads:
+        raise ValueError(f"Q has {H} heads, the cache {cache.heads}")
+    T, ldq = _heads_arg(Q, "Q", H, D)
+    _ndim(block_table, 2, "block_table")
+    _arg(block_table, i32, "block_table")
+    B, width = block_table.shape
+    _arg(q_start, i32, "q_start", (B + 1,))
+    _arg(kv_len, i32, "kv_len", (B,))
+    _ndim(mask, 2, "mask")
+    words = mask.shape[1]
+    _arg(mask, i32, "mask", (T, words))
+    if B > _I32 or width > _I32 or words > _I32:
+        raise SvdqError(-2, "svdq_kv4_tree_attention")
+    max_q, max_kv = _bound(max_q), _bound(max_kv)
+    out = _empty((T, H, D), torch.bfloat16, dev, stream, Q) if out is None else _arg(
+        out, torch.bfloat16, "out", (T, H, D))
+    if lse is not None:
+        _arg(lse, torch.float32, "lse", (T, H))
+    if work is None:
+        need = kv4_attention_workspace_bytes(cache, T, B, H, max_q, max_kv)
+        work = _empty(need, torch.uint8, dev, stream) if need else None
+    else:
+        _arg(work, torch.uint8, "work")
+    raw = _launch(dev, ("Q", "block_table", "q_start", "kv_len", "mask", "out", "lse", "work"),
+                  (Q, block_table, q_start, kv_len, mask, out, lse, work), stream)
+    st = lib().svdq_kv4_tree_attention(cache._ref, Q.data_ptr(), ldq, block_table.data_ptr(), width,
+                                       q_start.data_ptr(), kv_len.data_ptr(), mask.data_ptr(), words, B, T, H, max_q,
+                                       max_kv, D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
+                                       _ptr(work), 0 if work is None else work.numel(), raw)
+    if st:
+        raise SvdqError(st, "svdq_kv4_tree_attention")
+    return out
+
+
+TREE_MAX_WORDS = 32
+
+
+def kv4_tree_plan(cache: Kv4Cache, parent, q_start, kv_len, block_table, max_q: int, mask=None, position=None,
+                  slots=None, stream=None):
+    """Mask, positions and slots of drafted tokens (one kernel): parent [T] int32,
+    the number of each token's parent among its sequence's rows (smaller than its
+    own; -1: a child of the last known token); max_q bounds the rows of a sequence
+    (at most 1024) and gives the mask's words.  kv_len counts the drafted tokens.
+    Returns (mask [T][ceil(max_q / 32)], position [T], slots [T]), int32."""
+    torch = _tt()
+    i32 = torch.int32
+    dev = _cache_arg(cache)
+    _ndim(parent, 1, "parent")
+    _arg(parent, i32, "parent")
+    T = parent.shape[0]
+    _ndim(block_table, 2, "block_table")
+    _arg(block_table, i32, "block_table")
+    B, width = block_table.shape
+    _arg(q_start, i32, "q_start", (B + 1,))
+    _arg(kv_len, i32, "kv_len", (B,))
+    if T > _I32 or B > _I32 or width > _I32:
+        raise SvdqError(-2, "svdq_kv4_tree_plan")
+    if not 1 <= max_q <= 32 * TREE_MAX_WORDS:
+        raise ValueError(f"max_q must be 1 .. {32 * TREE_MAX_WORDS}, got {max_q}")
+    words = (max_q + 31) // 32
+    mask = _empty((T, words), i32, dev, stream) if mask is None else _arg(mask, i32, "mask", (T, words))
+    position = _empty((T,), i32, dev, stream, parent) if position is None else _arg(position, i32, "position", (T,))
+    slots = _empty((T,), i32, dev, stream, parent) if slots is None else _arg(slots, i32, "slots", (T,))
+    raw = _launch(dev, ("parent", "q_start", "kv_len", "block_table", "mask", "position", "slots"),
+                  (parent, q_start, kv_len, block_table, mask, position, slots), stream)
+    st = lib().svdq_kv4_tree_plan(parent.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+                                  width, cache.pages, cache.page_size, B, T, mask.data_ptr(), words,
+                                  position.data_ptr(), slots.data_ptr(), raw)
+    if st:
+        raise SvdqError(st, "svdq_kv4_tree_plan")
+    return mask, position, slots
+
+
+def kv4_keep_path(cache: Kv4Cache, path, q_start, kv_len, block_table, T: Optional[int] = None, new_len=None,
+                  stream=None):
+    """Moves the keys and values of each sequence's accepted rows, path [B][any]
+    int32 (ascending, ended by -1), behind the known tokens (one kernel).  T: the
+    step's rows; q_start's values are cut to it (None: not cut).  Returns the new
+    lengths [B] int32 (not kv_len itself)."""
+    torch = _tt()
+    i32 = torch.int32
+    dev = _cache_arg(cache)
+    _ndim(block_table, 2, "block_table")
+    _arg(block_table, i32, "block_table")
+    B, width = block_table.shape
+    _ndim(path, 2, "path")
+    longest = path.shape[1]
+    _arg(path, i32, "path", (B, longest))
+    _arg(q_start, i32, "q_start", (B + 1,))
+    _arg(kv_len, i32, "kv_len", (B,))
+    T = _I32 if T is None else T
+    if B > _I32 or width > _I32 or longest > _I32 or T > _I32:
+        raise SvdqError(-2, "svdq_kv4_keep_path")
+    new_len = _empty((B,), i32, dev, stream, kv_len) if new_len is None else _arg(new_len, i32, "new_len", (B,))
+    raw = _launch(dev, ("path", "q_start", "kv_len", "block_table", "new_len"),
+                  (path, q_start, kv_len, block_table, new_len), stream)
+    st = lib().svdq_kv4_keep_path(cache._ref, path.data_ptr(), longest, q_start.data_ptr(), kv_len.data_ptr(),
+                                  block_table.data_ptr(), width, B, T, new_len.data_ptr(), raw)
+    if st:
+        raise SvdqError(st, "svdq_kv4_keep_path")
+    return new_len
+
+
+def rope_frequencies(sections, theta: float = 10000.0, layout: int = ROPE_AXES_BLOCKS):
+    """Frequency (fp64) and axis (int32) of every pair of channels, for axes of
+    `sections` pairs each (host, numpy)."""
+    sec = np.ascontiguousarray(sections, np.int32)
+    if sec.ndim != 1:
+        raise ValueError("sections must be one-dimensional")
+    n = int(sec.clip(0).sum(dtype=np.int64))
+    freq, axis = np.empty(min(n, 128), np.float64), np.empty(min(n, 128), np.int32)
+    _check(lib().svdq_rope_frequencies(sec.ctypes.data, sec.size, float(theta), layout, freq.ctypes.data,
+                                       axis.ctypes.data), "svdq_rope_frequencies")
+    return freq, axis
+
+
+def rope_table(pos, freq, axis, cos=None, sin=None, stream=None):
+    """cos and sin [T][pairs] fp32 of pos[t][axis[p]] * freq[p] (one kernel): pos
+    [T][axes] int32, freq [pairs] fp64, axis [pairs] int32."""
+    torch = _tt()
+    f32 = torch.float32
+    _ndim(pos, 2, "pos")
+    _arg(pos, torch.int32, "pos")
+    T, axes = pos.shape
+    _ndim(freq, 1, "freq")
+    _arg(freq, torch.float64, "freq")
+    n = freq.shape[0]
+    _arg(axis, torch.int32, "axis", (n,))
+    if T > _I32 or axes > _I32 or n > _I32:
+        raise SvdqError(-2, "svdq_rope_table")
+    dev = pos.device
+    cos = _empty((T, n), f32, dev, stream) if cos is None else _arg(cos, f32, "cos", (T, n))
+    sin = _empty((T, n), f32, dev, stream, cos) if sin is None else _arg(sin, f32, "sin", (T, n))
+    raw = _launch(dev, ("freq", "axis", "cos", "sin"), (freq, axis, cos, sin), stream)
+    st = lib().svdq_rope_table(pos.data_ptr(), T, axes, freq.data_ptr(), axis.data_ptr(), n, cos.data_ptr(),
+                               sin.data_ptr(), raw)
+    if st:
+        raise SvdqError(st, "svdq_rope_table")
+    return cos, sin
+
+
+def _rope_args(cos, sin, index, T, norm_q, norm_k, D):
+    """Rows and pairs of the tables; checks what both rotating calls take."""
+    torch = _T
+    _ndim(cos, 2, "cos")
+    _arg(cos, torch.float32, "cos")
+    _arg(sin, torch.float32, "sin", cos.shape)
+    if norm_q is not None:
+        _arg(norm_q, torch.bfloat16, "norm_q", (D,))
+    if norm_k is not None:
+        _arg(norm_k, torch.bfloat16, "norm_k", (D,))
+    if index is not None:
+        _arg(index, torch.int32, "index", (T,))
+    rows, pairs = cos.shape
+    if rows > _I32 or pairs > _I32:
+        raise ValueError("tables of more rows than the library takes")
+    return rows, pairs
+
+
+def qk_norm_rope(Q, K, cos, sin, style: int = ROPE_ADJACENT, index=None, norm_q=None, norm_k=None, eps: float = 1e-6,
+                 Q_out=None, K_out=None, stream=None):
+    """RMS-norm (with a weight norm_q, norm_k [dim]; None: no norm on that side)
+    and rotation of query and key heads (one kernel).  Q [T][heads][dim], K
+    [T][heads_k][dim] or None, bf16, dim 64, 128 or 256, rows may be a stride
+    apart; cos, sin [rows][pairs] fp32 (rope_table), row of token t: index[t], or t;
+    tokens without a row are not turned.  Q_out and K_out may be Q and K (in place).
+    Returns (Q_out, K_out)."""
+    torch = _T or _tt()
+    bf = torch.bfloat16
+    _ndim(Q, 3, "Q")
+    H, D = Q.shape[1:]
+    T, ldq = _heads_arg(Q, "Q", H, D)
+    rows, pairs = _rope_args(cos, sin, index, T, norm_q, norm_k, D)
+    if T > _I32 or H > _I32 or D > _I32:
+        raise SvdqError(-2, "svdq_qk_norm_rope")
+    dev = Q.device
+    if Q_out is None:
+        Q_out = _empty((T, H, D), bf, dev, stream, Q)
+    TO, ldqo = _heads_arg(Q_out, "Q_out", H, D)
+    if TO != T:
+        raise ValueError(f"Q_out has shape {tuple(Q_out.shape)}, expected {tuple(Q.shape)}")
+    pK = pKo = None
+    Hk = ldk = ldko = 0
+    if K is not None:
+        _ndim(K, 3, "K")
+        Hk = K.shape[1]
+        TK, ldk = _heads_arg(K, "K", Hk, D)
+        if K_out is None:
+            K_out = _empty((T, Hk, D), bf, dev, stream, K)
+        TO, ldko = _heads_arg(K_out, "K_out", Hk, D)
+        if TK != T or TO != T:
+            raise ValueError("Q, K and K_out must have the same number of tokens")
+        if Hk > _I32:
+            raise SvdqError(-2, "svdq_qk_norm_rope")
+        pK, pKo = K.data_ptr(), K_out.data_ptr()
+    elif K_out is not None or norm_k is not None:
+        raise ValueError("K_out or norm_k without K")
+    raw = _launch(dev, ("K", "cos", "sin", "index", "norm_q", "norm_k", "Q_out", "K_out"),
+                  (K, cos, sin, index, norm_q, norm_k, Q_out, K_out), stream)
+    st = lib().svdq_qk_norm_rope(Q.data_ptr(), ldq, H, pK, ldk, Hk, T, D, _ptr(norm_q), _ptr(norm_k), eps,
+                                 cos.data_ptr(), sin.data_ptr(), _ptr(index), rows, pairs, style, Q_out.data_ptr(),
+                                 ldqo, pKo, ldko, raw)
+    if st:
+        raise SvdqError(st, "svdq_qk_norm_rope")
+    return Q_out, K_out
+
+
+def kv4_rope_append(cache: Kv4Cache, Q, K, V, cos, sin, slots, style: int = ROPE_ADJACENT, index=None, norm_q=None,
+                    norm_k=None, eps: float = 1e-6, Q_out=None, stream=None):
+    """qk_norm_rope on the way into the cache (one kernel): Q [T][heads][dim] to
+    Q_out (may be Q), K and V [T][cache heads][dim] into their slots [T] int32, K
+    normed and rotated first; the codes are those of qk_norm_rope and kv4_append.
+    Returns Q_out."""
+    torch = _T or _tt()
+    dev = _cache_arg(cache)
+    Hk, D = cache.heads, cache.dim
+    _ndim(Q, 3, "Q")
+    H = Q.shape[1]
+    T, ldq = _heads_arg(Q, "Q", H, D)
+    TK, ldk = _heads_arg(K, "K", Hk, D)
+    TV, ldv = _heads_arg(V, "V", Hk, D)
+    if TK != T or TV != T:
+        raise ValueError("Q, K and V must have the same number of tokens")
+    _arg(slots, torch.int32, "slots", (T,))
+    rows, pairs = _rope_args(cos, sin, index, T, norm_q, norm_k, D)
+    if T > _I32 or H > _I32:
+        raise SvdqError(-2, "svdq_kv4_rope_append")
+    if Q_out is None:
+        Q_out = _empty((T, H, D), torch.bfloat16, dev, stream, Q)
+    TO, ldqo = _heads_arg(Q_out, "Q_out", H, D)
+    if TO != T:
+        raise ValueError(f"Q_out has shape {tuple(Q_out.shape)}, expected {tuple(Q.shape)}")
+    raw = _launch(dev, ("Q", "K", "V", "cos", "sin", "slots", "index", "norm_q", "norm_k", "Q_out"),
+                  (Q, K, V, cos, sin, slots, index, norm_q, norm_k, Q_out), stream)
+    st = lib().svdq_kv4_rope_append(cache._ref, Q.data_ptr(), ldq, H, K.data_ptr(), V.data_ptr(), ldk, ldv,
+                                    _ptr(norm_q), _ptr(norm_k), eps, cos.data_ptr(), sin.data_ptr(), _ptr(index),
+                                    rows, pairs, style, slots.data_ptr(), T, Q_out.data_ptr(), ldqo, raw)
+    if st:
+        raise SvdqError(st, "svdq_kv4_rope_append")
+    return Q_out
 
 
 def to_device(packed: dict, device="cuda") -> dict:

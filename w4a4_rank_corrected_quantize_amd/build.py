@@ -36,6 +36,8 @@ SOURCES = {
     "residual_norm.hip": [],
     "lora.hip": [],
     "kv4_cache.hip": ["-ffp-contract=off"],
+    "rope.hip": ["-ffp-contract=off"],
+    "kv4_tree.hip": [],
     "kv4_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 

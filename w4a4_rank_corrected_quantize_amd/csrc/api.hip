@@ -39,6 +39,7 @@ svdq_status current_device_ok()
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }      // int32 index arrays
+bool aligned8(const void *p) { return ((uintptr_t)p & 7u) == 0; }      // fp64 arrays
 
 svdq_status check_common(int M, int K, int rank, svdq_precision prec)
 {
@@ -104,7 +105,7 @@ extern "C" const char *svdq_status_string(svdq_status status)
     return "unknown status";
 }
 
-extern "C" int svdq_version(void) { return 200; }
+extern "C" int svdq_version(void) { return 300; }
 
 extern "C" svdq_status svdq_check_device(void) { return current_device_ok(); }
 
@@ -493,11 +494,12 @@ extern "C" size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache
     return kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv);
 }
 
-extern "C" svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
-                                          const int32_t *block_table, int table_width, const int32_t *q_start,
-                                          const int32_t *kv_len, int B, int T, int heads_q, int max_q, int max_kv,
-                                          float scale, int causal, int window, uint16_t *O, float *lse, void *work,
-                                          size_t work_bytes, void *stream)
+// Both forms: causal rows, or a mask of drafted tokens.
+static svdq_status kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
+                                 const int32_t *block_table, int table_width, const int32_t *q_start,
+                                 const int32_t *kv_len, int B, int T, int heads_q, int max_q, int max_kv, float scale,
+                                 int causal, int window, const uint32_t *tree, int tree_words, uint16_t *O, float *lse,
+                                 void *work, size_t work_bytes, void *stream)
 {
     Kv4View c;
     svdq_status st = check_kv4(cache, c);
@@ -519,8 +521,197 @@ extern "C" svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uin
     const size_t need = kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv);
     if (need > 0 && (!work || work_bytes < need)) return SVDQ_ERR_INVALID_ARG;
     hipError_t e = launch_kv4_attention(c, Q, ldq, block_table, table_width, q_start, kv_len, B, T, heads_q, max_q,
-                                        max_kv, scale, causal, window, O, lse, (float *)work, (hipStream_t)stream);
+                                        max_kv, scale, causal, window, O, lse, (float *)work, (hipStream_t)stream,
+                                        tree, tree_words);
     return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+extern "C" svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
+                                          const int32_t *block_table, int table_width, const int32_t *q_start,
+                                          const int32_t *kv_len, int B, int T, int heads_q, int max_q, int max_kv,
+                                          float scale, int causal, int window, uint16_t *O, float *lse, void *work,
+                                          size_t work_bytes, void *stream)
+{
+    return kv4_attention(cache, Q, ldq, block_table, table_width, q_start, kv_len, B, T, heads_q, max_q, max_kv, scale,
+                         causal, window, nullptr, 0, O, lse, work, work_bytes, stream);
+}
+
+extern "C" svdq_status svdq_kv4_tree_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
+                                               const int32_t *block_table, int table_width, const int32_t *q_start,
+                                               const int32_t *kv_len, const uint32_t *mask, int mask_words, int B,
+                                               int T, int heads_q, int max_q, int max_kv, float scale, uint16_t *O,
+                                               float *lse, void *work, size_t work_bytes, void *stream)
+{
+    if (mask_words < 1 || (T > 0 && B > 0 && !mask)) return SVDQ_ERR_INVALID_ARG;
+    if (mask_words > SVDQ_TREE_MAX_WORDS || T < 0 || !elems_ok(T, mask_words)) return SVDQ_ERR_SHAPE;
+    if (!aligned4(mask)) return SVDQ_ERR_MISALIGNED;
+    return kv4_attention(cache, Q, ldq, block_table, table_width, q_start, kv_len, B, T, heads_q, max_q, max_kv, scale,
+                         0, 0, mask, mask_words, O, lse, work, work_bytes, stream);
+}
+
+// ------------------------------------------------ rotary positions
+
+extern "C" svdq_status svdq_rope_frequencies(const int *sections, int axes, double theta, svdq_rope_axes layout,
+                                             double *freq, int32_t *axis)
+{
+    if (!sections || !freq || !axis || axes < 1 || axes > SVDQ_ROPE_MAX_AXES) return SVDQ_ERR_INVALID_ARG;
+    if (layout != SVDQ_ROPE_AXES_BLOCKS && layout != SVDQ_ROPE_AXES_SECTIONS && layout != SVDQ_ROPE_AXES_INTERLEAVED)
+        return SVDQ_ERR_INVALID_ARG;
+    if (!(theta > 0.0) || theta > 1.7e308) return SVDQ_ERR_INVALID_ARG;
+    int64_t n = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 0) return SVDQ_ERR_INVALID_ARG;
+        n += sections[a];
+    }
+    if (n < 8 || n > 128 || n % 8 != 0) return SVDQ_ERR_SHAPE;
+    rope_frequencies(sections, axes, theta, layout, freq, axis);
+    return SVDQ_OK;
+}
+
+extern "C" svdq_status svdq_rope_table(const int32_t *pos, int T, int axes, const double *freq, const int32_t *axis,
+                                       int pairs, float *cos, float *sin, void *stream)
+{
+    if (T < 0 || axes < 1 || axes > SVDQ_ROPE_MAX_AXES) return SVDQ_ERR_INVALID_ARG;
+    if (pairs < 8 || pairs > 128 || pairs % 8 != 0 || !elems_ok(T, pairs) || !elems_ok(T, axes)) return SVDQ_ERR_SHAPE;
+    if (!freq || !axis || (T > 0 && (!pos || !cos || !sin))) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned4(pos) || !aligned8(freq) || !aligned4(axis) || !aligned16(cos) || !aligned16(sin))
+        return SVDQ_ERR_MISALIGNED;
+    svdq_status st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0) return SVDQ_OK;
+    return launch_rope_table(pos, T, axes, freq, axis, pairs, cos, sin, (hipStream_t)stream) == hipSuccess
+               ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+// The rotation's own arguments (pointers and sizes of Q and K apart).
+static svdq_status check_rope(int dim, double eps, const float *cos, const float *sin, int table_rows, int pairs,
+                              svdq_rope_pairs style)
+{
+    if (style != SVDQ_ROPE_ADJACENT && style != SVDQ_ROPE_HALVES) return SVDQ_ERR_INVALID_ARG;
+    if (!(eps >= 0.0) || eps > 1.7e308 || table_rows < 0) return SVDQ_ERR_INVALID_ARG;
+    if (pairs < 8 || pairs > dim / 2 || pairs % 8 != 0 || !elems_ok(table_rows, pairs)) return SVDQ_ERR_SHAPE;
+    return table_rows > 0 && (!cos || !sin) ? SVDQ_ERR_INVALID_ARG : SVDQ_OK;
+}
+
+extern "C" svdq_status svdq_qk_norm_rope(const uint16_t *Q, int64_t ldq, int heads_q, const uint16_t *K, int64_t ldk,
+                                         int heads_k, int T, int dim, const uint16_t *norm_q, const uint16_t *norm_k,
+                                         double eps, const float *cos, const float *sin, const int32_t *index,
+                                         int table_rows, int pairs, svdq_rope_pairs style, uint16_t *Q_out,
+                                         int64_t ldqo, uint16_t *K_out, int64_t ldko, void *stream)
+{
+    if (T < 0 || heads_q < 1 || heads_k < 0) return SVDQ_ERR_INVALID_ARG;
+    if (dim != 64 && dim != 128 && dim != 256) return SVDQ_ERR_UNSUPPORTED;
+    svdq_status st = check_rope(dim, eps, cos, sin, table_rows, pairs, style);
+    if (st != SVDQ_OK) return st;
+    if (heads_q > 65535 || heads_k > 65535 || !elems_ok(T, (int64_t)(heads_q + heads_k) * dim)) return SVDQ_ERR_SHAPE;
+    if (!kv4_stride_ok(ldq, heads_q, dim) || !kv4_stride_ok(ldqo, heads_q, dim)) return SVDQ_ERR_SHAPE;
+    if (heads_k > 0 && (!kv4_stride_ok(ldk, heads_k, dim) || !kv4_stride_ok(ldko, heads_k, dim))) return SVDQ_ERR_SHAPE;
+    if (heads_k == 0) K = norm_k = nullptr, K_out = nullptr;
+    if (T > 0 && (!Q || !Q_out || (heads_k > 0 && (!K || !K_out)))) return SVDQ_ERR_INVALID_ARG;
+    if (T > 0 && ((Q == Q_out && ldq != ldqo) || (heads_k > 0 && K == K_out && ldk != ldko))) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(K) || !aligned16(norm_q) || !aligned16(norm_k) || !aligned16(cos) ||
+        !aligned16(sin) || !aligned4(index) || !aligned16(Q_out) || !aligned16(K_out))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0) return SVDQ_OK;
+    RopeArgs r{};
+    r.Q = Q, r.K = K, r.wq = norm_q, r.wk = norm_k, r.Qo = Q_out, r.Ko = K_out, r.ldq = ldq, r.ldk = ldk;
+    r.ldqo = ldqo, r.ldko = ldko, r.cos = cos, r.sin = sin, r.index = index, r.eps = eps, r.T = T;
+    r.heads_q = heads_q, r.heads_k = heads_k, r.table_rows = table_rows, r.pairs = pairs;
+    return launch_qk_norm_rope(r, dim, style == SVDQ_ROPE_HALVES, (hipStream_t)stream) == hipSuccess ? SVDQ_OK
+                                                                                                      : SVDQ_ERR_HIP;
+}
+
+extern "C" svdq_status svdq_kv4_rope_append(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq, int heads_q,
+                                            const uint16_t *K, const uint16_t *V, int64_t ldk, int64_t ldv,
+                                            const uint16_t *norm_q, const uint16_t *norm_k, double eps,
+                                            const float *cos, const float *sin, const int32_t *index, int table_rows,
+                                            int pairs, svdq_rope_pairs style, const int32_t *slots, int T,
+                                            uint16_t *Q_out, int64_t ldqo, void *stream)
+{
+    Kv4View c;
+    svdq_status st = check_kv4(cache, c);
+    if (st != SVDQ_OK) return st;
+    if (T < 0 || heads_q < 1) return SVDQ_ERR_INVALID_ARG;
+    st = check_rope(c.dim, eps, cos, sin, table_rows, pairs, style);
+    if (st != SVDQ_OK) return st;
+    if (heads_q > 65535 || !elems_ok(T, (int64_t)(heads_q + c.heads) * c.dim)) return SVDQ_ERR_SHAPE;
+    if (!kv4_stride_ok(ldq, heads_q, c.dim) || !kv4_stride_ok(ldqo, heads_q, c.dim) ||
+        !kv4_stride_ok(ldk, c.heads, c.dim) || !kv4_stride_ok(ldv, c.heads, c.dim))
+        return SVDQ_ERR_SHAPE;
+    if (T > 0 && (!Q || !K || !V || !slots || !Q_out || (Q == Q_out && ldq != ldqo))) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(norm_q) || !aligned16(norm_k) ||
+        !aligned16(cos) || !aligned16(sin) || !aligned4(index) || !aligned4(slots) || !aligned16(Q_out))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0) return SVDQ_OK;
+    RopeArgs r{};
+    r.Q = Q, r.K = K, r.wq = norm_q, r.wk = norm_k, r.Qo = Q_out, r.ldq = ldq, r.ldk = ldk, r.ldqo = ldqo;
+    r.cos = cos, r.sin = sin, r.index = index, r.eps = eps, r.T = T, r.heads_q = heads_q;
+    r.table_rows = table_rows, r.pairs = pairs;
+    return launch_kv4_rope_append(c, r, style == SVDQ_ROPE_HALVES, V, ldv, slots, (hipStream_t)stream) == hipSuccess
+               ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+// ------------------------------------------------ drafted tokens
+
+// Sizes of a step's sequences and their pages.
+static svdq_status check_sequences(int pages, int page_size, int table_width, int B, int T, int &shift)
+{
+    if (B < 0 || T < 0 || pages < 1 || table_width < 1) return SVDQ_ERR_INVALID_ARG;
+    shift = 4;
+    while (shift < 8 && (1 << shift) != page_size) ++shift;
+    if ((1 << shift) != page_size) return SVDQ_ERR_UNSUPPORTED;
+    if (((int64_t)pages << shift) > INT32_MAX || ((int64_t)table_width << shift) > INT32_MAX - 4096)
+        return SVDQ_ERR_SHAPE;
+    return B < (1 << 24) ? SVDQ_OK : SVDQ_ERR_SHAPE;
+}
+
+extern "C" svdq_status svdq_kv4_tree_plan(const int32_t *parent, const int32_t *q_start, const int32_t *kv_len,
+                                          const int32_t *block_table, int table_width, int pages, int page_size, int B,
+                                          int T, uint32_t *mask, int mask_words, int32_t *position, int32_t *slots,
+                                          void *stream)
+{
+    Kv4Tables s{block_table, q_start, kv_len, table_width, 0, pages};
+    svdq_status st = check_sequences(pages, page_size, table_width, B, T, s.page_shift);
+    if (st != SVDQ_OK) return st;
+    if (mask_words < 1) return SVDQ_ERR_INVALID_ARG;
+    if (mask_words > SVDQ_TREE_MAX_WORDS || !elems_ok(T, mask_words)) return SVDQ_ERR_SHAPE;
+    if (T > 0 && B > 0 && (!parent || !q_start || !kv_len || !block_table || !mask)) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned4(parent) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) || !aligned4(mask) ||
+        !aligned4(position) || !aligned4(slots))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (T == 0 || B == 0) return SVDQ_OK;
+    return launch_kv4_tree_plan(parent, s, B, T, mask, mask_words, position, slots, (hipStream_t)stream) == hipSuccess
+               ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+extern "C" svdq_status svdq_kv4_keep_path(const svdq_kv4_cache *cache, const int32_t *path, int max_path,
+                                          const int32_t *q_start, const int32_t *kv_len, const int32_t *block_table,
+                                          int table_width, int B, int T, int32_t *new_len, void *stream)
+{
+    Kv4View c;
+    svdq_status st = check_kv4(cache, c);
+    if (st != SVDQ_OK) return st;
+    Kv4Tables s{block_table, q_start, kv_len, table_width, c.page_shift, c.pages};
+    int shift;
+    st = check_sequences(c.pages, cache->page_size, table_width, B, T, shift);
+    if (st != SVDQ_OK) return st;
+    if (max_path < 1) return SVDQ_ERR_INVALID_ARG;
+    if ((int64_t)B * c.heads >= (1 << 24) || !elems_ok(B, max_path)) return SVDQ_ERR_SHAPE;
+    if (B > 0 && (!path || !q_start || !kv_len || !block_table || !new_len || new_len == kv_len))
+        return SVDQ_ERR_INVALID_ARG;
+    if (!aligned4(path) || !aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) || !aligned4(new_len))
+        return SVDQ_ERR_MISALIGNED;
+    st = current_device_ok();
+    if (st != SVDQ_OK) return st;
+    if (B == 0) return SVDQ_OK;
+    return launch_kv4_keep_path(c, s, B, T, path, max_path, new_len, (hipStream_t)stream) == hipSuccess ? SVDQ_OK
+                                                                                                        : SVDQ_ERR_HIP;
 }
 
 // ------------------------------------------------ allocation-free split K

@@ -155,6 +155,8 @@ struct KvArgs {
     int64_t ldq;
     int T, B, heads_q, group, table_width, q_tiles, splits, split_steps, causal, window, cus;
     float scale;
+    const uint32_t *tree;                         // mask of the drafted tokens, tree_words per row
+    int tree_words;
 };
 
 // One step's codes and scales in flight.
@@ -370,18 +372,47 @@ __device__ __forceinline__ int ka_window(const KvArgs &a, int place)
     return a.causal && a.window > 0 ? (int)max((int64_t)place - a.window + 1, (int64_t)0) : 0;
 }
 
+// The drafted tokens that a column's row sees, from key `first` (the sequence's
+// first drafted token) on.
+template <int CT, bool TREE>
+struct KvTree {};
+template <int CT>
+struct KvTree<CT, true> {
+    const uint32_t *row[CT];
+    int first, words;
+};
+
+// Bit i of the result: the row sees key key0 + i; keys before the first drafted
+// token are seen, tokens past the mask not.
+template <int CT>
+__device__ __forceinline__ uint64_t ka_tree_bits(const KvTree<CT, true> &t, int ct, int key0)
+{
+    const int rel = key0 - t.first, w = rel >> 5, sh = rel & 31;
+    uint32_t x[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t m = t.row[ct][min(max(w + i, 0), t.words - 1)];
+        x[i] = w + i < 0 ? ~0u : (w + i < t.words ? m : 0u);
+    }
+    const uint64_t lo = x[0] | (uint64_t)x[1] << 32;
+    return sh ? lo >> sh | (uint64_t)x[2] << (64 - sh) : lo;
+}
+
 // A wave's rows: 16 CT query rows of one key head, column 16 ct + j each.
-template <int D, int CT>
+// TREE: rows of drafted tokens, which see the keys before these and their
+// ancestors among them.
+template <int D, int CT, bool TREE = false>
 struct KvRows {
     bf16x8 q[CT][D / 32];
     f32x4 acc[CT][D / 16];                        // O^T, tile (block n, half h) at 2 n + h
     float m[CT], l[CT];                           // running maximum; the lane part's share of the sum
     int hi_key[CT], lo_key[CT];                   // the columns' keys: lo <= key < hi
     int all_hi, all_lo;                           // over the columns: the least hi, the greatest lo
+    [[no_unique_address]] KvTree<CT, TREE> tree;
 };
 
-template <int D, bool INT4, int CT>
-__device__ __forceinline__ void ka_rows(KvRows<D, CT> &w, const KvArgs &a, int head, int qs, int qn, int kv, int64_t r0,
+template <int D, bool INT4, int CT, bool TREE>
+__device__ __forceinline__ void ka_rows(KvRows<D, CT, TREE> &w, const KvArgs &a, int head, int qs, int qn, int kv, int64_t r0,
                                         int64_t rows, int lane)
 {
     const int j = lane & 15, b = lane >> 4, G = a.group;
@@ -400,10 +431,12 @@ __device__ __forceinline__ void ka_rows(KvRows<D, CT> &w, const KvArgs &a, int h
         w.hi_key[ct] = a.causal ? min(place + 1, kv) : kv;
         w.lo_key[ct] = ka_window(a, place);
         w.all_hi = min(w.all_hi, w.hi_key[ct]), w.all_lo = max(w.all_lo, w.lo_key[ct]);
+        if constexpr (TREE) w.tree.row[ct] = a.tree + (int64_t)(qs + tok) * a.tree_words;
         w.m[ct] = -INFINITY, w.l[ct] = 0.0f;
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) w.acc[ct][n] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     }
+    if constexpr (TREE) w.tree.first = kv - qn, w.tree.words = a.tree_words, w.all_hi = min(w.all_hi, kv - qn);
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1)
         w.all_hi = min(w.all_hi, __shfl_xor(w.all_hi, d)), w.all_lo = max(w.all_lo, __shfl_xor(w.all_lo, d));
@@ -414,18 +447,22 @@ __device__ __forceinline__ void ka_rows(KvRows<D, CT> &w, const KvArgs &a, int h
 // row does not see become -infinity, and the reference m moves where a score
 // exceeds it by more than kLazy (seen in any lane): p is at most 2^kLazy then,
 // and its relative rounding the same.
-template <int D, int CT>
-__device__ __forceinline__ void ka_reference(KvRows<D, CT> &w, float (&p)[CT][16], int key0, int valid, float c2, int b)
+template <int D, int CT, bool TREE>
+__device__ __forceinline__ void ka_reference(KvRows<D, CT, TREE> &w, float (&p)[CT][16], int key0, int valid, float c2, int b)
 {
     if (key0 + 64 > w.all_hi || key0 < w.all_lo || valid != 15) {
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+        for (int ct = 0; ct < CT; ++ct) {
+            uint64_t bits = ~0ull;
+            if constexpr (TREE) bits = ka_tree_bits(w.tree, ct, key0) >> (4 * b);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int key = key0 + 16 * (i >> 2) + 4 * b + (i & 3);
-                const bool see = ((valid >> (i >> 2)) & 1) && key < w.hi_key[ct] && key >= w.lo_key[ct];
+                bool see = ((valid >> (i >> 2)) & 1) && key < w.hi_key[ct] && key >= w.lo_key[ct];
+                if constexpr (TREE) see = see && (bits >> (16 * (i >> 2) + (i & 3)) & 1);
                 p[ct][i] = see ? p[ct][i] : -INFINITY;
             }
+        }
     }
     float mx[CT];
     bool up = false;
@@ -450,8 +487,8 @@ __device__ __forceinline__ void ka_reference(KvRows<D, CT> &w, float (&p)[CT][16
 }
 
 // Probabilities, and their sum.
-template <int D, int CT>
-__device__ __forceinline__ void ka_exponentials(KvRows<D, CT> &w, float (&p)[CT][16], float c2)
+template <int D, int CT, bool TREE>
+__device__ __forceinline__ void ka_exponentials(KvRows<D, CT, TREE> &w, float (&p)[CT][16], float c2)
 {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
@@ -477,8 +514,8 @@ __device__ __forceinline__ void ka_p_operands(const float (&x)[16], bf16x8 (&pb)
 
 // Scores of a step: k_op(t, k) gives K's operand of run t and product step k, ks
 // the lane's INT4 scales.
-template <int D, bool INT4, int CT, class KOp>
-__device__ __forceinline__ void ka_scores(const KvRows<D, CT> &w, float (&p)[CT][16], const float *ks, KOp k_op)
+template <int D, bool INT4, int CT, class KOp, bool TREE>
+__device__ __forceinline__ void ka_scores(const KvRows<D, CT, TREE> &w, float (&p)[CT][16], const float *ks, KOp k_op)
 {
     constexpr int KS = D / 32, NG = INT4 ? D / 64 : 1;
 #pragma unroll
@@ -537,8 +574,8 @@ __device__ __forceinline__ void ka_p(KvP<D, INT4, CT> &o, const float (&p)[CT][1
 
 // O^T += V^T P^T: v_op(n, h, lo, hi) gives V's operands of block n and runs 2 h,
 // 2 h + 1.
-template <int D, bool INT4, int CT, class VOp>
-__device__ __forceinline__ void ka_values(KvRows<D, CT> &w, const KvP<D, INT4, CT> &pb, VOp v_op)
+template <int D, bool INT4, int CT, class VOp, bool TREE>
+__device__ __forceinline__ void ka_values(KvRows<D, CT, TREE> &w, const KvP<D, INT4, CT> &pb, VOp v_op)
 {
     constexpr int NB = D / 32, NG = KvP<D, INT4, CT>::NG;
 #pragma unroll
@@ -559,8 +596,8 @@ __device__ __forceinline__ void ka_values(KvRows<D, CT> &w, const KvP<D, INT4, C
 // Few rows: the wave converts its own codes, steps s0, s0 + stride, .. < s1.
 // Codes are one step ahead, their pages two; past the end the last run's page
 // is looked up and nothing of it is used.
-template <int D, bool INT4, int CT>
-__device__ __forceinline__ void ka_walk(KvRows<D, CT> &w, const KvArgs &a, ka_const_int *table, int head, const KvRange &g,
+template <int D, bool INT4, int CT, bool TREE>
+__device__ __forceinline__ void ka_walk(KvRows<D, CT, TREE> &w, const KvArgs &a, ka_const_int *table, int head, const KvRange &g,
                                         int s0, int stride, float c2, int lane)
 {
     constexpr int NG = KvStep<D, INT4>::NG;
@@ -760,8 +797,8 @@ __device__ __forceinline__ void ka_take_scores(float (&p)[CT][16], const f32x4 (
 // Bytes of one stage of K or of V.
 constexpr int ka_stage(int D) { return 128 * D; }
 
-template <int D, bool INT4, int CT>
-__device__ __forceinline__ void ka_walk_shared(KvRows<D, CT> &w, uint8_t *lds, const KvArgs &a, ka_const_int *table,
+template <int D, bool INT4, int CT, bool TREE>
+__device__ __forceinline__ void ka_walk_shared(KvRows<D, CT, TREE> &w, uint8_t *lds, const KvArgs &a, ka_const_int *table,
                                                int head, const KvRange &g, float c2, int wave, int lane)
 {
     constexpr int KS = D / 32, NB = D / 32, STAGE = ka_stage(D), NG = INT4 ? D / 64 : 0, NS = INT4 ? NG : 1;
@@ -943,14 +980,14 @@ __device__ __forceinline__ void ka_store(const KvArgs &a, int split, size_t row,
 }
 
 // 16 rows, shared by the block's waves, which take the steps in turn.
-template <int D, bool INT4>
+template <int D, bool INT4, bool TREE>
 __device__ __forceinline__ void ka_few_rows(float *om, const KvArgs &a, ka_const_int *table, int split, int head, int qs,
                                             int qn, int kv, int64_t r0, int64_t rows, int wave, int lane)
 {
     const int j = lane & 15, b = lane >> 4, G = a.group;
     float (*mm)[16] = reinterpret_cast<float (*)[16]>(om + 16 * (D + 4)), (*ll)[16] = mm + 4;
     const float c2 = a.scale * kLog2e;
-    KvRows<D, 1> w;
+    KvRows<D, 1, TREE> w;
     ka_rows<D, INT4, 1>(w, a, head, qs, qn, kv, r0, rows, lane);
     const KvRange g = ka_range(a, split, qn, kv, r0, min(r0 + 16, rows));
     ka_walk<D, INT4, 1>(w, a, table, head, g, g.s0 + wave, 4, c2, lane);
@@ -988,12 +1025,12 @@ __device__ __forceinline__ void ka_few_rows(float *om, const KvArgs &a, ka_const
 }
 
 // 64 CT rows, 16 CT per wave.
-template <int D, bool INT4, int CT>
+template <int D, bool INT4, int CT, bool TREE>
 __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_const_int *table, int split, int head,
                                              int qs, int qn, int kv, int64_t r0, int64_t rows, int wave, int lane)
 {
     const int j = lane & 15, b = lane >> 4, G = a.group;
-    KvRows<D, CT> w;
+    KvRows<D, CT, TREE> w;
     ka_rows<D, INT4, CT>(w, a, head, qs, qn, kv, r0 + 16 * CT * wave, rows, lane);
     const KvRange g = ka_range(a, split, qn, kv, r0, min(r0 + 64 * CT, rows));
     // Two blocks share a compute unit, so two waves a SIMD.  Blocks go out one per
@@ -1017,7 +1054,7 @@ __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_c
 
 // CT > 0: blocks of 64 CT rows for the sequences of more than 16.  0: every list
 // of rows is taken 16 at a time.
-template <int D, bool INT4, int CT>
+template <int D, bool INT4, int CT, bool TREE>
 __global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
 {
     constexpr int SUMS = 4 * (16 * (D + 4) + 8 * 16), STAGES = 4 * ka_stage(D);
@@ -1037,8 +1074,8 @@ __global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
     const int block_rows = CT == 0 || rows <= 16 ? 16 : 64 * CT;
     // the last tiles first: under a causal mask they are the longest
     for (int64_t qt = (rows + block_rows - 1) / block_rows - 1 - qt0; qt >= 0; qt -= a.q_tiles) {
-        if (block_rows == 16) ka_few_rows<D, INT4>(reinterpret_cast<float *>(lds), a, table, split, head, qs, qn, kv, 16 * qt, rows, wave, lane);
-        else if constexpr (CT > 0) ka_many_rows<D, INT4, CT>(lds, a, table, split, head, qs, qn, kv, 64 * CT * qt, rows, wave, lane);
+        if (block_rows == 16) ka_few_rows<D, INT4, TREE>(reinterpret_cast<float *>(lds), a, table, split, head, qs, qn, kv, 16 * qt, rows, wave, lane);
+        else if constexpr (CT > 0) ka_many_rows<D, INT4, CT, TREE>(lds, a, table, split, head, qs, qn, kv, 64 * CT * qt, rows, wave, lane);
     }
 }
 
@@ -1108,7 +1145,7 @@ size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, i
 hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq, const int32_t *table, int table_width,
                                 const int32_t *q_start, const int32_t *kv_len, int B, int T, int heads_q, int max_q,
                                 int max_kv, float scale, int causal, int window, uint16_t *O, float *lse, float *work,
-                                hipStream_t stream)
+                                hipStream_t stream, const uint32_t *tree, int tree_words)
 {
     const int cus = device_cu_count();
     const KvPlan p = kv4_plan(T, B, c.heads, heads_q / c.heads, max_q, max_kv, cus);
@@ -1116,16 +1153,18 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
     a.c = c, a.Q = Q, a.ldq = ldq, a.table = table, a.q_start = q_start, a.kv_len = kv_len, a.O = O, a.lse = lse;
     a.work = work, a.T = T, a.B = B, a.heads_q = heads_q, a.group = heads_q / c.heads, a.table_width = table_width;
     a.q_tiles = p.q_tiles, a.splits = p.splits, a.split_steps = p.split_steps, a.causal = causal, a.window = window, a.scale = scale;
-    a.cus = cus;
+    a.cus = cus, a.tree = tree, a.tree_words = tree_words;
     const dim3 grid((uint32_t)kv4_blocks(p, B, c.heads));
-#define KA_LAUNCH(D, I) \
-    (p.many ? kv4_attention_kernel<D, I, kKv4ManyTiles><<<grid, 256, 0, stream>>>(a) \
-            : kv4_attention_kernel<D, I, 0><<<grid, 256, 0, stream>>>(a))
+#define KA_LAUNCH_ROWS(D, I, TREE) \
+    (p.many ? kv4_attention_kernel<D, I, kKv4ManyTiles, TREE><<<grid, 256, 0, stream>>>(a) \
+            : kv4_attention_kernel<D, I, 0, TREE><<<grid, 256, 0, stream>>>(a))
+#define KA_LAUNCH(D, I) (tree ? KA_LAUNCH_ROWS(D, I, true) : KA_LAUNCH_ROWS(D, I, false))
     if (c.int4 && c.dim == 64) KA_LAUNCH(64, true);
     else if (c.int4) KA_LAUNCH(128, true);
     else if (c.dim == 64) KA_LAUNCH(64, false);
     else KA_LAUNCH(128, false);
 #undef KA_LAUNCH
+#undef KA_LAUNCH_ROWS
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t n = (int64_t)T * heads_q;

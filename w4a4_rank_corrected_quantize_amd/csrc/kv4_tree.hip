@@ -1,0 +1,169 @@
+// kv4_tree.hip -- drafted tokens as a tree: their mask, places and slots from
+// the nodes' parents, and the move of an accepted path to where the next
+// tokens follow it.  Both are a few bytes per token and bound by latency: one
+// launch each, no length known to the host.
+#include "kv4.h"
+
+namespace svdq {
+namespace {
+
+__device__ __forceinline__ int kt_clamp(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+// A slot of place `at` of a sequence, -1 for a place or page that is none.
+__device__ __forceinline__ int kt_slot(const Kv4Tables &s, int seq, int64_t at)
+{
+    if (at < 0 || at >= (int64_t)s.width << s.page_shift) return -1;
+    const int page = s.table[(int64_t)seq * s.width + (at >> s.page_shift)];
+    return (uint32_t)page < (uint32_t)s.pages ? (page << s.page_shift) + (int)(at & ((1 << s.page_shift) - 1)) : -1;
+}
+
+// A thread walks from its node up to the root: parents come before their
+// children, so the walk ends and the mask's words are met from the last to the
+// first.
+constexpr int KT_LDS = 2048;
+
+__global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__restrict__ parent, Kv4Tables s, int T,
+                                                            uint32_t *__restrict__ mask, int words,
+                                                            int32_t *__restrict__ position,
+                                                            int32_t *__restrict__ slots)
+{
+    __shared__ int up[KT_LDS];
+    const int seq = blockIdx.x;
+    const int q0 = kt_clamp(s.q_start[seq], 0, T), n = kt_clamp(s.q_start[seq + 1], q0, T) - q0;
+    const int kv = kt_clamp(s.kv_len[seq], 0, s.width << s.page_shift);
+    for (int i = threadIdx.x; i < min(n, KT_LDS); i += 256) up[i] = parent[q0 + i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 256) {
+        uint32_t *row = mask + (int64_t)(q0 + i) * words;
+        int w = words - 1, depth = -1;
+        uint32_t bits = 0;
+        for (int j = i; j >= 0;) {
+            for (; w > j >> 5; --w) row[w] = bits, bits = 0;
+            if (w == j >> 5) bits |= 1u << (j & 31);
+            ++depth;
+            const int p = j < KT_LDS ? up[j] : parent[q0 + j];
+            j = p < j ? p : -1;                            // a parent that is none: a root
+        }
+        for (; w >= 0; --w) row[w] = bits, bits = 0;
+        if (position) position[q0 + i] = kv - n + depth;
+        if (slots) slots[q0 + i] = kt_slot(s, seq, (int64_t)kv - n + i);
+    }
+}
+
+// Bytes of one token and head: K codes D / 2 in four parts, V codes D / 2 in
+// single bytes, the scales; each thread holds one piece of each token.
+template <bool INT4, int D>
+struct KtToken {
+    static constexpr int NG = INT4 ? D / 64 : D / 32;
+    static constexpr int KD = D / 8, VB = D / 2;           // dwords of K, bytes of V
+};
+
+// A block moves one sequence's path in one head.  It reads the pieces of 32
+// tokens, waits for all of them, and writes: a path's nodes ascend, so a node
+// lies at or behind its new place, and nothing that is written is read later.
+template <bool INT4, int D>
+__global__ __launch_bounds__(256) void kv4_keep_path_kernel(Kv4View c, Kv4Tables s, int T,
+                                                            const int32_t *__restrict__ path, int max_path,
+                                                            int32_t *__restrict__ new_len)
+{
+    typedef KtToken<INT4, D> Tok;
+    constexpr int NG = Tok::NG, CHUNK = 32;
+    __shared__ int src[CHUNK], dst[CHUNK];
+    const int head = blockIdx.x % c.heads, seq = blockIdx.x / c.heads, tid = threadIdx.x;
+    const int q0 = kt_clamp(s.q_start[seq], 0, T), n = kt_clamp(s.q_start[seq + 1], q0, T) - q0;
+    const int kv = kt_clamp(s.kv_len[seq], 0, s.width << s.page_shift);
+    const int32_t *nodes = path + (int64_t)seq * max_path;
+    const int most = min(max_path, n);
+    int kept = 0;
+    bool more = true;
+    for (int at = 0; at < most && more; at += CHUNK) {
+        // the chunk's nodes: a path ends at the first that is not behind the one before it
+        const int left = min(CHUNK, most - at);
+        __syncthreads();
+        if (tid < 64) {
+            const int i = at + tid;
+            const int node = tid < left ? nodes[i] : -1;
+            const int before = tid < left && i > 0 ? nodes[i - 1] : -1;
+            const bool good = tid < left && node > before && node < n;
+            const uint64_t bad = ~__ballot(good);
+            const int count = bad ? __builtin_ctzll(bad) : 64;
+            if (tid < CHUNK) {
+                const int64_t base = (int64_t)kv - n;
+                const bool move = tid < count && node != i;
+                const int a = move ? kt_slot(s, seq, base + node) : -1, b = move ? kt_slot(s, seq, base + i) : -1;
+                src[tid] = a >= 0 && b >= 0 ? a : -1;
+                dst[tid] = tid < count ? b : -2;           // -2: the path has ended
+            }
+        }
+        __syncthreads();
+        int count = 0;
+        while (count < left && dst[count] != -2) ++count;
+        kept += count;
+        more = count == CHUNK;
+        // pieces of 4 bytes of K, 1 of V, one scale each: unit u of token k
+        constexpr int UNITS = Tok::KD + Tok::VB + 2 * NG;
+        constexpr int PER = (CHUNK * UNITS + 255) / 256;
+        uint32_t held[PER];
+        auto place = [&](int slot, int u, uint8_t *&p) {
+            const size_t page = (size_t)(slot >> c.page_shift);
+            const int in = slot & ((1 << c.page_shift) - 1), r = in & 15;
+            const size_t run = (((page * c.heads + head) << c.page_shift) + in) >> 4;
+            if (u < Tok::KD) {
+                p = c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(r, 8 * u, D);
+                return 4;
+            }
+            u -= Tok::KD;
+            if (u < Tok::VB) {
+                p = c.v_codes + run * (8 * D) + kv4_v_offset(r, u >> 4, u & 15, D);
+                return 1;
+            }
+            u -= Tok::VB;
+            void *sc = u < NG ? c.k_scales : c.v_scales;
+            u = u < NG ? u : u - NG;
+            p = (uint8_t *)sc + (run * (16 * NG) + 16 * u + r) * (INT4 ? 4 : 1);
+            return INT4 ? 4 : 1;
+        };
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int e = tid + 256 * k, tok = e / UNITS, u = e % UNITS;
+            held[k] = 0;
+            if (tok >= count || src[tok] < 0) continue;
+            uint8_t *p;
+            if (place(src[tok], u, p) == 4) held[k] = *reinterpret_cast<const uint32_t *>(p);
+            else held[k] = *p;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces have arrived
+        __syncthreads();                                   // and every wave's
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int e = tid + 256 * k, tok = e / UNITS, u = e % UNITS;
+            if (tok >= count || src[tok] < 0) continue;
+            uint8_t *p;
+            if (place(dst[tok], u, p) == 4) *reinterpret_cast<uint32_t *>(p) = held[k];
+            else *p = (uint8_t)held[k];
+        }
+    }
+    if (head == 0 && tid == 0) new_len[seq] = kv - n + kept;
+}
+
+}  // namespace
+
+hipError_t launch_kv4_tree_plan(const int32_t *parent, const Kv4Tables &s, int B, int T, uint32_t *mask, int words,
+                                int32_t *position, int32_t *slots, hipStream_t stream)
+{
+    kv4_tree_plan_kernel<<<B, 256, 0, stream>>>(parent, s, T, mask, words, position, slots);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv4_keep_path(const Kv4View &c, const Kv4Tables &s, int B, int T, const int32_t *path, int max_path,
+                                int32_t *new_len, hipStream_t stream)
+{
+    const uint32_t grid = (uint32_t)B * c.heads;
+    if (c.int4 && c.dim == 64) kv4_keep_path_kernel<true, 64><<<grid, 256, 0, stream>>>(c, s, T, path, max_path, new_len);
+    else if (c.int4) kv4_keep_path_kernel<true, 128><<<grid, 256, 0, stream>>>(c, s, T, path, max_path, new_len);
+    else if (c.dim == 64) kv4_keep_path_kernel<false, 64><<<grid, 256, 0, stream>>>(c, s, T, path, max_path, new_len);
+    else kv4_keep_path_kernel<false, 128><<<grid, 256, 0, stream>>>(c, s, T, path, max_path, new_len);
+    return hipGetLastError();
+}
+
+}  // namespace svdq

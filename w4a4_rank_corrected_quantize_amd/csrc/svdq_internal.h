@@ -103,6 +103,23 @@ hipError_t launch_lora_linear(const uint16_t *X, const uint16_t *A, const uint16
                               const void *plan, const uint16_t *base, int M, int N, int K, int R, int n, uint16_t *Y,
                               float *work, hipStream_t stream);
 
+// Rotary positions (rope.hip): norm and rotation of a step's query and key
+// heads; Ko, ldko unused where the keys go into the cache.
+struct RopeArgs {
+    const uint16_t *Q, *K, *wq, *wk;
+    uint16_t *Qo, *Ko;
+    int64_t ldq, ldk, ldqo, ldko;
+    const float *cos, *sin;
+    const int32_t *index;
+    double eps;
+    int T, heads_q, heads_k, table_rows, pairs;
+    int parts;                      // waves per token, set by the launch
+};
+void rope_frequencies(const int *sections, int axes, double theta, svdq_rope_axes layout, double *freq, int32_t *axis);
+hipError_t launch_rope_table(const int32_t *pos, int T, int axes, const double *freq, const int32_t *axis, int pairs,
+                             float *cos, float *sin, hipStream_t stream);
+hipError_t launch_qk_norm_rope(RopeArgs r, int dim, bool halves, hipStream_t stream);
+
 // 4-bit key / value cache (kv4.h has the layout; kv4_cache.hip,
 // kv4_attention.hip).
 struct Kv4View {
@@ -114,11 +131,22 @@ struct Kv4View {
 hipError_t launch_kv4_append(const Kv4View &c, const uint16_t *K, const uint16_t *V, int64_t ldk, int64_t ldv,
                              const int32_t *slots, int T, hipStream_t stream);
 hipError_t launch_kv4_read(const Kv4View &c, const int32_t *slots, int T, float *K, float *V, hipStream_t stream);
+hipError_t launch_kv4_rope_append(const Kv4View &c, RopeArgs r, bool halves, const uint16_t *V, int64_t ldv,
+                                  const int32_t *slots, hipStream_t stream);
+// Sequences of a step: their pages, rows and keys.
+struct Kv4Tables {
+    const int32_t *table, *q_start, *kv_len;
+    int width, page_shift, pages;
+};
+hipError_t launch_kv4_tree_plan(const int32_t *parent, const Kv4Tables &s, int B, int T, uint32_t *mask, int words,
+                                int32_t *position, int32_t *slots, hipStream_t stream);
+hipError_t launch_kv4_keep_path(const Kv4View &c, const Kv4Tables &s, int B, int T, const int32_t *path, int max_path,
+                                int32_t *new_len, hipStream_t stream);
 // Splits of the keys keep their sums in `work` (0 bytes without a split).
 size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv);
 hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq, const int32_t *table, int table_width,
                                 const int32_t *q_start, const int32_t *kv_len, int B, int T, int heads_q, int max_q,
                                 int max_kv, float scale, int causal, int window, uint16_t *O, float *lse, float *work,
-                                hipStream_t stream);
+                                hipStream_t stream, const uint32_t *tree = nullptr, int tree_words = 0);
 
 }  // namespace svdq
