@@ -51,6 +51,7 @@
  *   - Ownership: the caller allocates and frees every buffer.  No call
  *     allocates device memory or keeps a pointer after it returns.
  *   - Device calls (svdq_quantize_act, svdq_w4a4_linear,
+ *     svdq_w4a4_linear_few, svdq_w4a4_linear_gated,
  *     svdq_w4a4_linear_requant, svdq_w4a4_linear_splitk,
  *     svdq_w4a4_linear_qkv_norm_rope, svdq_awq_w4a16_linear,
  *     svdq_residual_norm, svdq_lora_*, svdq_rope_table, svdq_qk_norm_rope,
@@ -107,6 +108,13 @@ typedef enum svdq_epilogue {
     SVDQ_EPI_GELU_TANH = 1, /* 0.5 y (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) after the bias */
     SVDQ_EPILOGUE_INT_RANGE_ = 0x7FFFFFFF    /* not an epilogue: every int is a valid value (calls reject it) */
 } svdq_epilogue;
+
+/* Activation of a gated linear's gate. */
+typedef enum svdq_activation {
+    SVDQ_ACT_SILU = 0,       /* g / (1 + exp(-g)) */
+    SVDQ_ACT_GELU_TANH = 1,  /* as SVDQ_EPI_GELU_TANH */
+    SVDQ_ACTIVATION_INT_RANGE_ = 0x7FFFFFFF  /* not an activation: every int is a valid value (calls reject it) */
+} svdq_activation;
 
 typedef enum svdq_norm {
     SVDQ_NORM_NONE = 0,
@@ -251,6 +259,41 @@ svdq_status svdq_w4a4_linear(const uint8_t *xq, const void *xscale, const float 
                              const uint8_t *wq, const void *wscale, const uint16_t *up,
                              const uint16_t *bias, int M, int N, int K, int rank,
                              svdq_precision prec, svdq_epilogue epi, uint16_t *Y, void *stream);
+
+/*
+ * svdq_w4a4_linear_few -- svdq_w4a4_linear for the few rows of a decoding step
+ * (single tokens, a tree of drafted tokens), where the tiles of svdq_w4a4_linear
+ * would leave most of the chip idle: one pass over the weights, 16 rows of them
+ * per block.  Arguments as for svdq_w4a4_linear, with
+ *   M            0 .. SVDQ_FEW_MAX_ROWS (SVDQ_ERR_UNSUPPORTED above)
+ * INT4: exact integer sums per group, scale product and accumulation in fp32.
+ * Partial sums over K are added in a fixed order, so results are deterministic;
+ * they may differ from svdq_w4a4_linear's in the last bf16 places.  One kernel
+ * launch.  Errors as for svdq_w4a4_linear.
+ */
+#define SVDQ_FEW_MAX_ROWS 64
+svdq_status svdq_w4a4_linear_few(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
+                                 const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int N, int K,
+                                 int rank, svdq_precision prec, svdq_epilogue epi, uint16_t *Y, void *stream);
+
+/*
+ * svdq_w4a4_linear_gated -- the first half of a gated MLP in one kernel: gate
+ * and up projection, activation and product,
+ *   Y_mf = act(y_mf) * y_m,F+f,   y = svdq_w4a4_linear of 2 F channels
+ * in fp32 from the sums to one rounding.
+ *   wq, wscale, up, bias   of 2 F output channels, the gate's F first, then the
+ *                up projection's: the packed tensors of the two weights on top of
+ *                each other (packed together, or apart with the same smoothing)
+ *   M, F, K      M >= 0, F >= 0 (either 0: no-op), F % 8 == 0, K % group == 0
+ *   act          svdq_activation
+ *   Y            [M][F] bf16 bits, device (out)
+ * Any M: up to SVDQ_FEW_MAX_ROWS rows run as in svdq_w4a4_linear_few, more in
+ * the tiles of svdq_w4a4_linear.  One kernel launch.  Errors as for
+ * svdq_w4a4_linear.
+ */
+svdq_status svdq_w4a4_linear_gated(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
+                                   const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int F, int K,
+                                   int rank, svdq_precision prec, svdq_activation act, uint16_t *Y, void *stream);
 
 /*
  * svdq_w4a4_linear_splitk_workspace_bytes -- device workspace that

@@ -11,6 +11,7 @@ Functions mirror the C ABI in include/svdq.h:
     pack_residual(W, smooth, down, up, prec=INT4)              host, numpy in/out
     quantize_act(X, smooth, down, prec=INT4, ...)              device, torch tensors
     w4a4_linear(xq, xscale, h, wq, wscale, up, bias, ...)      device, torch tensors
+    w4a4_linear_few(...), w4a4_linear_gated(...)                device, torch tensors
     w4a4_linear_requant(...)                                    device, torch tensors
     w4a4_linear_qkv_norm_rope(...)                              device, torch tensors
     awq_pack_weights(W)                                         host, numpy in/out
@@ -52,6 +53,9 @@ INT4 = 0
 MXFP4 = 1
 EPI_NONE = 0
 EPI_GELU_TANH = 1
+ACT_SILU = 0
+ACT_GELU_TANH = 1
+FEW_MAX_ROWS = 64
 NORM_NONE = 0
 NORM_RMS = 1
 NORM_LAYER = 2
@@ -76,7 +80,7 @@ EXPORTS = ("svdq_status_string", "svdq_version", "svdq_check_device", "svdq_pack
            "svdq_lora_workspace_bytes", "svdq_lora_plan", "svdq_lora_linear", "svdq_kv4_append", "svdq_kv4_read",
            "svdq_kv4_attention_workspace_bytes", "svdq_kv4_attention", "svdq_rope_frequencies", "svdq_rope_table",
            "svdq_qk_norm_rope", "svdq_kv4_rope_append", "svdq_kv4_tree_plan", "svdq_kv4_tree_attention",
-           "svdq_kv4_keep_path")
+           "svdq_kv4_keep_path", "svdq_w4a4_linear_few", "svdq_w4a4_linear_gated")
 
 
 class SvdqError(RuntimeError):
@@ -111,6 +115,10 @@ def lib():
         L.svdq_quantize_act.argtypes = [P, I, I, P, P, I, I, P, P, P, P]
         L.svdq_w4a4_linear.restype = I
         L.svdq_w4a4_linear.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P, P]
+        L.svdq_w4a4_linear_few.restype = I
+        L.svdq_w4a4_linear_few.argtypes = L.svdq_w4a4_linear.argtypes
+        L.svdq_w4a4_linear_gated.restype = I
+        L.svdq_w4a4_linear_gated.argtypes = L.svdq_w4a4_linear.argtypes
         L.svdq_w4a4_linear_splitk_workspace_bytes.restype = ctypes.c_size_t
         L.svdq_w4a4_linear_splitk_workspace_bytes.argtypes = [I, I, I, I]
         L.svdq_w4a4_linear_splitk.restype = I
@@ -736,6 +744,59 @@ def _mod_rows(D, gate, scale, shift):
     if B > _I32 or ld > _I32:
         raise SvdqError(-2, "svdq_residual_norm")
     return B, ld
+
+
+def _few_args(where, xq, xscale, h, wq, wscale, up, bias, prec, halves, Y, stream):
+    """Checks the operands of a linear whose weight has `halves` times its output
+    channels; returns Y and the library call's arguments up to K."""
+    torch = _T or _tt()
+    prec = _prec(prec)
+    u8, bf, f32 = torch.uint8, torch.bfloat16, torch.float32
+    sdt, g = (f32, 64) if prec == INT4 else (u8, 32)
+    _ndim(xq, 2, "xq")
+    _ndim(wq, 2, "wq")
+    _ndim(up, 2, "up")
+    M, KB = xq.shape
+    N, r = up.shape
+    K = 2 * KB
+    if xq.numel() >= _ELEMENTS or wq.numel() >= _ELEMENTS:
+        raise SvdqError(-2, where)
+    _arg(xq, u8, "xq")
+    _arg(xscale, sdt, "xscale", (M, K // g))
+    _arg(h, f32, "h", (M, r))
+    _arg(wq, u8, "wq", (N, KB))
+    _arg(wscale, sdt, "wscale", (N, K // g))
+    _arg(up, bf, "up")
+    if bias is not None:
+        _arg(bias, bf, "bias", (N,))
+    if N % halves:
+        raise ValueError(f"wq has {N} rows, expected a gate and an up projection of the same size")
+    C, dev = N // halves, xq.device
+    Y = _empty((M, C), bf, dev, stream) if Y is None else _arg(Y, bf, "Y", (M, C))
+    raw = _launch(dev, ("xscale", "h", "wq", "wscale", "up", "bias", "Y"), (xscale, h, wq, wscale, up, bias, Y), stream)
+    return Y, prec, raw, (xq.data_ptr(), xscale.data_ptr(), h.data_ptr(), wq.data_ptr(), wscale.data_ptr(),
+                          up.data_ptr(), _ptr(bias), M, C, K, r)
+
+
+def w4a4_linear_few(xq, xscale, h, wq, wscale, up, bias, prec: int = INT4, epi: int = EPI_NONE, Y=None, stream=None):
+    """w4a4_linear for up to FEW_MAX_ROWS rows (single tokens, drafted tokens):
+    one pass over the weights (one kernel)."""
+    Y, prec, raw, args = _few_args("svdq_w4a4_linear_few", xq, xscale, h, wq, wscale, up, bias, prec, 1, Y, stream)
+    st = lib().svdq_w4a4_linear_few(*args, prec, epi, Y.data_ptr(), raw)
+    if st:
+        raise SvdqError(st, "svdq_w4a4_linear_few")
+    return Y
+
+
+def w4a4_linear_gated(xq, xscale, h, wq, wscale, up, bias, prec: int = INT4, act: int = ACT_SILU, Y=None, stream=None):
+    """act(gate) * up of a gated MLP (one kernel): wq, wscale, up and bias hold the
+    gate projection's rows, then the up projection's.  Any number of rows; Y [M][F]
+    bf16."""
+    Y, prec, raw, args = _few_args("svdq_w4a4_linear_gated", xq, xscale, h, wq, wscale, up, bias, prec, 2, Y, stream)
+    st = lib().svdq_w4a4_linear_gated(*args, prec, act, Y.data_ptr(), raw)
+    if st:
+        raise SvdqError(st, "svdq_w4a4_linear_gated")
+    return Y
 
 
 class LoraPlan:

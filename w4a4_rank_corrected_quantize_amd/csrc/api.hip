@@ -153,6 +153,49 @@ extern "C" svdq_status svdq_w4a4_linear(const uint8_t *xq, const void *xscale, c
     return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
 }
 
+// Checks of a linear of N weight rows and C output channels (device and empty sizes included).
+static svdq_status check_linear(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
+                                const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int64_t N, int C,
+                                int K, int rank, svdq_precision prec, const uint16_t *Y)
+{
+    svdq_status st = check_common(M, K, rank, prec);
+    if (st != SVDQ_OK) return st;
+    if (C < 0) return SVDQ_ERR_INVALID_ARG;
+    if (C % 8 != 0 || !elems_ok(N, K) || !elems_ok(M, C)) return SVDQ_ERR_SHAPE;
+    if ((M > 0 && (!xq || !xscale || !h)) || (C > 0 && (!wq || !wscale || !up)) || (M > 0 && C > 0 && !Y))
+        return SVDQ_ERR_INVALID_ARG;
+    if (!aligned16(xq) || !aligned16(xscale) || !aligned16(h) || !aligned16(wq) || !aligned16(wscale) ||
+        !aligned16(up) || !aligned16(bias) || !aligned16(Y))
+        return SVDQ_ERR_MISALIGNED;
+    return current_device_ok();
+}
+
+extern "C" svdq_status svdq_w4a4_linear_few(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
+                                            const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int N,
+                                            int K, int rank, svdq_precision prec, svdq_epilogue epi, uint16_t *Y,
+                                            void *stream)
+{
+    if (epi != SVDQ_EPI_NONE && epi != SVDQ_EPI_GELU_TANH) return SVDQ_ERR_INVALID_ARG;
+    if (M > SVDQ_FEW_MAX_ROWS) return SVDQ_ERR_UNSUPPORTED;
+    svdq_status st = check_linear(xq, xscale, h, wq, wscale, up, bias, M, N, N, K, rank, prec, Y);
+    if (st != SVDQ_OK || M == 0 || N == 0) return st;
+    hipError_t e = launch_w4a4_few(xq, xscale, h, wq, wscale, up, bias, M, N, K, prec, epi, Y, (hipStream_t)stream);
+    return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
+extern "C" svdq_status svdq_w4a4_linear_gated(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
+                                              const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int F,
+                                              int K, int rank, svdq_precision prec, svdq_activation act, uint16_t *Y,
+                                              void *stream)
+{
+    if (act != SVDQ_ACT_SILU && act != SVDQ_ACT_GELU_TANH) return SVDQ_ERR_INVALID_ARG;
+    svdq_status st = check_linear(xq, xscale, h, wq, wscale, up, bias, M, 2 * (int64_t)F, F, K, rank, prec, Y);
+    if (st != SVDQ_OK || M == 0 || F == 0) return st;
+    hipError_t e = launch_w4a4_linear_gated(xq, xscale, h, wq, wscale, up, bias, M, F, K, prec, act, Y,
+                                            (hipStream_t)stream);
+    return e == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP;
+}
+
 extern "C" size_t svdq_w4a4_linear_splitk_workspace_bytes(int M, int N, int K, svdq_precision prec)
 {
     if (M <= 0 || N <= 0 || K <= 0 || (prec != SVDQ_INT4 && prec != SVDQ_MXFP4)) return 0;

@@ -41,6 +41,7 @@
 // applies GELU and rounds.
 #include "svdq_internal.h"
 #include "svdq_quant.h"
+#include "w4a4_epilogue.h"
 
 namespace svdq {
 namespace {
@@ -49,56 +50,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ float bf16_to_f32(uint32_t b) { return bits_f32(b << 16); }
-
-// two fp32 -> two bf16 (round to nearest even), packed low | high << 16
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    const f32x2 v = {lo, hi};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-}
-
-// GELU, tanh form: 0.5 y (1 + tanh(u)) = y / (1 + exp(-2u)),
-// u = sqrt(2/pi) (y + 0.044715 y^3); exp via the hardware exp2.
-__device__ __forceinline__ float gelu_tanh(float y)
-{
-    const float k1 = -2.302208198f;      // -2 sqrt(2/pi) log2(e)
-    const float k3 = -0.102943836f;      // -2 sqrt(2/pi) 0.044715 log2(e)
-    const float t = y * __builtin_fmaf(k3, y * y, k1);
-    return y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
-}
-
-// 8 fp32 values of h -> bf16 hi and lo parts (hi = bf16(h), lo = bf16(h - hi)).
-__device__ __forceinline__ void split_h(const float *hv, bf16x8 &hi8, bf16x8 &lo8)
-{
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        hi[i] = pack_bf16x2(hv[2 * i], hv[2 * i + 1]);
-        lo[i] = pack_bf16x2(hv[2 * i] - bf16_to_f32(hi[i] & 0xFFFFu), hv[2 * i + 1] - bf16_to_f32(hi[i] >> 16));
-    }
-    hi8 = __builtin_bit_cast(bf16x8, (uint4){hi[0], hi[1], hi[2], hi[3]});
-    lo8 = __builtin_bit_cast(bf16x8, (uint4){lo[0], lo[1], lo[2], lo[3]});
-}
-
-__device__ __forceinline__ void load_h8(const float *__restrict__ h, int m, int M, int k, float *hv)
-{
-    if (m < M) {
-        const float4 a = *reinterpret_cast<const float4 *>(h + (size_t)m * 32 + k);
-        const float4 b = *reinterpret_cast<const float4 *>(h + (size_t)m * 32 + k + 4);
-        hv[0] = a.x; hv[1] = a.y; hv[2] = a.z; hv[3] = a.w;
-        hv[4] = b.x; hv[5] = b.y; hv[6] = b.z; hv[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) hv[i] = 0.0f;
-    }
-}
-
 // Bias of 4 consecutive channels n..n+3 as 4 bf16 (zero when there is no
 // bias or n >= N).
 __device__ __forceinline__ uint2 bias4(const uint16_t *__restrict__ bias, int n, int N)
@@ -294,6 +245,7 @@ struct RequantArgs {
 constexpr int EPI_STORE = 0;      // y -> bf16 Y
 constexpr int EPI_REQUANT = 1;    // the next layer's activation step (RequantArgs)
 constexpr int EPI_QKNORM = 2;     // Q/K RMS-norm + rotary embedding of a QKV projection (QKNormArgs)
+constexpr int EPI_GATED = 3;      // act(gate) * up -> bf16 Y of N / 2 channels
 
 // The fused attention-input step: N = 3 H 128 output channels are H heads of
 // Q, then K, then V.  Q and K heads are RMS-normalized over their 128
@@ -614,6 +566,73 @@ __device__ __forceinline__ void qknorm_epilogue(const f32x16 (&acc)[I4_TN][I4_TM
     }
 }
 
+// Gated linears.  The weight has N = 2 F rows, gate f and up F + f, and a block
+// tile of 256 rows holds both rows of 128 channels, so that a lane ends up with
+// gate and up of the same outputs.  A wave's rows are 32 S gate rows, then the up
+// rows of the same channels; row v of block tile `tile`:
+template <int S>
+__device__ __forceinline__ int gated_row(int tile, int v, int N)
+{
+    const int w = v / (64 * S), i = v % (64 * S), half = i / (32 * S), F = N >> 1;
+    return half * F + min(128 * tile + 32 * S * w + i % (32 * S), F - 1);
+}
+
+// act(gate) * up for the lane's 4 consecutive channels, packed as 4 bf16.
+__device__ __forceinline__ uint2 gated4(const f32x16 &g, const f32x16 &u, int j, int gelu)
+{
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (gelu ? gelu_tanh(g[4 * j + e]) : silu(g[4 * j + e])) * u[4 * j + e];
+    return make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+}
+
+// Low-rank term and bias of weight row `row` of a 32x32 tile's lane, added to
+// two token tiles.
+__device__ __forceinline__ void gated_lowrank(f32x16 (&lr)[2], const f32x16 (&acc)[2], const bf16x8 (&hhi)[2][2],
+                                              const bf16x8 (&hlo)[2][2], const uint16_t *__restrict__ up,
+                                              const uint16_t *__restrict__ bias, int row, int N, int hk)
+{
+    bf16x8 ua[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+        ua[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(up + (size_t)row * 32 + 16 * s + 8 * hk));
+    const bf16x8 bq = bias_operand(bias, row, N, hk), ones = ones_operand(hk);
+#pragma unroll
+    for (int tm = 0; tm < 2; ++tm) lr[tm] = add_lowrank_bias(acc[tm], ua, hhi[tm], hlo[tm], bq, ones);
+}
+
+// Epilogue of the gated INT4 kernel: the block's 128 tokens x 128 channels are
+// staged as whole rows and stored as 256-byte segments.
+constexpr int GATED_STRIDE = 256 + 16;
+
+__device__ __forceinline__ void gated_epilogue(const f32x16 (&acc)[I4_TN][I4_TM], const bf16x8 (&hhi)[I4_TM][2],
+                                               const bf16x8 (&hlo)[I4_TM][2], const uint16_t *__restrict__ up,
+                                               const uint16_t *__restrict__ bias, int M, int N, int gelu,
+                                               uint16_t *__restrict__ Y, int tile_n, int m0, int wn, int wm, int tid,
+                                               int lane, uint8_t *smem)
+{
+    static_assert(I4_TN == 2 && I4_TM == 2, "a gate and an up tile per wave");
+    const int l32 = lane & 31, hk = lane >> 5, F = N >> 1;
+    f32x16 lr[2][2];
+#pragma unroll
+    for (int tn = 0; tn < 2; ++tn)
+        gated_lowrank(lr[tn], acc[tn], hhi, hlo, up, bias, gated_row<1>(tile_n, 64 * wn + 32 * tn + l32, N), N, hk);
+#pragma unroll
+    for (int tm = 0; tm < 2; ++tm)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint2 *>(smem + (wm * I4_WM + tm * 32 + l32) * GATED_STRIDE + 2 * (32 * wn + 8 * j + 4 * hk)) =
+                gated4(lr[0][tm], lr[1][tm], j, gelu);
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < I4_BM * 16 / I4_THREADS; ++it) {
+        const int idx = tid + I4_THREADS * it, r = idx >> 4, seg = idx & 15;
+        const int m = m0 + r, n = 128 * tile_n + 8 * seg;
+        if (m < M && n < F)
+            store_nt(Y + (size_t)m * F + n, *reinterpret_cast<const uint4 *>(smem + r * GATED_STRIDE + 16 * seg));
+    }
+}
+
 // Scale panels hold 8 groups of every W and X row of the block tile, a row of
 // 8 floats per matrix row; group g of row r sits at position g ^ sp_swz(r), so
 // that the 8-byte reads of 32 consecutive rows fall in distinct banks.
@@ -648,8 +667,9 @@ __global__ __launch_bounds__(I4_THREADS) void w4a4_int4_kernel(
     constexpr int WCH = I4_BN * 4, XCH = I4_BM * 4;
     static_assert(WCH == 2 * I4_THREADS && XCH == I4_THREADS, "loader shape");
     const int lseg = tid & 3, lr = tid >> 2;
-    const uint8_t *__restrict__ pw0 = wq + (size_t)min(n0 + lr, N - 1) * KB + lseg * 16;
-    const uint8_t *__restrict__ pw1 = wq + (size_t)min(n0 + lr + I4_BN / 2, N - 1) * KB + lseg * 16;
+    constexpr bool GATED = EPI == EPI_GATED;
+    const uint8_t *__restrict__ pw0 = wq + (size_t)(GATED ? gated_row<1>(tn_, lr, N) : min(n0 + lr, N - 1)) * KB + lseg * 16;
+    const uint8_t *__restrict__ pw1 = wq + (size_t)(GATED ? gated_row<1>(tn_, lr + I4_BN / 2, N) : min(n0 + lr + I4_BN / 2, N - 1)) * KB + lseg * 16;
     const uint8_t *__restrict__ px0 = xq + (size_t)min(m0 + lr, M - 1) * KB + lseg * 16;
     // Scales: threads [0, BN) turn the sw of W row t, threads [BN, BN + BM)
     // the sx of X row t - BN into the step's scale operands; the others idle.
@@ -661,14 +681,14 @@ __global__ __launch_bounds__(I4_THREADS) void w4a4_int4_kernel(
     const bool sc_w = tid < I4_BN, sc_x = tid >= I4_BN && tid < I4_BN + I4_BM;
     const uint32_t sp_lds0 = lds_offset(&sm.sp[0][0]);
     const int wave_u = __builtin_amdgcn_readfirstlane(wave);      // DMA bases and LDS offsets are uniform
-    const float *__restrict__ wsb = wscale + (size_t)n0 * G;      // the tile's first rows
+    const float *__restrict__ wsb = GATED ? wscale : wscale + (size_t)n0 * G;      // the tile's first rows
     const float *__restrict__ xsb = xscale + (size_t)m0 * G;
     uint32_t sp_off[6];                                          // byte offset of the lane's (row, group 0..7)
 #pragma unroll
     for (int j = 0; j < 6; ++j) {
         const int i = 6 * wave + j, d = 64 * i + lane, r = d >> 3;
         const int g = (d & 7) ^ sp_swz(r);
-        const int rr = r < I4_BN ? min(r, N - 1 - n0) : min(r - I4_BN, M - 1 - m0);
+        const int rr = r < I4_BN ? (GATED ? gated_row<1>(tn_, r, N) : min(r, N - 1 - n0)) : min(r - I4_BN, M - 1 - m0);
         sp_off[j] = (uint32_t)(rr * G + g) * 4u;
     }
     auto sp_issue = [&](int p) {
@@ -835,6 +855,11 @@ __global__ __launch_bounds__(I4_THREADS) void w4a4_int4_kernel(
     if constexpr (EPI == EPI_REQUANT) {
         requant_epilogue(acc, hhi, hlo, up, bias, M, N, gelu, rq, mb, nb, tn_, m0, wn, wm, tid, lane,
                          reinterpret_cast<float *>(&sm));
+        return;
+    }
+    if constexpr (EPI == EPI_GATED) {
+        static_assert(I4_BM * GATED_STRIDE <= sizeof(I4Smem), "the block's outputs fit in LDS");
+        gated_epilogue(acc, hhi, hlo, up, bias, M, N, gelu, Y, tn_, m0, wn, wm, tid, lane, reinterpret_cast<uint8_t *>(&sm));
         return;
     }
     if constexpr (EPI == EPI_QKNORM) {
@@ -1253,6 +1278,46 @@ __device__ __forceinline__ void wave_epilogue(const f32x16 (&acc)[TN][TM], const
     }
 }
 
+// Gated form of wave_epilogue, for a wave of 64 channels' gate rows (tiles 0, 1)
+// and up rows (2, 3) of block tile `tile_n`.
+__device__ __forceinline__ void gated_wave_epilogue(const f32x16 (&acc)[MX_TN][MX_TM], const float *__restrict__ h,
+                                                    const uint16_t *__restrict__ up,
+                                                    const uint16_t *__restrict__ bias, int M, int N, int gelu,
+                                                    uint16_t *__restrict__ Y, int mb, int tile_n, int wn,
+                                                    uint8_t *tile, int lane)
+{
+    static_assert(MX_TN == 4 && MX_TM == 2, "two gate and two up tiles per wave");
+    const int l32 = lane & 31, hk = lane >> 5;
+    bf16x8 hhi[MX_TM][2], hlo[MX_TM][2];
+#pragma unroll
+    for (int tm = 0; tm < MX_TM; ++tm)
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) {
+            float hv[8];
+            load_h8(h, mb + tm * 32 + l32, M, 16 * s2 + 8 * hk, hv);
+            split_h(hv, hhi[tm][s2], hlo[tm][s2]);
+        }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        f32x16 lr[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            gated_lowrank(lr[k], acc[t + 2 * k], hhi, hlo, up, bias, gated_row<2>(tile_n, 128 * wn + 64 * k + 32 * t + l32, N),
+                          N, hk);
+#pragma unroll
+        for (int tm = 0; tm < MX_TM; ++tm)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                stage4(tile, tm * 32 + l32, t * 32 + 8 * j + 4 * hk, gated4(lr[0][tm], lr[1][tm], j, gelu));
+    }
+    // the staged rows are read back by other lanes of this wave
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    flush_tile(tile, Y, mb, 128 * tile_n + 64 * wn, M, N >> 1, lane);
+}
+
+template <bool GATED>
 __global__ __launch_bounds__(MX_THREADS) void w4a4_mxfp4_kernel(
     const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xscale, const float *__restrict__ h,
     const uint8_t *__restrict__ wq, const uint8_t *__restrict__ wscale, const uint16_t *__restrict__ up,
@@ -1280,7 +1345,7 @@ __global__ __launch_bounds__(MX_THREADS) void w4a4_mxfp4_kernel(
     const int wlast = N - 1 - n0;                        // rows past N clamp to the last row
     const uint8_t *__restrict__ xsrc0 = xq + (size_t)min(m0 + lrow, M - 1) * KB;
     const uint8_t *__restrict__ xsrc1 = xq + (size_t)min(m0 + lrow + 64, M - 1) * KB;
-    const uint8_t *__restrict__ wssrc = wscale + (size_t)min(n0 + tid, N - 1) * NB;
+    const uint8_t *__restrict__ wssrc = wscale + (size_t)(GATED ? gated_row<2>(tn_, tid, N) : min(n0 + tid, N - 1)) * NB;
     const uint8_t *__restrict__ xssrc = xscale + (size_t)min(m0 + (tid & 127), M - 1) * NB;
     const bool aligned_scales = (NB & 3) == 0;
     int wofs[4], xofs[2];
@@ -1290,7 +1355,10 @@ __global__ __launch_bounds__(MX_THREADS) void w4a4_mxfp4_kernel(
     for (int i = 0; i < 2; ++i) xofs[i] = (lrow + 64 * i) * MX_STRIDE + mx_seg(lrow + 64 * i, lseg) * 16;
     const uint8_t *wrow[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wrow[i] = (lrow + 64 * i <= wlast) ? wsrc + wstep * i : wq + (size_t)(N - 1) * KB;
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (GATED) wrow[i] = wq + (size_t)gated_row<2>(tn_, lrow + 64 * i, N) * KB;
+        else wrow[i] = (lrow + 64 * i <= wlast) ? wsrc + wstep * i : wq + (size_t)(N - 1) * KB;
+    }
 
     uint4 rw[4], rx[2];
     uint32_t rsw, rsx;
@@ -1375,8 +1443,9 @@ __global__ __launch_bounds__(MX_THREADS) void w4a4_mxfp4_kernel(
 #undef MX_GLOAD
 #undef MX_LSTORE
 
-    wave_epilogue<MX_TN, MX_TM>(acc, h, up, bias, M, N, gelu, Y, m0 + wm * MX_WM, n0 + wn * MX_WN,
-                reinterpret_cast<uint8_t *>(&sm) + wave * OUT_TILE_BYTES, lane);
+    uint8_t *tile = reinterpret_cast<uint8_t *>(&sm) + wave * OUT_TILE_BYTES;
+    if constexpr (GATED) gated_wave_epilogue(acc, h, up, bias, M, N, gelu, Y, m0 + wm * MX_WM, tn_, wn, tile, lane);
+    else wave_epilogue<MX_TN, MX_TM>(acc, h, up, bias, M, N, gelu, Y, m0 + wm * MX_WM, n0 + wn * MX_WN, tile, lane);
 }
 
 // --------------------------------------------------- MXFP4, LDS-DMA pipeline
@@ -1671,6 +1740,7 @@ constexpr int MXE_STORE = 0;      // y -> bf16 Y
 constexpr int MXE_REQUANT = 1;    // the next layer's activation step (RequantArgs)
 constexpr int MXE_PARTIAL = 2;    // fp32 partial sums of one K slice (split K)
 constexpr int MXE_QKNORM = 3;     // Q/K RMS-norm + rotary embedding of a QKV projection (QKNormArgs)
+constexpr int MXE_GATED = 4;      // act(gate) * up -> bf16 Y of N / 2 channels
 
 // Split K: work item t is tile t % tiles over K slice t / tiles, of S slices
 // of `sps` 256-channel steps each (the last one may be shorter); the slice's
@@ -1692,6 +1762,7 @@ __global__ __launch_bounds__(MXD_THREADS) void w4a4_mxfp4_dma_kernel(
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform
     const int wn = wave & 1, wm = wave >> 1;            // 2 (n) x 4 (m) waves
+    constexpr bool GATED = MODE == MXE_GATED;
     const int tiles_n = (N + MXD_BN - 1) / MXD_BN, tiles_m = (M + MXD_BM - 1) / MXD_BM;
     const int tiles = tiles_n * tiles_m;
     const int KB = K >> 1;          // code bytes per row
@@ -1711,10 +1782,12 @@ __global__ __launch_bounds__(MXD_THREADS) void w4a4_mxfp4_dma_kernel(
         for (int i = 0; i < 4; ++i) {
             const int r = 8 * (8 * i + wave) + (lane >> 3);        // block 8 i + wave
             const int seg = mxd_seg(r, lane & 7);      // LDS slot lane & 7 holds this global segment
-            wvo[i] = (uint32_t)(min(n0 + r, N - 1) * KB + 16 * seg);
+            if constexpr (GATED) wvo[i] = (uint32_t)(gated_row<2>(tn_, r, N) * KB + 16 * seg);
+            else wvo[i] = (uint32_t)(min(n0 + r, N - 1) * KB + 16 * seg);
             xvo[i] = (uint32_t)(min(m0 + r, M - 1) * KB + 16 * seg);
         }
-        ewo = (uint32_t)(min(n0 + 32 * wave + (lane >> 1), N - 1) * NB + 4 * (lane & 1));
+        if constexpr (GATED) ewo = (uint32_t)(gated_row<2>(tn_, 32 * wave + (lane >> 1), N) * NB + 4 * (lane & 1));
+        else ewo = (uint32_t)(min(n0 + 32 * wave + (lane >> 1), N - 1) * NB + 4 * (lane & 1));
         exo = (uint32_t)(min(m0 + 32 * wave + (lane >> 1), M - 1) * NB + 4 * (lane & 1));
     };
     auto issue = [&](int st, int sg) {
@@ -1834,7 +1907,7 @@ __global__ __launch_bounds__(MXD_THREADS) void w4a4_mxfp4_dma_kernel(
         // next tile's prefetch would hold (the requantizing one spilled 35
         // VGPRs with it): those modes run one tile per block, and so do the
         // split-K partial sums, whose items never outnumber the CUs
-        constexpr bool persistent = MODE == MXE_STORE;
+        constexpr bool persistent = MODE == MXE_STORE || MODE == MXE_GATED;
         const int tnext = persistent ? t + (int)gridDim.x : items;
         const int nst_done = nst;
         if (persistent && tnext < items) {
@@ -1901,6 +1974,9 @@ __global__ __launch_bounds__(MXD_THREADS) void w4a4_mxfp4_dma_kernel(
             static_assert(2 * MXD_BM * 32 * sizeof(float) <= sizeof(MXDStage), "partial sums fit in a stage");
             requant_epilogue_mx(acc, h, up, bias, M, N, gelu, rq, mb, nb, tile_n, tile_m0, wn, wm, tid, lane,
                                 reinterpret_cast<float *>(&stage[last]));
+        } else if constexpr (MODE == MXE_GATED) {
+            gated_wave_epilogue(acc, h, up, bias, M, N, gelu, Y, mb, tile_n, wn,
+                                reinterpret_cast<uint8_t *>(&stage[last]) + wave * OUT_TILE_BYTES, lane);
         } else {
             wave_epilogue<MX_TN, MX_TM>(acc, h, up, bias, M, N, gelu, Y, mb, nb,
                                         reinterpret_cast<uint8_t *>(&stage[last]) + wave * OUT_TILE_BYTES, lane);
@@ -1950,9 +2026,35 @@ hipError_t launch_w4a4_linear(const uint8_t *xq, const void *xscale, const float
                                Y, RequantArgs{}, SplitArgs{nullptr, 1, K >> 8}, QKNormArgs{});
         } else {
             const int tiles = ((N + MX_BN - 1) / MX_BN) * ((M + MX_BM - 1) / MX_BM);
-            hipLaunchKernelGGL(w4a4_mxfp4_kernel, dim3((unsigned)tiles), dim3(MX_THREADS), 0, stream, xq,
+            hipLaunchKernelGGL(w4a4_mxfp4_kernel<false>, dim3((unsigned)tiles), dim3(MX_THREADS), 0, stream, xq,
                                (const uint8_t *)xscale, h, wq, (const uint8_t *)wscale, up, bias, M, N, K, gelu, Y);
         }
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_w4a4_linear_gated(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
+                                    const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int F, int K,
+                                    svdq_precision prec, svdq_activation act, uint16_t *Y, hipStream_t stream)
+{
+    if (M <= kFewRows) return launch_w4a4_few_gated(xq, xscale, h, wq, wscale, up, bias, M, F, K, prec, act, Y, stream);
+    const int gelu = act == SVDQ_ACT_GELU_TANH ? 1 : 0, N = 2 * F;
+    const int tiles_n = (N + I4_BN - 1) / I4_BN;       // both rows of 128 channels in every kernel's tile
+    static_assert(I4_BN == 256 && MX_BN == 256 && MXD_BN == 256, "gated_row's tiles");
+    if (prec == SVDQ_INT4) {
+        const int tiles = tiles_n * ((M + I4_BM - 1) / I4_BM);
+        hipLaunchKernelGGL(w4a4_int4_kernel<EPI_GATED>, dim3((unsigned)tiles), dim3(I4_THREADS), 0, stream, xq,
+                           (const float *)xscale, h, wq, (const float *)wscale, up, bias, M, N, K, gelu, Y,
+                           RequantArgs{}, QKNormArgs{});
+    } else if (requant_supported(M, N, K, prec)) {     // the LDS-DMA kernel's range
+        const int tiles = tiles_n * ((M + MXD_BM - 1) / MXD_BM), ncu = device_cu_count();
+        hipLaunchKernelGGL(w4a4_mxfp4_dma_kernel<MXE_GATED>, dim3((unsigned)(tiles < ncu ? tiles : ncu)),
+                           dim3(MXD_THREADS), 0, stream, xq, (const uint8_t *)xscale, h, wq, (const uint8_t *)wscale, up,
+                           bias, M, N, K, gelu, Y, RequantArgs{}, SplitArgs{nullptr, 1, K >> 8}, QKNormArgs{});
+    } else {
+        const int tiles = tiles_n * ((M + MX_BM - 1) / MX_BM);
+        hipLaunchKernelGGL(w4a4_mxfp4_kernel<true>, dim3((unsigned)tiles), dim3(MX_THREADS), 0, stream, xq,
+                           (const uint8_t *)xscale, h, wq, (const uint8_t *)wscale, up, bias, M, N, K, gelu, Y);
     }
     return hipGetLastError();
 }
