@@ -61,12 +61,17 @@ struct FewArgs {
 };
 constexpr int FEW_NONE = 0, FEW_GELU = 1, FEW_SILU = 2;
 
-// Bytes of a tile of 16 rows in a stage: a line of codes per row, then its
-// scales (INT4: fp32 [4 groups][16 rows]; MXFP4: a dword per lane and product).
-template <bool INT4>
+// Forms: INT4; MXFP4 with rows of scales that start on 4 bytes (K % 128 == 0);
+// MXFP4 with rows of scales that start anywhere.
+constexpr int FEW_INT4 = 0, FEW_MX = 1, FEW_MX_ODD = 2;
+
+// Bytes of a tile of 16 rows in a stage: a line of codes per row, then its scales:
+// fp32 [4 groups][16 rows]; dwords of four blocks [2][16 rows]; a dword per block,
+// lane and product.
+template <int FORM>
 struct FewTile {
-    static constexpr int kCodes = 16 * 128, kScales = INT4 ? 256 : 512, kBytes = kCodes + kScales;
-    static constexpr int kLoads = INT4 ? 3 : 4;
+    static constexpr int kCodes = 16 * 128, kScales = FORM == FEW_INT4 ? 256 : FORM == FEW_MX ? 128 : 512;
+    static constexpr int kBytes = kCodes + kScales, kLoads = FORM == FEW_MX_ODD ? 4 : 3;
 };
 
 // 16-byte segment s of row r lies at s ^ (r / 2 % 8): 16 rows' reads of a
@@ -80,22 +85,28 @@ struct FewRows {
     uint32_t code[2], scale;            // byte offsets of the lane's rows
 };
 
-template <bool INT4>
+// PARTS waves share the loads of a tile: part p has the lines of rows 8 p .. and
+// half of the scales.
+template <int FORM, int PARTS = 1>
 __device__ __forceinline__ void fw_issue(uint32_t lds, const FewRows &o, const uint8_t *q, const void *scales, int st,
-                                         int segs, int lane)
+                                         int segs, int lane, int part = 0)
 {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int r = 8 * j + (lane >> 3);
-        const int s = min(8 * st + fw_seg(r, lane & 7), segs - 1);
-        fw_dma16(lds + 1024 * j, o.code[j] + 16 * s, q);
-    }
-    lds += FewTile<INT4>::kCodes;
-    if constexpr (INT4) {
-        fw_dma4(lds, o.scale + 4 * min(4 * st + (lane >> 4), segs / 2 - 1), scales);
+    static_assert(PARTS == 1 || PARTS == 2, "a tile's two loads of lines");
+    auto line = [&](int j) {
+        const int s = min(8 * st + fw_seg(8 * j + (lane >> 3), lane & 7), segs - 1);
+        fw_dma16(lds + 1024 * j, (j ? o.code[1] : o.code[0]) + 16 * s, q);
+    };
+    if (PARTS == 1 || part == 0) line(0);
+    if (PARTS == 1 || part == 1) line(1);
+    lds += FewTile<FORM>::kCodes;
+    if constexpr (FORM == FEW_INT4) {
+        if (PARTS == 1 || lane >> 5 == part) fw_dma4(lds, o.scale + 4 * min(4 * st + (lane >> 4), segs / 2 - 1), scales);
+    } else if constexpr (FORM == FEW_MX) {
+        if (PARTS == 1 ? lane < 32 : lane >> 4 == part) fw_dma4(lds, o.scale + 4 * min(2 * st + (lane >> 4), segs / 4 - 1), scales);
     } else {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) fw_dma1(lds + 256 * s, o.scale + min(8 * st + 2 * (lane >> 4) + s, segs - 1), scales);
+        for (int s = 0; s < 2; ++s)
+            if (PARTS == 1 || part == s) fw_dma1(lds + 256 * s, o.scale + min(8 * st + 2 * (lane >> 4) + s, segs - 1), scales);
     }
 }
 
@@ -114,32 +125,83 @@ __device__ __forceinline__ void fw_widen(uint2 w, long &a, long &b)
     b = (long)((uint64_t)o1 << 32 | e1);
 }
 
-template <bool INT4, int RT, int CT, bool GATED, int W, int DEPTH>
-__global__ __launch_bounds__(64 * W) void w4a4_few_kernel(FewArgs a)
+// X kept whole in LDS: row r at r * fw_xrow, its 16-byte unit u at u ^ (r % 16);
+// then the rows' scales as dwords (INT4: fp32; MXFP4: a byte each), an odd number
+// apart: 16 rows' reads fall into different banks.
+__host__ __device__ constexpr int fw_xrow(int K) { return ((K >> 1) + 255) & ~255; }
+__host__ __device__ constexpr int fw_xscales(int K, bool int4) { return (int4 ? K >> 6 : K >> 5) | 1; }
+__host__ __device__ constexpr int64_t fw_xbytes(int M, int K, bool int4)
 {
-    typedef FewTile<INT4> Tile;
-    constexpr int STAGE = (RT + CT) * Tile::kBytes, NL = (RT + CT) * Tile::kLoads;
-    constexpr int RING = W * DEPTH * STAGE, SUMS = W * RT * CT * 1024;
-    static_assert(NL * (DEPTH - 1) <= 63, "the loads in flight are counted in 6 bits");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[RING > SUMS ? RING : SUMS];
+    return (int64_t)M * (fw_xrow(K) + 4 * (int64_t)fw_xscales(K, int4));
+}
+
+template <int FORM, int W>
+__device__ __forceinline__ void fw_load_x(uint32_t lds, const FewArgs &a, int wave, int lane)
+{
+    constexpr bool INT4 = FORM == FEW_INT4;
+    const int KB = a.K >> 1, segs = KB >> 4, ns = INT4 ? a.K >> 6 : a.K >> 5;
+    const int xrow = fw_xrow(a.K), xs = fw_xscales(a.K, INT4), nc = (xrow + 1023) >> 10, nd = (ns + 63) >> 6;
+    for (int i = wave; i < a.M * nc; i += W) {
+        const int r = i / nc, c = i % nc, u = 64 * c + lane;
+        if (u < xrow >> 4) fw_dma16(lds + r * xrow + 1024 * c, (uint32_t)r * KB + 16 * min(u ^ (r & 15), segs - 1), a.xq);
+    }
+    for (int i = wave; i < a.M * nd; i += W) {
+        const int r = i / nd, c = i % nd, g = 64 * c + lane;
+        const uint32_t to = lds + a.M * xrow + 4 * (r * xs + 64 * c);
+        if (g < ns) {
+            if constexpr (INT4) fw_dma4(to, 4 * ((uint32_t)r * ns + g), a.xscale);
+            else fw_dma1(to, (uint32_t)r * ns + g, a.xscale);
+        }
+    }
+}
+
+// Waits until at most `stages` stages of N loads each are in flight.
+template <int N, int MOST>
+__device__ __forceinline__ void fw_wait_stages(int stages)
+{
+    static_assert(MOST <= 4 && N * MOST <= 63, "the loads in flight are counted in 6 bits");
+    if (MOST > 3 && stages == 4) fw_wait<(MOST > 3 ? 4 * N : 0)>();
+    else if (MOST > 2 && stages == 3) fw_wait<(MOST > 2 ? 3 * N : 0)>();
+    else if (MOST > 1 && stages == 2) fw_wait<(MOST > 1 ? 2 * N : 0)>();
+    else if (MOST > 0 && stages == 1) fw_wait<N>();
+    else fw_wait<0>();
+}
+
+// W = WN WK waves: WN sets of 16 RT rows, the lines of each taken in turn by WK
+// waves.  XB > 0: X is kept whole in XB bytes of LDS; 0: it goes through the ring,
+// where the WN waves of the same lines share it.
+template <int FORM, int RT, int CT, bool GATED, int WN, int WK, int DEPTH, int XB>
+__global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
+{
+    typedef FewTile<FORM> Tile;
+    constexpr bool INT4 = FORM == FEW_INT4, XS = XB > 0;
+    constexpr int W = WN * WK, NT = GATED ? RT / 2 : RT, KH = GATED ? 2 : 1;     // tiles of output channels, weight rows of each
+    constexpr int XT = XS ? 0 : CT, NL = RT * Tile::kLoads + XT * (WN == 1 ? Tile::kLoads : 2);
+    constexpr int XRING = DEPTH * WK * XT * Tile::kBytes, RING = XRING + DEPTH * W * RT * Tile::kBytes;
+    constexpr int SUMS = W * RT * CT * 1024, FIRST = RING > SUMS ? RING : SUMS;
+    constexpr int UPS = WN * RT;                           // tiles of weight rows: up rows (1024 bytes) and biases (256) of each
+    constexpr int LDS = FIRST + UPS * 1280 + CT * 2048 + XB;
+    static_assert(!XS || CT == 1, "few enough rows");
+    static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave % WN, wk = wave / WN;
     const int j16 = lane & 15, b = lane >> 4;
-    constexpr int NT = GATED ? RT / 2 : RT;              // tiles of output channels
-    const int n0 = blockIdx.x * (16 * NT);
+    const int n0 = blockIdx.x * (16 * NT * WN);
     const int KB = a.K >> 1, segs = KB >> 4, stages = (segs + 7) >> 3;
     const int srow = INT4 ? 4 * (a.K >> 6) : a.K >> 5;   // bytes of a row's scales
 
-    // row of the weight: tile t, row r
-    auto wrow = [&](int t, int r) {
-        const int n = min(n0 + 16 * (GATED ? t >> 1 : t) + r, a.N - 1);
+    // row of the weight: tile t of set w, row r
+    auto wrow = [&](int w, int t, int r) {
+        const int n = min(n0 + 16 * (NT * w + (GATED ? t >> 1 : t)) + r, a.N - 1);
         return GATED && (t & 1) ? a.N + n : n;
     };
     FewRows wo[RT], xo[CT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) wo[t].code[j] = (uint32_t)wrow(t, 8 * j + (lane >> 3)) * KB;
-        wo[t].scale = (uint32_t)wrow(t, j16) * srow;
+        for (int j = 0; j < 2; ++j) wo[t].code[j] = (uint32_t)wrow(wn, t, 8 * j + (lane >> 3)) * KB;
+        wo[t].scale = (uint32_t)wrow(wn, t, j16) * srow;
     }
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
@@ -147,35 +209,77 @@ __global__ __launch_bounds__(64 * W) void w4a4_few_kernel(FewArgs a)
         for (int j = 0; j < 2; ++j) xo[c].code[j] = (uint32_t)min(16 * c + 8 * j + (lane >> 3), a.M - 1) * KB;
         xo[c].scale = (uint32_t)min(16 * c + j16, a.M - 1) * srow;
     }
-    uint8_t *ring = lds + wave * (DEPTH * STAGE);
-    const uint32_t ring0 = fw_lds(ring);
+    const uint32_t lds0 = fw_lds(lds);
+    auto xtile = [&](int i, int c) { return (((i % DEPTH) * WK + wk) * XT + c) * Tile::kBytes; };
+    auto wtile = [&](int i, int t) { return XRING + (((i % DEPTH) * W + wave) * RT + t) * Tile::kBytes; };
     auto issue = [&](int i) {
-        const int st = wave + i * W;
-        const uint32_t at = ring0 + (uint32_t)(i % DEPTH) * STAGE;
+        const int st = wk + i * WK;
 #pragma unroll
-        for (int t = 0; t < RT; ++t) fw_issue<INT4>(at + t * Tile::kBytes, wo[t], a.wq, a.wscale, st, segs, lane);
+        for (int t = 0; t < RT; ++t) fw_issue<FORM>(lds0 + wtile(i, t), wo[t], a.wq, a.wscale, st, segs, lane);
 #pragma unroll
-        for (int c = 0; c < CT; ++c) fw_issue<INT4>(at + (RT + c) * Tile::kBytes, xo[c], a.xq, a.xscale, st, segs, lane);
+        for (int c = 0; c < XT; ++c) fw_issue<FORM, WN>(lds0 + xtile(i, c), xo[c], a.xq, a.xscale, st, segs, lane, wn);
     };
-    const int mine = wave < stages ? (stages - wave + W - 1) / W : 0;
+    const int mine = wk < stages ? (stages - wk + WK - 1) / WK : 0;
 
     f32x4 acc[RT][CT];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[t][c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    // the epilogue's operands, ahead of the stages: whoever waits for a stage has
+    // waited for them
+    uint8_t *epi_up = lds + FIRST, *epi_bias = epi_up + UPS * 1024, *epi_h = epi_bias + UPS * 256;
+    for (int u = wave; u < UPS + CT; u += W) {
+        if (u < UPS) {
+            const int w = u / RT, t = u % RT;
+            fw_dma16(lds0 + FIRST + 1024 * u, (uint32_t)wrow(w, t, lane >> 2) * 64 + 16 * (lane & 3), a.up);
+            if (a.bias) {
+                const int n = min(n0 + 16 * (NT * w + (GATED ? t >> 1 : t)) + 2 * (lane & 7), a.N - 2);
+                fw_dma4(lds0 + FIRST + 1024 * UPS + 256 * u, 2 * (uint32_t)(GATED && (t & 1) ? a.N + n : n), a.bias);
+            }
+        } else {
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i)
+            for (int j = 0; j < 2; ++j)
+                fw_dma16(lds0 + FIRST + 1280 * UPS + 2048 * (u - UPS) + 1024 * j,
+                         (uint32_t)min(16 * (u - UPS) + 8 * j + (lane >> 3), a.M - 1) * 128 + 16 * (lane & 7), a.h);
+        }
+    }
+    const uint8_t *xl = lds + LDS - XB;
+    if constexpr (XS) fw_load_x<FORM, W>(lds0 + LDS - XB, a, wave, lane);
+    // WN = 1: a wave's ring is its own, DEPTH stages ahead.  Else one barrier per
+    // stage, and the place that a stage leaves is filled after the next one's.
+    constexpr int AHEAD = WN == 1 ? DEPTH : DEPTH - 1;
+    static_assert(AHEAD >= 1, "a stage is on its way before it is read");
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
         if (i < mine) issue(i);
-    for (int i = 0; i < mine; ++i) {
+    const int xr = min(j16, a.M - 1), xrow = fw_xrow(a.K);
+    const float *xls = reinterpret_cast<const float *>(xl + a.M * xrow) + xr * fw_xscales(a.K, INT4);
+    if constexpr (XS) {
+        fw_wait_stages<NL, AHEAD>(min(AHEAD, mine));       // the wave's share of X has arrived
+        __syncthreads();
+    }
+    // the lane's E8M0 byte for product s of a tile (in the low byte)
+    auto e8m0 = [&](const uint8_t *tile, int s) {
+        const uint8_t *p = tile + Tile::kCodes;
+        if constexpr (FORM == FEW_MX) return (int)(*reinterpret_cast<const uint32_t *>(p + 64 * (b >> 1) + 4 * j16) >> (8 * (2 * (b & 1) + s)));
+        else return *reinterpret_cast<const int *>(p + 256 * s + 4 * lane);
+    };
+    // the lane's 16-byte unit u of X, tile c
+    auto xunit = [&](const uint8_t *S, int c, int st, int u) {
+        return XS ? xl + xr * xrow + 16 * ((8 * st + u) ^ xr) : S + c * Tile::kBytes + j16 * 128 + 16 * fw_seg(j16, u);
+    };
+    const int rounds = WN == 1 ? mine : (stages + WK - 1) / WK;      // a barrier in each: the same for all waves
+    for (int i = 0; i < rounds; ++i) {
         // this stage's loads are done: all but those of the stages after it
-        const int after = min(DEPTH - 1, mine - 1 - i);
-        if (after == 0) fw_wait<0>();
-        else if (after == 1) fw_wait<NL>();
-        else if (DEPTH > 3 && after == 3) fw_wait<NL * (DEPTH > 3 ? 3 : 0)>();
-        else if (DEPTH > 2) fw_wait<NL * (DEPTH > 2 ? 2 : 0)>();
-        const uint8_t *S = ring + (i % DEPTH) * STAGE;
-        const int st = wave + i * W;
+        fw_wait_stages<NL, AHEAD - 1>(min(AHEAD - 1, max(mine - 1 - i, 0)));
+        if constexpr (WN > 1) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");     // every wave's, and the stage before is read
+            if (i + AHEAD < mine) issue(i + AHEAD);
+            if (i >= mine) continue;
+        }
+        const uint8_t *SX = lds + xtile(i, 0), *SW = lds + wtile(i, 0);
+        const int st = wk + i * WK;
         if constexpr (INT4) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -185,13 +289,13 @@ __global__ __launch_bounds__(64 * W) void w4a4_few_kernel(FewArgs a)
                 float sx[CT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
-                    const uint8_t *p = S + (RT + c) * Tile::kBytes;
-                    fw_widen(*reinterpret_cast<const uint2 *>(p + at), x0[c], x1[c]);
-                    sx[c] = *reinterpret_cast<const float *>(p + Tile::kCodes + 4 * (16 * g + j16));
+                    fw_widen(*reinterpret_cast<const uint2 *>(xunit(SX, c, st, 2 * g + (b >> 1)) + 8 * (b & 1)), x0[c], x1[c]);
+                    sx[c] = XS ? xls[4 * st + g]
+                               : *reinterpret_cast<const float *>(SX + c * Tile::kBytes + Tile::kCodes + 4 * (16 * g + j16));
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const uint8_t *p = S + t * Tile::kBytes;
+                    const uint8_t *p = SW + t * Tile::kBytes;
                     long w0, w1;
                     fw_widen(*reinterpret_cast<const uint2 *>(p + at), w0, w1);
                     const f32x4 sw = *reinterpret_cast<const f32x4 *>(p + Tile::kCodes + 4 * (16 * g + 4 * b));
@@ -214,29 +318,29 @@ __global__ __launch_bounds__(64 * W) void w4a4_few_kernel(FewArgs a)
                 int ex[CT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
-                    const uint8_t *p = S + (RT + c) * Tile::kBytes;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(p + at);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(xunit(SX, c, st, 2 * b + s));
                     x[c] = (i32x8){in ? (int)v.x : 0, in ? (int)v.y : 0, in ? (int)v.z : 0, in ? (int)v.w : 0, 0, 0, 0, 0};
-                    ex[c] = *reinterpret_cast<const int *>(p + Tile::kCodes + 256 * s + 4 * lane);
+                    ex[c] = XS ? __builtin_bit_cast(int, xls[min(8 * st + 2 * b + s, segs - 1)])
+                               : e8m0(SX + c * Tile::kBytes, s);
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const uint8_t *p = S + t * Tile::kBytes;
+                    const uint8_t *p = SW + t * Tile::kBytes;
                     const uint4 v = *reinterpret_cast<const uint4 *>(p + at);
                     const i32x8 w = {(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-                    const int ew = *reinterpret_cast<const int *>(p + Tile::kCodes + 256 * s + 4 * lane);
+                    const int ew = e8m0(p, s);
 #pragma unroll
                     for (int c = 0; c < CT; ++c)
                         acc[t][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[c], acc[t][c], 4, 4, 0, ew, 0, ex[c]);
                 }
             }
         }
-        if (i + DEPTH < mine) {
+        if (WN == 1 && i + DEPTH < mine) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read: its place is free
             issue(i + DEPTH);
         }
     }
-    // the waves' sums: tile (t, c) of wave w at w RT CT + t CT + c
+    // the waves' sums: tile (t, c) of wave w at (w RT + t) CT + c
     f32x4 *sums = reinterpret_cast<f32x4 *>(lds);
     __syncthreads();
 #pragma unroll
@@ -244,60 +348,107 @@ __global__ __launch_bounds__(64 * W) void w4a4_few_kernel(FewArgs a)
 #pragma unroll
         for (int c = 0; c < CT; ++c) sums[64 * ((wave * RT + t) * CT + c) + lane] = acc[t][c];
     __syncthreads();
-    // wave u finishes the output tiles u, u + W, ..: lane (j16, b) has channels
-    // 4 b .. 4 b + 3 of row j16
-    for (int u = wave; u < NT * CT; u += W) {
-        const int c = u % CT, m = 16 * c + j16, mc = min(m, a.M - 1);
+    // a wave finishes one output tile after the other: lane (j16, b) has channels 4 b
+    // .. 4 b + 3 of row j16
+    for (int u = wave; u < WN * NT * CT; u += W) {
+        const int c = u % CT, nt = u / CT, w = nt / NT;
         bf16x8 hhi, hlo;
-        float hv[8];
-        load_h8(a.h, mc, a.M, 8 * b, hv);
-        split_h(hv, hhi, hlo);
-        f32x4 y[GATED ? 2 : 1];
+        split_h(reinterpret_cast<const float *>(epi_h + 2048 * c + 128 * j16 + 32 * b), hhi, hlo);
+        f32x4 y[KH];
 #pragma unroll
-        for (int k = 0; k < (GATED ? 2 : 1); ++k) {
-            const int t = GATED ? 2 * (u / CT) + k : u / CT;
+        for (int k = 0; k < KH; ++k) {
+            const int t = GATED ? 2 * (nt % NT) + k : nt % NT;
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < W; ++w) v += sums[64 * ((w * RT + t) * CT + c) + lane];
+            for (int g = 0; g < WK; ++g) v += sums[64 * (((g * WN + w) * RT + t) * CT + c) + lane];
             if (INT4) v *= 262144.0f;
-            const bf16x8 ua = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(a.up + (size_t)wrow(t, j16) * 32 + 8 * b));
+            const bf16x8 ua = *reinterpret_cast<const bf16x8 *>(epi_up + 1024 * (w * RT + t) + 64 * j16 + 16 * b);
             v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ua, hhi, v, 0, 0, 0);
             v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ua, hlo, v, 0, 0, 0);
             if (a.bias) {
-                const uint2 bi = *reinterpret_cast<const uint2 *>(a.bias + min((int)(n0 + 16 * (GATED ? t >> 1 : t) + 4 * b), a.N - 4) + (GATED && k ? a.N : 0));
+                const uint2 bi = *reinterpret_cast<const uint2 *>(epi_bias + 256 * (w * RT + t) + 8 * b);
                 v[0] += bf16_to_f32(bi.x & 0xFFFFu), v[1] += bf16_to_f32(bi.x >> 16);
                 v[2] += bf16_to_f32(bi.y & 0xFFFFu), v[3] += bf16_to_f32(bi.y >> 16);
             }
             y[k] = v;
         }
-        const int n = n0 + 16 * (u / CT) + 4 * b;
+        const int m = 16 * c + j16, n = n0 + 16 * nt + 4 * b;
         if (m >= a.M || n >= a.N) continue;
         f32x4 o = y[0];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (a.act == FEW_GELU) o[k] = gelu_tanh(o[k]);
             else if (a.act == FEW_SILU) o[k] = silu(o[k]);
-            if (GATED) o[k] *= y[GATED ? 1 : 0][k];
+            if (GATED) o[k] *= y[KH - 1][k];
         }
         *reinterpret_cast<uint2 *>(a.Y + (size_t)m * a.N + n) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }
 }
 
-template <bool INT4, int CT, bool GATED>
+// Launches WN WK waves per block of RTN tiles of channels each, with as many
+// stages in flight as LDS and the count of loads take, up to DEPTHS.
+template <int FORM, int CT, bool GATED, int WN, int WK, int RTN, int DEPTHS, int XB>
 void few_launch(const FewArgs &a, hipStream_t stream)
 {
-    constexpr int RT = GATED ? 2 : 1, NT = GATED ? RT / 2 : RT;
-    constexpr int W = CT == 4 ? 4 : 8, DEPTH = CT == 1 && !GATED ? 3 : 2;
-    const uint32_t grid = (uint32_t)((a.N + 16 * NT - 1) / (16 * NT));
-    w4a4_few_kernel<INT4, RT, CT, GATED, W, DEPTH><<<grid, 64 * W, 0, stream>>>(a);
+    typedef FewTile<FORM> Tile;
+    constexpr int RT = RTN * (GATED ? 2 : 1), W = WN * WK, XT = XB ? 0 : CT;
+    constexpr int STAGE = (WK * XT + W * RT) * Tile::kBytes, LOADS = RT * Tile::kLoads + XT * (WN == 1 ? Tile::kLoads : 2);
+    constexpr int ROOM = (160 * 1024 - XB - WN * RT * 1280 - CT * 2048) / STAGE;
+    constexpr int LEAST = ROOM < 63 / LOADS ? ROOM : 63 / LOADS, DEPTH = DEPTHS < LEAST ? DEPTHS : LEAST;
+    if constexpr (WN > 1 && DEPTH < (WK > 2 ? 3 : 2)) {
+        few_launch<FORM, CT, GATED, WN, WK / 2, RTN, DEPTHS, XB>(a, stream);
+    } else {
+        const uint32_t grid = (uint32_t)((a.N + 16 * RTN * WN - 1) / (16 * RTN * WN));
+        w4a4_few_kernel<FORM, RT, CT, GATED, WN, WK, DEPTH, XB><<<grid, 64 * W, 0, stream>>>(a);
+    }
 }
 
-template <bool INT4, bool GATED>
+// X in the ring.  The fewer tiles of 16 channels per compute unit, the fewer of
+// them a block takes; the more, the more share the lines of X that come from the
+// L2 (48 rows, us, one tile of channels per block / two / four: 28672 channels of
+// 4096, MXFP4 35 / 28 / 23, INT4 46 / 44 / 42; 6144 channels 11 / 8.4 / 11 and 14
+// / 12 / 21; 4096 of 14336 15 / 19 / 28 and 20 / 33 / 62).  INT4 with three or four
+// tiles of rows is held by the widening, which eight waves of a tile share
+// (2 x 6912 channels, 64 rows: 22 us, two tiles per block 25).
+template <int FORM, int CT, bool GATED>
+void few_ring(const FewArgs &a, hipStream_t stream)
+{
+    constexpr bool INT4 = FORM == FEW_INT4;
+    const int64_t tiles = (a.N + 15) / 16, cus = device_cu_count();
+    if (tiles > 3 * cus) few_launch<FORM, CT, GATED, 2, 2, 2, 4, 0>(a, stream);
+    else if (tiles > cus && !(INT4 && CT > 2)) few_launch<FORM, CT, GATED, 2, 4, 1, 3, 0>(a, stream);
+    else few_launch<FORM, CT, GATED, 1, INT4 ? 8 : 4, 1, INT4 ? 2 : 4, 0>(a, stream);
+}
+
+// X whole in LDS: up to a block per compute unit eight waves per tile, else four
+// and more blocks (one row, us, four / eight waves: 4096 channels of 14336 INT4
+// 13.8 / 10.4; 2 x 14336 of 4096 INT4 17.5 / 24.8, MXFP4 13.5 / 18.1).
+template <int FORM, bool GATED, int XB>
+void few_whole(const FewArgs &a, hipStream_t stream)
+{
+    if ((a.N + 15) / 16 <= device_cu_count()) few_launch<FORM, 1, GATED, 1, 8, 1, 2, XB>(a, stream);
+    else few_launch<FORM, 1, GATED, 1, 4, 1, 2, XB>(a, stream);
+}
+
+template <int FORM, bool GATED>
 void few_rows(const FewArgs &a, hipStream_t stream)
 {
-    if (a.M <= 16) few_launch<INT4, 1, GATED>(a, stream);
-    else if (a.M <= 32) few_launch<INT4, 2, GATED>(a, stream);
-    else few_launch<INT4, 4, GATED>(a, stream);
+    // whole where it takes no more LDS than the ring's places for it would
+    const int64_t x = fw_xbytes(a.M, a.K, FORM == FEW_INT4);
+    if (a.M <= 16 && x <= 8192) few_whole<FORM, GATED, 8192>(a, stream);
+    else if (a.M <= 16 && x <= 17408) few_whole<FORM, GATED, 17408>(a, stream);
+    else if (a.M <= 16) few_ring<FORM, 1, GATED>(a, stream);
+    else if (a.M <= 32) few_ring<FORM, 2, GATED>(a, stream);
+    else if (a.M <= 48) few_ring<FORM, 3, GATED>(a, stream);
+    else few_ring<FORM, 4, GATED>(a, stream);
+}
+
+template <bool GATED>
+void few(const FewArgs &a, svdq_precision prec, hipStream_t stream)
+{
+    if (prec == SVDQ_INT4) few_rows<FEW_INT4, GATED>(a, stream);
+    else if (a.K % 128 == 0) few_rows<FEW_MX, GATED>(a, stream);
+    else few_rows<FEW_MX_ODD, GATED>(a, stream);
 }
 
 }  // namespace
@@ -307,8 +458,7 @@ hipError_t launch_w4a4_few(const uint8_t *xq, const void *xscale, const float *h
                            svdq_precision prec, svdq_epilogue epi, uint16_t *Y, hipStream_t stream)
 {
     const FewArgs a{xq, wq, xscale, wscale, h, up, bias, Y, M, N, K, epi == SVDQ_EPI_GELU_TANH ? FEW_GELU : FEW_NONE};
-    if (prec == SVDQ_INT4) few_rows<true, false>(a, stream);
-    else few_rows<false, false>(a, stream);
+    few<false>(a, prec, stream);
     return hipGetLastError();
 }
 
@@ -317,8 +467,7 @@ hipError_t launch_w4a4_few_gated(const uint8_t *xq, const void *xscale, const fl
                                  svdq_precision prec, svdq_activation act, uint16_t *Y, hipStream_t stream)
 {
     const FewArgs a{xq, wq, xscale, wscale, h, up, bias, Y, M, N, K, act == SVDQ_ACT_GELU_TANH ? FEW_GELU : FEW_SILU};
-    if (prec == SVDQ_INT4) few_rows<true, true>(a, stream);
-    else few_rows<false, true>(a, stream);
+    few<true>(a, prec, stream);
     return hipGetLastError();
 }
 
