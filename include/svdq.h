@@ -263,15 +263,16 @@ svdq_status svdq_w4a4_linear(const uint8_t *xq, const void *xscale, const float 
 /*
  * svdq_w4a4_linear_few -- svdq_w4a4_linear for the few rows of a decoding step
  * (single tokens, a tree of drafted tokens), where the tiles of svdq_w4a4_linear
- * would leave most of the chip idle: one pass over the weights, 16 rows of them
- * per block.  Arguments as for svdq_w4a4_linear, with
+ * would leave most of the chip idle: one pass over the weights per 64 rows of X,
+ * 16 weight rows or a few times that per block.  Meant for up to 64 rows, and for
+ * more where the output is narrow.  Arguments as for svdq_w4a4_linear, with
  *   M            0 .. SVDQ_FEW_MAX_ROWS (SVDQ_ERR_UNSUPPORTED above)
  * INT4: exact integer sums per group, scale product and accumulation in fp32.
  * Partial sums over K are added in a fixed order, so results are deterministic;
  * they may differ from svdq_w4a4_linear's in the last bf16 places.  One kernel
  * launch.  Errors as for svdq_w4a4_linear.
  */
-#define SVDQ_FEW_MAX_ROWS 64
+#define SVDQ_FEW_MAX_ROWS 256
 svdq_status svdq_w4a4_linear_few(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
                                  const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int N, int K,
                                  int rank, svdq_precision prec, svdq_epilogue epi, uint16_t *Y, void *stream);
@@ -287,7 +288,7 @@ svdq_status svdq_w4a4_linear_few(const uint8_t *xq, const void *xscale, const fl
  *   M, F, K      M >= 0, F >= 0 (either 0: no-op), F % 8 == 0, K % group == 0
  *   act          svdq_activation
  *   Y            [M][F] bf16 bits, device (out)
- * Any M: up to SVDQ_FEW_MAX_ROWS rows run as in svdq_w4a4_linear_few, more in
+ * Any M: few rows (how many depends on F) run as in svdq_w4a4_linear_few, more in
  * the tiles of svdq_w4a4_linear.  One kernel launch.  Errors as for
  * svdq_w4a4_linear.
  */

@@ -99,7 +99,7 @@ def _untouched(buf):
 
 
 @pytest.mark.parametrize("prec", PRECS)
-@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 48, 64])
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 48, 64, 65, 130, 256])
 @pytest.mark.parametrize("N,K", [(8, 64), (40, 192), (1000, 320), (264, 4096), (16, 11008)])
 def test_few_rows(prec, M, N, K):
     _say(f"linear_few prec={prec} {M}x{K}->{N}")
@@ -125,7 +125,8 @@ def test_few_rows_odd_blocks(K):
 
 
 GATED = [(1, 8, 64), (3, 24, 320), (16, 136, 1024), (17, 200, 192), (64, 72, 512), (65, 8, 64), (100, 136, 320),
-         (128, 128, 512), (129, 1000, 256), (300, 264, 768), (513, 392, 96 * 4), (260, 120, 4096)]
+         (128, 128, 512), (129, 1000, 256), (300, 264, 768), (513, 392, 96 * 4), (260, 120, 4096), (257, 8, 64), (40, 12296, 320), (200, 7000, 128),
+         (64, 28680, 64)]
 
 
 @pytest.mark.parametrize("prec", PRECS)
@@ -145,7 +146,7 @@ def test_gated(prec, M, F, K, act):
 
 @pytest.mark.parametrize("K", [32, 96, 160, 416])
 def test_gated_tiles_of_odd_blocks(K):
-    p = _problem(K, 150, 2 * 136, K, svdq.MXFP4, True)
+    p = _problem(K, 300, 2 * 136, K, svdq.MXFP4, True)
     y, d = _sums(p, 0.0)
     (a, da), u, du = _act(y[:, :136], d[:, :136], "silu"), y[:, 136:], d[:, 136:]
     _close(svdq.w4a4_linear_gated(*p["args"], svdq.MXFP4), a * u, a.abs() * du + u.abs() * da + da * du)

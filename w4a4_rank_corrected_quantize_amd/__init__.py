@@ -55,7 +55,7 @@ EPI_NONE = 0
 EPI_GELU_TANH = 1
 ACT_SILU = 0
 ACT_GELU_TANH = 1
-FEW_MAX_ROWS = 64
+FEW_MAX_ROWS = 256
 NORM_NONE = 0
 NORM_RMS = 1
 NORM_LAYER = 2
@@ -779,8 +779,8 @@ def _few_args(where, xq, xscale, h, wq, wscale, up, bias, prec, halves, Y, strea
 
 
 def w4a4_linear_few(xq, xscale, h, wq, wscale, up, bias, prec: int = INT4, epi: int = EPI_NONE, Y=None, stream=None):
-    """w4a4_linear for up to FEW_MAX_ROWS rows (single tokens, drafted tokens):
-    one pass over the weights (one kernel)."""
+    """w4a4_linear for few rows (single tokens, drafted tokens; at most
+    FEW_MAX_ROWS): one pass over the weights per 64 rows (one kernel)."""
     Y, prec, raw, args = _few_args("svdq_w4a4_linear_few", xq, xscale, h, wq, wscale, up, bias, prec, 1, Y, stream)
     st = lib().svdq_w4a4_linear_few(*args, prec, epi, Y.data_ptr(), raw)
     if st:

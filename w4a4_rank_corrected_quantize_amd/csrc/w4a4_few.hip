@@ -1,15 +1,18 @@
-// w4a4_few.hip -- the W4A4 linear for few rows (up to 64): decoding steps and
-// trees of drafted tokens, where the product is one pass over the weights.
+// w4a4_few.hip -- the W4A4 linear for few rows: decoding steps and trees of
+// drafted tokens, where the product is one pass over the weights (one per 64
+// rows).
 //
 //   y_mn = sum_g sx_mg sw_ng P_mng + sum_j h_mj up[n][j] + b_n   [GELU-tanh]
 //   gated: y_mf = act(gate_mf) up_mf, the two rows f and F + f of the weight
 //
-// A block owns 16 RT output rows of the weight (gated: 8 RT channels, their
-// gate and up rows) and all rows of X; its waves take the row's 128-byte lines
-// in turn.  A wave's stage is one line (256 channels) of 16 RT weight rows and
-// 16 CT rows of X with their scales.  It reaches LDS by DMA in whole lines (8
-// lanes per line), DEPTH stages ahead, in a ring of the wave's own: no barrier
-// until the waves' fp32 sums meet.
+// A block owns WN sets of 16 RT rows of the weight (gated: 8 RT channels, their
+// gate and up rows) and up to 64 rows of X; WK waves per set take the rows'
+// 128-byte lines in turn.  A wave's stage is one line (256 channels) of its set's
+// rows and of 16 CT rows of X, with their scales.  It reaches LDS by DMA in whole
+// lines (8 lanes per line), several stages ahead.  One row of X up to a few are
+// kept whole in LDS instead; with one set per block the ring is the wave's own and
+// needs no barrier until the waves' fp32 sums meet, with two they share the lines
+// of X.
 //
 // Products.  MXFP4: v_mfma_scale_f32_16x16x128_f8f6f4 takes codes and E8M0
 // scales as they are.  INT4: a group's 64 codes, widened to exact E4M3 bytes (q
@@ -58,6 +61,7 @@ struct FewArgs {
     const uint16_t *up, *bias;
     uint16_t *Y;
     int M, N, K, act;                   // act: FEW_*
+    int chunks;                         // sets of 16 CT rows, set by the launch
 };
 constexpr int FEW_NONE = 0, FEW_GELU = 1, FEW_SILU = 2;
 
@@ -187,7 +191,15 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave % WN, wk = wave / WN;
     const int j16 = lane & 15, b = lane >> 4;
-    const int n0 = blockIdx.x * (16 * NT * WN);
+    // blocks 8 apart (the same XCD) take the sets of rows of the same channels in turn
+    int tile = blockIdx.x, m0 = 0;
+    if (a.chunks > 1) {
+        const int per = 8 * a.chunks, in = tile % per;
+        tile = tile / per * 8 + in % 8;
+        m0 = in / 8 * (16 * CT);
+    }
+    const int n0 = tile * (16 * NT * WN);
+    if (n0 >= a.N) return;
     const int KB = a.K >> 1, segs = KB >> 4, stages = (segs + 7) >> 3;
     const int srow = INT4 ? 4 * (a.K >> 6) : a.K >> 5;   // bytes of a row's scales
 
@@ -206,8 +218,8 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) xo[c].code[j] = (uint32_t)min(16 * c + 8 * j + (lane >> 3), a.M - 1) * KB;
-        xo[c].scale = (uint32_t)min(16 * c + j16, a.M - 1) * srow;
+        for (int j = 0; j < 2; ++j) xo[c].code[j] = (uint32_t)min(m0 + 16 * c + 8 * j + (lane >> 3), a.M - 1) * KB;
+        xo[c].scale = (uint32_t)min(m0 + 16 * c + j16, a.M - 1) * srow;
     }
     const uint32_t lds0 = fw_lds(lds);
     auto xtile = [&](int i, int c) { return (((i % DEPTH) * WK + wk) * XT + c) * Tile::kBytes; };
@@ -241,7 +253,7 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 fw_dma16(lds0 + FIRST + 1280 * UPS + 2048 * (u - UPS) + 1024 * j,
-                         (uint32_t)min(16 * (u - UPS) + 8 * j + (lane >> 3), a.M - 1) * 128 + 16 * (lane & 7), a.h);
+                         (uint32_t)min(m0 + 16 * (u - UPS) + 8 * j + (lane >> 3), a.M - 1) * 128 + 16 * (lane & 7), a.h);
         }
     }
     const uint8_t *xl = lds + LDS - XB;
@@ -372,7 +384,7 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
             }
             y[k] = v;
         }
-        const int m = 16 * c + j16, n = n0 + 16 * nt + 4 * b;
+        const int m = m0 + 16 * c + j16, n = n0 + 16 * nt + 4 * b;
         if (m >= a.M || n >= a.N) continue;
         f32x4 o = y[0];
 #pragma unroll
@@ -398,7 +410,8 @@ void few_launch(const FewArgs &a, hipStream_t stream)
     if constexpr (WN > 1 && DEPTH < (WK > 2 ? 3 : 2)) {
         few_launch<FORM, CT, GATED, WN, WK / 2, RTN, DEPTHS, XB>(a, stream);
     } else {
-        const uint32_t grid = (uint32_t)((a.N + 16 * RTN * WN - 1) / (16 * RTN * WN));
+        const uint32_t tiles = (uint32_t)((a.N + 16 * RTN * WN - 1) / (16 * RTN * WN));
+        const uint32_t grid = a.chunks > 1 ? (tiles + 7) / 8 * 8 * a.chunks : tiles;
         w4a4_few_kernel<FORM, RT, CT, GATED, WN, WK, DEPTH, XB><<<grid, 64 * W, 0, stream>>>(a);
     }
 }
@@ -431,15 +444,18 @@ void few_whole(const FewArgs &a, hipStream_t stream)
 }
 
 template <int FORM, bool GATED>
-void few_rows(const FewArgs &a, hipStream_t stream)
+void few_rows(FewArgs a, hipStream_t stream)
 {
+    // more than 64 rows in equal sets of whole tiles
+    a.chunks = (a.M + 63) / 64;
+    const int rows = (a.M + a.chunks - 1) / a.chunks;
     // whole where it takes no more LDS than the ring's places for it would
     const int64_t x = fw_xbytes(a.M, a.K, FORM == FEW_INT4);
-    if (a.M <= 16 && x <= 8192) few_whole<FORM, GATED, 8192>(a, stream);
-    else if (a.M <= 16 && x <= 17408) few_whole<FORM, GATED, 17408>(a, stream);
-    else if (a.M <= 16) few_ring<FORM, 1, GATED>(a, stream);
-    else if (a.M <= 32) few_ring<FORM, 2, GATED>(a, stream);
-    else if (a.M <= 48) few_ring<FORM, 3, GATED>(a, stream);
+    if (rows <= 16 && x <= 8192) few_whole<FORM, GATED, 8192>(a, stream);
+    else if (rows <= 16 && x <= 17408) few_whole<FORM, GATED, 17408>(a, stream);
+    else if (rows <= 16) few_ring<FORM, 1, GATED>(a, stream);
+    else if (rows <= 32) few_ring<FORM, 2, GATED>(a, stream);
+    else if (rows <= 48) few_ring<FORM, 3, GATED>(a, stream);
     else few_ring<FORM, 4, GATED>(a, stream);
 }
 
@@ -457,7 +473,7 @@ hipError_t launch_w4a4_few(const uint8_t *xq, const void *xscale, const float *h
                            const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int N, int K,
                            svdq_precision prec, svdq_epilogue epi, uint16_t *Y, hipStream_t stream)
 {
-    const FewArgs a{xq, wq, xscale, wscale, h, up, bias, Y, M, N, K, epi == SVDQ_EPI_GELU_TANH ? FEW_GELU : FEW_NONE};
+    const FewArgs a{xq, wq, xscale, wscale, h, up, bias, Y, M, N, K, epi == SVDQ_EPI_GELU_TANH ? FEW_GELU : FEW_NONE, 1};
     few<false>(a, prec, stream);
     return hipGetLastError();
 }
@@ -466,7 +482,7 @@ hipError_t launch_w4a4_few_gated(const uint8_t *xq, const void *xscale, const fl
                                  const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int N, int K,
                                  svdq_precision prec, svdq_activation act, uint16_t *Y, hipStream_t stream)
 {
-    const FewArgs a{xq, wq, xscale, wscale, h, up, bias, Y, M, N, K, act == SVDQ_ACT_GELU_TANH ? FEW_GELU : FEW_SILU};
+    const FewArgs a{xq, wq, xscale, wscale, h, up, bias, Y, M, N, K, act == SVDQ_ACT_GELU_TANH ? FEW_GELU : FEW_SILU, 1};
     few<true>(a, prec, stream);
     return hipGetLastError();
 }

@@ -2033,11 +2033,25 @@ hipError_t launch_w4a4_linear(const uint8_t *xq, const void *xscale, const float
     return hipGetLastError();
 }
 
+// Few rows' kernel or tiles.  The tiles take about as long for any few rows (one
+// round of them), the other's time grows with the channels and the sets of 64 rows,
+// by 9, 12, 14 and 16 parts for one to four tiles of 16 rows.  2 x 14336 channels
+// of 4096, us: INT4 64 rows 39, tiles 60; 128 rows 73 and 62; MXFP4 128 rows 36 and
+// 42, 192 rows 51 and 45.  2 x 6912: INT4 192 rows 57 and 60, 256 rows 69 and 61;
+// MXFP4 256 rows 43 and 43.  2 x 2048: 256 rows 22 and 57, 15 and 35.
+static bool few_gated(int M, int F, svdq_precision prec)
+{
+    if (M > kFewRows) return false;
+    const int parts[4] = {9, 12, 14, 16}, sets = (M + 63) / 64, rows = (M + sets - 1) / sets;
+    const int64_t cost = (int64_t)((F + 15) / 16) * sets * parts[(rows - 1) / 16];
+    return cost <= 16 * (prec == SVDQ_INT4 ? 5 : 7) * (int64_t)device_cu_count();
+}
+
 hipError_t launch_w4a4_linear_gated(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
                                     const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int F, int K,
                                     svdq_precision prec, svdq_activation act, uint16_t *Y, hipStream_t stream)
 {
-    if (M <= kFewRows) return launch_w4a4_few_gated(xq, xscale, h, wq, wscale, up, bias, M, F, K, prec, act, Y, stream);
+    if (few_gated(M, F, prec)) return launch_w4a4_few_gated(xq, xscale, h, wq, wscale, up, bias, M, F, K, prec, act, Y, stream);
     const int gelu = act == SVDQ_ACT_GELU_TANH ? 1 : 0, N = 2 * F;
     const int tiles_n = (N + I4_BN - 1) / I4_BN;       // both rows of 128 channels in every kernel's tile
     static_assert(I4_BN == 256 && MX_BN == 256 && MXD_BN == 256, "gated_row's tiles");
