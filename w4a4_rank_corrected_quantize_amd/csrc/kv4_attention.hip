@@ -1075,7 +1075,16 @@ __global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
     // the last tiles first: under a causal mask they are the longest
     for (int64_t qt = (rows + block_rows - 1) / block_rows - 1 - qt0; qt >= 0; qt -= a.q_tiles) {
         if (block_rows == 16) ka_few_rows<D, INT4, TREE>(reinterpret_cast<float *>(lds), a, table, split, head, qs, qn, kv, 16 * qt, rows, wave, lane);
-        else if constexpr (CT > 0) ka_many_rows<D, INT4, CT, TREE>(lds, a, table, split, head, qs, qn, kv, 64 * CT * qt, rows, wave, lane);
+        else if constexpr (CT > 0) {
+            // a tree's last tile often is half of one
+            if constexpr (TREE && CT > 1) {
+                if (rows - 64 * CT * qt <= 64) {
+                    ka_many_rows<D, INT4, 1, TREE>(lds, a, table, split, head, qs, qn, kv, 64 * CT * qt, rows, wave, lane);
+                    continue;
+                }
+            }
+            ka_many_rows<D, INT4, CT, TREE>(lds, a, table, split, head, qs, qn, kv, 64 * CT * qt, rows, wave, lane);
+        }
     }
 }
 
@@ -1148,7 +1157,8 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
                                 hipStream_t stream, const uint32_t *tree, int tree_words)
 {
     const int cus = device_cu_count();
-    const KvPlan p = kv4_plan(T, B, c.heads, heads_q / c.heads, max_q, max_kv, cus);
+    const KvPlan p = tree ? kv4_tree_plan(T, B, c.heads, heads_q / c.heads, c.dim, max_q, max_kv, cus)
+                          : kv4_plan(T, B, c.heads, heads_q / c.heads, max_q, max_kv, cus);
     KvArgs a{};
     a.c = c, a.Q = Q, a.ldq = ldq, a.table = table, a.q_start = q_start, a.kv_len = kv_len, a.O = O, a.lse = lse;
     a.work = work, a.T = T, a.B = B, a.heads_q = heads_q, a.group = heads_q / c.heads, a.table_width = table_width;

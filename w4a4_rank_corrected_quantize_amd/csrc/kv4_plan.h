@@ -15,11 +15,11 @@ struct KvPlan {
     int q_tiles, splits, split_steps;             // a split's least length (many rows: its length within the bound)
 };
 
-inline KvPlan kv4_plan(int T, int B, int heads, int group, int max_q, int max_kv, int cus)
+inline KvPlan kv4_plan_form(bool many, int T, int B, int heads, int group, int max_q, int max_kv, int cus)
 {
     KvPlan p;
     const int64_t rows = (int64_t)(max_q < T ? max_q : T) * group;
-    p.many = rows > 16;
+    p.many = many;
     const int block_rows = p.many ? 64 * kKv4ManyTiles : 16;
     const int64_t tiles = (rows + block_rows - 1) / block_rows;
     // blocks of rows: at most every sequence's, and the rows' own number and one more per sequence
@@ -53,6 +53,29 @@ inline KvPlan kv4_plan(int T, int B, int heads, int group, int max_q, int max_kv
     const int64_t cap = kMaxBlocks / ((int64_t)B * heads * p.splits);
     p.q_tiles = (int)(tiles > cap ? cap : tiles);
     return p;
+}
+
+inline KvPlan kv4_plan(int T, int B, int heads, int group, int max_q, int max_kv, int cus)
+{
+    return kv4_plan_form((int64_t)(max_q < T ? max_q : T) * group > 16, T, B, heads, group, max_q, max_kv, cus);
+}
+
+// Trees of drafted tokens: more than 16 rows go 16 to a block as well while these
+// are few.  A block of many rows takes as long per step for 17 rows as for 128 (heads
+// of 128 1.3 us, one of 16 rows 0.3), so that 16 x 8 tokens over 8000 keys, 32 heads
+// over 8 of 64, INT4, take 39 us instead of 67, 8 over 1000 keys 9 instead of 15;
+// beyond a block per compute unit (heads of 64: three) it loses (16 x 16 tokens over
+// 8000 keys, heads of 128, MXFP4: 106 and 91 us; of 64 58 and 70).  At most as many
+// splits as kv4_plan has, so that its workspace serves both.
+inline KvPlan kv4_tree_plan(int T, int B, int heads, int group, int dim, int max_q, int max_kv, int cus)
+{
+    const KvPlan p = kv4_plan(T, B, heads, group, max_q, max_kv, cus);
+    if (!p.many) return p;
+    const int64_t rows = (int64_t)(max_q < T ? max_q : T) * group, per = (rows + 15) / 16, own = (int64_t)T * group / 16 + B;
+    if ((per * B < own ? per * B : own) * heads > (dim == 64 ? 3 : 1) * (int64_t)cus) return p;
+    KvPlan f = kv4_plan_form(false, T, B, heads, group, max_q, max_kv, cus);
+    if (f.splits > p.splits) f.splits = p.splits;
+    return f;
 }
 
 // Blocks of 256 threads of the first kernel.
