@@ -686,8 +686,8 @@ svdq_status svdq_rope_table(const int32_t *pos, int T, int axes, const double *f
  *   u = x / sqrt(mean_d(x_d^2) + eps) w (or x, without a weight);
  *   pair (a, b) of u -> (a cos - b sin, b cos + a sin); channels behind 2 pairs
  *   are u
- * in 64 bits from the loads to one rounding (to fp32 and from there to bf16,
- * each to nearest even).
+ * rounded to bf16 (nearest even) once: queries from fp32, keys from 64 bits by way
+ * of fp32, so that the 4 bits they may go on to are those of the exact key.
  *   Q, K       [T][heads_q][dim], [T][heads_k][dim] bf16 bits, device; row t
  *              at t * ldq, t * ldk elements (>= heads * dim, % 8 == 0): slices of
  *              a QKV product.  heads_q >= 1, heads_k >= 0 (0: K, K_out, norm_k are

@@ -17,10 +17,12 @@ __device__ __forceinline__ int kt_slot(const Kv4Tables &s, int seq, int64_t at)
     return (uint32_t)page < (uint32_t)s.pages ? (page << s.page_shift) + (int)(at & ((1 << s.page_shift) - 1)) : -1;
 }
 
-// A thread walks from its node up to the root: parents come before their
-// children, so the walk ends and the mask's words are met from the last to the
-// first.
-constexpr int KT_LDS = 2048;
+// Up to 256 rows: a thread per row, whose mask and nearest unmet ancestor double
+// their reach in every round, mask_i |= mask_a, a = ancestor of a; the depth is the
+// number of bits.  More rows: a thread walks from its node up to the root.  Parents
+// come before their children, so both end, and the walk meets the mask's words from
+// the last to the first.
+constexpr int KT_LDS = 2048, KT_FAST = 256;
 
 __global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__restrict__ parent, Kv4Tables s, int T,
                                                             uint32_t *__restrict__ mask, int words,
@@ -28,12 +30,49 @@ __global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__res
                                                             int32_t *__restrict__ slots)
 {
     __shared__ int up[KT_LDS];
-    const int seq = blockIdx.x;
+    __shared__ uint32_t seen[KT_FAST / 32][KT_FAST];
+    const int seq = blockIdx.x, tid = threadIdx.x;
     const int q0 = kt_clamp(s.q_start[seq], 0, T), n = kt_clamp(s.q_start[seq + 1], q0, T) - q0;
     const int kv = kt_clamp(s.kv_len[seq], 0, s.width << s.page_shift);
-    for (int i = threadIdx.x; i < min(n, KT_LDS); i += 256) up[i] = parent[q0 + i];
+    if (n <= KT_FAST) {
+        const int own = (n + 31) >> 5;                     // words that hold bits
+        const bool in = tid < n;
+        int a = in ? parent[q0 + tid] : -1;
+        a = a >= 0 && a < tid ? a : -1;                    // a parent that is none: a root
+        const int slot = in && slots ? kt_slot(s, seq, (int64_t)kv - n + tid) : 0;
+        uint32_t m[KT_FAST / 32];
+#pragma unroll
+        for (int w = 0; w < KT_FAST / 32; ++w) m[w] = w == tid >> 5 ? 1u << (tid & 31) : 0u;
+        while (true) {
+            up[tid] = a;
+#pragma unroll
+            for (int w = 0; w < KT_FAST / 32; ++w)
+                if (w < own) seen[w][tid] = m[w];
+            if (!__syncthreads_or(a >= 0)) break;
+            if (a >= 0) {
+#pragma unroll
+                for (int w = 0; w < KT_FAST / 32; ++w)
+                    if (w < own) m[w] |= seen[w][a];
+                a = up[a];
+            }
+            __syncthreads();                               // every read of this round is done
+        }
+        if (!in) return;
+        uint32_t *row = mask + (int64_t)(q0 + tid) * words;
+        int bits = 0;
+#pragma unroll
+        for (int w = 0; w < KT_FAST / 32; ++w) {
+            bits += __popc(m[w]);
+            if (w < words) row[w] = m[w];
+        }
+        for (int w = KT_FAST / 32; w < words; ++w) row[w] = 0;
+        if (position) position[q0 + tid] = kv - n + bits - 1;
+        if (slots) slots[q0 + tid] = slot;
+        return;
+    }
+    for (int i = tid; i < min(n, KT_LDS); i += 256) up[i] = parent[q0 + i];
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += 256) {
+    for (int i = tid; i < n; i += 256) {
         uint32_t *row = mask + (int64_t)(q0 + i) * words;
         int w = words - 1, depth = -1;
         uint32_t bits = 0;
@@ -50,15 +89,15 @@ __global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__res
     }
 }
 
-// Bytes of one token and head: K codes D / 2 in four parts, V codes D / 2 in
-// single bytes, the scales; each thread holds one piece of each token.
+// Pieces of one token and head: the dwords of K's codes, the codes of V that lie in
+// one lane's part (a byte in every dword of D / 8 bytes), the scales.
 template <bool INT4, int D>
 struct KtToken {
-    static constexpr int NG = INT4 ? D / 64 : D / 32;
-    static constexpr int KD = D / 8, VB = D / 2;           // dwords of K, bytes of V
+    static constexpr int NG = INT4 ? D / 64 : D / 32, KD = D / 8, VB = D / 32;
+    static constexpr int kUnits = KD + 16 + 2 * NG;
 };
 
-// A block moves one sequence's path in one head.  It reads the pieces of 32
+// A block moves one sequence's path in one head.  It reads the pieces of 64
 // tokens, waits for all of them, and writes: a path's nodes ascend, so a node
 // lies at or behind its new place, and nothing that is written is read later.
 template <bool INT4, int D>
@@ -67,8 +106,8 @@ __global__ __launch_bounds__(256) void kv4_keep_path_kernel(Kv4View c, Kv4Tables
                                                             int32_t *__restrict__ new_len)
 {
     typedef KtToken<INT4, D> Tok;
-    constexpr int NG = Tok::NG, CHUNK = 32;
-    __shared__ int src[CHUNK], dst[CHUNK];
+    constexpr int NG = Tok::NG, CHUNK = 64;
+    __shared__ int src[CHUNK], dst[CHUNK], found;
     const int head = blockIdx.x % c.heads, seq = blockIdx.x / c.heads, tid = threadIdx.x;
     const int q0 = kt_clamp(s.q_start[seq], 0, T), n = kt_clamp(s.q_start[seq + 1], q0, T) - q0;
     const int kv = kt_clamp(s.kv_len[seq], 0, s.width << s.page_shift);
@@ -80,67 +119,78 @@ __global__ __launch_bounds__(256) void kv4_keep_path_kernel(Kv4View c, Kv4Tables
         // the chunk's nodes: a path ends at the first that is not behind the one before it
         const int left = min(CHUNK, most - at);
         __syncthreads();
-        if (tid < 64) {
+        if (tid < CHUNK) {
             const int i = at + tid;
             const int node = tid < left ? nodes[i] : -1;
             const int before = tid < left && i > 0 ? nodes[i - 1] : -1;
-            const bool good = tid < left && node > before && node < n;
-            const uint64_t bad = ~__ballot(good);
-            const int count = bad ? __builtin_ctzll(bad) : 64;
-            if (tid < CHUNK) {
-                const int64_t base = (int64_t)kv - n;
-                const bool move = tid < count && node != i;
-                const int a = move ? kt_slot(s, seq, base + node) : -1, b = move ? kt_slot(s, seq, base + i) : -1;
-                src[tid] = a >= 0 && b >= 0 ? a : -1;
-                dst[tid] = tid < count ? b : -2;           // -2: the path has ended
-            }
+            const uint64_t bad = ~__ballot(tid < left && node > before && node < n);
+            const int count = bad ? __builtin_ctzll(bad) : CHUNK;
+            const int64_t base = (int64_t)kv - n;
+            const bool move = tid < count && node != i;
+            const int a = move ? kt_slot(s, seq, base + node) : -1, b = move ? kt_slot(s, seq, base + i) : -1;
+            src[tid] = b >= 0 ? a : -1, dst[tid] = b;
+            if (tid == 0) found = count;
         }
         __syncthreads();
-        int count = 0;
-        while (count < left && dst[count] != -2) ++count;
+        const int count = found;
         kept += count;
         more = count == CHUNK;
-        // pieces of 4 bytes of K, 1 of V, one scale each: unit u of token k
-        constexpr int UNITS = Tok::KD + Tok::VB + 2 * NG;
-        constexpr int PER = (CHUNK * UNITS + 255) / 256;
+        constexpr int UNITS = Tok::kUnits, PER = (CHUNK * UNITS + 255) / 256;
         uint32_t held[PER];
+        // unit u of the token in `slot`: its place, and which of the three it is
         auto place = [&](int slot, int u, uint8_t *&p) {
             const size_t page = (size_t)(slot >> c.page_shift);
             const int in = slot & ((1 << c.page_shift) - 1), r = in & 15;
             const size_t run = (((page * c.heads + head) << c.page_shift) + in) >> 4;
             if (u < Tok::KD) {
                 p = c.k_codes + run * (8 * D) + kv4_k_offset<INT4>(r, 8 * u, D);
-                return 4;
+                return 0;
             }
             u -= Tok::KD;
-            if (u < Tok::VB) {
-                p = c.v_codes + run * (8 * D) + kv4_v_offset(r, u >> 4, u & 15, D);
+            if (u < 16) {
+                p = c.v_codes + run * (8 * D) + kv4_v_offset(r, 0, u, D);
                 return 1;
             }
-            u -= Tok::VB;
+            u -= 16;
             void *sc = u < NG ? c.k_scales : c.v_scales;
             u = u < NG ? u : u - NG;
             p = (uint8_t *)sc + (run * (16 * NG) + 16 * u + r) * (INT4 ? 4 : 1);
-            return INT4 ? 4 : 1;
+            return 2;
         };
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
+            if (256 * k >= count * UNITS) break;
             const int e = tid + 256 * k, tok = e / UNITS, u = e % UNITS;
             held[k] = 0;
             if (tok >= count || src[tok] < 0) continue;
             uint8_t *p;
-            if (place(src[tok], u, p) == 4) held[k] = *reinterpret_cast<const uint32_t *>(p);
-            else held[k] = *p;
+            const int kind = place(src[tok], u, p);
+            if (kind == 1) {
+#pragma unroll
+                for (int i = 0; i < Tok::VB; ++i) held[k] |= (uint32_t)p[4 * i] << (8 * i);
+            } else if (INT4 || kind == 0) {
+                held[k] = *reinterpret_cast<const uint32_t *>(p);
+            } else {
+                held[k] = *p;
+            }
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's pieces have arrived
         __syncthreads();                                   // and every wave's
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
+            if (256 * k >= count * UNITS) break;
             const int e = tid + 256 * k, tok = e / UNITS, u = e % UNITS;
             if (tok >= count || src[tok] < 0) continue;
             uint8_t *p;
-            if (place(dst[tok], u, p) == 4) *reinterpret_cast<uint32_t *>(p) = held[k];
-            else *p = (uint8_t)held[k];
+            const int kind = place(dst[tok], u, p);
+            if (kind == 1) {
+#pragma unroll
+                for (int i = 0; i < Tok::VB; ++i) p[4 * i] = (uint8_t)(held[k] >> (8 * i));
+            } else if (INT4 || kind == 0) {
+                *reinterpret_cast<uint32_t *>(p) = held[k];
+            } else {
+                *p = (uint8_t)held[k];
+            }
         }
     }
     if (head == 0 && tid == 0) new_len[seq] = kv - n + kept;

@@ -5,11 +5,12 @@
 //   angle_tp = pos_t,axis(p) freq_p;   u = x / sqrt(mean(x^2) + eps) w
 //   a' = a cos - b sin, b' = b cos + a sin   for the pair (a, b) of u
 //
-// Everything between the loads and the one rounding to bf16 is 64 bits: a key
-// goes on into 4 bits, where a last place of fp32 next to a rounding border
-// would move a code by a whole step, and vector fp64 runs here at the rate of
-// fp32.  So codes are those of the exactly rotated key, whatever order a
-// kernel sums in.
+// Keys: everything between the loads and the one rounding to bf16 is 64 bits.  A
+// key goes on into 4 bits, where a last place of fp32 next to a rounding border
+// would move a code by a whole step; so its codes are those of the exactly rotated
+// key, whatever order a kernel sums in, and the two kernels agree.  Queries end in
+// bf16 and are fp32 (the conversions to and from fp64 took most of the time), but
+// for heads whose squares leave its range.
 //
 // A head is D / 16 lanes of 16 channels: two pieces of 8 (16 bytes each, a
 // head's pieces next to each other in a wave's load), chosen so that both
@@ -61,27 +62,18 @@ __device__ __forceinline__ void rp_cos_sin(double a, float &c, float &s)
     s = n & 2 ? -y : y;
 }
 
-// Four pairs of a token per thread.
-__global__ __launch_bounds__(256) void rope_table_kernel(const int32_t *__restrict__ pos, int64_t n4, int axes,
+__global__ __launch_bounds__(256) void rope_table_kernel(const int32_t *__restrict__ pos, int64_t n, int axes,
                                                          const double *__restrict__ freq,
                                                          const int32_t *__restrict__ axis, int pairs,
                                                          float *__restrict__ cos, float *__restrict__ sin)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n4) return;
-    const int q4 = pairs >> 2;
-    const int64_t t = i / q4;
-    const int p = 4 * (int)(i % q4);
-    float c[4], s[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int a = axis[p + k];
-        const bool in = (uint32_t)a < (uint32_t)axes;
-        const int at = pos[t * axes + (in ? a : 0)];
-        rp_cos_sin(in ? (double)at * freq[p + k] : 0.0, c[k], s[k]);
-    }
-    reinterpret_cast<float4 *>(cos)[i] = make_float4(c[0], c[1], c[2], c[3]);
-    reinterpret_cast<float4 *>(sin)[i] = make_float4(s[0], s[1], s[2], s[3]);
+    if (i >= n) return;
+    const int64_t t = i / pairs;
+    const int p = (int)(i % pairs), a = axis[p];
+    const bool in = (uint32_t)a < (uint32_t)axes;
+    const int at = pos[t * axes + (in ? a : 0)];
+    rp_cos_sin(in ? (double)at * freq[p] : 0.0, cos[i], sin[i]);
 }
 
 // Channels of a lane's two pieces, and the pairs that they hold.
@@ -110,7 +102,7 @@ __device__ __forceinline__ RopeLane<D, HALVES> rp_lane(int i, int pairs)
 
 // A lane's eight cosines and sines of a token.
 struct RopeTurn {
-    double c[8], s[8];
+    float c[8], s[8];
 };
 
 template <int D, bool HALVES>
@@ -133,14 +125,15 @@ __device__ __forceinline__ RopeTurn rp_turn(const RopeArgs &r, const RopeLane<D,
     return o;
 }
 
-__device__ __forceinline__ void rp_unpack8(const uint4 &u, double *f)
+template <class F>
+__device__ __forceinline__ void rp_unpack8(const uint4 &u, F *f)
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[2 * i] = bits_f32(w[i] << 16), f[2 * i + 1] = bits_f32(w[i] & 0xFFFF0000u);
 }
 
-// 1 / sqrt(x): the instruction's estimate and two Newton steps.
+// 1 / sqrt(x): fp64 from the instruction's estimate by two Newton steps.
 __device__ __forceinline__ double rp_rsqrt(double x)
 {
     const double h = 0.5 * x;
@@ -148,24 +141,30 @@ __device__ __forceinline__ double rp_rsqrt(double x)
     y *= __builtin_fma(-h * y, y, 1.5);
     return y * __builtin_fma(-h * y, y, 1.5);
 }
+__device__ __forceinline__ float rp_rsqrt(float x) { return __builtin_amdgcn_rsqf(x); }
 
-// Norm (w given) and rotation of a lane's pieces xa, xb in place.
-template <int D, bool HALVES>
-__device__ __forceinline__ void rp_apply(uint4 &xa, uint4 &xb, const uint16_t *w, const RopeLane<D, HALVES> &l,
+__device__ __forceinline__ double rp_fma(double a, double b, double c) { return __builtin_fma(a, b, c); }
+__device__ __forceinline__ float rp_fma(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+
+// Norm (with the lane's weights g, if there is one) and rotation of a lane's pieces
+// xa, xb in place.  fp32: nothing is done and true returned where some head of the
+// wave has a sum of squares that fp32 may not hold to its last places.
+template <class F, int D, bool HALVES>
+__device__ __forceinline__ bool rp_apply(uint4 &xa, uint4 &xb, bool norm, const uint4 &ga, const uint4 &gb,
                                          const RopeTurn &r, double eps)
 {
-    double u[16];
+    F u[16];
     rp_unpack8(xa, u), rp_unpack8(xb, u + 8);
-    double ss = 0.0;
+    if (norm) {
+        F ss = 0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) ss = __builtin_fma(u[k], u[k], ss);
+        for (int k = 0; k < 16; ++k) ss = rp_fma(u[k], u[k], ss);
 #pragma unroll
-    for (int d = 1; d < D / 16; d <<= 1) ss += __shfl_xor(ss, d);
-    if (w) {
-        const double rs = rp_rsqrt(__builtin_fma(ss, 1.0 / D, eps));
-        double g[16];
-        rp_unpack8(*reinterpret_cast<const uint4 *>(w + l.a), g);
-        rp_unpack8(*reinterpret_cast<const uint4 *>(w + l.b), g + 8);
+        for (int d = 1; d < D / 16; d <<= 1) ss += __shfl_xor(ss, d);
+        if (sizeof(F) == 4 && __any(!(ss > (F)1e-25 && ss < (F)1e35))) return true;
+        const F rs = rp_rsqrt(rp_fma(ss, (F)(1.0 / D), (F)eps));
+        F g[16];
+        rp_unpack8(ga, g), rp_unpack8(gb, g + 8);
 #pragma unroll
         for (int k = 0; k < 16; ++k) u[k] = u[k] * rs * g[k];
     }
@@ -173,15 +172,52 @@ __device__ __forceinline__ void rp_apply(uint4 &xa, uint4 &xb, const uint16_t *w
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const int a = HALVES ? p : 2 * p, b = HALVES ? p + 8 : 2 * p + 1;
-        o[a] = (float)__builtin_fma(u[a], r.c[p], -(u[b] * r.s[p]));
-        o[b] = (float)__builtin_fma(u[b], r.c[p], u[a] * r.s[p]);
+        const F c = r.c[p], s = r.s[p];
+        o[a] = (float)rp_fma(u[a], c, -(u[b] * s));
+        o[b] = (float)rp_fma(u[b], c, u[a] * s);
     }
     xa = make_uint4(rp_pack2(o[0], o[1]), rp_pack2(o[2], o[3]), rp_pack2(o[4], o[5]), rp_pack2(o[6], o[7]));
     xb = make_uint4(rp_pack2(o[8], o[9]), rp_pack2(o[10], o[11]), rp_pack2(o[12], o[13]), rp_pack2(o[14], o[15]));
+    return false;
 }
 
-// A wave's share of one token's heads: every parts-th set of 64 / (D / 16)
-// heads, queries first, then keys (none of them in the cache's form).
+// A lane's norm weights.
+template <int D, bool HALVES>
+__device__ __forceinline__ void rp_weights(const uint16_t *w, const RopeLane<D, HALVES> &l, uint4 &ga, uint4 &gb)
+{
+    ga = gb = make_uint4(0u, 0u, 0u, 0u);
+    if (w) ga = *reinterpret_cast<const uint4 *>(w + l.a), gb = *reinterpret_cast<const uint4 *>(w + l.b);
+}
+
+// One token's heads of one kind, sets first, first + step, .. of 64 / (D / 16) heads
+// each.
+template <class F, int D, bool HALVES>
+__device__ __forceinline__ void rp_heads(const uint16_t *x, uint16_t *y, int heads, int first, int step,
+                                         const uint16_t *w, const RopeLane<D, HALVES> &l, const RopeTurn &turn,
+                                         double eps, int lane)
+{
+    constexpr int L = D / 16, S = 64 / L;
+    uint4 ga, gb;
+    rp_weights<D, HALVES>(w, l, ga, gb);
+    auto load = [&](int set, uint4 &a, uint4 &b) {
+        const int64_t h = min(set * S + lane / L, heads - 1);      // heads past the last repeat it, never stored
+        a = *reinterpret_cast<const uint4 *>(x + h * D + l.a), b = *reinterpret_cast<const uint4 *>(x + h * D + l.b);
+    };
+    uint4 na, nb;
+    load(first, na, nb);
+    for (int set = first; set * S < heads; set += step) {
+        uint4 xa = na, xb = nb;
+        load(set + step, na, nb);
+        if (rp_apply<F, D, HALVES>(xa, xb, w != nullptr, ga, gb, turn, eps))
+            rp_apply<double, D, HALVES>(xa, xb, true, ga, gb, turn, eps);
+        const int64_t h = set * S + lane / L;
+        if (h >= heads) continue;
+        *reinterpret_cast<uint4 *>(y + h * D + l.a) = xa;
+        *reinterpret_cast<uint4 *>(y + h * D + l.b) = xb;
+    }
+}
+
+// A wave's share of one token: every parts-th set of heads, queries, then keys.
 template <int D, bool HALVES>
 __device__ __forceinline__ void rp_rows(const RopeArgs &r, int64_t item, int lane)
 {
@@ -189,26 +225,14 @@ __device__ __forceinline__ void rp_rows(const RopeArgs &r, int64_t item, int lan
     if (item >= (int64_t)r.T * r.parts) return;
     const int t = (int)(item / r.parts), part = (int)(item % r.parts);
     const RopeLane<D, HALVES> l = rp_lane<D, HALVES>(lane % L, r.pairs);
-    const int heads = r.heads_q + r.heads_k, step = r.parts * S;
-    int h = part * S + lane / L;
-    auto source = [&](int hh) {
-        const int g = min(hh, heads - 1);                  // heads past the last repeat it, never stored
-        return g < r.heads_q ? r.Q + t * r.ldq + (int64_t)g * D : r.K + t * r.ldk + (int64_t)(g - r.heads_q) * D;
-    };
-    const uint16_t *p = source(h);
-    uint4 na = *reinterpret_cast<const uint4 *>(p + l.a), nb = *reinterpret_cast<const uint4 *>(p + l.b);
     const RopeTurn turn = rp_turn(r, l, t);
-    for (int h0 = part * S; h0 < heads; h0 += step, h += step) {
-        uint4 xa = na, xb = nb;
-        p = source(h + step);
-        na = *reinterpret_cast<const uint4 *>(p + l.a), nb = *reinterpret_cast<const uint4 *>(p + l.b);
-        rp_apply(xa, xb, h < r.heads_q ? r.wq : r.wk, l, turn, r.eps);
-        if (h >= heads) continue;
-        uint16_t *o = h < r.heads_q ? r.Qo + t * r.ldqo + (int64_t)h * D
-                                    : r.Ko + t * r.ldko + (int64_t)(h - r.heads_q) * D;
-        *reinterpret_cast<uint4 *>(o + l.a) = xa;
-        *reinterpret_cast<uint4 *>(o + l.b) = xb;
-    }
+    const int nq = (r.heads_q + S - 1) / S;
+    if (part < nq)
+        rp_heads<float, D, HALVES>(r.Q + t * r.ldq, r.Qo + t * r.ldqo, r.heads_q, part, r.parts, r.wq, l, turn, r.eps, lane);
+    // the keys' sets follow the queries'
+    const int first = part >= nq ? part - nq : (r.parts - (nq - part) % r.parts) % r.parts;
+    if (r.heads_k > 0 && first * S < r.heads_k)
+        rp_heads<double, D, HALVES>(r.K + t * r.ldk, r.Ko + t * r.ldko, r.heads_k, first, r.parts, r.wk, l, turn, r.eps, lane);
 }
 
 template <int D, bool HALVES>
@@ -243,7 +267,9 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_rope_append_kernel(Kv4View c, 
         const RopeLane<D, HALVES> l = rp_lane<D, HALVES>(tid % L, r.pairs);
         const uint16_t *p = r.K + t * r.ldk + (int64_t)head * D;
         uint4 xa = *reinterpret_cast<const uint4 *>(p + l.a), xb = *reinterpret_cast<const uint4 *>(p + l.b);
-        rp_apply(xa, xb, r.wk, l, rp_turn(r, l, t), r.eps);
+        uint4 ga, gb;
+        rp_weights<D, HALVES>(r.wk, l, ga, gb);
+        rp_apply<double, D, HALVES>(xa, xb, r.wk != nullptr, ga, gb, rp_turn(r, l, t), r.eps);
         *reinterpret_cast<uint4 *>(kr + tid / L * ROW + l.a) = xa;
         *reinterpret_cast<uint4 *>(kr + tid / L * ROW + l.b) = xb;
     }
@@ -256,9 +282,9 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_rope_append_kernel(Kv4View c, 
 
 // Waves per token: as many as give eight waves per compute unit, at most one
 // per set of heads.
-int rope_parts(int T, int heads, int D)
+int rope_parts(int T, int heads_q, int heads_k, int D)
 {
-    const int sets = (heads + 64 / (D / 16) - 1) / (64 / (D / 16));
+    const int S = 64 / (D / 16), sets = (heads_q + S - 1) / S + (heads_k + S - 1) / S;
     const int64_t want = (8 * (int64_t)device_cu_count() + T - 1) / T;
     return (int)(want < sets ? want : sets);
 }
@@ -283,14 +309,14 @@ void rope_frequencies(const int *sections, int axes, double theta, svdq_rope_axe
 hipError_t launch_rope_table(const int32_t *pos, int T, int axes, const double *freq, const int32_t *axis, int pairs,
                              float *cos, float *sin, hipStream_t stream)
 {
-    const int64_t n4 = (int64_t)T * (pairs / 4);
-    rope_table_kernel<<<(uint32_t)((n4 + 255) / 256), 256, 0, stream>>>(pos, n4, axes, freq, axis, pairs, cos, sin);
+    const int64_t n = (int64_t)T * pairs;
+    rope_table_kernel<<<(uint32_t)((n + 255) / 256), 256, 0, stream>>>(pos, n, axes, freq, axis, pairs, cos, sin);
     return hipGetLastError();
 }
 
 hipError_t launch_qk_norm_rope(RopeArgs r, int dim, bool halves, hipStream_t stream)
 {
-    r.parts = rope_parts(r.T, r.heads_q + r.heads_k, dim);
+    r.parts = rope_parts(r.T, r.heads_q, r.heads_k, dim);
     const uint32_t grid = (uint32_t)(((int64_t)r.T * r.parts + 3) / 4);
     if (dim == 64) halves ? qk_norm_rope_kernel<64, true><<<grid, 256, 0, stream>>>(r) : qk_norm_rope_kernel<64, false><<<grid, 256, 0, stream>>>(r);
     else if (dim == 128) halves ? qk_norm_rope_kernel<128, true><<<grid, 256, 0, stream>>>(r) : qk_norm_rope_kernel<128, false><<<grid, 256, 0, stream>>>(r);
@@ -302,7 +328,7 @@ hipError_t launch_kv4_rope_append(const Kv4View &c, RopeArgs r, bool halves, con
                                   const int32_t *slots, hipStream_t stream)
 {
     r.heads_k = 0;                                         // the waves of rows take the queries alone
-    r.parts = rope_parts(r.T, r.heads_q, c.dim);
+    r.parts = rope_parts(r.T, r.heads_q, 0, c.dim);
     const int tb = 2048 / c.dim;
     const uint32_t kv = (uint32_t)((r.T + tb - 1) / tb) * c.heads;
     const uint32_t grid = kv + (uint32_t)(((int64_t)r.T * r.parts + 3) / 4);
