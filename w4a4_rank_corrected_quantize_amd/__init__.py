@@ -576,10 +576,20 @@ _ELEMENTS = 1 << 30        # SVDQ_MAX_ELEMENTS
 
 
 def _tt():
-    global _T
+    global _T, _BF, _F32, _F64, _U8, _INT32, _raw_stream, _current_device
     if _T is None:
         _T = _torch()
+        _BF, _F32, _F64, _U8, _INT32 = _T.bfloat16, _T.float32, _T.float64, _T.uint8, _T.int32
+        _raw_stream = getattr(_T._C, "_cuda_getCurrentRawStream", None)
+        _current_device = getattr(_T._C, "_cuda_getDevice", None)
     return _T
+
+
+# The calls of a decoding step take about 4 us in the library and its launch, and
+# the checks one by one (_arg, _launch) as long again.  So they first ask for
+# everything at once, with outputs given or new ones like their inputs, on the
+# current stream; what that does not let through goes the way of the single checks,
+# which take it or say what is wrong.
 
 
 def _bad(t, dtype, name, shape):
@@ -778,25 +788,54 @@ def _few_args(where, xq, xscale, h, wq, wscale, up, bias, prec, halves, Y, strea
                           up.data_ptr(), _ptr(bias), M, C, K, r)
 
 
+def _few_call(where, call, xq, xscale, h, wq, wscale, up, bias, prec, halves, last, Y, stream):
+    if _T is None:
+        _tt()
+    raw = None
+    try:
+        M, KB = xq.shape
+        N, r = up.shape
+        C, dev = N // halves, xq.get_device()
+        sdt, G = (_F32, KB >> 5) if prec == INT4 else (_U8, KB >> 4)
+        if Y is None and stream is None and dev >= 0:
+            Y = xq.new_empty((M, C), dtype=_BF)
+        if (stream is None and dev >= 0 and dev == _current_device() == wq.get_device() == xscale.get_device()
+                == wscale.get_device() == h.get_device() == up.get_device() == Y.get_device()
+                and xq.dtype is _U8 and wq.dtype is _U8 and xscale.dtype is sdt and wscale.dtype is sdt
+                and h.dtype is _F32 and up.dtype is _BF and Y.dtype is _BF and C * halves == N
+                and xscale.shape == (M, G) and h.shape == (M, r) and wq.shape == (N, KB) and wscale.shape == (N, G)
+                and Y.shape == (M, C) and xq.is_contiguous() and wq.is_contiguous() and xscale.is_contiguous()
+                and wscale.is_contiguous() and h.is_contiguous() and up.is_contiguous() and Y.is_contiguous()
+                and (bias is None or (bias.dtype is _BF and bias.shape == (N,) and bias.get_device() == dev
+                                      and bias.is_contiguous()))
+                and M * KB < _ELEMENTS and N * KB < _ELEMENTS and prec in (INT4, MXFP4)):
+            raw = _raw_stream(dev)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if raw is None:
+        Y, prec, raw, (_, _, _, _, _, _, _, M, C, K, r) = _few_args(where, xq, xscale, h, wq, wscale, up, bias, prec, halves,
+                                                                   Y, stream)
+        KB = K // 2
+    st = call(xq.data_ptr(), xscale.data_ptr(), h.data_ptr(), wq.data_ptr(), wscale.data_ptr(), up.data_ptr(),
+              None if bias is None else bias.data_ptr(), M, C, 2 * KB, r, prec, last, Y.data_ptr(), raw)
+    if st:
+        raise SvdqError(st, where)
+    return Y
+
+
 def w4a4_linear_few(xq, xscale, h, wq, wscale, up, bias, prec: int = INT4, epi: int = EPI_NONE, Y=None, stream=None):
     """w4a4_linear for few rows (single tokens, drafted tokens; at most
     FEW_MAX_ROWS): one pass over the weights per 64 rows (one kernel)."""
-    Y, prec, raw, args = _few_args("svdq_w4a4_linear_few", xq, xscale, h, wq, wscale, up, bias, prec, 1, Y, stream)
-    st = lib().svdq_w4a4_linear_few(*args, prec, epi, Y.data_ptr(), raw)
-    if st:
-        raise SvdqError(st, "svdq_w4a4_linear_few")
-    return Y
+    return _few_call("svdq_w4a4_linear_few", (_lib or lib()).svdq_w4a4_linear_few, xq, xscale, h, wq, wscale, up, bias,
+                     prec, 1, epi, Y, stream)
 
 
 def w4a4_linear_gated(xq, xscale, h, wq, wscale, up, bias, prec: int = INT4, act: int = ACT_SILU, Y=None, stream=None):
     """act(gate) * up of a gated MLP (one kernel): wq, wscale, up and bias hold the
     gate projection's rows, then the up projection's.  Any number of rows; Y [M][F]
     bf16."""
-    Y, prec, raw, args = _few_args("svdq_w4a4_linear_gated", xq, xscale, h, wq, wscale, up, bias, prec, 2, Y, stream)
-    st = lib().svdq_w4a4_linear_gated(*args, prec, act, Y.data_ptr(), raw)
-    if st:
-        raise SvdqError(st, "svdq_w4a4_linear_gated")
-    return Y
+    return _few_call("svdq_w4a4_linear_gated", (_lib or lib()).svdq_w4a4_linear_gated, xq, xscale, h, wq, wscale, up,
+                     bias, prec, 2, act, Y, stream)
 
 
 class LoraPlan:
@@ -916,6 +955,7 @@ class Kv4Cache:
         self._k_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
         self._v_scales = torch.empty((pages, heads, runs, g, 16), dtype=sdt, device=device)
         self.device = self._k_codes.device
+        self.index = self._k_codes.get_device()           # -1 on the CPU
         self._struct = _Kv4Struct(self._k_codes.data_ptr(), self._k_scales.data_ptr(), self._v_codes.data_ptr(),
                                   self._v_scales.data_ptr(), pages, page_size, heads, dim, prec)
         self._ref = ctypes.addressof(self._struct)
@@ -1059,36 +1099,59 @@ def kv4_tree_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, mask, m
     """kv4_attention of drafted tokens: row i of a sequence's n sees the keys
     before place kv_len - n, and of the drafted ones those in its mask [T][words]
     int32 (kv4_tree_plan).  Workspace as for kv4_attention."""
-    torch = _tt()
-    i32 = torch.int32
-    dev = _cache_arg(cache)
-    _ndim(Q, 3, "Q")
-    H, D = Q.shape[1], cache.dim
-    if H == 0 or H % cache.heads:
-        raise ValueError(f"Q has {H} heads, the cache {cache.heads}")
-    T, ldq = _heads_arg(Q, "Q", H, D)
-    _ndim(block_table, 2, "block_table")
-    _arg(block_table, i32, "block_table")
-    B, width = block_table.shape
-    _arg(q_start, i32, "q_start", (B + 1,))
-    _arg(kv_len, i32, "kv_len", (B,))
-    _ndim(mask, 2, "mask")
-    words = mask.shape[1]
-    _arg(mask, i32, "mask", (T, words))
-    if B > _I32 or width > _I32 or words > _I32:
-        raise SvdqError(-2, "svdq_kv4_tree_attention")
-    max_q, max_kv = _bound(max_q), _bound(max_kv)
-    out = _empty((T, H, D), torch.bfloat16, dev, stream, Q) if out is None else _arg(
-        out, torch.bfloat16, "out", (T, H, D))
-    if lse is not None:
-        _arg(lse, torch.float32, "lse", (T, H))
-    if work is None:
-        need = kv4_attention_workspace_bytes(cache, T, B, H, max_q, max_kv)
-        work = _empty(need, torch.uint8, dev, stream) if need else None
-    else:
-        _arg(work, torch.uint8, "work")
-    raw = _launch(dev, ("Q", "block_table", "q_start", "kv_len", "mask", "out", "lse", "work"),
-                  (Q, block_table, q_start, kv_len, mask, out, lse, work), stream)
+    torch = _T or _tt()
+    raw = None
+    try:
+        T, H, D = Q.shape
+        ldq, sh, sd = Q.stride()
+        B, width = block_table.shape
+        words, dev = mask.shape[1], Q.get_device()
+        if (stream is None and out is not None and work is not None and dev >= 0
+                and dev == _current_device() == cache.index == block_table.get_device() == q_start.get_device()
+                == kv_len.get_device() == mask.get_device() == out.get_device() == work.get_device()
+                and Q.dtype is _BF and out.dtype is _BF and block_table.dtype is _INT32 and q_start.dtype is _INT32
+                and kv_len.dtype is _INT32 and mask.dtype is _INT32 and work.dtype is _U8 and D == cache.dim and sd == 1
+                and sh == D and H and H % cache.heads == 0 and q_start.shape == (B + 1,) and kv_len.shape == (B,)
+                and mask.shape == (T, words) and out.shape == Q.shape and out.is_contiguous() and mask.is_contiguous()
+                and block_table.is_contiguous() and q_start.is_contiguous() and kv_len.is_contiguous()
+                and work.is_contiguous() and 0 <= max_q <= _I32 and 0 <= max_kv <= _I32
+                and T < _I32 and B < _I32 and width < _I32
+                and (lse is None or (lse.dtype is _F32 and lse.shape == (T, H) and lse.get_device() == dev
+                                     and lse.is_contiguous()))):
+            raw = _raw_stream(dev)
+            ldq = ldq if T > 1 else H * D
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if raw is None:
+        i32 = torch.int32
+        dev = _cache_arg(cache)
+        _ndim(Q, 3, "Q")
+        H, D = Q.shape[1], cache.dim
+        if H == 0 or H % cache.heads:
+            raise ValueError(f"Q has {H} heads, the cache {cache.heads}")
+        T, ldq = _heads_arg(Q, "Q", H, D)
+        _ndim(block_table, 2, "block_table")
+        _arg(block_table, i32, "block_table")
+        B, width = block_table.shape
+        _arg(q_start, i32, "q_start", (B + 1,))
+        _arg(kv_len, i32, "kv_len", (B,))
+        _ndim(mask, 2, "mask")
+        words = mask.shape[1]
+        _arg(mask, i32, "mask", (T, words))
+        if B > _I32 or width > _I32 or words > _I32:
+            raise SvdqError(-2, "svdq_kv4_tree_attention")
+        max_q, max_kv = _bound(max_q), _bound(max_kv)
+        out = _empty((T, H, D), torch.bfloat16, dev, stream, Q) if out is None else _arg(
+            out, torch.bfloat16, "out", (T, H, D))
+        if lse is not None:
+            _arg(lse, torch.float32, "lse", (T, H))
+        if work is None:
+            need = kv4_attention_workspace_bytes(cache, T, B, H, max_q, max_kv)
+            work = _empty(need, torch.uint8, dev, stream) if need else None
+        else:
+            _arg(work, torch.uint8, "work")
+        raw = _launch(dev, ("Q", "block_table", "q_start", "kv_len", "mask", "out", "lse", "work"),
+                      (Q, block_table, q_start, kv_len, mask, out, lse, work), stream)
     st = lib().svdq_kv4_tree_attention(cache._ref, Q.data_ptr(), ldq, block_table.data_ptr(), width,
                                        q_start.data_ptr(), kv_len.data_ptr(), mask.data_ptr(), words, B, T, H, max_q,
                                        max_kv, D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
@@ -1108,27 +1171,46 @@ def kv4_tree_plan(cache: Kv4Cache, parent, q_start, kv_len, block_table, max_q: 
     own; -1: a child of the last known token); max_q bounds the rows of a sequence
     (at most 1024) and gives the mask's words.  kv_len counts the drafted tokens.
     Returns (mask [T][ceil(max_q / 32)], position [T], slots [T]), int32."""
-    torch = _tt()
-    i32 = torch.int32
-    dev = _cache_arg(cache)
-    _ndim(parent, 1, "parent")
-    _arg(parent, i32, "parent")
-    T = parent.shape[0]
-    _ndim(block_table, 2, "block_table")
-    _arg(block_table, i32, "block_table")
-    B, width = block_table.shape
-    _arg(q_start, i32, "q_start", (B + 1,))
-    _arg(kv_len, i32, "kv_len", (B,))
-    if T > _I32 or B > _I32 or width > _I32:
-        raise SvdqError(-2, "svdq_kv4_tree_plan")
-    if not 1 <= max_q <= 32 * TREE_MAX_WORDS:
-        raise ValueError(f"max_q must be 1 .. {32 * TREE_MAX_WORDS}, got {max_q}")
-    words = (max_q + 31) // 32
-    mask = _empty((T, words), i32, dev, stream) if mask is None else _arg(mask, i32, "mask", (T, words))
-    position = _empty((T,), i32, dev, stream, parent) if position is None else _arg(position, i32, "position", (T,))
-    slots = _empty((T,), i32, dev, stream, parent) if slots is None else _arg(slots, i32, "slots", (T,))
-    raw = _launch(dev, ("parent", "q_start", "kv_len", "block_table", "mask", "position", "slots"),
-                  (parent, q_start, kv_len, block_table, mask, position, slots), stream)
+    torch = _T or _tt()
+    raw = None
+    try:
+        T, = parent.shape
+        B, width = block_table.shape
+        dev = parent.get_device()
+        if (stream is None and dev >= 0 and dev == _current_device() == cache.index == block_table.get_device()
+                == q_start.get_device() == kv_len.get_device() and parent.dtype is _INT32 and block_table.dtype is _INT32
+                and q_start.dtype is _INT32 and kv_len.dtype is _INT32 and q_start.shape == (B + 1,)
+                and kv_len.shape == (B,) and parent.is_contiguous() and block_table.is_contiguous()
+                and q_start.is_contiguous() and kv_len.is_contiguous() and 1 <= max_q <= 32 * TREE_MAX_WORDS
+                and T < _I32 and B < _I32 and width < _I32):
+            words = (max_q + 31) // 32
+            if mask is None and position is None and slots is None:
+                mask, position = parent.new_empty((T, words)), torch.empty_like(parent)
+                slots = torch.empty_like(parent)
+                raw = _raw_stream(dev)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if raw is None:
+        i32 = torch.int32
+        dev = _cache_arg(cache)
+        _ndim(parent, 1, "parent")
+        _arg(parent, i32, "parent")
+        T = parent.shape[0]
+        _ndim(block_table, 2, "block_table")
+        _arg(block_table, i32, "block_table")
+        B, width = block_table.shape
+        _arg(q_start, i32, "q_start", (B + 1,))
+        _arg(kv_len, i32, "kv_len", (B,))
+        if T > _I32 or B > _I32 or width > _I32:
+            raise SvdqError(-2, "svdq_kv4_tree_plan")
+        if not 1 <= max_q <= 32 * TREE_MAX_WORDS:
+            raise ValueError(f"max_q must be 1 .. {32 * TREE_MAX_WORDS}, got {max_q}")
+        words = (max_q + 31) // 32
+        mask = _empty((T, words), i32, dev, stream) if mask is None else _arg(mask, i32, "mask", (T, words))
+        position = _empty((T,), i32, dev, stream, parent) if position is None else _arg(position, i32, "position", (T,))
+        slots = _empty((T,), i32, dev, stream, parent) if slots is None else _arg(slots, i32, "slots", (T,))
+        raw = _launch(dev, ("parent", "q_start", "kv_len", "block_table", "mask", "position", "slots"),
+                      (parent, q_start, kv_len, block_table, mask, position, slots), stream)
     st = lib().svdq_kv4_tree_plan(parent.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
                                   width, cache.pages, cache.page_size, B, T, mask.data_ptr(), words,
                                   position.data_ptr(), slots.data_ptr(), raw)
@@ -1143,23 +1225,38 @@ def kv4_keep_path(cache: Kv4Cache, path, q_start, kv_len, block_table, T: Option
     int32 (ascending, ended by -1), behind the known tokens (one kernel).  T: the
     step's rows; q_start's values are cut to it (None: not cut).  Returns the new
     lengths [B] int32 (not kv_len itself)."""
-    torch = _tt()
-    i32 = torch.int32
-    dev = _cache_arg(cache)
-    _ndim(block_table, 2, "block_table")
-    _arg(block_table, i32, "block_table")
-    B, width = block_table.shape
-    _ndim(path, 2, "path")
-    longest = path.shape[1]
-    _arg(path, i32, "path", (B, longest))
-    _arg(q_start, i32, "q_start", (B + 1,))
-    _arg(kv_len, i32, "kv_len", (B,))
-    T = _I32 if T is None else T
-    if B > _I32 or width > _I32 or longest > _I32 or T > _I32:
-        raise SvdqError(-2, "svdq_kv4_keep_path")
-    new_len = _empty((B,), i32, dev, stream, kv_len) if new_len is None else _arg(new_len, i32, "new_len", (B,))
-    raw = _launch(dev, ("path", "q_start", "kv_len", "block_table", "new_len"),
-                  (path, q_start, kv_len, block_table, new_len), stream)
+    torch = _T or _tt()
+    raw = None
+    try:
+        B, longest = path.shape
+        width, dev = block_table.shape[1], path.get_device()
+        if (stream is None and new_len is None and T is None and dev >= 0
+                and dev == _current_device() == cache.index == block_table.get_device() == q_start.get_device()
+                == kv_len.get_device() and path.dtype is _INT32 and block_table.dtype is _INT32
+                and q_start.dtype is _INT32 and kv_len.dtype is _INT32 and block_table.shape == (B, width)
+                and q_start.shape == (B + 1,) and kv_len.shape == (B,) and path.is_contiguous()
+                and block_table.is_contiguous() and q_start.is_contiguous() and kv_len.is_contiguous()
+                and B < _I32 and longest < _I32 and width < _I32):
+            new_len, T, raw = torch.empty_like(kv_len), _I32, _raw_stream(dev)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if raw is None:
+        i32 = torch.int32
+        dev = _cache_arg(cache)
+        _ndim(block_table, 2, "block_table")
+        _arg(block_table, i32, "block_table")
+        B, width = block_table.shape
+        _ndim(path, 2, "path")
+        longest = path.shape[1]
+        _arg(path, i32, "path", (B, longest))
+        _arg(q_start, i32, "q_start", (B + 1,))
+        _arg(kv_len, i32, "kv_len", (B,))
+        T = _I32 if T is None else T
+        if B > _I32 or width > _I32 or longest > _I32 or T > _I32:
+            raise SvdqError(-2, "svdq_kv4_keep_path")
+        new_len = _empty((B,), i32, dev, stream, kv_len) if new_len is None else _arg(new_len, i32, "new_len", (B,))
+        raw = _launch(dev, ("path", "q_start", "kv_len", "block_table", "new_len"),
+                      (path, q_start, kv_len, block_table, new_len), stream)
     st = lib().svdq_kv4_keep_path(cache._ref, path.data_ptr(), longest, q_start.data_ptr(), kv_len.data_ptr(),
                                   block_table.data_ptr(), width, B, T, new_len.data_ptr(), raw)
     if st:
@@ -1183,21 +1280,35 @@ def rope_frequencies(sections, theta: float = 10000.0, layout: int = ROPE_AXES_B
 def rope_table(pos, freq, axis, cos=None, sin=None, stream=None):
     """cos and sin [T][pairs] fp32 of pos[t][axis[p]] * freq[p] (one kernel): pos
     [T][axes] int32, freq [pairs] fp64, axis [pairs] int32."""
-    torch = _tt()
-    f32 = torch.float32
-    _ndim(pos, 2, "pos")
-    _arg(pos, torch.int32, "pos")
-    T, axes = pos.shape
-    _ndim(freq, 1, "freq")
-    _arg(freq, torch.float64, "freq")
-    n = freq.shape[0]
-    _arg(axis, torch.int32, "axis", (n,))
-    if T > _I32 or axes > _I32 or n > _I32:
-        raise SvdqError(-2, "svdq_rope_table")
-    dev = pos.device
-    cos = _empty((T, n), f32, dev, stream) if cos is None else _arg(cos, f32, "cos", (T, n))
-    sin = _empty((T, n), f32, dev, stream, cos) if sin is None else _arg(sin, f32, "sin", (T, n))
-    raw = _launch(dev, ("freq", "axis", "cos", "sin"), (freq, axis, cos, sin), stream)
+    torch = _T or _tt()
+    raw = None
+    try:
+        T, axes = pos.shape
+        n, = freq.shape
+        dev = pos.get_device()
+        if (stream is None and cos is None and sin is None and dev >= 0
+                and dev == _current_device() == freq.get_device() == axis.get_device() and pos.dtype is _INT32
+                and axis.dtype is _INT32 and freq.dtype is _F64 and axis.shape == (n,) and pos.is_contiguous()
+                and freq.is_contiguous() and axis.is_contiguous() and T < _I32 and axes < _I32 and n < _I32):
+            cos = pos.new_empty((T, n), dtype=_F32)
+            sin, raw = torch.empty_like(cos), _raw_stream(dev)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if raw is None:
+        f32 = torch.float32
+        _ndim(pos, 2, "pos")
+        _arg(pos, torch.int32, "pos")
+        T, axes = pos.shape
+        _ndim(freq, 1, "freq")
+        _arg(freq, torch.float64, "freq")
+        n = freq.shape[0]
+        _arg(axis, torch.int32, "axis", (n,))
+        if T > _I32 or axes > _I32 or n > _I32:
+            raise SvdqError(-2, "svdq_rope_table")
+        dev = pos.device
+        cos = _empty((T, n), f32, dev, stream) if cos is None else _arg(cos, f32, "cos", (T, n))
+        sin = _empty((T, n), f32, dev, stream, cos) if sin is None else _arg(sin, f32, "sin", (T, n))
+        raw = _launch(dev, ("freq", "axis", "cos", "sin"), (freq, axis, cos, sin), stream)
     st = lib().svdq_rope_table(pos.data_ptr(), T, axes, freq.data_ptr(), axis.data_ptr(), n, cos.data_ptr(),
                                sin.data_ptr(), raw)
     if st:
@@ -1223,6 +1334,39 @@ def _rope_args(cos, sin, index, T, norm_q, norm_k, D):
     return rows, pairs
 
 
+def _rope_fast(Q, K, V, Q_out, cos, sin, index, norm_q, norm_k):
+    """Whether everything that both rotating calls take fits at once: the device and
+    the row strides of Q, K, V and Q_out (V, Q_out may be None); else None."""
+    T, H, D = Q.shape
+    Hk, dev = K.shape[1], Q.get_device()
+    ldq, hq, dq = Q.stride()
+    ldk, hk, dk = K.stride()
+    if not (dev >= 0 and dev == _current_device() == K.get_device() == cos.get_device() == sin.get_device()
+            and Q.dtype is _BF and K.dtype is _BF and cos.dtype is _F32 and sin.dtype is _F32 and Hk
+            and dq == 1 and dk == 1 and hq == D and hk == D and K.shape == (T, Hk, D) and cos.dim() == 2
+            and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous() and 0 < T < _I32 > H
+            and cos.shape[0] < _I32):
+        return None
+    for w in (norm_q, norm_k):
+        if w is not None and not (w.dtype is _BF and w.shape == (D,) and w.get_device() == dev and w.is_contiguous()):
+            return None
+    if index is not None and not (index.dtype is _INT32 and index.shape == (T,) and index.get_device() == dev
+                                  and index.is_contiguous()):
+        return None
+    ldv = ldo = H * D
+    if V is not None:
+        ldv, hv, dv = V.stride()
+        if not (V.dtype is _BF and V.shape == (T, Hk, D) and dv == 1 and hv == D and V.get_device() == dev):
+            return None
+    if Q_out is not None:
+        ldo, ho, do = Q_out.stride()
+        if not (Q_out.dtype is _BF and Q_out.shape == (T, H, D) and do == 1 and ho == D and Q_out.get_device() == dev):
+            return None
+    if T == 1:                                          # a single row's stride does not matter
+        ldq, ldk, ldv, ldo = H * D, Hk * D, Hk * D, H * D
+    return dev, T, H, D, Hk, ldq, ldk, ldv, ldo
+
+
 def qk_norm_rope(Q, K, cos, sin, style: int = ROPE_ADJACENT, index=None, norm_q=None, norm_k=None, eps: float = 1e-6,
                  Q_out=None, K_out=None, stream=None):
     """RMS-norm (with a weight norm_q, norm_k [dim]; None: no norm on that side)
@@ -1232,37 +1376,49 @@ def qk_norm_rope(Q, K, cos, sin, style: int = ROPE_ADJACENT, index=None, norm_q=
     tokens without a row are not turned.  Q_out and K_out may be Q and K (in place).
     Returns (Q_out, K_out)."""
     torch = _T or _tt()
-    bf = torch.bfloat16
-    _ndim(Q, 3, "Q")
-    H, D = Q.shape[1:]
-    T, ldq = _heads_arg(Q, "Q", H, D)
-    rows, pairs = _rope_args(cos, sin, index, T, norm_q, norm_k, D)
-    if T > _I32 or H > _I32 or D > _I32:
-        raise SvdqError(-2, "svdq_qk_norm_rope")
-    dev = Q.device
-    if Q_out is None:
-        Q_out = _empty((T, H, D), bf, dev, stream, Q)
-    TO, ldqo = _heads_arg(Q_out, "Q_out", H, D)
-    if TO != T:
-        raise ValueError(f"Q_out has shape {tuple(Q_out.shape)}, expected {tuple(Q.shape)}")
-    pK = pKo = None
-    Hk = ldk = ldko = 0
-    if K is not None:
-        _ndim(K, 3, "K")
-        Hk = K.shape[1]
-        TK, ldk = _heads_arg(K, "K", Hk, D)
-        if K_out is None:
-            K_out = _empty((T, Hk, D), bf, dev, stream, K)
-        TO, ldko = _heads_arg(K_out, "K_out", Hk, D)
-        if TK != T or TO != T:
-            raise ValueError("Q, K and K_out must have the same number of tokens")
-        if Hk > _I32:
+    raw = None
+    if stream is None and Q_out is None and K_out is None:
+        try:
+            fit = _rope_fast(Q, K, None, None, cos, sin, index, norm_q, norm_k)
+            if fit is not None:
+                dev, T, H, D, Hk, ldq, ldk, _, ldqo = fit
+                rows, pairs = cos.shape
+                Q_out, K_out = Q.new_empty((T, H, D)), K.new_empty((T, Hk, D))
+                pK, pKo, ldko, raw = K.data_ptr(), K_out.data_ptr(), Hk * D, _raw_stream(dev)
+        except (AttributeError, TypeError, ValueError, IndexError):
+            pass
+    if raw is None:
+        bf = torch.bfloat16
+        _ndim(Q, 3, "Q")
+        H, D = Q.shape[1:]
+        T, ldq = _heads_arg(Q, "Q", H, D)
+        rows, pairs = _rope_args(cos, sin, index, T, norm_q, norm_k, D)
+        if T > _I32 or H > _I32 or D > _I32:
             raise SvdqError(-2, "svdq_qk_norm_rope")
-        pK, pKo = K.data_ptr(), K_out.data_ptr()
-    elif K_out is not None or norm_k is not None:
-        raise ValueError("K_out or norm_k without K")
-    raw = _launch(dev, ("K", "cos", "sin", "index", "norm_q", "norm_k", "Q_out", "K_out"),
-                  (K, cos, sin, index, norm_q, norm_k, Q_out, K_out), stream)
+        dev = Q.device
+        if Q_out is None:
+            Q_out = _empty((T, H, D), bf, dev, stream, Q)
+        TO, ldqo = _heads_arg(Q_out, "Q_out", H, D)
+        if TO != T:
+            raise ValueError(f"Q_out has shape {tuple(Q_out.shape)}, expected {tuple(Q.shape)}")
+        pK = pKo = None
+        Hk = ldk = ldko = 0
+        if K is not None:
+            _ndim(K, 3, "K")
+            Hk = K.shape[1]
+            TK, ldk = _heads_arg(K, "K", Hk, D)
+            if K_out is None:
+                K_out = _empty((T, Hk, D), bf, dev, stream, K)
+            TO, ldko = _heads_arg(K_out, "K_out", Hk, D)
+            if TK != T or TO != T:
+                raise ValueError("Q, K and K_out must have the same number of tokens")
+            if Hk > _I32:
+                raise SvdqError(-2, "svdq_qk_norm_rope")
+            pK, pKo = K.data_ptr(), K_out.data_ptr()
+        elif K_out is not None or norm_k is not None:
+            raise ValueError("K_out or norm_k without K")
+        raw = _launch(dev, ("K", "cos", "sin", "index", "norm_q", "norm_k", "Q_out", "K_out"),
+                      (K, cos, sin, index, norm_q, norm_k, Q_out, K_out), stream)
     st = lib().svdq_qk_norm_rope(Q.data_ptr(), ldq, H, pK, ldk, Hk, T, D, _ptr(norm_q), _ptr(norm_k), eps,
                                  cos.data_ptr(), sin.data_ptr(), _ptr(index), rows, pairs, style, Q_out.data_ptr(),
                                  ldqo, pKo, ldko, raw)
@@ -1278,26 +1434,41 @@ def kv4_rope_append(cache: Kv4Cache, Q, K, V, cos, sin, slots, style: int = ROPE
     normed and rotated first; the codes are those of qk_norm_rope and kv4_append.
     Returns Q_out."""
     torch = _T or _tt()
-    dev = _cache_arg(cache)
-    Hk, D = cache.heads, cache.dim
-    _ndim(Q, 3, "Q")
-    H = Q.shape[1]
-    T, ldq = _heads_arg(Q, "Q", H, D)
-    TK, ldk = _heads_arg(K, "K", Hk, D)
-    TV, ldv = _heads_arg(V, "V", Hk, D)
-    if TK != T or TV != T:
-        raise ValueError("Q, K and V must have the same number of tokens")
-    _arg(slots, torch.int32, "slots", (T,))
-    rows, pairs = _rope_args(cos, sin, index, T, norm_q, norm_k, D)
-    if T > _I32 or H > _I32:
-        raise SvdqError(-2, "svdq_kv4_rope_append")
-    if Q_out is None:
-        Q_out = _empty((T, H, D), torch.bfloat16, dev, stream, Q)
-    TO, ldqo = _heads_arg(Q_out, "Q_out", H, D)
-    if TO != T:
-        raise ValueError(f"Q_out has shape {tuple(Q_out.shape)}, expected {tuple(Q.shape)}")
-    raw = _launch(dev, ("Q", "K", "V", "cos", "sin", "slots", "index", "norm_q", "norm_k", "Q_out"),
-                  (Q, K, V, cos, sin, slots, index, norm_q, norm_k, Q_out), stream)
+    raw = None
+    if stream is None:
+        try:
+            fit = _rope_fast(Q, K, V, Q_out, cos, sin, index, norm_q, norm_k)
+            if (fit is not None and fit[0] == cache.index == slots.get_device() and fit[3] == cache.dim
+                    and fit[4] == cache.heads and slots.dtype is _INT32 and slots.shape == (fit[1],)
+                    and slots.is_contiguous()):
+                dev, T, H, D, Hk, ldq, ldk, ldv, ldqo = fit
+                rows, pairs = cos.shape
+                if Q_out is None:
+                    Q_out = Q.new_empty((T, H, D))
+                raw = _raw_stream(dev)
+        except (AttributeError, TypeError, ValueError, IndexError):
+            pass
+    if raw is None:
+        dev = _cache_arg(cache)
+        Hk, D = cache.heads, cache.dim
+        _ndim(Q, 3, "Q")
+        H = Q.shape[1]
+        T, ldq = _heads_arg(Q, "Q", H, D)
+        TK, ldk = _heads_arg(K, "K", Hk, D)
+        TV, ldv = _heads_arg(V, "V", Hk, D)
+        if TK != T or TV != T:
+            raise ValueError("Q, K and V must have the same number of tokens")
+        _arg(slots, torch.int32, "slots", (T,))
+        rows, pairs = _rope_args(cos, sin, index, T, norm_q, norm_k, D)
+        if T > _I32 or H > _I32:
+            raise SvdqError(-2, "svdq_kv4_rope_append")
+        if Q_out is None:
+            Q_out = _empty((T, H, D), torch.bfloat16, dev, stream, Q)
+        TO, ldqo = _heads_arg(Q_out, "Q_out", H, D)
+        if TO != T:
+            raise ValueError(f"Q_out has shape {tuple(Q_out.shape)}, expected {tuple(Q.shape)}")
+        raw = _launch(dev, ("Q", "K", "V", "cos", "sin", "slots", "index", "norm_q", "norm_k", "Q_out"),
+                      (Q, K, V, cos, sin, slots, index, norm_q, norm_k, Q_out), stream)
     st = lib().svdq_kv4_rope_append(cache._ref, Q.data_ptr(), ldq, H, K.data_ptr(), V.data_ptr(), ldk, ldv,
                                     _ptr(norm_q), _ptr(norm_k), eps, cos.data_ptr(), sin.data_ptr(), _ptr(index),
                                     rows, pairs, style, slots.data_ptr(), T, Q_out.data_ptr(), ldqo, raw)
