@@ -573,6 +573,7 @@ def nf4_w4a16_linear(X, wq, qabs, chunk, bias=None, Y=None, stream=None):
 _T = None        # torch, after the first call
 _I32 = 0x7FFFFFFF          # the largest size the C interface takes (ctypes passes the low 32 bits of a larger one on)
 _ELEMENTS = 1 << 30        # SVDQ_MAX_ELEMENTS
+_MISFIT = (AttributeError, TypeError, ValueError, IndexError)     # of an argument that is no tensor of this form
 
 
 def _tt():
@@ -810,7 +811,7 @@ def _few_call(where, call, xq, xscale, h, wq, wscale, up, bias, prec, halves, la
                                       and bias.is_contiguous()))
                 and M * KB < _ELEMENTS and N * KB < _ELEMENTS and prec in (INT4, MXFP4)):
             raw = _raw_stream(dev)
-    except (AttributeError, TypeError, ValueError):
+    except _MISFIT:
         pass
     if raw is None:
         Y, prec, raw, (_, _, _, _, _, _, _, M, C, K, r) = _few_args(where, xq, xscale, h, wq, wscale, up, bias, prec, halves,
@@ -1120,7 +1121,7 @@ def kv4_tree_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, mask, m
                                      and lse.is_contiguous()))):
             raw = _raw_stream(dev)
             ldq = ldq if T > 1 else H * D
-    except (AttributeError, TypeError, ValueError):
+    except _MISFIT:
         pass
     if raw is None:
         i32 = torch.int32
@@ -1188,7 +1189,7 @@ def kv4_tree_plan(cache: Kv4Cache, parent, q_start, kv_len, block_table, max_q: 
                 mask, position = parent.new_empty((T, words)), torch.empty_like(parent)
                 slots = torch.empty_like(parent)
                 raw = _raw_stream(dev)
-    except (AttributeError, TypeError, ValueError):
+    except _MISFIT:
         pass
     if raw is None:
         i32 = torch.int32
@@ -1238,7 +1239,7 @@ def kv4_keep_path(cache: Kv4Cache, path, q_start, kv_len, block_table, T: Option
                 and block_table.is_contiguous() and q_start.is_contiguous() and kv_len.is_contiguous()
                 and B < _I32 and longest < _I32 and width < _I32):
             new_len, T, raw = torch.empty_like(kv_len), _I32, _raw_stream(dev)
-    except (AttributeError, TypeError, ValueError):
+    except _MISFIT:
         pass
     if raw is None:
         i32 = torch.int32
@@ -1292,7 +1293,7 @@ def rope_table(pos, freq, axis, cos=None, sin=None, stream=None):
                 and freq.is_contiguous() and axis.is_contiguous() and T < _I32 and axes < _I32 and n < _I32):
             cos = pos.new_empty((T, n), dtype=_F32)
             sin, raw = torch.empty_like(cos), _raw_stream(dev)
-    except (AttributeError, TypeError, ValueError):
+    except _MISFIT:
         pass
     if raw is None:
         f32 = torch.float32
@@ -1385,7 +1386,7 @@ def qk_norm_rope(Q, K, cos, sin, style: int = ROPE_ADJACENT, index=None, norm_q=
                 rows, pairs = cos.shape
                 Q_out, K_out = Q.new_empty((T, H, D)), K.new_empty((T, Hk, D))
                 pK, pKo, ldko, raw = K.data_ptr(), K_out.data_ptr(), Hk * D, _raw_stream(dev)
-        except (AttributeError, TypeError, ValueError, IndexError):
+        except _MISFIT:
             pass
     if raw is None:
         bf = torch.bfloat16
@@ -1446,7 +1447,7 @@ def kv4_rope_append(cache: Kv4Cache, Q, K, V, cos, sin, slots, style: int = ROPE
                 if Q_out is None:
                     Q_out = Q.new_empty((T, H, D))
                 raw = _raw_stream(dev)
-        except (AttributeError, TypeError, ValueError, IndexError):
+        except _MISFIT:
             pass
     if raw is None:
         dev = _cache_arg(cache)
