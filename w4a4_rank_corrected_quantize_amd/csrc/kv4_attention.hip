@@ -157,6 +157,7 @@ struct KvArgs {
     float scale;
     const uint32_t *tree;                         // mask of the drafted tokens, tree_words per row
     int tree_words;
+    int even;                                     // > 0: parts of a tile's keys that the workspace holds (KvEven)
 };
 
 // One step's codes and scales in flight.
@@ -1052,6 +1053,145 @@ __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_c
     }
 }
 
+// Even division of a batch of trees.  Units are (sequence, tile of rows, head), in
+// that order, each of cost w per step of 64 keys and kUnit for its start; block i
+// takes the costs i L .. (i + 1) L - 1, and so a unit's last keys, whole units, and
+// another one's first.  L comes from the lengths, which the device alone knows, so
+// that all blocks end at about the same time and none waits for a long sequence's.
+// A unit in one block is stored as it is; one in several leaves its sums in the
+// workspace, part by part, and its number of parts with every row.
+struct KvEven {
+    static constexpr int kFull = 5, kHalf = 3, kUnit = 16;          // a tile of up to 64 rows is a half
+};
+
+__device__ __forceinline__ int64_t ka_uniform(int64_t x)
+{
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)x));
+}
+
+// A sequence's rows and keys, and its units' costs.
+struct KvSeq {
+    int qs, qn, kv, full, rest;                   // full tiles; rows of the last one, 0 for none
+    int64_t cost_full, cost_rest, cost;           // of a unit; of all heads' units
+};
+
+template <class P>
+__device__ __forceinline__ KvSeq ka_seq(const KvArgs &a, P q_start, P kv_len, int seq)
+{
+    KvSeq s;
+    s.qs = min(max(q_start[seq], 0), a.T);
+    s.qn = min(max(q_start[seq + 1], s.qs), a.T) - s.qs;
+    s.kv = min(max(kv_len[seq], 0), a.table_width << a.c.page_shift);
+    const int64_t rows = (int64_t)s.qn * a.group, steps = (s.kv + 63) >> 6;
+    s.full = (int)(rows >> 7), s.rest = (int)(rows & 127);
+    if (s.rest > 64) ++s.full, s.rest = 0;        // more than half of a tile: a full one
+    s.cost_full = KvEven::kFull * steps + KvEven::kUnit, s.cost_rest = KvEven::kHalf * steps + KvEven::kUnit;
+    s.cost = (s.full * s.cost_full + (s.rest ? s.cost_rest : 0)) * a.c.heads;
+    return s;
+}
+
+// One unit's steps g.s0 .. g.s1 - 1; part: its number among `parts`.
+template <int D, bool INT4, int CT>
+__device__ __forceinline__ void ka_unit(uint8_t *lds, const KvArgs &a, ka_const_int *table, const KvSeq &s, int head,
+                                        int64_t r0, KvRange g, int part, int parts, int wave, int lane)
+{
+    const int j = lane & 15, b = lane >> 4, G = a.group;
+    const int64_t rows = (int64_t)s.qn * G;
+    KvRows<D, CT, true> w;
+    ka_rows<D, INT4, CT>(w, a, head, s.qs, s.qn, s.kv, r0 + 16 * CT * wave, rows, lane);
+    ka_walk_shared<D, INT4, CT>(w, lds, a, table, head, g, a.scale * kLog2e, wave, lane);
+    const size_t n = (size_t)a.T * a.heads_q;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const float l = ka_sum_parts(w.l[ct]), m = w.m[ct];
+        const int64_t r = r0 + 16 * CT * wave + 16 * ct + j;
+        if (r >= rows) continue;
+        const size_t row = (size_t)(s.qs + (int)(r / G)) * a.heads_q + head * G + (int)(r % G);
+        if (parts > 1) {
+            float *o = a.work + (part * n + row) * D, *ml = a.work + a.even * n * D + 2 * (part * n + row);
+            if (m != -INFINITY) {                 // else not read
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) *reinterpret_cast<f32x4 *>(o + 16 * k + 4 * b) = w.acc[ct][k];
+            }
+            if (b == 0) ml[0] = m * a.scale, ml[1] = l;
+        } else {
+            const float f = ka_inverse(l);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const f32x4 o = w.acc[ct][k] * f;
+                *reinterpret_cast<uint2 *>(a.O + row * D + 16 * k + 4 * b) = make_uint2(ka_pack2(o[0], o[1]), ka_pack2(o[2], o[3]));
+            }
+            if (b == 0 && a.lse) a.lse[row] = ka_lse(m, l, a.scale);
+        }
+        if (part == 0 && b == 0) reinterpret_cast<int *>(a.work + a.even * n * (D + 2))[row] = parts;
+    }
+}
+
+template <int D, bool INT4, int CT>
+__device__ __forceinline__ void ka_even(uint8_t *lds, const KvArgs &a, int wave, int lane)
+{
+    // all costs and the greatest unit's, 64 sequences at a time
+    int64_t total = 0, most = 0;
+    for (int s0 = 0; s0 < a.B; s0 += 64) {
+        int64_t c = 0, u = 0;
+        if (s0 + lane < a.B) {
+            const KvSeq s = ka_seq(a, a.q_start, a.kv_len, s0 + lane);
+            c = s.cost, u = s.full ? s.cost_full : (s.rest ? s.cost_rest : 0);
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d), u = max(u, (int64_t)__shfl_xor(u, d));
+        total += c, most = max(most, u);
+    }
+    total = ka_uniform(total), most = ka_uniform(most);
+    const int64_t blocks = gridDim.x, parts = a.even - 1;
+    const int64_t L = max(max((total + blocks - 1) / blocks, (most + parts - 1) / parts), (int64_t)KvEven::kUnit);
+    const int64_t lo = L * blockIdx.x, hi = min(lo + L, total);
+    if (lo >= hi) return;
+    // the sequence that lo falls into, and where it begins
+    int64_t first = 0;
+    int seq = 0;
+    for (int s0 = 0; s0 < a.B; s0 += 64) {
+        int64_t c = s0 + lane < a.B ? ka_seq(a, a.q_start, a.kv_len, s0 + lane).cost : 0, up = c;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t x = __shfl_up(up, d);
+            up += lane >= d ? x : 0;
+        }
+        const int before = __popcll(__ballot(first + up <= lo));     // whole sequences before lo
+        if (before < 64) {
+            first = ka_uniform(first + __shfl(up - c, before)), seq = s0 + before;
+            break;
+        }
+        first = ka_uniform(first + __shfl(up, 63));
+    }
+    if ((blockIdx.x / (uint32_t)a.cus) & 1) __builtin_amdgcn_s_setprio(2);
+    for (int64_t at = lo; at < hi; ++seq) {
+        const KvSeq s = ka_seq(a, (ka_const_int *)a.q_start, (ka_const_int *)a.kv_len, seq);
+        ka_const_int *table = (ka_const_int *)a.table + (size_t)seq * a.table_width;
+        const int64_t full = s.cost_full * s.full * a.c.heads;
+        const int steps = (s.kv + 63) >> 6;
+        while (at < hi && at < first + s.cost) {
+            const bool half = at - first >= full;
+            const int64_t cost = half ? s.cost_rest : s.cost_full, begin0 = first + (half ? full : 0);
+            const int unit = (int)((at - begin0) / cost), w = half ? KvEven::kHalf : KvEven::kFull;
+            const int64_t begin = begin0 + unit * cost, b0 = begin / L;
+            const int head = unit % a.c.heads, tile = half ? s.full : unit / a.c.heads;
+            // steps up to a cost x of the unit
+            auto upto = [&](int64_t x) {
+                const int64_t y = x - begin - KvEven::kUnit;
+                return y <= 0 ? 0 : (int)min((y + w - 1) / w, (int64_t)steps);
+            };
+            const KvRange g = {lo <= begin ? 0 : upto(lo), hi >= begin + cost ? steps : upto(hi), 0, s.kv};
+            const int count = (int)((begin + cost - 1) / L - b0) + 1, part = (int)(blockIdx.x - b0);
+            if (half) ka_unit<D, INT4, 1>(lds, a, table, s, head, (int64_t)128 * tile, g, part, count, wave, lane);
+            else ka_unit<D, INT4, CT>(lds, a, table, s, head, (int64_t)128 * tile, g, part, count, wave, lane);
+            at = begin + cost;
+        }
+        first += s.cost;
+    }
+}
+
 // CT > 0: blocks of 64 CT rows for the sequences of more than 16.  0: every list
 // of rows is taken 16 at a time.
 template <int D, bool INT4, int CT, bool TREE>
@@ -1060,6 +1200,13 @@ __global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
     constexpr int SUMS = 4 * (16 * (D + 4) + 8 * 16), STAGES = 4 * ka_stage(D);
     __shared__ __attribute__((aligned(16))) uint8_t lds[CT > 0 && STAGES > SUMS ? STAGES : SUMS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (TREE && CT > 0) {
+        static_assert(CT == 2, "tiles of 128 rows");
+        if (a.even) {
+            ka_even<D, INT4, CT>(lds, a, wave, lane);
+            return;
+        }
+    }
     // workgroups go to the XCDs in turn: rotating each round of heads and
     // sequences by one spreads a long sequence's tiles and splits over all
     const int n = a.c.heads * a.B, round = blockIdx.x / n;
@@ -1092,7 +1239,9 @@ __global__ __launch_bounds__(256, 2) void kv4_attention_kernel(KvArgs a)
 // with the splits p, p + P, .., the parts added in order.  Every split of every
 // row of a sequence has been written, the ones without keys as a maximum of
 // -infinity alone.
-template <int D, int P>
+// EVEN: a row's parts are as many as the first kernel noted; a single one is stored
+// already.
+template <int D, int P, bool EVEN>
 __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 {
     constexpr int L = D / 4, R = 256 / (L * P);
@@ -1106,14 +1255,22 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
     const bool in = row < n && row >= (int64_t)a.q_start[0] * a.heads_q && row < (int64_t)a.q_start[a.B] * a.heads_q;
     if (P == 1 && !in) return;
     const int64_t at = in ? row : 0;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.work + (size_t)a.splits * n * D) + at;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.work + (size_t)(EVEN ? a.even : a.splits) * n * D) + at;
     const float *part = a.work + at * D + c;
+    int splits = a.splits;
+    bool skip = false;
+    if constexpr (EVEN) {
+        splits = in ? min(reinterpret_cast<const int *>(a.work + (size_t)a.even * n * (D + 2))[at], a.even) : 1;
+        skip = splits <= 1;
+        if (skip) splits = 0;
+        if (P == 1 && skip) return;
+    }
     float mx = -INFINITY, sum = 0.0f;
     f32x4 o = {};
 #pragma unroll 4
-    for (int s = p; s < a.splits; s += P) mx = fmaxf(mx, ml[s * n].x);
+    for (int s = p; s < splits; s += P) mx = fmaxf(mx, ml[s * n].x);
 #pragma unroll 4
-    for (int s = p; s < a.splits; s += P) {
+    for (int s = p; s < splits; s += P) {
         const float2 v = ml[s * n];
         const bool none = v.x == -INFINITY;              // its sums are not written: any valid address, and 0
         const float f = none ? 0.0f : __builtin_amdgcn_exp2f((v.x - mx) * kLog2e);
@@ -1126,7 +1283,7 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
         os[p][r * L + lane] = o;
         if (lane == 0) mls[p][r] = make_float2(mx, sum);
         __syncthreads();
-        if (p > 0 || !in) return;
+        if (p > 0 || !in || (EVEN && skip)) return;
 #pragma unroll
         for (int q = 1; q < P; ++q) mx = fmaxf(mx, mls[q][r].x);
         o = (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
@@ -1148,7 +1305,10 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv)
 {
     const KvPlan p = kv4_plan(T, B, heads, heads_q / heads, max_q, max_kv, device_cu_count());
-    return p.splits > 1 ? (size_t)p.splits * T * heads_q * (dim + 2) * sizeof(float) : 0;
+    if (p.splits == 1) return 0;
+    // trees: further parts, and every row's number of them
+    const size_t row = (size_t)(p.splits + (p.many ? kKv4EvenParts : 0)) * (dim + 2) + (p.many ? 1 : 0);
+    return row * T * heads_q * sizeof(float);
 }
 
 hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq, const int32_t *table, int table_width,
@@ -1164,7 +1324,8 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
     a.work = work, a.T = T, a.B = B, a.heads_q = heads_q, a.group = heads_q / c.heads, a.table_width = table_width;
     a.q_tiles = p.q_tiles, a.splits = p.splits, a.split_steps = p.split_steps, a.causal = causal, a.window = window, a.scale = scale;
     a.cus = cus, a.tree = tree, a.tree_words = tree_words;
-    const dim3 grid((uint32_t)kv4_blocks(p, B, c.heads));
+    a.even = tree && p.many && p.splits > 1 ? p.splits + kKv4EvenParts : 0;
+    const dim3 grid(a.even ? 2u * (uint32_t)cus : (uint32_t)kv4_blocks(p, B, c.heads));
 #define KA_LAUNCH_ROWS(D, I, TREE) \
     (p.many ? kv4_attention_kernel<D, I, kKv4ManyTiles, TREE><<<grid, 256, 0, stream>>>(a) \
             : kv4_attention_kernel<D, I, 0, TREE><<<grid, 256, 0, stream>>>(a))
@@ -1178,11 +1339,13 @@ hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t n = (int64_t)T * heads_q;
-#define KA_COMBINE(D, P) \
-    kv4_combine_kernel<D, P><<<(uint32_t)((n * (D / 4 * P) + 255) / 256), 256, 0, stream>>>(a)
+#define KA_COMBINE_PARTS(D, P, EVEN) \
+    kv4_combine_kernel<D, P, EVEN><<<(uint32_t)((n * (D / 4 * P) + 255) / 256), 256, 0, stream>>>(a)
+#define KA_COMBINE(D, P) (a.even ? KA_COMBINE_PARTS(D, P, true) : KA_COMBINE_PARTS(D, P, false))
     if (p.splits <= 4) c.dim == 64 ? KA_COMBINE(64, 1) : KA_COMBINE(128, 1);
     else c.dim == 64 ? KA_COMBINE(64, 8) : KA_COMBINE(128, 8);
 #undef KA_COMBINE
+#undef KA_COMBINE_PARTS
     return hipGetLastError();
 }
 

@@ -8,6 +8,10 @@ namespace svdq {
 
 constexpr int kKv4ManyTiles = 2;                  // 16-row tiles per wave of a block of many rows
 
+// Even division of the tree attention's work: parts of a tile's keys that the
+// workspace holds, beyond the splits of the fixed division.
+constexpr int kKv4EvenParts = 2;
+
 // Form, tiles of rows and splits of the keys, from the sizes and the caller's
 // bounds.
 struct KvPlan {
