@@ -131,12 +131,20 @@ __device__ __forceinline__ void fw_widen(uint2 w, long &a, long &b)
 
 // X kept whole in LDS: row r at r * fw_xrow, its 16-byte unit u at u ^ (r % 16);
 // then the rows' scales as dwords (INT4: fp32; MXFP4: a byte each), an odd number
-// apart: 16 rows' reads fall into different banks.
+// apart: 16 rows' reads fall into different banks.  INT4 with room for it: then
+// the rows once more, widened, 16 bytes for every 8, in the same order (once per
+// block instead of by every wave and tile).
 __host__ __device__ constexpr int fw_xrow(int K) { return ((K >> 1) + 255) & ~255; }
+__host__ __device__ constexpr int fw_xwide(int K) { return (K + 255) & ~255; }
 __host__ __device__ constexpr int fw_xscales(int K, bool int4) { return (int4 ? K >> 6 : K >> 5) | 1; }
-__host__ __device__ constexpr int64_t fw_xbytes(int M, int K, bool int4)
+// where the widened rows begin
+__host__ __device__ constexpr int64_t fw_xnarrow(int M, int K, bool int4)
 {
-    return (int64_t)M * (fw_xrow(K) + 4 * (int64_t)fw_xscales(K, int4));
+    return ((int64_t)M * (fw_xrow(K) + 4 * (int64_t)fw_xscales(K, int4)) + 15) & ~(int64_t)15;
+}
+__host__ __device__ constexpr int64_t fw_xbytes(int M, int K, bool int4, bool wide)
+{
+    return fw_xnarrow(M, K, int4) + (wide ? (int64_t)M * fw_xwide(K) : 0);
 }
 
 template <int FORM, int W>
@@ -172,9 +180,9 @@ __device__ __forceinline__ void fw_wait_stages(int stages)
 }
 
 // W = WN WK waves: WN sets of 16 RT rows, the lines of each taken in turn by WK
-// waves.  XB > 0: X is kept whole in XB bytes of LDS; 0: it goes through the ring,
-// where the WN waves of the same lines share it.
-template <int FORM, int RT, int CT, bool GATED, int WN, int WK, int DEPTH, int XB>
+// waves.  XB > 0: X is kept whole in XB bytes of LDS (XW: and widened); 0: it goes
+// through the ring, where the WN waves of the same lines share it.
+template <int FORM, int RT, int CT, bool GATED, int WN, int WK, int DEPTH, int XB, bool XW>
 __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
 {
     typedef FewTile<FORM> Tile;
@@ -267,9 +275,23 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
         if (i < mine) issue(i);
     const int xr = min(j16, a.M - 1), xrow = fw_xrow(a.K);
     const float *xls = reinterpret_cast<const float *>(xl + a.M * xrow) + xr * fw_xscales(a.K, INT4);
+    static_assert(!XW || (XS && INT4), "only INT4 is widened");
+    uint8_t *xw = lds + LDS - XB + (XW ? fw_xnarrow(a.M, a.K, INT4) : 0);
+    const int xwide = fw_xwide(a.K);
     if constexpr (XS) {
         fw_wait_stages<NL, AHEAD>(min(AHEAD, mine));       // the wave's share of X has arrived
         __syncthreads();
+        if constexpr (XW) {
+            const int units = segs * 2;                    // of 8 code bytes
+            for (int i = threadIdx.x; i < a.M * units; i += 64 * W) {
+                const int r = i / units, u = i % units;
+                long x0, x1;
+                fw_widen(*reinterpret_cast<const uint2 *>(xl + r * xrow + 16 * ((u >> 1) ^ (r & 15)) + 8 * (u & 1)), x0, x1);
+                long *o = reinterpret_cast<long *>(xw + r * xwide + 16 * (u ^ (r & 15)));
+                o[0] = x0, o[1] = x1;
+            }
+            __syncthreads();
+        }
     }
     // the lane's E8M0 byte for product s of a tile (in the low byte)
     auto e8m0 = [&](const uint8_t *tile, int s) {
@@ -301,7 +323,12 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
                 float sx[CT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
-                    fw_widen(*reinterpret_cast<const uint2 *>(xunit(SX, c, st, 2 * g + (b >> 1)) + 8 * (b & 1)), x0[c], x1[c]);
+                    if constexpr (XW) {
+                        const long *x = reinterpret_cast<const long *>(xw + xr * xwide + 16 * ((4 * (4 * st + g) + b) ^ xr));
+                        x0[c] = x[0], x1[c] = x[1];
+                    } else {
+                        fw_widen(*reinterpret_cast<const uint2 *>(xunit(SX, c, st, 2 * g + (b >> 1)) + 8 * (b & 1)), x0[c], x1[c]);
+                    }
                     sx[c] = XS ? xls[4 * st + g]
                                : *reinterpret_cast<const float *>(SX + c * Tile::kBytes + Tile::kCodes + 4 * (16 * g + j16));
                 }
@@ -399,7 +426,7 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
 
 // Launches WN WK waves per block of RTN tiles of channels each, with as many
 // stages in flight as LDS and the count of loads take, up to DEPTHS.
-template <int FORM, int CT, bool GATED, int WN, int WK, int RTN, int DEPTHS, int XB>
+template <int FORM, int CT, bool GATED, int WN, int WK, int RTN, int DEPTHS, int XB, bool XW = false>
 void few_launch(const FewArgs &a, hipStream_t stream)
 {
     typedef FewTile<FORM> Tile;
@@ -408,11 +435,11 @@ void few_launch(const FewArgs &a, hipStream_t stream)
     constexpr int ROOM = (160 * 1024 - XB - WN * RT * 1280 - CT * 2048) / STAGE;
     constexpr int LEAST = ROOM < 63 / LOADS ? ROOM : 63 / LOADS, DEPTH = DEPTHS < LEAST ? DEPTHS : LEAST;
     if constexpr (WN > 1 && DEPTH < (WK > 2 ? 3 : 2)) {
-        few_launch<FORM, CT, GATED, WN, WK / 2, RTN, DEPTHS, XB>(a, stream);
+        few_launch<FORM, CT, GATED, WN, WK / 2, RTN, DEPTHS, XB, XW>(a, stream);
     } else {
         const uint32_t tiles = (uint32_t)((a.N + 16 * RTN * WN - 1) / (16 * RTN * WN));
         const uint32_t grid = a.chunks > 1 ? (tiles + 7) / 8 * 8 * a.chunks : tiles;
-        w4a4_few_kernel<FORM, RT, CT, GATED, WN, WK, DEPTH, XB><<<grid, 64 * W, 0, stream>>>(a);
+        w4a4_few_kernel<FORM, RT, CT, GATED, WN, WK, DEPTH, XB, XW><<<grid, 64 * W, 0, stream>>>(a);
     }
 }
 
@@ -436,11 +463,11 @@ void few_ring(const FewArgs &a, hipStream_t stream)
 // X whole in LDS: up to a block per compute unit eight waves per tile, else four
 // and more blocks (one row, us, four / eight waves: 4096 channels of 14336 INT4
 // 13.8 / 10.4; 2 x 14336 of 4096 INT4 17.5 / 24.8, MXFP4 13.5 / 18.1).
-template <int FORM, bool GATED, int XB>
+template <int FORM, bool GATED, int XB, bool XW>
 void few_whole(const FewArgs &a, hipStream_t stream)
 {
-    if ((a.N + 15) / 16 <= device_cu_count()) few_launch<FORM, 1, GATED, 1, 8, 1, 2, XB>(a, stream);
-    else few_launch<FORM, 1, GATED, 1, 4, 1, 2, XB>(a, stream);
+    if ((a.N + 15) / 16 <= device_cu_count()) few_launch<FORM, 1, GATED, 1, 8, 1, 2, XB, XW>(a, stream);
+    else few_launch<FORM, 1, GATED, 1, 4, 1, 2, XB, XW>(a, stream);
 }
 
 template <int FORM, bool GATED>
@@ -449,10 +476,15 @@ void few_rows(FewArgs a, hipStream_t stream)
     // more than 64 rows in equal sets of whole tiles
     a.chunks = (a.M + 63) / 64;
     const int rows = (a.M + a.chunks - 1) / a.chunks;
-    // whole where it takes no more LDS than the ring's places for it would
-    const int64_t x = fw_xbytes(a.M, a.K, FORM == FEW_INT4);
-    if (rows <= 16 && x <= 8192) few_whole<FORM, GATED, 8192>(a, stream);
-    else if (rows <= 16 && x <= 17408) few_whole<FORM, GATED, 17408>(a, stream);
+    // whole where it takes no more LDS than the ring's places for it would, and
+    // widened where that fits too (INT4, one row / two, us: 6144 channels of 4096
+    // 6.8 / 7.1, not widened 7.3 / 7.5; 28672 channels 16.2 / 16.5 and 17.3 / 17.5)
+    constexpr bool INT4 = FORM == FEW_INT4;
+    const int64_t x = fw_xbytes(a.M, a.K, INT4, false), wide = fw_xbytes(a.M, a.K, INT4, INT4);
+    if (INT4 && rows <= 16 && wide <= 8192) few_whole<FORM, GATED, 8192, INT4>(a, stream);
+    else if (INT4 && rows <= 16 && wide <= 17408) few_whole<FORM, GATED, 17408, INT4>(a, stream);
+    else if (rows <= 16 && x <= 8192) few_whole<FORM, GATED, 8192, false>(a, stream);
+    else if (rows <= 16 && x <= 17408) few_whole<FORM, GATED, 17408, false>(a, stream);
     else if (rows <= 16) few_ring<FORM, 1, GATED>(a, stream);
     else if (rows <= 32) few_ring<FORM, 2, GATED>(a, stream);
     else if (rows <= 48) few_ring<FORM, 3, GATED>(a, stream);
