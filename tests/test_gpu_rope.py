@@ -176,6 +176,28 @@ def test_values_far_apart():
     assert bool((q[0] == 0).all()) and bool((k[0] == 0).all())
 
 
+@pytest.mark.parametrize("style", STYLES)
+def test_infinite_values(style):
+    """A head with an infinity: 1 / sqrt(inf) = 0, so its finite values become 0 and its infinity, and what that is
+    rotated with, no number; other heads are as ever."""
+    D, T = 128, 4
+    x = _rand(1, T, 6, D)
+    x[2, 3, 7] = math.inf
+    x[3, 0, 9] = -math.inf
+    cos, sin = _tables(9, T, D // 2)
+    w = _weight(1, D)
+    q, k = svdq.qk_norm_rope(x, x, cos, sin, style=style, norm_q=w, norm_k=w)
+    clean = torch.where(torch.isinf(x), torch.zeros_like(x), x)
+    wantq, wantk = svdq.qk_norm_rope(clean, clean, cos, sin, style=style, norm_q=w, norm_k=w)
+    for got, want in ((q, wantq), (k, wantk)):
+        for t, h, d in ((2, 3, 7), (3, 0, 9)):
+            bad = torch.zeros(D, dtype=torch.bool, device="cuda")
+            bad[d] = bad[d ^ 1 if style == svdq.ROPE_ADJACENT else (d + D // 2) % D] = True
+            assert torch.equal(torch.isnan(got[t, h]), bad) and bool((got[t, h][~bad] == 0).all())
+            want[t, h] = got[t, h] = 0
+        assert torch.equal(got, want)
+
+
 # ---------------------------------------------------------- on into the cache
 
 @pytest.mark.parametrize("prec", PRECS)

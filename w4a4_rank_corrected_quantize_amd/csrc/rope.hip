@@ -133,13 +133,14 @@ __device__ __forceinline__ void rp_unpack8(const uint4 &u, F *f)
     for (int i = 0; i < 4; ++i) f[2 * i] = bits_f32(w[i] << 16), f[2 * i + 1] = bits_f32(w[i] & 0xFFFF0000u);
 }
 
-// 1 / sqrt(x): fp64 from the instruction's estimate by two Newton steps.
+// 1 / sqrt(x): fp64 from the instruction's estimate by two Newton steps (which
+// would make 0 inf of the zero that an infinity has).
 __device__ __forceinline__ double rp_rsqrt(double x)
 {
-    const double h = 0.5 * x;
-    double y = __builtin_amdgcn_rsq(x);
+    const double h = 0.5 * x, e = __builtin_amdgcn_rsq(x);
+    double y = e * __builtin_fma(-h * e, e, 1.5);
     y *= __builtin_fma(-h * y, y, 1.5);
-    return y * __builtin_fma(-h * y, y, 1.5);
+    return e == 0.0 ? 0.0 : y;
 }
 __device__ __forceinline__ float rp_rsqrt(float x) { return __builtin_amdgcn_rsqf(x); }
 
@@ -147,13 +148,14 @@ __device__ __forceinline__ double rp_fma(double a, double b, double c) { return 
 __device__ __forceinline__ float rp_fma(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
 
 // Norm (with the lane's weights g, if there is one) and rotation of a lane's pieces
-// xa, xb in place.  fp32: nothing is done and true returned where some head of the
-// wave has a sum of squares that fp32 may not hold to its last places.
+// xa, xb, into ya, yb.  fp32: true where the head has a sum of squares that fp32 may
+// not hold to its last places.
 template <class F, int D, bool HALVES>
-__device__ __forceinline__ bool rp_apply(uint4 &xa, uint4 &xb, bool norm, const uint4 &ga, const uint4 &gb,
-                                         const RopeTurn &r, double eps)
+__device__ __forceinline__ bool rp_apply(const uint4 &xa, const uint4 &xb, uint4 &ya, uint4 &yb, bool norm,
+                                         const uint4 &ga, const uint4 &gb, const RopeTurn &r, double eps)
 {
     F u[16];
+    bool out = false;
     rp_unpack8(xa, u), rp_unpack8(xb, u + 8);
     if (norm) {
         F ss = 0;
@@ -161,7 +163,7 @@ __device__ __forceinline__ bool rp_apply(uint4 &xa, uint4 &xb, bool norm, const 
         for (int k = 0; k < 16; ++k) ss = rp_fma(u[k], u[k], ss);
 #pragma unroll
         for (int d = 1; d < D / 16; d <<= 1) ss += __shfl_xor(ss, d);
-        if (sizeof(F) == 4 && __any(!(ss > (F)1e-25 && ss < (F)1e35))) return true;
+        out = sizeof(F) == 4 && !(ss > (F)1e-25 && ss < (F)1e35);
         const F rs = rp_rsqrt(rp_fma(ss, (F)(1.0 / D), (F)eps));
         F g[16];
         rp_unpack8(ga, g), rp_unpack8(gb, g + 8);
@@ -176,9 +178,9 @@ __device__ __forceinline__ bool rp_apply(uint4 &xa, uint4 &xb, bool norm, const 
         o[a] = (float)rp_fma(u[a], c, -(u[b] * s));
         o[b] = (float)rp_fma(u[b], c, u[a] * s);
     }
-    xa = make_uint4(rp_pack2(o[0], o[1]), rp_pack2(o[2], o[3]), rp_pack2(o[4], o[5]), rp_pack2(o[6], o[7]));
-    xb = make_uint4(rp_pack2(o[8], o[9]), rp_pack2(o[10], o[11]), rp_pack2(o[12], o[13]), rp_pack2(o[14], o[15]));
-    return false;
+    ya = make_uint4(rp_pack2(o[0], o[1]), rp_pack2(o[2], o[3]), rp_pack2(o[4], o[5]), rp_pack2(o[6], o[7]));
+    yb = make_uint4(rp_pack2(o[8], o[9]), rp_pack2(o[10], o[11]), rp_pack2(o[12], o[13]), rp_pack2(o[14], o[15]));
+    return out;
 }
 
 // A lane's norm weights.
@@ -206,14 +208,19 @@ __device__ __forceinline__ void rp_heads(const uint16_t *x, uint16_t *y, int hea
     uint4 na, nb;
     load(first, na, nb);
     for (int set = first; set * S < heads; set += step) {
-        uint4 xa = na, xb = nb;
+        const uint4 xa = na, xb = nb;
+        uint4 ya, yb;
         load(set + step, na, nb);
-        if (rp_apply<F, D, HALVES>(xa, xb, w != nullptr, ga, gb, turn, eps))
-            rp_apply<double, D, HALVES>(xa, xb, true, ga, gb, turn, eps);
+        const bool out = rp_apply<F, D, HALVES>(xa, xb, ya, yb, w != nullptr, ga, gb, turn, eps);
+        if (__any(out)) {                                  // for these heads alone: the others' bits stay
+            uint4 za, zb;
+            rp_apply<double, D, HALVES>(xa, xb, za, zb, true, ga, gb, turn, eps);
+            if (out) ya = za, yb = zb;
+        }
         const int64_t h = set * S + lane / L;
         if (h >= heads) continue;
-        *reinterpret_cast<uint4 *>(y + h * D + l.a) = xa;
-        *reinterpret_cast<uint4 *>(y + h * D + l.b) = xb;
+        *reinterpret_cast<uint4 *>(y + h * D + l.a) = ya;
+        *reinterpret_cast<uint4 *>(y + h * D + l.b) = yb;
     }
 }
 
@@ -266,12 +273,12 @@ __global__ __launch_bounds__(KC_THREADS) void kv4_rope_append_kernel(Kv4View c, 
         const int t = min(t0 + tid / L, r.T - 1);
         const RopeLane<D, HALVES> l = rp_lane<D, HALVES>(tid % L, r.pairs);
         const uint16_t *p = r.K + t * r.ldk + (int64_t)head * D;
-        uint4 xa = *reinterpret_cast<const uint4 *>(p + l.a), xb = *reinterpret_cast<const uint4 *>(p + l.b);
-        uint4 ga, gb;
+        const uint4 xa = *reinterpret_cast<const uint4 *>(p + l.a), xb = *reinterpret_cast<const uint4 *>(p + l.b);
+        uint4 ga, gb, ya, yb;
         rp_weights<D, HALVES>(r.wk, l, ga, gb);
-        rp_apply<double, D, HALVES>(xa, xb, r.wk != nullptr, ga, gb, rp_turn(r, l, t), r.eps);
-        *reinterpret_cast<uint4 *>(kr + tid / L * ROW + l.a) = xa;
-        *reinterpret_cast<uint4 *>(kr + tid / L * ROW + l.b) = xb;
+        rp_apply<double, D, HALVES>(xa, xb, ya, yb, r.wk != nullptr, ga, gb, rp_turn(r, l, t), r.eps);
+        *reinterpret_cast<uint4 *>(kr + tid / L * ROW + l.a) = ya;
+        *reinterpret_cast<uint4 *>(kr + tid / L * ROW + l.b) = yb;
     }
     float fk[8], fv[8];
     kc_unpack8(vv, fv);
