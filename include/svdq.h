@@ -785,9 +785,10 @@ svdq_status svdq_kv4_rope_append(const svdq_kv4_cache *cache, const uint16_t *Q,
 svdq_status svdq_kv4_read(const svdq_kv4_cache *cache, const int32_t *slots, int T, float *K, float *V,
                           void *stream);
 
-/* Device bytes that svdq_kv4_attention needs for these sizes on the current
- * device (partial sums where the keys are split over blocks); 0 without a
- * split, for sizes it does not take, or without a gfx950 device. */
+/* Device bytes that are enough for svdq_kv4_attention and
+ * svdq_kv4_tree_attention at these sizes on the current device (partial sums
+ * where the keys are split over blocks); 0 without a split, for sizes they do
+ * not take, or without a gfx950 device. */
 size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache, int T, int B, int heads_q, int max_q,
                                           int max_kv);
 
@@ -876,6 +877,9 @@ svdq_status svdq_kv4_tree_plan(const int32_t *parent, const int32_t *q_start, co
  *                see each other, or nothing (device, 4-byte aligned).  Bits past a
  *                sequence's rows are not used
  * Other arguments, workspace, arithmetic and errors as for svdq_kv4_attention.
+ * Deterministic for given sizes, bounds and lengths: where the keys are split, how
+ * they are cut, and so the last places of a row, may depend on the q_start and
+ * kv_len of the whole batch.
  */
 svdq_status svdq_kv4_tree_attention(const svdq_kv4_cache *cache, const uint16_t *Q, int64_t ldq,
                                     const int32_t *block_table, int table_width, const int32_t *q_start,

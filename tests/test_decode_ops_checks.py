@@ -281,7 +281,7 @@ def _keep(**kw):
     (_plan, INVALID, dict(mask=None)), (_plan, INVALID, dict(table=None)), (_plan, MISALIGNED, dict(parent=P + 1)),
     (_plan, MISALIGNED, dict(mask=P + 2)), (_plan, MISALIGNED, dict(pos=P + 2)), (_plan, MISALIGNED, dict(slots=P + 3)),
     (_attend, INVALID, dict(words=0)), (_attend, SHAPE, dict(words=33)), (_attend, INVALID, dict(mask=None)),
-    (_attend, MISALIGNED, dict(mask=P + 2)), (_attend, INVALID, dict(B=-1)),
+    (_attend, MISALIGNED, dict(mask=P + 2)), (_attend, INVALID, dict(B=-1)), (_attend, INVALID, dict(T=-1)),
     (_attend, SHAPE, dict(hq=3)), (_attend, INVALID, dict(mq=0)), (_attend, INVALID, dict(mk=0)),
     (_attend, INVALID, dict(scale=0.0)), (_attend, INVALID, dict(scale=math.nan)), (_attend, SHAPE, dict(ldq=64)),
     (_attend, INVALID, dict(Q=None)), (_attend, INVALID, dict(O=None)), (_attend, INVALID, dict(kl=None)),

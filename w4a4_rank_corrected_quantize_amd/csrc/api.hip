@@ -534,7 +534,7 @@ extern "C" size_t svdq_kv4_attention_workspace_bytes(const svdq_kv4_cache *cache
     Kv4View c;
     if (check_kv4(cache, c) != SVDQ_OK || check_kv4_attention(c, T, B, heads_q, max_q, max_kv) != SVDQ_OK) return 0;
     if (T == 0 || B == 0 || current_device_ok() != SVDQ_OK) return 0;
-    return kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv);
+    return kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv, true);      // enough for both
 }
 
 // Both forms: causal rows, or a mask of drafted tokens.
@@ -561,7 +561,7 @@ static svdq_status kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q,
     st = current_device_ok();
     if (st != SVDQ_OK) return st;
     if (T == 0 || B == 0) return SVDQ_OK;
-    const size_t need = kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv);
+    const size_t need = kv4_attention_work_bytes(T, B, heads_q, c.heads, c.dim, max_q, max_kv, tree != nullptr);
     if (need > 0 && (!work || work_bytes < need)) return SVDQ_ERR_INVALID_ARG;
     hipError_t e = launch_kv4_attention(c, Q, ldq, block_table, table_width, q_start, kv_len, B, T, heads_q, max_q,
                                         max_kv, scale, causal, window, O, lse, (float *)work, (hipStream_t)stream,
@@ -586,7 +586,7 @@ extern "C" svdq_status svdq_kv4_tree_attention(const svdq_kv4_cache *cache, cons
                                                float *lse, void *work, size_t work_bytes, void *stream)
 {
     if (mask_words < 1 || (T > 0 && B > 0 && !mask)) return SVDQ_ERR_INVALID_ARG;
-    if (mask_words > SVDQ_TREE_MAX_WORDS || T < 0 || !elems_ok(T, mask_words)) return SVDQ_ERR_SHAPE;
+    if (mask_words > SVDQ_TREE_MAX_WORDS || (T > 0 && !elems_ok(T, mask_words))) return SVDQ_ERR_SHAPE;
     if (!aligned4(mask)) return SVDQ_ERR_MISALIGNED;
     return kv4_attention(cache, Q, ldq, block_table, table_width, q_start, kv_len, B, T, heads_q, max_q, max_kv, scale,
                          0, 0, mask, mask_words, O, lse, work, work_bytes, stream);

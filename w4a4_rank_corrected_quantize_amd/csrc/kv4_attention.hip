@@ -1304,12 +1304,13 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(KvArgs a)
 
 }  // namespace
 
-size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv)
+size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv,
+                                bool tree)
 {
     const KvPlan p = kv4_plan(T, B, heads, heads_q / heads, max_q, max_kv, device_cu_count());
     if (p.splits == 1) return 0;
-    // trees: further parts, and every row's number of them
-    const size_t row = (size_t)(p.splits + (p.many ? kKv4EvenParts : 0)) * (dim + 2) + (p.many ? 1 : 0);
+    tree = tree && p.many;                        // further parts, and every row's number of them
+    const size_t row = (size_t)(p.splits + (tree ? kKv4EvenParts : 0)) * (dim + 2) + (tree ? 1 : 0);
     return row * T * heads_q * sizeof(float);
 }
 

@@ -156,7 +156,8 @@ hipError_t launch_kv4_tree_plan(const int32_t *parent, const Kv4Tables &s, int B
 hipError_t launch_kv4_keep_path(const Kv4View &c, const Kv4Tables &s, int B, int T, const int32_t *path, int max_path,
                                 int32_t *new_len, hipStream_t stream);
 // Splits of the keys keep their sums in `work` (0 bytes without a split).
-size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv);
+size_t kv4_attention_work_bytes(int T, int B, int heads_q, int heads, int dim, int max_q, int max_kv,
+                                bool tree);
 hipError_t launch_kv4_attention(const Kv4View &c, const uint16_t *Q, int64_t ldq, const int32_t *table, int table_width,
                                 const int32_t *q_start, const int32_t *kv_len, int B, int T, int heads_q, int max_q,
                                 int max_kv, float scale, int causal, int window, uint16_t *O, float *lse, float *work,
