@@ -860,8 +860,9 @@ svdq_status svdq_kv4_attention(const svdq_kv4_cache *cache, const uint16_t *Q, i
  *   position     [T] int32, device (out), or NULL: kv_len - n + the number of
  *                ancestors, the token's position in its text
  *   slots        [T] int32, device (out), or NULL: the slot of the row's place,
- *                -1 where the table has none
- * Rows of no sequence keep what the outputs hold.  One kernel launch.  Errors:
+ *                -1 where the table has none and for rows of no sequence (a
+ *                padded step's), so that appending writes nothing there
+ * Rows of no sequence keep what mask and position hold.  One kernel launch.  Errors:
  * SVDQ_ERR_INVALID_ARG, SVDQ_ERR_SHAPE, SVDQ_ERR_UNSUPPORTED (page_size),
  * SVDQ_ERR_MISALIGNED (4 bytes), SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_ERR_HIP.
  */

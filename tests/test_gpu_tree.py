@@ -92,8 +92,25 @@ def test_plan(counts, P, chain):
         want = [int(table[b, (prefix[b] + i) // P]) for i in range(n)]
         want = [v * P + (prefix[b] + i) % P if v >= 0 else -1 for i, v in enumerate(want)]
         assert slots[at:at + n].tolist() == want
-    for t in (mask, position, slots):
-        assert bool((t[starts[-1]:] == 77).all())
+    assert bool((mask[starts[-1]:] == 77).all()) and bool((position[starts[-1]:] == 77).all())
+    assert bool((slots[starts[-1]:] == -1).all())
+
+
+@pytest.mark.parametrize("starts", [(3, 5, 9), (0, 0), (2, 2, 2), (7,)])
+def test_rows_of_no_sequence_have_no_slot(starts):
+    """A padded step: rows before and behind the sequences write nothing when they are appended with the others."""
+    B, T = len(starts) - 1, 300
+    c = svdq.Kv4Cache(4, 16, 2, 64)
+    table = torch.arange(2 * B, dtype=I32, device="cuda").view(B, 2)
+    kv_len = torch.tensor([b - a for a, b in zip(starts, starts[1:])], dtype=I32, device="cuda")
+    _, _, slots = svdq.kv4_tree_plan(c, torch.full((T,), -1, dtype=I32, device="cuda"),
+                                     torch.tensor(starts, dtype=I32, device="cuda"), kv_len, table, 8,
+                                     slots=torch.full((T,), 5, dtype=I32, device="cuda"))
+    want = [-1] * T
+    for b in range(B):
+        for i in range(starts[b], starts[b + 1]):
+            want[i] = 32 * b + i - starts[b]
+    assert slots.tolist() == want
 
 
 def test_plan_of_parents_that_are_none():

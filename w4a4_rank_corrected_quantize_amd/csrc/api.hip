@@ -728,7 +728,7 @@ extern "C" svdq_status svdq_kv4_tree_plan(const int32_t *parent, const int32_t *
         return SVDQ_ERR_MISALIGNED;
     st = current_device_ok();
     if (st != SVDQ_OK) return st;
-    if (T == 0 || B == 0) return SVDQ_OK;
+    if (T == 0 || (B == 0 && !slots)) return SVDQ_OK;
     return launch_kv4_tree_plan(parent, s, B, T, mask, mask_words, position, slots, (hipStream_t)stream) == hipSuccess
                ? SVDQ_OK : SVDQ_ERR_HIP;
 }

@@ -24,7 +24,7 @@ __device__ __forceinline__ int kt_slot(const Kv4Tables &s, int seq, int64_t at)
 // the last to the first.
 constexpr int KT_LDS = 2048, KT_FAST = 256;
 
-__global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__restrict__ parent, Kv4Tables s, int T,
+__global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__restrict__ parent, Kv4Tables s, int T, int B,
                                                             uint32_t *__restrict__ mask, int words,
                                                             int32_t *__restrict__ position,
                                                             int32_t *__restrict__ slots)
@@ -32,8 +32,16 @@ __global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__res
     __shared__ int up[KT_LDS];
     __shared__ uint32_t seen[KT_FAST / 32][KT_FAST];
     const int seq = blockIdx.x, tid = threadIdx.x;
+    // rows of no sequence have no slot: appended with the others they write nothing
+    auto none = [&](int from, int to) {
+        if (slots)
+            for (int i = from + tid; i < to; i += 256) slots[i] = -1;
+    };
+    if (B == 0) return none(0, T);
     const int q0 = kt_clamp(s.q_start[seq], 0, T), n = kt_clamp(s.q_start[seq + 1], q0, T) - q0;
     const int kv = kt_clamp(s.kv_len[seq], 0, s.width << s.page_shift);
+    if (seq == 0) none(0, q0);
+    if (seq == B - 1) none(q0 + n, T);
     if (n <= KT_FAST) {
         const int own = (n + 31) >> 5;                     // words that hold bits
         const bool in = tid < n;
@@ -201,7 +209,7 @@ __global__ __launch_bounds__(256) void kv4_keep_path_kernel(Kv4View c, Kv4Tables
 hipError_t launch_kv4_tree_plan(const int32_t *parent, const Kv4Tables &s, int B, int T, uint32_t *mask, int words,
                                 int32_t *position, int32_t *slots, hipStream_t stream)
 {
-    kv4_tree_plan_kernel<<<B, 256, 0, stream>>>(parent, s, T, mask, words, position, slots);
+    kv4_tree_plan_kernel<<<B > 0 ? B : 1, 256, 0, stream>>>(parent, s, T, B, mask, words, position, slots);
     return hipGetLastError();
 }
 
