@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__res
                                                             int32_t *__restrict__ slots)
 {
     __shared__ int up[KT_LDS];
-    __shared__ uint32_t seen[KT_FAST / 32][KT_FAST];
+    __shared__ uint32_t seen[2][KT_FAST / 32 * KT_FAST];
     const int seq = blockIdx.x, tid = threadIdx.x;
     // rows of no sequence have no slot: appended with the others they write nothing
     auto none = [&](int from, int to) {
@@ -51,19 +51,23 @@ __global__ __launch_bounds__(256) void kv4_tree_plan_kernel(const int32_t *__res
         uint32_t m[KT_FAST / 32];
 #pragma unroll
         for (int w = 0; w < KT_FAST / 32; ++w) m[w] = w == tid >> 5 ? 1u << (tid & 31) : 0u;
-        while (true) {
-            up[tid] = a;
+        // after r rounds a row has met 2^r - 1 ancestors, of at most n - 1
+        for (int r = 0; 1 << r < n; ++r) {
+            int *ups = up + (r & 1) * KT_FAST;
+            uint32_t *sees = seen[r & 1] + tid;
+            if (in) {
+                ups[tid] = a;
 #pragma unroll
-            for (int w = 0; w < KT_FAST / 32; ++w)
-                if (w < own) seen[w][tid] = m[w];
-            if (!__syncthreads_or(a >= 0)) break;
+                for (int w = 0; w < KT_FAST / 32; ++w)
+                    if (w < own) sees[w * KT_FAST] = m[w];
+            }
+            __syncthreads();                               // the round before the last has been read
             if (a >= 0) {
 #pragma unroll
                 for (int w = 0; w < KT_FAST / 32; ++w)
-                    if (w < own) m[w] |= seen[w][a];
-                a = up[a];
+                    if (w < own) m[w] |= sees[w * KT_FAST + a - tid];
+                a = ups[a];
             }
-            __syncthreads();                               // every read of this round is done
         }
         if (!in) return;
         uint32_t *row = mask + (int64_t)(q0 + tid) * words;
