@@ -872,6 +872,7 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT, TREE> &w, uint8_t *
         // operand read ahead, E exponentials and their bf16 pairs
         auto scores = [&] {
             constexpr int E = CT * 16 / KO;
+            static_assert(E * KO == CT * 16 && (E == 1 || E % 2 == 0), "exponentials in pairs; one per piece: a pair in every other");
             f32x4 sc[CT][4];
 #pragma unroll
             for (int i = 0; i < KO; ++i) {
@@ -886,7 +887,7 @@ __device__ __forceinline__ void ka_walk_shared(KvRows<D, CT, TREE> &w, uint8_t *
                     sc[ct][i & 3] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], w.q[ct][i >> 2], sc[ct][i & 3], 0, 0, 0);
                 if (i + 4 < KO) kf[i + 4] = ka_lds_read(lk, 1024 * (KS * (i & 3) + ((i + 4) >> 2)));
                 else if (MIX) ka_v_read<NB>(vf, lv, i + 4 - KO);
-                if (MIX) {
+                if (MIX && (E > 1 || i % 2 == 0)) {
 #pragma unroll
                     for (int e = E * i; e < E * (i + 1); e += 2) ka_exp_pair<D, INT4, CT>(pb, cur, sum, base, c2, vsc, e);
                 }
