@@ -236,12 +236,12 @@ def test_split_keys(prec, D, q):
 @pytest.mark.parametrize("D,Hk", [(64, 8), (128, 4)])
 @pytest.mark.parametrize("long", [0, 1, 5])
 def test_many_rows(prec, D, Hk, long):
-    """Enough trees for tiles of 128 rows and of 64, with the keys whole (no prefix above 200) or divided evenly over the
+    """Enough trees for tiles of 128 rows and of 64, with the keys whole (no prefix above 150) or divided evenly over the
     blocks (1500 and 7500), for trees of every remainder of a tile."""
     _say(f"many rows prec={prec} D={D} Hk={Hk} long={long}")
     rng = random.Random(D + long)
     counts = [40, 33, 16, 48, 64, 20, 5, 0, 47, 32, 31, 63, 1, 44, 39, 55]
-    lens = [(q, q + (rng.randint(0, 200) if not long else rng.choice([0, 30, 1500 * long // (1 + b % 3)])))
+    lens = [(q, q + (rng.randint(0, 150) if not long else rng.choice([0, 30, 1500 * long // (1 + b % 3)])))
             for b, q in enumerate(counts)]
     x = _batch(prec, D, Hk, 4, 64, lens, seed=D)
     sees = [_above(_parents(b, n, 0.7)) for b, (n, _) in enumerate(lens)]
