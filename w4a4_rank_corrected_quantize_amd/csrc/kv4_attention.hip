@@ -57,6 +57,16 @@
 //   8 sequences of 1 .. 700 rows over up to 6000 keys, 16 heads over 4 of 64,
 //   INT4, causal: 103 us = 288 TFLOP/s; some 780 pieces of about 20 steps over
 //   512 places, two rounds.
+// Trees of drafted tokens (TREE): the same walk with a mask of the drafted keys, which
+// only steps that reach them read (three words per column).
+//   8 tokens over 1000 keys, 32 heads over 8 of 128, INT4: 9.0 + 2.5 us, latencies as
+//   for one token.
+//   16 x 24 .. 64 tokens over 3642 .. 16348 keys, 32 heads over 8 of 128, MXFP4 (106
+//   GF): 158 us and 10 for the sums, with the plan 167 in a graph = 637 TFLOP/s; the
+//   fixed division instead of KvEven 230.  Bound by the tiles' padding (18 %, half tiles
+//   at 4 / 5 of a full one) and instruction issue: a full tile's step takes 1.25 us of
+//   a compute unit, 1.19 in 4608 x 4608.
+//   9 x 1 .. 130 tokens over up to 5000 keys, 12 heads over 4 of 64, INT4: 31 + 4.4 us.
 // Not kept: 48 rows per wave and three waves per SIMD (spills), 64 rows and one
 // wave per SIMD (443 us: nothing beside a wave's waits), a branch
 // around the rescaling per column (copies of the sums), ordering hints instead
@@ -1063,7 +1073,8 @@ __device__ __forceinline__ void ka_many_rows(uint8_t *lds, const KvArgs &a, ka_c
 // workspace, part by part, and its number of parts with every row.
 struct KvEven {
     // a tile of up to 64 rows: half the products, the same conversions and waits (3
-    // of 5 per step: 179 us for the batch below, 4: 169)
+    // of 5 per step: 183 us for 16 x 24 .. 64 tokens over 3642 .. 16348 keys, 4: 172;
+    // 16 x 1 .. 64 over up to 16000, INT4: 157 and 148)
     static constexpr int kFull = 5, kHalf = 4, kUnit = 16;
 };
 
