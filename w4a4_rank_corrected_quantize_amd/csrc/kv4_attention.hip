@@ -1084,6 +1084,13 @@ __device__ __forceinline__ int64_t ka_uniform(int64_t x)
                      (uint32_t)__builtin_amdgcn_readfirstlane((int)x));
 }
 
+// x / y of what is the same in all lanes and not negative: costs pass 32 bits for
+// batches alone that no card holds, and a 64-bit division takes some 400 cycles.
+__device__ __forceinline__ int64_t ka_div(int64_t x, int64_t y)
+{
+    return (uint64_t)(x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+}
+
 // A sequence's rows and keys, and its units' costs.
 struct KvSeq {
     int qs, qn, kv, full, rest;                   // full tiles; rows of the last one, 0 for none
@@ -1145,33 +1152,36 @@ __device__ __forceinline__ void ka_unit(uint8_t *lds, const KvArgs &a, ka_const_
 template <int D, bool INT4, int CT>
 __device__ __forceinline__ void ka_even(uint8_t *lds, const KvArgs &a, int wave, int lane)
 {
-    // all costs and the greatest unit's, 64 sequences at a time
-    int64_t total = 0, most = 0;
-    for (int s0 = 0; s0 < a.B; s0 += 64) {
-        int64_t c = 0, u = 0;
+    // 64 sequences at a time: their costs, up to each, and the greatest unit's
+    int64_t c = 0, up = 0, total = 0;
+    int most = 0;
+    auto scan = [&](int s0, bool first_time) {
+        c = 0;
         if (s0 + lane < a.B) {
             const KvSeq s = ka_seq(a, a.q_start, a.kv_len, s0 + lane);
-            c = s.cost, u = s.full ? s.cost_full : (s.rest ? s.cost_rest : 0);
+            c = s.cost;
+            most = max(most, (int)(s.full ? s.cost_full : (s.rest ? s.cost_rest : 0)));
         }
+        up = c;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d), u = max(u, (int64_t)__shfl_xor(u, d));
-        total += c, most = max(most, u);
-    }
-    total = ka_uniform(total), most = ka_uniform(most);
-    const int64_t blocks = gridDim.x, parts = a.even - 1;
-    const int64_t L = max(max((total + blocks - 1) / blocks, (most + parts - 1) / parts), (int64_t)KvEven::kUnit);
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t x = __shfl_up(up, d);
+            up += lane >= d ? x : 0;
+        }
+        if (first_time) total += ka_uniform(__shfl(up, 63));
+    };
+    for (int s0 = 0; s0 < a.B; s0 += 64) scan(s0, true);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+    const int64_t blocks = gridDim.x, parts = a.even - 1, longest = __builtin_amdgcn_readfirstlane(most);
+    const int64_t L = max(max(ka_div(total + blocks - 1, blocks), ka_div(longest + parts - 1, parts)), (int64_t)KvEven::kUnit);
     const int64_t lo = L * blockIdx.x, hi = min(lo + L, total);
     if (lo >= hi) return;
     // the sequence that lo falls into, and where it begins
     int64_t first = 0;
     int seq = 0;
     for (int s0 = 0; s0 < a.B; s0 += 64) {
-        int64_t c = s0 + lane < a.B ? ka_seq(a, a.q_start, a.kv_len, s0 + lane).cost : 0, up = c;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t x = __shfl_up(up, d);
-            up += lane >= d ? x : 0;
-        }
+        if (a.B > 64) scan(s0, false);
         const int before = __popcll(__ballot(first + up <= lo));     // whole sequences before lo
         if (before < 64) {
             first = ka_uniform(first + __shfl(up - c, before)), seq = s0 + before;
@@ -1188,16 +1198,17 @@ __device__ __forceinline__ void ka_even(uint8_t *lds, const KvArgs &a, int wave,
         while (at < hi && at < first + s.cost) {
             const bool half = at - first >= full;
             const int64_t cost = half ? s.cost_rest : s.cost_full, begin0 = first + (half ? full : 0);
-            const int unit = (int)((at - begin0) / cost), w = half ? KvEven::kHalf : KvEven::kFull;
-            const int64_t begin = begin0 + unit * cost, b0 = begin / L;
+            const int unit = (int)ka_div(at - begin0, cost);
+            const int64_t begin = begin0 + unit * cost, b0 = ka_div(begin, L);
             const int head = unit % a.c.heads, tile = half ? s.full : unit / a.c.heads;
             // steps up to a cost x of the unit
             auto upto = [&](int64_t x) {
-                const int64_t y = x - begin - KvEven::kUnit;
-                return y <= 0 ? 0 : (int)min((y + w - 1) / w, (int64_t)steps);
+                const int y = (int)(x - begin) - KvEven::kUnit;      // within a unit
+                const int n = half ? (y + KvEven::kHalf - 1) / KvEven::kHalf : (y + KvEven::kFull - 1) / KvEven::kFull;
+                return y <= 0 ? 0 : min(n, steps);
             };
             const KvRange g = {lo <= begin ? 0 : upto(lo), hi >= begin + cost ? steps : upto(hi), 0, s.kv};
-            const int count = (int)((begin + cost - 1) / L - b0) + 1, part = (int)(blockIdx.x - b0);
+            const int count = (int)(ka_div(begin + cost - 1, L) - b0) + 1, part = (int)(blockIdx.x - b0);
             if (half) ka_unit<D, INT4, 1>(lds, a, table, s, head, (int64_t)128 * tile, g, part, count, wave, lane);
             else ka_unit<D, INT4, CT>(lds, a, table, s, head, (int64_t)128 * tile, g, part, count, wave, lane);
             at = begin + cost;
