@@ -124,9 +124,10 @@ __global__ __launch_bounds__(256) void kv4_keep_path_kernel(Kv4View c, Kv4Tables
     constexpr int NG = Tok::NG, CHUNK = 64;
     __shared__ int src[CHUNK], dst[CHUNK], found;
     const int head = blockIdx.x % c.heads, seq = blockIdx.x / c.heads, tid = threadIdx.x;
+    const int32_t *nodes = path + (int64_t)seq * max_path;
+    int next = tid < min(CHUNK, max_path) ? nodes[tid] : -1;        // beside the lengths, which it does not wait for
     const int q0 = kt_clamp(s.q_start[seq], 0, T), n = kt_clamp(s.q_start[seq + 1], q0, T) - q0;
     const int kv = kt_clamp(s.kv_len[seq], 0, s.width << s.page_shift);
-    const int32_t *nodes = path + (int64_t)seq * max_path;
     const int most = min(max_path, n);
     int kept = 0;
     bool more = true;
@@ -135,9 +136,10 @@ __global__ __launch_bounds__(256) void kv4_keep_path_kernel(Kv4View c, Kv4Tables
         const int left = min(CHUNK, most - at);
         __syncthreads();
         if (tid < CHUNK) {
-            const int i = at + tid;
-            const int node = tid < left ? nodes[i] : -1;
-            const int before = tid < left && i > 0 ? nodes[i - 1] : -1;
+            const int i = at + tid, node = next;
+            int before = __shfl_up(node, 1);
+            if (tid == 0) before = at > 0 ? nodes[at - 1] : -1;
+            next = i + CHUNK < max_path ? nodes[i + CHUNK] : -1;
             const uint64_t bad = ~__ballot(tid < left && node > before && node < n);
             const int count = bad ? __builtin_ctzll(bad) : CHUNK;
             const int64_t base = (int64_t)kv - n;
