@@ -1384,7 +1384,8 @@ def qk_norm_rope(Q, K, cos, sin, style: int = ROPE_ADJACENT, index=None, norm_q=
             if fit is not None:
                 dev, T, H, D, Hk, ldq, ldk, _, ldqo = fit
                 rows, pairs = cos.shape
-                Q_out, K_out = Q.new_empty((T, H, D)), K.new_empty((T, Hk, D))
+                Q_out = torch.empty_like(Q) if ldq == H * D else Q.new_empty((T, H, D))      # like: 0.3 us less
+                K_out = torch.empty_like(K) if ldk == Hk * D else K.new_empty((T, Hk, D))
                 pK, pKo, ldko, raw = K.data_ptr(), K_out.data_ptr(), Hk * D, _raw_stream(dev)
         except _MISFIT:
             pass
@@ -1445,7 +1446,7 @@ def kv4_rope_append(cache: Kv4Cache, Q, K, V, cos, sin, slots, style: int = ROPE
                 dev, T, H, D, Hk, ldq, ldk, ldv, ldqo = fit
                 rows, pairs = cos.shape
                 if Q_out is None:
-                    Q_out = Q.new_empty((T, H, D))
+                    Q_out = torch.empty_like(Q) if ldq == H * D else Q.new_empty((T, H, D))
                 raw = _raw_stream(dev)
         except _MISFIT:
             pass

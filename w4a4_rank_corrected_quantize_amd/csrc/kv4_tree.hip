@@ -4,7 +4,7 @@
 // launch each, no length known to the host.  Measured: the plan of 8 nodes 2.6
 // us, of 16 x 24 .. 64 nodes 5.2, of 9 x 1 .. 130 nodes 5.4 (a walk per row up to the
 // root 7.4); a path of 8 nodes, 8 heads of 128, 2.9 us; 64 paths of up to 64 nodes, 8
-// heads, 8.4 us (a node at a time 10.6).
+// heads, 8.1 us (a node at a time 10.6).
 #include "kv4.h"
 
 namespace svdq {
