@@ -41,9 +41,9 @@ NO_CLOCK = False
 # measured on; otherwise traffic is null.
 TRAFFIC = {
     # FETCH_SIZE 73696.8 KiB / 0.50002 + WRITE_SIZE 110607.1 KiB / 1.00000 (per dispatch)
-    "fc1": {"source": "w4a4_gemm.hip", "source_sha": "fd8434b09a0b456a", "bytes": 264186680},
+    "fc1": {"source": "w4a4_gemm.hip", "source_sha": "cbd4ef2b5042054d", "bytes": 264186680},
     # FETCH_SIZE 70211.1 KiB / 0.50002 + WRITE_SIZE 110593.5 KiB / 1.00000
-    "mx_fc1": {"source": "w4a4_gemm.hip", "source_sha": "fd8434b09a0b456a", "bytes": 257034325},
+    "mx_fc1": {"source": "w4a4_gemm.hip", "source_sha": "cbd4ef2b5042054d", "bytes": 257034325},
     # FETCH_SIZE 15680 KiB / 0.50002 + WRITE_SIZE 36 KiB / 1.00000
     "awq_mod": {"source": "awq_gemv.hip", "source_sha": "fda4dd7b5f7b1013", "bytes": 32148220},
     # FETCH_SIZE 197078 KiB / 0.50002 + WRITE_SIZE 110594 KiB / 1.00000

@@ -288,7 +288,7 @@ svdq_status svdq_w4a4_linear_few(const uint8_t *xq, const void *xscale, const fl
  *   M, F, K      M >= 0, F >= 0 (either 0: no-op), F % 8 == 0, K % group == 0
  *   act          svdq_activation
  *   Y            [M][F] bf16 bits, device (out)
- * Any M: few rows (how many depends on F) run as in svdq_w4a4_linear_few, more in
+ * Any M: few rows (how many depends on F and K) run as in svdq_w4a4_linear_few, more in
  * the tiles of svdq_w4a4_linear.  One kernel launch.  Errors as for
  * svdq_w4a4_linear.
  */

@@ -153,6 +153,25 @@ def test_gated_tiles_of_odd_blocks(K):
 
 
 @pytest.mark.parametrize("prec", PRECS)
+@pytest.mark.parametrize("M,F,K", [(1500, 1000, 320), (1029, 2056, 512), (1100, 2000, 4096), (1601, 904, 768),
+                                   (1300, 1288, 64), (1500, 1000, 416), (1500, 1000, 96), (2049, 776, 160),
+                                   (1025, 1152, 1024), (700, 4104, 256)])
+def test_gated_of_many_rows(prec, M, F, K):
+    """The tiles: rows and channels that end inside one, K of whole and broken steps, with a bias and without."""
+    if prec == svdq.INT4 and K % 64:
+        K = 128 * (K // 64)
+    _say(f"linear_gated tiles prec={prec} {M}x{K}->{F}")
+    p = _problem(F, M, 2 * F, K, prec, bias=M % 2 == 0)
+    y, d = _sums(p, 2.0 ** -15 if prec == svdq.INT4 else 0.0)
+    buf, Y = _out(M, F)
+    for act, name in ((svdq.ACT_SILU, "silu"), (svdq.ACT_GELU_TANH, "gelu")):
+        (a, da), u, du = _act(y[:, :F], d[:, :F], name), y[:, F:], d[:, F:]
+        svdq.w4a4_linear_gated(*p["args"], prec, act=act, Y=Y)
+        _close(Y, a * u, a.abs() * du + u.abs() * da + da * du)
+    _untouched(buf)
+
+
+@pytest.mark.parametrize("prec", PRECS)
 def test_gated_of_more_tiles_than_compute_units(prec):
     """Several tiles per block of the persistent kernel, several rounds of the other."""
     M, F, K = 2100, 4488, 256

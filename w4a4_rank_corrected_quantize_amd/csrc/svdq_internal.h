@@ -63,9 +63,8 @@ hipError_t launch_w4a4_linear_qknorm(const uint8_t *xq, const void *xscale, cons
                                      float eps, const float *rope_cos, const float *rope_sin, uint16_t *Y,
                                      hipStream_t stream);
 
-// Few rows (M <= kFewRows): one pass over the weights (w4a4_few.hip).  Gated: N
-// output channels, weight rows N + N; any M (the few rows' kernel or the tiles').
-constexpr int kFewRows = SVDQ_FEW_MAX_ROWS;
+// Few rows: one pass over the weights per 64 (w4a4_few.hip).  Gated: N output
+// channels, weight rows N + N; any M (the few rows' kernel or the tiles').
 hipError_t launch_w4a4_few(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
                            const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int N, int K,
                            svdq_precision prec, svdq_epilogue epi, uint16_t *Y, hipStream_t stream);

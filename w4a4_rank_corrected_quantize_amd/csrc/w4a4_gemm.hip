@@ -2037,25 +2037,36 @@ hipError_t launch_w4a4_linear(const uint8_t *xq, const void *xscale, const float
     return hipGetLastError();
 }
 
-// Few rows' kernel or tiles.  The tiles take about as long for any few rows (one
-// round of them), the other's time grows with the channels and the sets of 64 rows,
-// by 9, 12, 14 and 16 parts for one to four tiles of 16 rows.  2 x 14336 channels
-// of 4096, us: INT4 64 rows 39, tiles 60; 128 rows 73 and 62; MXFP4 128 rows 36 and
-// 42, 192 rows 51 and 45.  2 x 6912: INT4 192 rows 57 and 60, 256 rows 69 and 61;
-// MXFP4 256 rows 43 and 43.  2 x 2048: 256 rows 22 and 57, 15 and 35.
-static bool few_gated(int M, int F, svdq_precision prec)
+// Few rows' kernel or tiles, by their times (us, k = K / 1024).  The tiles take one
+// round of them for all that this asks about; the other a round per compute unit's
+// sets of 64 rows x 16 channels, each 9, 12, 14 or 16 sixteenths for one to four tiles
+// of 16 rows.  Measured, few / tiles:
+//   INT4: 2 x 1024 channels of 1024, 768 rows 15.8 / 20.0, 1024 rows 21.0 / 19.9; of
+//   4096, 300 rows 20 / 57, 1024 rows 38 / 57; 2 x 4096 of 2560, 300 and 384 rows 37.6 /
+//   38.5 and 44.8 / 39.2; 2 x 6912 of 11008, 256 and 300 rows 140 / 151 and 174 / 149;
+//   2 x 14336 of 4096, 64 and 128 rows 39 / 60 and 73 / 62, of 11008, 128 rows 185 / 153.
+//   MXFP4: 2 x 1024 of 4096, 300 rows 12 / 34, 1024 rows 23 / 35; 2 x 2048 of 4096, 768
+//   and 1024 rows 33 / 36 and 43 / 35; 2 x 14336 of 4096, 128 and 192 rows 36 / 42 and
+//   51 / 45; K % 128 != 0: 2 x 4096 of 4128, 512 and 768 rows 58 / 67 and 85 / 67; 2 x
+//   14336, 192 and 256 rows 56 / 71 and 74 / 72.
+static bool few_gated(int M, int F, int K, svdq_precision prec)
 {
-    if (M > kFewRows) return false;
-    const int parts[4] = {9, 12, 14, 16}, sets = (M + 63) / 64, rows = (M + sets - 1) / sets;
-    const int64_t cost = (int64_t)((F + 15) / 16) * sets * parts[(rows - 1) / 16];
-    return cost <= 16 * (prec == SVDQ_INT4 ? 5 : 7) * (int64_t)device_cu_count();
+    const double parts[4] = {9.0 / 16, 12.0 / 16, 14.0 / 16, 1.0}, k = K / 1024.0;
+    const int64_t sets = ((int64_t)M + 63) / 64, rows = (M + sets - 1) / sets, channels = ((int64_t)F + 15) / 16;
+    const int64_t cus = device_cu_count(), rounds = (channels * sets + cus - 1) / cus;
+    const bool wide = channels > 3 * cus;                 // few_ring's form for many channels
+    double few, tiles;
+    if (prec == SVDQ_INT4) few = wide ? 1.2 + 2.25 * k : 3.6 + 1.4 * k, tiles = 6.9 + 12.5 * k;
+    else if (K % 128 == 0) few = (2.4 + 0.8 * k) * (wide ? 0.92 : 1.0), tiles = 7.7 + 6.8 * k;
+    else few = (2.5 + 1.2 * k) * (wide ? 0.7 : 1.0), tiles = 7.9 + 14.5 * k;
+    return (double)rounds * parts[(rows - 1) / 16] * few <= tiles + 1e-4 * k * F;
 }
 
 hipError_t launch_w4a4_linear_gated(const uint8_t *xq, const void *xscale, const float *h, const uint8_t *wq,
                                     const void *wscale, const uint16_t *up, const uint16_t *bias, int M, int F, int K,
                                     svdq_precision prec, svdq_activation act, uint16_t *Y, hipStream_t stream)
 {
-    if (few_gated(M, F, prec)) return launch_w4a4_few_gated(xq, xscale, h, wq, wscale, up, bias, M, F, K, prec, act, Y, stream);
+    if (few_gated(M, F, K, prec)) return launch_w4a4_few_gated(xq, xscale, h, wq, wscale, up, bias, M, F, K, prec, act, Y, stream);
     const int gelu = act == SVDQ_ACT_GELU_TANH ? 1 : 0, N = 2 * F;
     const int tiles_n = (N + I4_BN - 1) / I4_BN;       // both rows of 128 channels in every kernel's tile
     static_assert(I4_BN == 256 && MX_BN == 256 && MXD_BN == 256, "gated_row's tiles");
