@@ -250,6 +250,76 @@ def test_many_rows(prec, D, Hk, long):
 
 
 @pytest.mark.parametrize("prec", PRECS)
+@pytest.mark.parametrize("D,Hk", [(64, 3), (128, 1)])
+@pytest.mark.parametrize("B", [64, 65, 150])
+def test_many_sequences(prec, D, Hk, B):
+    """As many trees as the division looks at at once, and more; some without rows, some without a prefix."""
+    _say(f"many sequences prec={prec} D={D} Hk={Hk} B={B}")
+    rng = random.Random(B + D)
+    lens = [(q, q + rng.choice([0, 40, 130, 700])) for q in (rng.choice([0, 3, 12, 18, 33, 40]) for _ in range(B))]
+    lens[0], lens[-1] = (40, 740), (0, 0)
+    x = _batch(prec, D, Hk, 8, 32, lens, seed=B)
+    sees = [_above(_parents(b, n, 0.6)) for b, (n, _) in enumerate(lens)]
+    out, lse = _call(x, _masks(x, sees, 2))
+    _verify(x, out, lse, sees, 2, D ** -0.5)
+
+
+@pytest.mark.parametrize("prec", PRECS)
+@pytest.mark.parametrize("D,Hk", [(64, 8), (128, 4)])
+def test_divided_keys_captured_and_on_two_streams(prec, D, Hk):
+    """The even division follows the lengths that a replay finds, reads nothing of a workspace that it has not written,
+    and two calls at once keep apart."""
+    _say(f"divided keys captured prec={prec} D={D} Hk={Hk}")
+    counts = [40, 33, 16, 48, 64, 20, 5, 0, 47, 32, 31, 63, 1, 44, 39, 55]
+    x, y = (_batch(prec, D, Hk, 4, 64, [(q, q + (b * (211 + 89 * k)) % 1700) for b, q in enumerate(counts)], seed=D + k)
+            for k in range(2))
+    masks = [_masks(z, [_above(_parents(b, n, 0.5)) for b, n in enumerate(counts)], 2) for z in (x, y)]
+    T, H = x["Q"].shape[:2]
+    work = [svdq.kv4_attention_workspace(z["c"], T, 16, H, 64, 1800) for z in (x, y)]
+    assert all(w is not None for w in work)
+    out, lse = [torch.empty_like(z["Q"]) for z in (x, y)], [torch.empty(T, H, device="cuda") for _ in range(2)]
+
+    def call(k, **kw):
+        z = (x, y)[k]
+        return svdq.kv4_tree_attention(z["Q"], z["c"], z["table"], z["q_start"], z["kv_len"], masks[k], 64, 1800,
+                                       out=out[k], lse=lse[k], work=work[k], **kw)
+
+    def clear(k):
+        out[k].fill_(-7.0), lse[k].fill_(123.0), work[k].fill_(255)
+
+    full = x["kv_len"].clone()
+    lengths = [full, torch.minimum(full, x["q_start"].diff() + 300), x["q_start"].diff(), torch.minimum(full, torch.full_like(full, 900))]
+    want = []
+    for n in lengths:
+        x["kv_len"].copy_(n)
+        clear(0), call(0)
+        want.append((out[0].clone(), lse[0].clone()))
+    assert all(bool(torch.isfinite(o.float()).all()) for o, _ in want)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call(0)
+    for i in (1, 0, 3, 2, 1):
+        x["kv_len"].copy_(lengths[i])
+        clear(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[i][0]) and torch.equal(lse[0], want[i][1]), i
+    x["kv_len"].copy_(full)
+    clear(1), call(1)
+    other = out[1].clone(), lse[1].clone()
+    clear(0), clear(1)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for k, st in enumerate(streams):
+            call(k, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0][0]) and torch.equal(lse[0], want[0][1])
+    assert torch.equal(out[1], other[0]) and torch.equal(lse[1], other[1])
+
+
+@pytest.mark.parametrize("prec", PRECS)
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_chain_is_the_causal_form(prec, D):
     """A chain's rows see what the causal mask lets them see: the same bits."""
