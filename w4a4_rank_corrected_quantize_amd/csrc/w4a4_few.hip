@@ -255,8 +255,8 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
     for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[t][c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    // the epilogue's operands, ahead of the stages: whoever waits for a stage has
-    // waited for them
+    // the epilogue's operands, ahead of the stages: other waves read them, so a wave
+    // waits for its share before the sums' barrier, whether it has a stage or not
     uint8_t *epi_up = lds + FIRST, *epi_bias = epi_up + UPS * 1024, *epi_h = epi_bias + UPS * 256;
     for (int u = wave; u < UPS + CT; u += W) {
         if (u < UPS) {
@@ -388,8 +388,11 @@ __global__ __launch_bounds__(64 * WN * WK) void w4a4_few_kernel(FewArgs a)
             issue(i + DEPTH);
         }
     }
-    // the waves' sums: tile (t, c) of wave w at (w RT + t) CT + c
+    // the waves' sums: tile (t, c) of wave w at (w RT + t) CT + c.  The compiler does
+    // not know of the loads to LDS: a wave without a stage has not waited for its
+    // operands of the epilogue yet (one that had a stage has nothing under way)
     f32x4 *sums = reinterpret_cast<f32x4 *>(lds);
+    fw_wait<0>();
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < RT; ++t)
