@@ -106,9 +106,11 @@ __device__ __forceinline__ RopeLane<D, HALVES> rp_lane(int i, int pairs)
     return l;
 }
 
-// A lane's eight cosines and sines of a token.
+// A lane's eight cosines and sines of a token, those of four pairs each turned or
+// not; some: a lane of the wave has pairs that are not.
 struct RopeTurn {
     float c[8], s[8];
+    bool on[2], some;
 };
 
 template <int D, bool HALVES>
@@ -121,13 +123,15 @@ __device__ __forceinline__ RopeTurn rp_turn(const RopeArgs &r, const RopeLane<D,
     for (int h = 0; h < 2; ++h) {
         const int p = h ? l.pb : l.pa;
         float4 c = make_float4(1.0f, 1.0f, 1.0f, 1.0f), s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in && p < r.pairs) {
+        o.on[h] = in && p < r.pairs;
+        if (o.on[h]) {
             c = *reinterpret_cast<const float4 *>(r.cos + (int64_t)row * r.pairs + p);
             s = *reinterpret_cast<const float4 *>(r.sin + (int64_t)row * r.pairs + p);
         }
         o.c[4 * h] = c.x, o.c[4 * h + 1] = c.y, o.c[4 * h + 2] = c.z, o.c[4 * h + 3] = c.w;
         o.s[4 * h] = s.x, o.s[4 * h + 1] = s.y, o.s[4 * h + 2] = s.z, o.s[4 * h + 3] = s.w;
     }
+    o.some = __any(!o.on[0] || !o.on[1]);
     return o;
 }
 
@@ -183,6 +187,13 @@ __device__ __forceinline__ bool rp_apply(const uint4 &xa, const uint4 &xb, uint4
         const F c = r.c[p], s = r.s[p];
         o[a] = (float)rp_fma(u[a], c, -(u[b] * s));
         o[b] = (float)rp_fma(u[b], c, u[a] * s);
+    }
+    if (r.some) {                                          // not by 1 and 0: an infinity would reach its neighbour
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const bool on = r.on[HALVES ? (k & 7) >> 2 : k >> 3];
+            o[k] = on ? o[k] : (float)u[k];
+        }
     }
     ya = make_uint4(rp_pack2(o[0], o[1]), rp_pack2(o[2], o[3]), rp_pack2(o[4], o[5]), rp_pack2(o[6], o[7]));
     yb = make_uint4(rp_pack2(o[8], o[9]), rp_pack2(o[10], o[11]), rp_pack2(o[12], o[13]), rp_pack2(o[14], o[15]));
