@@ -770,7 +770,7 @@ def _few_args(where, xq, xscale, h, wq, wscale, up, bias, prec, halves, Y, strea
     M, KB = xq.shape
     N, r = up.shape
     K = 2 * KB
-    if xq.numel() >= _ELEMENTS or wq.numel() >= _ELEMENTS:
+    if xq.numel() >= _ELEMENTS or wq.numel() >= _ELEMENTS or max(M, N, K, r) > _I32:
         raise SvdqError(-2, where)
     _arg(xq, u8, "xq")
     _arg(xscale, sdt, "xscale", (M, K // g))
@@ -809,7 +809,8 @@ def _few_call(where, call, xq, xscale, h, wq, wscale, up, bias, prec, halves, la
                 and wscale.is_contiguous() and h.is_contiguous() and up.is_contiguous() and Y.is_contiguous()
                 and (bias is None or (bias.dtype is _BF and bias.shape == (N,) and bias.get_device() == dev
                                       and bias.is_contiguous()))
-                and M * KB < _ELEMENTS and N * KB < _ELEMENTS and prec in (INT4, MXFP4)):
+                and M * KB < _ELEMENTS and N * KB < _ELEMENTS and M < _I32 and N < _I32 and KB < _ELEMENTS and r < _I32
+                and prec in (INT4, MXFP4)):
             raw = _raw_stream(dev)
     except _MISFIT:
         pass
@@ -1116,7 +1117,7 @@ def kv4_tree_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, mask, m
                 and mask.shape == (T, words) and out.shape == Q.shape and out.is_contiguous() and mask.is_contiguous()
                 and block_table.is_contiguous() and q_start.is_contiguous() and kv_len.is_contiguous()
                 and work.is_contiguous() and 0 <= max_q <= _I32 and 0 <= max_kv <= _I32
-                and T < _I32 and B < _I32 and width < _I32
+                and T < _I32 and B < _I32 and width < _I32 and words < _I32 and H < _I32
                 and (lse is None or (lse.dtype is _F32 and lse.shape == (T, H) and lse.get_device() == dev
                                      and lse.is_contiguous()))):
             raw = _raw_stream(dev)
@@ -1139,7 +1140,7 @@ def kv4_tree_attention(Q, cache: Kv4Cache, block_table, q_start, kv_len, mask, m
         _ndim(mask, 2, "mask")
         words = mask.shape[1]
         _arg(mask, i32, "mask", (T, words))
-        if B > _I32 or width > _I32 or words > _I32:
+        if T > _I32 or B > _I32 or H > _I32 or width > _I32 or words > _I32:
             raise SvdqError(-2, "svdq_kv4_tree_attention")
         max_q, max_kv = _bound(max_q), _bound(max_kv)
         out = _empty((T, H, D), torch.bfloat16, dev, stream, Q) if out is None else _arg(
@@ -1252,7 +1253,7 @@ def kv4_keep_path(cache: Kv4Cache, path, q_start, kv_len, block_table, T: Option
         _arg(path, i32, "path", (B, longest))
         _arg(q_start, i32, "q_start", (B + 1,))
         _arg(kv_len, i32, "kv_len", (B,))
-        T = _I32 if T is None else T
+        T = _I32 if T is None else max(T, -1)
         if B > _I32 or width > _I32 or longest > _I32 or T > _I32:
             raise SvdqError(-2, "svdq_kv4_keep_path")
         new_len = _empty((B,), i32, dev, stream, kv_len) if new_len is None else _arg(new_len, i32, "new_len", (B,))
@@ -1346,7 +1347,7 @@ def _rope_fast(Q, K, V, Q_out, cos, sin, index, norm_q, norm_k):
             and Q.dtype is _BF and K.dtype is _BF and cos.dtype is _F32 and sin.dtype is _F32 and Hk
             and dq == 1 and dk == 1 and hq == D and hk == D and K.shape == (T, Hk, D) and cos.dim() == 2
             and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous() and 0 < T < _I32 > H
-            and cos.shape[0] < _I32):
+            and cos.shape[0] < _I32 and cos.shape[1] < _I32 and D < _I32 and Hk < _I32):
         return None
     for w in (norm_q, norm_k):
         if w is not None and not (w.dtype is _BF and w.shape == (D,) and w.get_device() == dev and w.is_contiguous()):
