@@ -113,3 +113,11 @@ def test_a_negative_bound_on_rows_stays_negative(library, monkeypatch):
     for T in (-1, 6 - BIG):
         svdq.kv4_keep_path(_cache(), m(2, 5, dtype=I32), *args[3:5], args[2], T=T)
         assert library.calls.pop()[1][8] == -1
+
+
+def test_values_that_are_none_are_refused(library):
+    """V is no optional argument: the single checks say so."""
+    cos = m(3, 32, dtype=F32)
+    with pytest.raises(TypeError, match="V must be a torch tensor"):
+        svdq.kv4_rope_append(_cache(), m(3, 4, 64), m(3, 2, 64), None, cos, cos, m(3, dtype=I32))
+    assert not library.calls

@@ -1441,7 +1441,7 @@ def kv4_rope_append(cache: Kv4Cache, Q, K, V, cos, sin, slots, style: int = ROPE
     if stream is None:
         try:
             fit = _rope_fast(Q, K, V, Q_out, cos, sin, index, norm_q, norm_k)
-            if (fit is not None and fit[0] == cache.index == slots.get_device() and fit[3] == cache.dim
+            if (fit is not None and V is not None and fit[0] == cache.index == slots.get_device() and fit[3] == cache.dim
                     and fit[4] == cache.heads and slots.dtype is _INT32 and slots.shape == (fit[1],)
                     and slots.is_contiguous()):
                 dev, T, H, D, Hk, ldq, ldk, ldv, ldqo = fit
