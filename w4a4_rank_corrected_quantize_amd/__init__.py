@@ -39,6 +39,7 @@ Y bf16 [M][N].  Calls are enqueued on the current torch stream (or `stream`).
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Optional
 
@@ -1269,9 +1270,10 @@ def kv4_keep_path(cache: Kv4Cache, path, q_start, kv_len, block_table, T: Option
 def rope_frequencies(sections, theta: float = 10000.0, layout: int = ROPE_AXES_BLOCKS):
     """Frequency (fp64) and axis (int32) of every pair of channels, for axes of
     `sections` pairs each (host, numpy)."""
-    sec = np.ascontiguousarray(sections, np.int32)
-    if sec.ndim != 1:
+    if np.ndim(sections) != 1:
         raise ValueError("sections must be one-dimensional")
+    # what passes int32 stays too many, or negative, for the library to refuse
+    sec = np.array([min(max(operator.index(n), -1), _I32) for n in sections], np.int32)
     n = int(sec.clip(0).sum(dtype=np.int64))
     freq, axis = np.empty(min(n, 128), np.float64), np.empty(min(n, 128), np.int32)
     _check(lib().svdq_rope_frequencies(sec.ctypes.data, sec.size, float(theta), layout, freq.ctypes.data,
