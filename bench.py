@@ -37,17 +37,17 @@ NO_CLOCK = False
 # HBM traffic per launch of a workload's kernel, from two rocprofv3 --pmc runs
 # (FETCH_SIZE, then WRITE_SIZE) of this script, each divided by what the same
 # counter reads for a plain 512 MiB copy (--copy-calibration).  An entry is
-# only reported while the kernel source still hashes to the value it was
-# measured on; otherwise traffic is null.
+# only reported while the kernel source, with the device code that it includes,
+# still hashes to the value it was measured on; otherwise traffic is null.
 TRAFFIC = {
-    # FETCH_SIZE 73696.8 KiB / 0.50002 + WRITE_SIZE 110607.1 KiB / 1.00000 (per dispatch)
-    "fc1": {"source": "w4a4_gemm.hip", "source_sha": "cbd4ef2b5042054d", "bytes": 264186680},
-    # FETCH_SIZE 70211.1 KiB / 0.50002 + WRITE_SIZE 110593.5 KiB / 1.00000
-    "mx_fc1": {"source": "w4a4_gemm.hip", "source_sha": "cbd4ef2b5042054d", "bytes": 257034325},
-    # FETCH_SIZE 15680 KiB / 0.50002 + WRITE_SIZE 36 KiB / 1.00000
-    "awq_mod": {"source": "awq_gemv.hip", "source_sha": "fda4dd7b5f7b1013", "bytes": 32148220},
-    # FETCH_SIZE 197078 KiB / 0.50002 + WRITE_SIZE 110594 KiB / 1.00000
-    "nf4_fc1": {"source": "nf4_gemm.hip", "source_sha": "84b8f49923726640", "bytes": 516848112},
+    # FETCH_SIZE 73572.1 KiB / 0.50002 + WRITE_SIZE 110601.9 KiB / 1.00000 (per dispatch)
+    "fc1": {"source": "w4a4_gemm.hip", "source_sha": "783bff217a40e369", "bytes": 263925397},
+    # FETCH_SIZE 70190.8 KiB / 0.50002 + WRITE_SIZE 110600.1 KiB / 1.00000
+    "mx_fc1": {"source": "w4a4_gemm.hip", "source_sha": "783bff217a40e369", "bytes": 256998955},
+    # FETCH_SIZE 15680.0 KiB / 0.50002 + WRITE_SIZE 36.0 KiB / 1.00000
+    "awq_mod": {"source": "awq_gemv.hip", "source_sha": "8e9f775e255a96a4", "bytes": 32148095},
+    # FETCH_SIZE 197077.9 KiB / 0.50002 + WRITE_SIZE 110597.2 KiB / 1.00000
+    "nf4_fc1": {"source": "nf4_gemm.hip", "source_sha": "9324426f1560d454", "bytes": 516849367},
 }
 
 
@@ -63,10 +63,23 @@ def measured_traffic(workload):
 
 
 def _source_sha(name):
+    """Hash of a kernel source and of the device code in the headers that it
+    includes, without comments and blanks."""
     import hashlib
-    path = os.path.join(ROOT, "w4a4_rank_corrected_quantize_amd", "csrc", name)
-    with open(path, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+    import re
+    csrc = os.path.join(ROOT, "w4a4_rank_corrected_quantize_amd", "csrc")
+    todo, seen, digest = [name], set(), hashlib.sha256()
+    while todo:
+        path = os.path.join(csrc, todo.pop(0))
+        if path in seen or not os.path.exists(path):      # include/svdq.h: declarations
+            continue
+        seen.add(path)
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        todo += re.findall(r'#include "([^"]+)"', text)
+        if path.endswith(".hip") or "__device__" in text:
+            digest.update("".join(text.split()).encode())
+    return digest.hexdigest()[:16]
 
 
 def copy_calibration(mib):
