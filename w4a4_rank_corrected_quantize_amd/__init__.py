@@ -810,8 +810,7 @@ def _few_call(where, call, xq, xscale, h, wq, wscale, up, bias, prec, halves, la
                 and wscale.is_contiguous() and h.is_contiguous() and up.is_contiguous() and Y.is_contiguous()
                 and (bias is None or (bias.dtype is _BF and bias.shape == (N,) and bias.get_device() == dev
                                       and bias.is_contiguous()))
-                and M * KB < _ELEMENTS and N * KB < _ELEMENTS and M < _I32 and N < _I32 and KB < _ELEMENTS and r < _I32
-                and prec in (INT4, MXFP4)):
+                and M * KB < _ELEMENTS and N * KB < _ELEMENTS and r == RANK and prec in (INT4, MXFP4)):
             raw = _raw_stream(dev)
     except _MISFIT:
         pass
