@@ -264,9 +264,12 @@ svdq_status svdq_w4a4_linear(const uint8_t *xq, const void *xscale, const float 
  * svdq_w4a4_linear_few -- svdq_w4a4_linear for the few rows of a decoding step
  * (single tokens, a tree of drafted tokens), where the tiles of svdq_w4a4_linear
  * would leave most of the chip idle: one pass over the weights per 64 rows of X,
- * 16 weight rows or a few times that per block.  Meant for up to 64 rows, and for
- * more where the output is narrow.  Arguments as for svdq_w4a4_linear, with
- *   M            0 .. SVDQ_FEW_MAX_ROWS (SVDQ_ERR_UNSUPPORTED above)
+ * 16 weight rows or a few times that per block.  Faster than svdq_w4a4_linear for
+ * up to 64 rows (measured for K 1024 .. 11008, N 1024 .. 28672), and for more while
+ * M N stays below about 1.5 million (INT4 of K about 1024: 1 million): 256 rows of
+ * 6144 channels, 128 of 12288.  Arguments as for svdq_w4a4_linear, with
+ *   M            0 .. SVDQ_FEW_MAX_ROWS (SVDQ_ERR_UNSUPPORTED above: more rows, a
+ *                batch of many trees, go to svdq_w4a4_linear)
  * INT4: exact integer sums per group, scale product and accumulation in fp32.
  * Partial sums over K are added in a fixed order, so results are deterministic;
  * they may differ from svdq_w4a4_linear's in the last bf16 places.  One kernel
@@ -877,6 +880,9 @@ svdq_status svdq_kv4_tree_plan(const int32_t *parent, const int32_t *q_start, co
  *   mask, mask_words   as written by svdq_kv4_tree_plan, or any other: rows that
  *                see each other, or nothing (device, 4-byte aligned).  Bits past a
  *                sequence's rows are not used
+ * All drafted tokens are appended first, those too that no row sees (what their
+ * places hold has to be finite, as what svdq_kv4_append writes is).  There is no
+ * window: every row sees all keys before the drafted ones.
  * Other arguments, workspace, arithmetic and errors as for svdq_kv4_attention.
  * Deterministic for given sizes, bounds and lengths: where the keys are split, how
  * they are cut, and so the last places of a row, may depend on the q_start and

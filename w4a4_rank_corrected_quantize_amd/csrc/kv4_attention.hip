@@ -59,14 +59,17 @@
 //   512 places, two rounds.
 // Trees of drafted tokens (TREE): the same walk with a mask of the drafted keys, which
 // only steps that reach them read (three words per column).
-//   8 tokens over 1000 keys, 32 heads over 8 of 128, INT4: 9.0 + 2.5 us, latencies as
+//   8 tokens over 1000 keys, 32 heads over 8 of 128, INT4: 8.5 + 3.1 us, latencies as
 //   for one token.
 //   16 x 24 .. 64 tokens over 3642 .. 16348 keys, 32 heads over 8 of 128, MXFP4 (106
-//   GF): 158 us and 10 for the sums, with the plan 167 in a graph = 637 TFLOP/s; the
-//   fixed division instead of KvEven 230.  Bound by the tiles' padding (18 %, half tiles
-//   at 4 / 5 of a full one) and instruction issue: a full tile's step takes 1.25 us of
-//   a compute unit, 1.19 in 4608 x 4608.
-//   9 x 1 .. 130 tokens over up to 5000 keys, 12 heads over 4 of 64, INT4: 31 + 4.4 us.
+//   GF): 148 us and 10 for the sums (warm trace, one batch again and again); three
+//   batches in turn, with the plan, 168 in a graph = 635 TFLOP/s; the fixed division
+//   instead of KvEven 230.  Bound by the tiles' padding (18 %, half tiles at 4 / 5 of a
+//   full one) and instruction issue: a full tile's step takes 1.25 us of a compute unit,
+//   1.19 in 4608 x 4608.  INT4: 193 us and 10, 213 in a graph = 500 TFLOP/s: the same
+//   products and 1.6 times the vector instructions (scales of keys and values in fp32).
+//   9 x 1 .. 130 tokens over up to 5000 keys, 12 heads over 4 of 64: INT4 32 + 4.6 us,
+//   MXFP4 31 + 4.6.
 // Not kept: 48 rows per wave and three waves per SIMD (spills), 64 rows and one
 // wave per SIMD (443 us: nothing beside a wave's waits), a branch
 // around the rescaling per column (copies of the sums), ordering hints instead

@@ -18,10 +18,12 @@
 // sines and takes one head after the other.
 //
 // What bounds it, and what it measured: 4608 tokens, 48 heads of 128, norm: 23.2
-// us for 116 MB = 5.0 TB/s, a large copy's rate (5.1); keys and queries alike in 64
-// bits 25.6 (conversions).  The table of their angles 3.4 us.  4063 tokens, 28 + 4
-// heads of queries and keys, 4 of values, into the INT4 cache: 17.4 us for 71 MB: the
-// keys' and values' blocks (64 bits, then the quantizer) beside the copy.  One token, 32 heads over 8: 4.1 us, a launch and loads in turn.
+// us for 116 MB = 5.0 TB/s, a large copy's rate (5.1), the same heads again and again
+// 20.9 (of 48 pairs 20.6); keys and queries alike in 64 bits 25.6 (conversions).  The
+// table of their angles 3.2 us.  4063 tokens, 28 + 4 heads of queries and keys, 4 of
+// values, into the INT4 cache: 17.8 us for 71 MB: the keys' and values' blocks (64
+// bits, then the quantizer) beside the copy.  One token, 32 heads over 8: 4.1 us, a
+// launch and loads in turn.
 #include "kv4_codes.h"
 
 #include <cmath>

@@ -24,14 +24,17 @@
 // low parts) and the epilogue follow in fp32, rounded once.  Results depend on
 // the sizes alone.
 //
-// What bounds it, and what it measured (in a graph, other weights in between):
-//   1 x 4096 -> 2 x 14336, MXFP4: 11.3 us for 64 MB = 5.7 TB/s: the memory (part of
-//   it still lies in the last-level cache); INT4 17.6 us for 66 MB, the widening
-//   of the codes beside it.
-//   1 x 4096 -> 6144, INT4: 6.5 us for 14.6 MB: 384 blocks of one wave's length, a
-//   launch (2.5 us), two latencies of memory and the sum of eight waves.
-//   48 x 11008 -> 4096, MXFP4: 9.6 us for 24.9 MB: every block reads all of X from
-//   the L2 (68 MB in all) next to its weights.
+// What bounds it, and what it measured (in a graph; weights out of the HBM, over 1
+// GB of others in between / three sets in turn, which the last-level cache holds in
+// part):
+//   1 x 4096 -> 2 x 14336, MXFP4: 14.9 / 11.7 us for 64 MB = 4.3 TB/s: the memory;
+//   INT4 18.4 / 14.7 us for 68 MB, the widening of the codes beside it.
+//   1 x 4096 -> 6144, INT4: 6.8 / 6.3 us for 14.6 MB: 384 blocks of one wave's length,
+//   a launch (2.5 us), two latencies of memory and the sum of eight waves.
+//   48 x 11008 -> 4096, MXFP4: 12.7 / 9.7 us for 24.9 MB: every block reads all of X
+//   from the L2 (68 MB in all) next to its weights; INT4 16.1 / 13.3, 48 x 14336 20.2 /
+//   16.3: every wave widens its lines of X for one tile of channels.
+//   64 x 4096 -> 2 x 14336: MXFP4 21.9 / 17.5, INT4 40.1 / 36.1 us, the widening.
 #include "svdq_internal.h"
 #include "svdq_quant.h"
 #include "w4a4_epilogue.h"
