@@ -2,9 +2,9 @@
 // the nodes' parents, and the move of an accepted path to where the next
 // tokens follow it.  Both are a few bytes per token and bound by latency: one
 // launch each, no length known to the host.  Measured: the plan of 8 nodes 2.6
-// us, of 16 x 24 .. 64 nodes 5.2, of 9 x 1 .. 130 nodes 5.4 (a walk per row up to the
+// us, of 16 x 24 .. 64 nodes 5.1, of 9 x 1 .. 130 nodes 4.7 (a walk per row up to the
 // root 7.4); a path of 8 nodes, 8 heads of 128, 2.9 us; 64 paths of up to 64 nodes, 8
-// heads, 8.1 us (a node at a time 10.6).
+// heads, 7.0 us (a node at a time 10.6).
 #include "kv4.h"
 
 namespace svdq {
